@@ -109,6 +109,14 @@ enum {
                                    masked calls by themselves */
 };
 
+/* Element type of a cache's pages. */
+enum {
+  MOE_W4A16_CACHE_BF16 = 0,
+  MOE_W4A16_CACHE_E4M3 = 1 /* 8-bit float (4 exponent, 3 mantissa bits, no infinities); value = element * scale */
+};
+/* Element type of the residual stream of moe_w4a16_block_norm. */
+enum { MOE_W4A16_RESIDUAL_BF16 = 0, MOE_W4A16_RESIDUAL_F32 = 1 };
+
 #define MOE_W4A16_MAGIC 0x34413457u /* "W4A4" little-endian tag */
 #define MOE_W4A16_VERSION 1u
 #define MOE_W4A16_MAX_EXPERTS 1024
@@ -116,6 +124,12 @@ enum {
 #define MOE_W4A16_STATIC_SCRATCH_BYTES (64u << 20) /* scratch of moe_w4a16_indexed_noalloc */
 #define MOE_W4A16_WAIT_LIMIT_NS 2000000000ull      /* default limit of a device pipeline wait */
 #define MOE_W4A16_ROUTED_MAX_ROWS 4096             /* routed rows of a moe_w4a16_indexed_routed call */
+
+#define MOE_W4A16_LATENT_DIM 576                   /* channels of a latent cache row ... */
+#define MOE_W4A16_LATENT_VALUE_DIM 512             /* ... of which the first are the values */
+#define MOE_W4A16_MAX_HEAD_DIM 256                 /* head_dim of moe_w4a16_paged_attention: 16, 32, ... 256 */
+#define MOE_W4A16_MAX_PAGE_SIZE 4096               /* tokens of a cache page */
+#define MOE_W4A16_MAX_NORM_WIDTH 32768             /* row length of moe_w4a16_block_norm */
 
 /* Host-side description of a prepared weight, filled by moe_w4a16_prepare and
  * passed by address to every GEMM call (host pointer). */
@@ -423,6 +437,173 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_masked(const uint16_t* a3, int num_expe
                                   int expected_m, const moe_w4a16_desc* desc, const void* prepared,
                                   const int32_t* row_ids, int num_tokens, int top_k, const float* topk_weights,
                                   uint32_t flags, uint16_t* c, void* ws, size_t ws_bytes, moe_w4a16_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged cache and the attention that reads it: the half of a decoder layer's
+ * decode step beside the MoE FFN.
+ *
+ * A cache is a pool of pages of page_size tokens. Which pages a sequence owns is
+ * its row of `tables` (int32 [num_seqs, table_stride], the first max_pages
+ * columns): token j of the sequence sits in page tables[seq][j / page_size] at
+ * offset j % page_size. A negative entry is no page: its tokens (freed ones, as
+ * behind a sliding window) are not seen. `lens` (int32 [num_seqs]) holds the
+ * token counts, `refs` (int32 [num_pages]) how many table rows hold each page; a
+ * page is free when its count is 0. Pages are always taken lowest free id first,
+ * in the order of the call's entries, so every result is unique.
+ * Lengths above max_pages * page_size, page ids at or above num_pages and sequence
+ * ids outside [0, num_seqs) are skipped (lengths: cut) and recorded in `ws` as
+ * MOE_W4A16_ERR_BAD_INDEX.
+ * ------------------------------------------------------------------------- */
+
+/* A layer's pages (host pointer; `k` and `v` are device pointers). Element (page p,
+ * token t, head h, channel c) sits at p * page_stride + t * token_stride +
+ * h * head_stride + c, in elements; the strides are the same for k and v. k, v and
+ * the strides are multiples of 16 bytes. */
+typedef struct moe_w4a16_pages {
+  void* k;
+  void* v;              /* NULL for a latent cache */
+  int32_t dtype;        /* MOE_W4A16_CACHE_* */
+  int32_t num_pages;
+  int32_t page_size;    /* 1 .. MOE_W4A16_MAX_PAGE_SIZE tokens */
+  int32_t reserved;     /* 0 */
+  int64_t page_stride, token_stride, head_stride;
+  float k_scale, v_scale; /* E4M3: an element stands for element * scale; BF16: 1 */
+} moe_w4a16_pages;
+
+/* Workspace bytes of the two attention calls for num_heads query heads over
+ * num_kv_heads cache heads of head_dim channels (latent: 1 head of
+ * MOE_W4A16_LATENT_DIM). Independent of batch and lengths. Zero it once
+ * (moe_w4a16_workspace_init); every call leaves its counters at zero. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_attention_workspace_size(int num_heads, int num_kv_heads, int head_dim,
+                                                                  size_t* bytes);
+
+/* Attention of one new token per sequence over a paged cache, grouped heads: query
+ * head h reads cache head h / (num_heads / num_kv_heads).
+ *   s[j] = scale * k_scale * <q, K_j> over the seen tokens j, max(0, len - window) <= j < len
+ *   (window 0: all), whose table entry is a page;
+ *   out = v_scale * sum_j exp(s[j] - m) V_j / l,  lse = m + ln l,  m = max s, l = sum_j exp(s[j] - m);
+ *   nothing seen: out = 0, lse = -infinity.
+ * Scores, maxima, sums and outputs are FP32 (the products take the probabilities
+ * rounded to BF16, or to FP16 over E4M3 pages); the output is rounded once. What lies
+ * in unseen slots, NaN included, does not reach the result.
+ *   q    bf16 [batch, num_heads, head_dim], q_stride elements between sequences; 16-byte aligned
+ *   head_dim  a multiple of 16, at most MOE_W4A16_MAX_HEAD_DIM (else UNSUPPORTED)
+ *   seq_ids  int32 [batch]: the row of tables and lens of each query (NULL: query b reads row b)
+ *   out  bf16 [batch, num_heads, head_dim] dense; lse float [batch, num_heads] or NULL */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_attention(const uint16_t* q, int64_t q_stride, int batch, int num_heads,
+                                                         int num_kv_heads, int head_dim, const moe_w4a16_pages* cache,
+                                                         const int32_t* tables, int64_t table_stride, int max_pages,
+                                                         const int32_t* lens, const int32_t* seq_ids, int num_seqs,
+                                                         float scale, int window, uint16_t* out, float* lse, void* ws,
+                                                         size_t ws_bytes, moe_w4a16_stream_t stream);
+
+/* The same over a latent cache, BF16 only: one row of MOE_W4A16_LATENT_DIM channels per
+ * token (cache->k; cache->v is NULL) is every head's key, its first
+ * MOE_W4A16_LATENT_VALUE_DIM channels every head's value.
+ *   q    bf16 [batch, num_heads, MOE_W4A16_LATENT_DIM] (queries already taken into the latent space)
+ *   out  bf16 [batch, num_heads, MOE_W4A16_LATENT_VALUE_DIM] */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_latent_attention(const uint16_t* q, int64_t q_stride, int batch, int num_heads,
+                                                          const moe_w4a16_pages* cache, const int32_t* tables,
+                                                          int64_t table_stride, int max_pages, const int32_t* lens,
+                                                          const int32_t* seq_ids, int num_seqs, float scale, int window,
+                                                          uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                                          moe_w4a16_stream_t stream);
+
+/* Writes new tokens' rows into their pages. Row i goes to token positions[i] of sequence
+ * seq_ids[i]; a negative position is skipped, a position without a page recorded as
+ * MOE_W4A16_ERR_BAD_INDEX. E4M3 pages: the element nearest to k / k_scale (ties to even, cut to
+ * +-448, NaN stays NaN). Two rows for one slot: either may win.
+ *   k, v   bf16 [num_tokens, num_heads, head_dim], k_stride / v_stride elements between tokens,
+ *          16-byte aligned; v NULL with cache->v NULL (a latent cache)
+ *   head_dim  a multiple of 8 (E4M3: 16)
+ *   ws     at least MOE_W4A16_WS_HEADER_BYTES */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_append(const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                                      int64_t v_stride, int num_tokens, int num_heads, int head_dim,
+                                                      const moe_w4a16_pages* cache, const int32_t* tables,
+                                                      int64_t table_stride, int max_pages, int num_seqs,
+                                                      const int32_t* seq_ids, const int32_t* positions, void* ws,
+                                                      size_t ws_bytes, moe_w4a16_stream_t stream);
+
+/* Workspace bytes of the calls below for a pool of num_pages pages and `count` entries. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_workspace_size(int num_pages, int count, size_t* bytes);
+
+/* Grows sequences: entry i adds counts[i] tokens (counts NULL: one) to sequence seq_ids[i],
+ * taking free pages where the new length needs them, and returns the old length (the first
+ * new token's position) in positions[i]. An entry whose pages are no longer there, or whose
+ * new length passes max_pages * page_size, is left as it was, positions[i] = -1, and recorded
+ * as MOE_W4A16_ERR_CAPACITY: entry i gets its pages if the entries up to and including it
+ * need no more than are free. Sequence ids of a call are distinct. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_extend(int32_t* refs, int num_pages, int32_t* tables,
+                                                      int64_t table_stride, int max_pages, int32_t* lens, int num_seqs,
+                                                      const int32_t* seq_ids, const int32_t* counts, int count,
+                                                      int page_size, int32_t* positions, void* ws, size_t ws_bytes,
+                                                      moe_w4a16_stream_t stream);
+
+/* A pool's storage as the page copies see it (host pointer): plane i (a layer's keys, a
+ * layer's values, ...) holds page p as page_bytes consecutive bytes at base + i * plane_stride
+ * + p * page_stride. All byte counts and addresses are multiples of 16. */
+typedef struct moe_w4a16_pool {
+  void* base;
+  int32_t num_planes, num_pages;
+  int64_t plane_stride, page_stride, page_bytes;
+} moe_w4a16_pool;
+
+/* Forks: sequence children[i] (empty) becomes a copy of parents[i]. Full pages are shared
+ * (refs + 1); a partly filled last page is copied, in every plane, into a free page of the
+ * child's own. Freed entries of the parent stay freed. A fork whose page is no longer there
+ * is left empty and recorded as MOE_W4A16_ERR_CAPACITY; a child that is not empty as
+ * MOE_W4A16_ERR_BAD_INDEX. Children are distinct and none is a parent of the same call. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_fork(const moe_w4a16_pool* pool, int32_t* refs, int32_t* tables,
+                                                    int64_t table_stride, int max_pages, int32_t* lens, int num_seqs,
+                                                    const int32_t* parents, const int32_t* children, int count,
+                                                    int page_size, void* ws, size_t ws_bytes,
+                                                    moe_w4a16_stream_t stream);
+
+/* Frees: keep NULL: every page of sequence seq_ids[i] (refs - 1, table entries -1) and its
+ * length becomes 0. Otherwise only the pages wholly before its newest keep[i] tokens, and its
+ * length stays unless keep[i] <= 0. A sequence named twice is freed once. A count that is already 0
+ * is recorded as MOE_W4A16_ERR_BAD_INDEX and stays 0. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_free(int32_t* refs, int num_pages, int32_t* tables,
+                                                    int64_t table_stride, int max_pages, int32_t* lens, int num_seqs,
+                                                    const int32_t* seq_ids, const int32_t* keep, int count,
+                                                    int page_size, void* ws, size_t ws_bytes,
+                                                    moe_w4a16_stream_t stream);
+
+/* Copies page src[i] to page dst[i] in every plane. No dst is a src or another dst of the call. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_copy(const moe_w4a16_pool* pool, const int32_t* src, const int32_t* dst,
+                                                    int count, void* ws, size_t ws_bytes, moe_w4a16_stream_t stream);
+
+/* Compacts: with L pages in use, the used pages with ids >= L move, in ascending order, into
+ * the free ids below L, in every plane; refs and tables follow.
+ *   refs_out   int32 [num_pages] (may be refs); tables_out int32 [num_seqs, table_stride] (may be
+ *              tables), of which the first max_pages columns are written
+ *   page_map   int32 [num_pages] out: new id of each page, -1 for free ones
+ *   num_live   int32 [1] out: L */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_compact(const moe_w4a16_pool* pool, const int32_t* refs,
+                                                       const int32_t* tables, int64_t table_stride, int max_pages,
+                                                       int num_seqs, int32_t* refs_out, int32_t* tables_out,
+                                                       int32_t* page_map, int32_t* num_live, void* ws, size_t ws_bytes,
+                                                       moe_w4a16_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms around a block (attention or FFN) on the residual stream, in one pass:
+ *   u = x, or x / sqrt(mean(x^2) + eps) * w_post       (w_post NULL: x itself)
+ *   h' = residual_scale * h + block_scale * gate * u     (gate NULL: 1)
+ *   y = h' / sqrt(mean(h'^2) + eps) * w_pre             (the next block's input)
+ * in FP32, each output rounded once (y from the unrounded h').
+ *   x      bf16 [rows, n], the block's output; NULL: h' = residual_scale * h
+ *   h      [rows, n] of residual_dtype (MOE_W4A16_RESIDUAL_*); h_out the same or NULL, may be h
+ *   gate   bf16 [gate_rows, n] dense or NULL; gate_rows divides rows, row t takes gate row
+ *          t / (rows / gate_rows): one for all tokens, one per sequence, one per token
+ *   w_post, w_pre  bf16 [n]; w_pre and y both or neither; x NULL needs gate and w_post NULL
+ *   n      1 .. MOE_W4A16_MAX_NORM_WIDTH; strides in elements between rows (any; multiples of 8
+ *          with 16-byte aligned pointers take the vector path) */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_block_norm(const uint16_t* x, int64_t x_stride, const void* h, int64_t h_stride,
+                                                    int residual_dtype, const uint16_t* gate, int gate_rows,
+                                                    const uint16_t* w_post, const uint16_t* w_pre, int rows, int n,
+                                                    float eps, float residual_scale, float block_scale, void* h_out,
+                                                    int64_t h_out_stride, uint16_t* y, int64_t y_stride,
+                                                    moe_w4a16_stream_t stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

@@ -476,3 +476,13 @@ def masked(a3: torch.Tensor, masked_m: torch.Tensor, expected_m: int, pw: Prepar
                                      _ptr(pw.buffer), _ptr(row_ids), num_tokens, top_k, _ptr(topk_weights), flags,
                                      _ptr(out), _ptr(ws), ws.numel(), _stream(dev)), "masked")
     return out
+
+
+# ---------------------------------------------------------------------------
+# paged cache, attention over it, norms around a block
+# ---------------------------------------------------------------------------
+
+from .block import (CACHE_BF16, CACHE_E4M3, LATENT_DIM, LATENT_VALUE_DIM, MAX_HEAD_DIM, MAX_NORM_WIDTH,  # noqa: E402,F401
+                    MAX_PAGE_SIZE, RESIDUAL_BF16, RESIDUAL_F32, attention_workspace, attention_workspace_size,
+                    block_norm, cache_append, cache_compact, cache_copy, cache_extend, cache_fork, cache_free,
+                    cache_workspace, cache_workspace_size, latent_attention, paged_attention)

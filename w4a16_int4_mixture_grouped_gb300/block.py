@@ -1,0 +1,437 @@
+"""Binding of the paged cache, the attention that reads it and the block norms.
+
+The half of a decoder layer's decode step beside the MoE FFN. As in the package
+itself: argument marshalling only, names as in include/moe_w4a16.h without the
+``moe_w4a16_`` prefix, MoeW4A16Error on a non-OK status. A call runs on the
+current stream of its tensors' device; the page calls record what they find
+wrong on the device (ids out of range, no free page) in the workspace, to be
+read with get_device_error.
+
+A cache's pages are tensors [num_pages, page_size, heads, dim] (latent:
+[num_pages, page_size, 576]) of torch.bfloat16 or torch.float8_e4m3fn whose
+last dimension is dense; tables int32 [num_seqs, max_pages] hold each sequence's
+pages in order, -1 where there is none, lens int32 [num_seqs] the token counts,
+refs int32 [num_pages] how many tables hold a page.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import MoeW4A16Error, WS_HEADER_BYTES, lib, workspace_init
+
+CACHE_BF16, CACHE_E4M3 = 0, 1
+RESIDUAL_BF16, RESIDUAL_F32 = 0, 1
+LATENT_DIM, LATENT_VALUE_DIM = 576, 512
+MAX_HEAD_DIM, MAX_PAGE_SIZE, MAX_NORM_WIDTH = 256, 4096, 32768
+
+_CACHE_DTYPES = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3}
+_BF16 = torch.bfloat16
+_I32 = torch.int32
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("num_planes", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("plane_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
+
+
+_P, _I, _L, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_PAGES, _POOL = ctypes.POINTER(Pages), ctypes.POINTER(Pool)
+_SIGNATURES = {
+    "attention_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
+    "paged_attention": [_P, _L, _I, _I, _I, _I, _PAGES, _P, _L, _I, _P, _P, _I, _F, _I, _P, _P, _P, _SZ, _P],
+    "latent_attention": [_P, _L, _I, _I, _PAGES, _P, _L, _I, _P, _P, _I, _F, _I, _P, _P, _P, _SZ, _P],
+    "cache_append": [_P, _L, _P, _L, _I, _I, _I, _PAGES, _P, _L, _I, _I, _P, _P, _P, _SZ, _P],
+    "cache_workspace_size": [_I, _I, ctypes.POINTER(_SZ)],
+    "cache_extend": [_P, _I, _P, _L, _I, _P, _I, _P, _P, _I, _I, _P, _P, _SZ, _P],
+    "cache_fork": [_POOL, _P, _P, _L, _I, _P, _I, _P, _P, _I, _I, _P, _SZ, _P],
+    "cache_free": [_P, _I, _P, _L, _I, _P, _I, _P, _P, _I, _I, _P, _SZ, _P],
+    "cache_copy": [_POOL, _P, _P, _I, _P, _SZ, _P],
+    "cache_compact": [_POOL, _P, _P, _L, _I, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "block_norm": [_P, _L, _P, _L, _I, _P, _I, _P, _P, _I, _I, _F, _F, _F, _P, _L, _P, _L, _P],
+}
+_FN = {}
+for _name, _args in _SIGNATURES.items():
+    _fn = getattr(lib, "moe_w4a16_" + _name)
+    _fn.restype = ctypes.c_int
+    _fn.argtypes = _args
+    _FN[_name] = _fn
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """The C entry point on dev's current stream (made current for the launch where it is not)."""
+    if torch.cuda.current_device() == dev.index:
+        status = _FN[name](*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = _FN[name](*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        raise MoeW4A16Error(status, name)
+
+
+def _need(t: torch.Tensor, name: str, dtype, dim: int, dev: Optional[torch.device] = None) -> torch.Tensor:
+    """A CUDA tensor of that type and rank whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    if t.stride(-1) != 1 and t.size(-1) > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return t
+
+
+def _vector(t: Optional[torch.Tensor], name: str, n: int, dev: torch.device, dtype=_I32) -> Optional[int]:
+    """Address of a dense 1-D tensor of n elements (None for None)."""
+    if t is None:
+        return None
+    _need(t, name, dtype, 1, dev)
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return t.data_ptr()
+
+
+def _rows_dense(t: torch.Tensor, name: str) -> torch.Tensor:
+    """The trailing two dimensions [heads, dim] lie dense behind each other."""
+    if t.dim() == 3 and t.size(1) > 1 and t.stride(1) != t.size(2):
+        raise ValueError(f"{name}: heads must be dense")
+    return t
+
+
+def _outer_stride(t: torch.Tensor) -> int:
+    """Stride of the first dimension (of a single row: the row's own length)."""
+    return t.stride(0) if t.size(0) > 1 else t[0].numel()
+
+
+def _table(tables: torch.Tensor, dev: torch.device) -> Tuple[int, int, int, int]:
+    """(address, row stride, max_pages, num_seqs)."""
+    _need(tables, "tables", _I32, 2, dev)
+    s, m = tables.shape
+    return tables.data_ptr(), (tables.stride(0) if s > 1 else m), m, s
+
+
+def _pages(k: torch.Tensor, v: Optional[torch.Tensor], dev: torch.device, k_scale: float, v_scale: float) -> Pages:
+    rank = 4 if v is not None else 3
+    _need(k, "k_pages", None, rank, dev)
+    if k.dtype not in _CACHE_DTYPES:
+        raise TypeError(f"pages have dtype {k.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
+    st = k.stride()
+    if v is not None:
+        _need(v, "v_pages", k.dtype, 4, dev)
+        if v.shape != k.shape or v.stride() != st:
+            raise ValueError("k_pages and v_pages must have the same shape and strides")
+    c = Pages()
+    c.k = k.data_ptr()
+    c.v = v.data_ptr() if v is not None else None
+    c.dtype = _CACHE_DTYPES[k.dtype]
+    c.num_pages, c.page_size = k.shape[0], k.shape[1]
+    c.page_stride, c.token_stride = st[0], st[1]
+    c.head_stride = st[2] if v is not None else k.shape[2]
+    c.k_scale, c.v_scale = k_scale, v_scale
+    return c
+
+
+def _pool(pool: torch.Tensor) -> Pool:
+    """pool [planes, num_pages, ...], each page dense."""
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
+        raise ValueError("pool must be a CUDA tensor")
+    if pool.dim() < 3:
+        raise ValueError("pool must be [planes, num_pages, ...]")
+    size = pool.element_size()
+    dense = 1
+    for n, s in zip(reversed(pool.shape[2:]), reversed(pool.stride()[2:])):
+        if n > 1 and s != dense:
+            raise ValueError("pool: each page must be dense")
+        dense *= n
+    p = Pool()
+    p.base = pool.data_ptr()
+    p.num_planes, p.num_pages = pool.shape[0], pool.shape[1]
+    p.plane_stride, p.page_stride, p.page_bytes = pool.stride(0) * size, pool.stride(1) * size, dense * size
+    return p
+
+
+def _ws(ws: torch.Tensor, dev: torch.device) -> Tuple[int, int]:
+    _need(ws, "ws", torch.uint8, 1, dev)
+    return ws.data_ptr(), ws.numel()
+
+
+def _alloc_ws(nbytes: int, device) -> torch.Tensor:
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    ws = torch.empty(max(nbytes, WS_HEADER_BYTES), dtype=torch.uint8, device=dev)
+    workspace_init(ws)
+    return ws
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+def attention_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    out = _SZ(0)
+    status = _FN["attention_workspace_size"](num_heads, num_kv_heads, head_dim, ctypes.byref(out))
+    if status != 0:
+        raise MoeW4A16Error(status, "attention_workspace_size")
+    return int(out.value)
+
+
+def attention_workspace(batch: int, num_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """Allocates (through torch) and zeroes a workspace for either attention call (latent: one head of 576). It
+    does not depend on the lengths, and one made for a batch serves any other."""
+    del batch
+    return _alloc_ws(attention_workspace_size(num_heads, num_kv_heads, head_dim), device)
+
+
+def _attention_out(q, width, out, lse):
+    b, h = q.shape[0], q.shape[1]
+    if out is None:
+        out = q.new_empty((b, h, width))
+    else:
+        _need(out, "out", _BF16, 3, q.device)
+        if out.shape != (b, h, width) or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous [{b}, {h}, {width}]")
+    if lse is None:
+        lse = torch.empty((b, h), dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", torch.float32, 2, q.device)
+        if lse.shape != (b, h) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{b}, {h}]")
+    return out, lse
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, tables: torch.Tensor,
+                    lens: torch.Tensor, ws: torch.Tensor, scale: Optional[float] = None, window: int = 0,
+                    k_scale: float = 1.0, v_scale: float = 1.0, seq_ids: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One new token per sequence over its pages: q [B, H, D] -> (out bf16 [B, H, D], lse float [B, H]).
+
+    scale defaults to D ** -0.5; window counts the newest tokens seen (0: all); seq_ids [B] names the row of
+    tables and lens of each query (default: row b)."""
+    _rows_dense(_need(q, "q", _BF16, 3), "q")
+    dev = q.device
+    b, h, d = q.shape
+    c = _pages(k_pages, v_pages, dev, k_scale, v_scale)
+    if v_pages is None or k_pages.shape[3] != d:
+        raise ValueError(f"pages must hold keys and values of {d} channels")
+    ta, ts, mp, ns = _table(tables, dev)
+    out, lse = _attention_out(q, d, out, lse)
+    wa, wn = _ws(ws, dev)
+    _call("paged_attention", dev, q.data_ptr(), _outer_stride(q) if b else h * d, b, h, k_pages.shape[2], d,
+          ctypes.byref(c), ta, ts, mp, _vector(lens, "lens", ns, dev), _vector(seq_ids, "seq_ids", b, dev), ns,
+          d ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), wa, wn)
+    return out, lse
+
+
+def latent_attention(q: torch.Tensor, pages: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, ws: torch.Tensor,
+                     scale: float, window: int = 0, seq_ids: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The same over a latent cache: q [B, H, 576], pages [P, S, 576] -> (out bf16 [B, H, 512], lse [B, H])."""
+    _rows_dense(_need(q, "q", _BF16, 3), "q")
+    dev = q.device
+    b, h, d = q.shape
+    c = _pages(pages, None, dev, 1.0, 1.0)
+    if d != LATENT_DIM or pages.shape[2] != LATENT_DIM:
+        raise ValueError(f"q and pages must have {LATENT_DIM} channels")
+    ta, ts, mp, ns = _table(tables, dev)
+    out, lse = _attention_out(q, LATENT_VALUE_DIM, out, lse)
+    wa, wn = _ws(ws, dev)
+    _call("latent_attention", dev, q.data_ptr(), _outer_stride(q) if b else h * d, b, h, ctypes.byref(c), ta, ts, mp,
+          _vector(lens, "lens", ns, dev), _vector(seq_ids, "seq_ids", b, dev), ns, scale, window, out.data_ptr(),
+          lse.data_ptr(), wa, wn)
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# cache
+# ---------------------------------------------------------------------------
+
+def cache_append(k: torch.Tensor, k_pages: torch.Tensor, tables: torch.Tensor, seq_ids: torch.Tensor,
+                 positions: torch.Tensor, ws: torch.Tensor, v: Optional[torch.Tensor] = None,
+                 v_pages: Optional[torch.Tensor] = None, k_scale: float = 1.0, v_scale: float = 1.0) -> None:
+    """Writes rows k, v [T, heads, dim] (latent: k [T, 576] alone) to token positions[i] of sequence seq_ids[i]."""
+    latent = v_pages is None
+    if (v is None) != latent:
+        raise ValueError("v and v_pages go together")
+    _rows_dense(_need(k, "k", _BF16, 2 if latent else 3), "k")
+    dev = k.device
+    c = _pages(k_pages, v_pages, dev, k_scale, v_scale)
+    if tuple(k_pages.shape[2:]) != tuple(k.shape[1:]):
+        raise ValueError(f"rows are {tuple(k.shape[1:])}, pages hold {tuple(k_pages.shape[2:])}")
+    n = k.shape[0]
+    heads, dim = (1, k.shape[1]) if latent else k.shape[1:]
+    if not latent:
+        _rows_dense(_need(v, "v", _BF16, 3, dev), "v")
+        if v.shape != k.shape:
+            raise ValueError("k and v must have the same shape")
+    ta, ts, mp, ns = _table(tables, dev)
+    wa, wn = _ws(ws, dev)
+    _call("cache_append", dev, k.data_ptr(), _outer_stride(k) if n else heads * dim,
+          None if latent else v.data_ptr(), 0 if latent else (_outer_stride(v) if n else heads * dim), n, heads, dim,
+          ctypes.byref(c), ta, ts, mp, ns, _vector(seq_ids, "seq_ids", n, dev),
+          _vector(positions, "positions", n, dev), wa, wn)
+
+
+def cache_workspace_size(num_pages: int, count: int) -> int:
+    out = _SZ(0)
+    status = _FN["cache_workspace_size"](num_pages, count, ctypes.byref(out))
+    if status != 0:
+        raise MoeW4A16Error(status, "cache_workspace_size")
+    return int(out.value)
+
+
+def cache_workspace(num_pages: int, count: int, device=None) -> torch.Tensor:
+    """Allocates (through torch) and zeroes a workspace for page calls of up to `count` entries on a pool of
+    num_pages pages; it also serves cache_append and cache_copy."""
+    return _alloc_ws(cache_workspace_size(num_pages, count), device)
+
+
+def cache_extend(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, seq_ids: torch.Tensor, page_size: int,
+                 ws: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Grows the sequences by counts tokens (default one each), taking free pages; -> positions [n], each
+    sequence's old length, -1 where it did not fit."""
+    _need(refs, "refs", _I32, 1)
+    dev = refs.device
+    n = seq_ids.numel()
+    ta, ts, mp, ns = _table(tables, dev)
+    if out is None:
+        out = torch.empty(n, dtype=_I32, device=dev)
+    wa, wn = _ws(ws, dev)
+    _call("cache_extend", dev, refs.data_ptr(), refs.numel(), ta, ts, mp, _vector(lens, "lens", ns, dev), ns,
+          _vector(seq_ids, "seq_ids", n, dev), _vector(counts, "counts", n, dev), n, page_size,
+          _vector(out, "out", n, dev), wa, wn)
+    return out
+
+
+def cache_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
+               children: torch.Tensor, page_size: int, ws: torch.Tensor) -> None:
+    """Makes each (empty) children[i] a copy of parents[i]: full pages shared, a partly filled last page of pool
+    [planes, num_pages, ...] copied in every plane."""
+    p = _pool(pool)
+    dev = pool.device
+    n = parents.numel()
+    ta, ts, mp, ns = _table(tables, dev)
+    wa, wn = _ws(ws, dev)
+    _call("cache_fork", dev, ctypes.byref(p), _vector(refs, "refs", p.num_pages, dev), ta, ts, mp,
+          _vector(lens, "lens", ns, dev), ns, _vector(parents, "parents", n, dev),
+          _vector(children, "children", n, dev), n, page_size, wa, wn)
+
+
+def cache_free(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, seq_ids: torch.Tensor, page_size: int,
+               ws: torch.Tensor, keep: Optional[torch.Tensor] = None) -> None:
+    """Frees the sequences' pages; with keep [n], only those wholly before the newest keep[i] tokens."""
+    _need(refs, "refs", _I32, 1)
+    dev = refs.device
+    n = seq_ids.numel()
+    ta, ts, mp, ns = _table(tables, dev)
+    wa, wn = _ws(ws, dev)
+    _call("cache_free", dev, refs.data_ptr(), refs.numel(), ta, ts, mp, _vector(lens, "lens", ns, dev), ns,
+          _vector(seq_ids, "seq_ids", n, dev), _vector(keep, "keep", n, dev), n, page_size, wa, wn)
+
+
+def cache_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor) -> None:
+    """pool[:, dst[i]] = pool[:, src[i]]; no destination is a source or another destination."""
+    p = _pool(pool)
+    dev = pool.device
+    n = src.numel()
+    wa, wn = _ws(ws, dev)
+    _call("cache_copy", dev, ctypes.byref(p), _vector(src, "src", n, dev), _vector(dst, "dst", n, dev), n, wa, wn)
+
+
+def cache_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, ws: torch.Tensor,
+                  refs_out: Optional[torch.Tensor] = None, tables_out: Optional[torch.Tensor] = None):
+    """Moves the pages in use to the front of the pool -> (refs, tables, page_map [num_pages], num_live [1]).
+
+    The new counts and tables are new tensors unless refs_out / tables_out (which may be refs / tables) are given."""
+    p = _pool(pool)
+    dev = pool.device
+    ra = _vector(refs, "refs", p.num_pages, dev)
+    ta, ts, mp, ns = _table(tables, dev)
+    if refs_out is None:
+        refs_out = torch.empty(p.num_pages, dtype=_I32, device=dev)
+    if tables_out is None:
+        tables_out = torch.empty_strided(tables.shape, (ts, 1), dtype=_I32, device=dev)
+    to, tos, _, _ = _table(tables_out, dev)
+    if tables_out.shape != tables.shape or tos != ts:
+        raise ValueError("tables_out must have the shape and strides of tables")
+    page_map = torch.empty(p.num_pages, dtype=_I32, device=dev)
+    num_live = torch.empty(1, dtype=_I32, device=dev)
+    wa, wn = _ws(ws, dev)
+    _call("cache_compact", dev, ctypes.byref(p), ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", p.num_pages, dev),
+          to, page_map.data_ptr(), num_live.data_ptr(), wa, wn)
+    return refs_out, tables_out, page_map, num_live
+
+
+# ---------------------------------------------------------------------------
+# norms
+# ---------------------------------------------------------------------------
+
+def block_norm(x: Optional[torch.Tensor], residual: torch.Tensor, w_post: Optional[torch.Tensor] = None,
+               w_pre: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               residual_scale: float = 1.0, block_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+               y: Optional[torch.Tensor] = None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """The norms around a block, in one pass -> (h', y):
+
+    h' = residual_scale * residual + block_scale * gate * norm(x) * w_post, y = norm(h') * w_pre.
+
+    x bf16 [T, n] (None: the norm before the first block; h' is then the residual itself unless residual_scale
+    changes it), residual bf16 or float32 [T, n]; without w_post x enters as it is, without w_pre y is None.
+    gate bf16 [n], or [G, n] with G dividing T (row t takes gate row t // (T // G)). out may be residual."""
+    _need(residual, "residual", None, 2)
+    dev = residual.device
+    if residual.dtype is _BF16:
+        kind = RESIDUAL_BF16
+    elif residual.dtype is torch.float32:
+        kind = RESIDUAL_F32
+    else:
+        raise TypeError(f"residual has dtype {residual.dtype}, expected torch.bfloat16 or torch.float32")
+    t, n = residual.shape
+    if x is not None and _need(x, "x", _BF16, 2, dev).shape != residual.shape:
+        raise ValueError("x and residual must have the same shape")
+    gate_rows = 1
+    if gate is not None:
+        _need(gate, "gate", _BF16, gate.dim(), dev)
+        if gate.dim() not in (1, 2) or gate.shape[-1] != n or not gate.is_contiguous():
+            raise ValueError(f"gate must be contiguous [{n}] or [G, {n}]")
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+    same = x is None and residual_scale == 1.0 and out is None       # the residual passes through unchanged
+    if same:
+        out = None
+    elif out is None:
+        out = torch.empty((t, n), dtype=residual.dtype, device=dev)
+    elif _need(out, "out", residual.dtype, 2, dev).shape != residual.shape:
+        raise ValueError("out and residual must have the same shape")
+    if w_pre is None:
+        if y is not None:
+            raise ValueError("y needs w_pre")
+    elif y is None:
+        y = torch.empty((t, n), dtype=_BF16, device=dev)
+    elif _need(y, "y", _BF16, 2, dev).shape != residual.shape:
+        raise ValueError("y and residual must have the same shape")
+
+    def stride(a):
+        return 0 if a is None else (a.stride(0) if t > 1 else n)
+
+    def ptr(a):
+        return None if a is None else a.data_ptr()
+
+    _call("block_norm", dev, ptr(x), stride(x), residual.data_ptr(), stride(residual), kind, ptr(gate), gate_rows,
+          _vector(w_post, "w_post", n, dev, _BF16), _vector(w_pre, "w_pre", n, dev, _BF16), t, n, eps, residual_scale,
+          block_scale, ptr(out), stride(out), ptr(y), stride(y))
+    return (residual if same else out), y
