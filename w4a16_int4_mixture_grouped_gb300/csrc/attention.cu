@@ -1,99 +1,622 @@
-// Attention of one new token per sequence over a paged cache.
+// Attention of one new token per sequence over a paged cache, grouped heads.
 //
-// Simple form: one CTA per (sequence, query head), tokens in strides of the CTA, a running
-// maximum and sum per thread joined at the end.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
+// For each sequence and cache head: scores s = q K^T of the up to 16 query heads that share it, a
+// softmax over the seen tokens with a running maximum and sum, and o = p V. Every key and value is
+// read once; at 4 flops a byte and query head the bound is HBM, so the kernel is built around
+// keeping copies in flight:
+//
+//   * One CTA of four warps takes an equal share of all tiles of all sequences (split.cuh), whatever
+//     the lengths; rows that cross a CTA's range are joined by the last CTA to arrive, in order, from
+//     FP32 parts. One launch, no host knowledge of the lengths.
+//   * Within a tile each warp owns its own tokens: its own ring of shared-memory stages filled by
+//     its own cp.async, its own maximum, sum and accumulator. No barrier in the loop; the four
+//     warps are joined once per row.
+//   * The query heads of a cache head are the 16 rows of m16n8k16 MMAs (rows 8-15 are left out where
+//     the group has at most 8 heads), so a key or value is loaded from shared memory once for all heads.
+//     Warp-level MMA reaches: a 16-row MMA per 256 bytes is a tenth of its rate at full HBM speed.
+//   * Unseen slots (past the end, before the window, freed pages) are not read: their rows are
+//     zero-filled and their scores are -infinity, so nothing in them reaches the result.
+//   * The probabilities enter the value product as BF16 (E4M3 pages: FP16, keys and values converted
+//     exactly, queries scaled by a power of two per row). Their sum is taken in FP32 before that rounding.
 #include <cuda_runtime.h>
 
 #include "block.h"
 #include "common.cuh"
+#include "split.cuh"
 
 namespace moe {
 namespace attn {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;                // query heads of a work row (MMA M)
 
-template <bool E4M3>
-__device__ __forceinline__ float element(const void* base, int64_t i) {
-  if (E4M3) return static_cast<float>(static_cast<const __nv_fp8_e4m3*>(base)[i]);
-  return bf16_to_f32(static_cast<const uint16_t*>(base)[i]);
+template <int DP, bool E4M3>
+struct Cfg {
+  static constexpr int kElem = E4M3 ? 1 : 2;
+  static constexpr int kRowBytes = DP * kElem;
+  static constexpr int kChunks = kRowBytes / 16;
+  // tokens of a warp's stage: 8 KB of keys and values (16 KB for 256 BF16 channels)
+  static constexpr int kTok = DP * kElem <= 128 ? 32 : 16;
+  static constexpr int kStageBytes = 2 * kTok * kRowBytes;
+  static constexpr int kStages = kStageBytes <= 4096 ? 6 : 3;
+  static constexpr int kTile = kWarps * kTok;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kPitch = DP + 4;                                  // floats of a joined row
+  static constexpr int kJoinBytes = kWarps * kRows * kPitch * 4;
+  static constexpr int kBufBytes = kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes;
+};
+
+// Position of 16-byte chunk c of token row r: rows r .. r+7 at one chunk (ldmatrix) fall on eight
+// different 16-byte banks groups.
+template <int CHUNKS>
+__device__ __forceinline__ int swz(int r, int c) {
+  if (CHUNKS >= 8) return r * CHUNKS + (c ^ (r & 7));
+  return r * CHUNKS + (c ^ ((r >> 1) & 3));                               // 64-byte rows: two to a bank line
+}
+// 8-bit keys are read as 16-byte rows of four lanes, two token rows at a time.
+template <int CHUNKS>
+__device__ __forceinline__ int swz_key8(int r, int c) {
+  if (CHUNKS >= 8) return r * CHUNKS + (c ^ ((r & 1) << 2));
+  return r * CHUNKS + c;
 }
 
-// DV channels of values per row (the latent form: 512 of 576); values at the key's own base when V is null.
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p, int dv) {
-  __shared__ float qs[kLatentDim], prob[kThreads], red[kThreads / 32];
-  __shared__ int64_t rows[kThreads];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  int seq, lo, hi;
-  seen_range(p, b, seq, lo, hi);
-  for (int c = tid; c < p.dim; c += kThreads) qs[c] = bf16_to_f32(p.q[b * p.q_stride + int64_t(h) * p.dim + c]);
-  __syncthreads();
-  const void* values = p.v != nullptr ? p.v : p.k;
-  const int64_t head = int64_t(h / p.group) * p.head_stride;
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = lo; j0 < hi; j0 += kThreads) {
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    int64_t row = -1;
-    if (j < hi) {
-      const int page = p.t.tables[int64_t(seq) * p.t.table_stride + j / p.t.page_size];
-      if (page >= p.t.num_pages) set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
-      if (page >= 0 && page < p.t.num_pages) {
-        row = int64_t(page) * p.page_stride + int64_t(j % p.t.page_size) * p.token_stride + head;
-        float d = 0.f;
-        for (int c = 0; c < p.dim; ++c) d = fmaf(qs[c], element<E4M3>(p.k, row + c), d);
-        s = d * p.score_scale;
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    mma_16816(d, a, b0, b1);
+}
+// Rows 0-7 alone: the other rows of A are zero, their results dropped.
+template <bool F16>
+__device__ __forceinline__ void mma_half(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  float x[4] = {d[0], d[1], 0.f, 0.f};
+  const uint32_t a[4] = {a0, 0u, a2, 0u};
+  mma<F16>(x, a, b0, b1);
+  d[0] = x[0];
+  d[1] = x[1];
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A part of a row: M and L of its 16 heads, then the unnormalised accumulator [16][DP].
+template <int DP>
+constexpr int part_floats() { return 2 * kRows + kRows * DP; }
+
+template <int DP, bool E4M3, bool HALF>
+__global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p, float* parts, int* counters) {
+  using C = Cfg<DP, E4M3>;
+  constexpr int NR = HALF ? 2 : 4;               // accumulator registers of an MMA that are used
+  constexpr int HR = HALF ? 1 : 2;               // head rows of a thread (g, and g + 8)
+  constexpr int NT = C::kTok / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ SeqCache cache;
+  __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
+  __shared__ int last_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+  const int chunks = (p.group + kRows - 1) / kRows;
+  const int rows = p.kv_heads * chunks;          // work rows of a sequence
+
+  // total tiles, and the sequence at which this CTA's range begins
+  int64_t total = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kSeqCache) {
+    load_ranges(p, b0, &cache, kThreads);
+    total += int64_t(cached_tiles(&cache, C::kTile)) * rows;
+    // sequences that see nothing: zeros, spread over the CTAs
+    for (int i = 0; i < kSeqCache && b0 + i < p.batch; ++i) {
+      if (cache.s[i].hi > cache.s[i].lo || (b0 + i) % gridDim.x != blockIdx.x) continue;
+      const int64_t head0 = int64_t(b0 + i) * p.heads;
+      for (int64_t e = threadIdx.x; e < int64_t(p.heads) * p.dim / 8; e += kThreads)
+        reinterpret_cast<uint4*>(p.out + head0 * p.dim)[e] = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr)
+        for (int h = threadIdx.x; h < p.heads; h += kThreads) p.lse[head0 + h] = -INFINITY;
+    }
+  }
+  if (total == 0) return;
+  const int ctas = static_cast<int>(min(int64_t(gridDim.x), total));
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  int64_t x = cta_begin(total, ctas, blockIdx.x);
+  const int64_t x_end = cta_begin(total, ctas, blockIdx.x + 1);
+
+  // find sequence b with its first tile `first` on the line (the last chunk of ranges is still cached)
+  int cached = (p.batch - 1) / kSeqCache * kSeqCache, b = 0;
+  int64_t first = 0;
+  for (int b0 = 0;; b0 += kSeqCache) {
+    if (cached != b0) load_ranges(p, b0, &cache, kThreads);
+    cached = b0;
+    const int64_t n = int64_t(cached_tiles(&cache, C::kTile)) * rows;
+    if (x < first + n) {
+      b = b0;
+      break;
+    }
+    first += n;
+  }
+  {
+    // within the chunk: each lane takes four consecutive sequences
+    int n[kSeqCache / 32], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqCache / 32; ++k) {
+      const SeqRange r = cache.s[lane * (kSeqCache / 32) + k];
+      n[k] = tiles_of(r.lo, r.hi, C::kTile);
+      sum += n[k];
+    }
+    int pre = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    const int64_t after = first + int64_t(pre) * rows;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, x < after)) - 1;
+    int64_t mine = after - int64_t(sum) * rows;
+    int bb = b + lane * (kSeqCache / 32);
+    for (int k = 0; k < kSeqCache / 32 && x >= mine + int64_t(n[k]) * rows; ++k) {
+      mine += int64_t(n[k]) * rows;
+      ++bb;
+    }
+    b = __shfl_sync(0xffffffffu, bb, owner);
+    first = __shfl_sync(0xffffffffu, mine, owner);
+  }
+
+  while (x < x_end) {
+    if (b >= cached + kSeqCache) {
+      cached += kSeqCache;
+      load_ranges(p, cached, &cache, kThreads);
+    }
+    const SeqRange sr = cache.s[b - cached];
+    const int ntiles = tiles_of(sr.lo, sr.hi, C::kTile);
+    if (x >= first + int64_t(ntiles) * rows) {
+      first += int64_t(ntiles) * rows;
+      ++b;
+      continue;
+    }
+    const int r = static_cast<int>((x - first) / ntiles);
+    const int64_t row0 = first + int64_t(r) * ntiles;
+    const int tile0 = static_cast<int>(x - row0);
+    const int tile1 = static_cast<int>(min(int64_t(ntiles), x_end - row0));
+    const int kvh = r / chunks, hc = r % chunks;
+    const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
+    const int64_t head_off = int64_t(kvh) * p.head_stride;
+    const int32_t* table = p.t.tables + int64_t(sr.row) * p.t.table_stride;
+    const int tok0 = (sr.lo / C::kTile + tile0) * C::kTile + warp * C::kTok;   // this warp's first token
+    const int n = tile1 - tile0;
+
+    // ---- copies of stage i: the page ids of the next stage are read one stage ahead
+    auto entry_of = [&](int i) -> int {
+      const int tok = tok0 + i * C::kTile + (lane & (C::kTok - 1));
+      if (i >= n || tok < sr.lo || tok >= sr.hi) return -1;
+      return table[tok / p.t.page_size];
+    };
+    int entry = entry_of(0);
+    uint32_t masks[C::kStages];                   // seen tokens of the stages in flight
+    auto issue = [&](int i, int slot) -> uint32_t {
+      uint32_t seen = 0;
+      if (i < n) {
+        const int tok = tok0 + i * C::kTile + (lane & (C::kTok - 1));
+        if (entry >= p.t.num_pages) {
+          set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
+          entry = -1;
+        }
+        int64_t off = -1;
+        if (entry >= 0)
+          off = int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride + head_off;
+        seen = __ballot_sync(0xffffffffu, off >= 0);
+        if (seen != 0) {
+          const uint32_t kd = ring + slot * C::kStageBytes, vd = kd + C::kTok * C::kRowBytes;
+          const uint8_t* kb = static_cast<const uint8_t*>(p.k);
+          const uint8_t* vb = static_cast<const uint8_t*>(p.v);
+#pragma unroll
+          for (int j = 0; j < C::kTok * C::kChunks / 32; ++j) {
+            const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
+            const int64_t o = __shfl_sync(0xffffffffu, off, tr);
+            const bool ok = o >= 0 && c * 16 < p.dim * C::kElem;
+            const int64_t at = ok ? o * C::kElem + c * 16 : 0;
+            cp_async16(kd + 16 * (E4M3 ? swz_key8<C::kChunks>(tr, c) : swz<C::kChunks>(tr, c)), kb + at, ok ? 16 : 0);
+            cp_async16(vd + 16 * swz<C::kChunks>(tr, c), vb + at, ok ? 16 : 0);
+          }
+        }
+        entry = entry_of(i + 1);
+      }
+      cp_async_commit();
+      return seen;
+    };
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) masks[s] = issue(s, s);
+
+    // ---- queries as MMA A fragments
+    constexpr int KS = DP / 16;
+    uint32_t qa[KS][HALF ? 2 : 4];
+    float qscale[HR];
+#pragma unroll
+    for (int hh = 0; hh < HR; ++hh) {
+      const int row = g + 8 * hh;
+      const uint16_t* src = p.q + int64_t(b) * p.q_stride + int64_t(head0 + row) * p.dim;
+      qscale[hh] = p.score_scale;
+      if (!E4M3) {
+        // (row, k 2t..2t+1) and (row, k 2t+8..2t+9) of each 16-channel step
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int d = ks * 16 + half * 8 + 2 * t;
+            qa[ks][HALF ? half : 2 * half + hh] =
+                row < heads && d < p.dim ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
+          }
+      } else {
+        // the channels in the order in which a lane reads 8-bit keys: step s of a 64-channel block
+        // takes channels 16 t + 4 s .. + 3 of lane t. Scaled into the FP16 range by a power of two.
+        uint2 raw[KS];
+        float top = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int d = (ks >> 2) * 64 + 16 * t + 4 * (ks & 3);
+          raw[ks] = row < heads && d < p.dim ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0u, 0u);
+          const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            top = fmaxf(top, fmaxf(fabsf(bf16_to_f32(static_cast<uint16_t>(w[j]))),
+                                   fabsf(bf16_to_f32(static_cast<uint16_t>(w[j] >> 16)))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // top in [2^e, 2^(e+1)): scale by 2^-e (two factors, each a normal number for any e)
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        if (top == 0.f || e > 127) e = 0;
+        e = max(e, -126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
+        const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
+        qscale[hh] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23) *
+                     __uint_as_float(static_cast<uint32_t>(127 + (e - e / 2)) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            qa[ks][HALF ? half : 2 * half + hh] =
+                pack_f16x2_rn(bf16_to_f32(static_cast<uint16_t>(w[half])) * down * down2,
+                              bf16_to_f32(static_cast<uint16_t>(w[half] >> 16)) * down * down2);
+        }
       }
     }
-    rows[tid] = row;
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
+
+    // m: what the exponents are taken against, the maximum seen so far (E4M3: 15 below it, so that FP16
+    // probabilities reach 2^15 and lose nothing down to 2^-39 of the largest)
+    constexpr float kLift = E4M3 ? 15.f : 0.f;
+    float top_of[HR], m[HR], l[HR], o[DP / 8][NR];
+#pragma unroll
+    for (int hh = 0; hh < HR; ++hh) {
+      top_of[hh] = -INFINITY;
+      m[hh] = -INFINITY;
+      l[hh] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < NR; ++k) o[i][k] = 0.f;
+
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+      {
+        const int ahead = i + C::kStages - 1;
+        const int to = slot == 0 ? C::kStages - 1 : slot - 1;
+        const uint32_t seen = issue(ahead, to);
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+          if (s == to) masks[s] = seen;
+      }
+      cp_async_wait<C::kStages - 1>();
+      __syncwarp();
+      uint32_t seen = 0;
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s)
+        if (s == slot) seen = masks[s];
+      if (seen != 0) {
+        const uint32_t ks0 = ring + slot * C::kStageBytes, vs0 = ks0 + C::kTok * C::kRowBytes;
+        // ---- scores
+        float s[NT][NR];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < NR; ++k) s[j][k] = 0.f;
+        if (!E4M3) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+              uint32_t b4[4];
+              const int tr = j * 8 + (lane & 7) + ((lane >> 4) << 3), c = ks * 2 + ((lane >> 3) & 1);
+              ldsm_x4(ks0 + 16 * swz<C::kChunks>(tr, c), b4[0], b4[1], b4[2], b4[3]);
+              if constexpr (HALF) {
+                mma_half<false>(s[j], qa[ks][0], qa[ks][1], b4[0], b4[1]);
+                mma_half<false>(s[j + 1], qa[ks][0], qa[ks][1], b4[2], b4[3]);
+              } else {
+                mma<false>(s[j], qa[ks], b4[0], b4[1]);
+                mma<false>(s[j + 1], qa[ks], b4[2], b4[3]);
+              }
+            }
+        } else {
+#pragma unroll
+          for (int kb = 0; kb < DP / 64; ++kb)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const uint4 w4 = lds128(ks0 + 16 * swz_key8<C::kChunks>(j * 8 + g, kb * 4 + t));
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+              for (int st = 0; st < 4; ++st) {
+                const uint32_t b0 = e4m3x2_to_f16x2(w[st] & 0xffffu), b1 = e4m3x2_to_f16x2(w[st] >> 16);
+                if constexpr (HALF) mma_half<true>(s[j], qa[kb * 4 + st][0], qa[kb * 4 + st][1], b0, b1);
+                else mma<true>(s[j], qa[kb * 4 + st], b0, b1);
+              }
+            }
+        }
+        // ---- running softmax (in units of log 2)
+        bool moved = false;
+        float keep[HR];
+#pragma unroll
+        for (int hh = 0; hh < HR; ++hh) {
+          float top = top_of[hh];
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float v = s[j][2 * hh + k] * qscale[hh];
+              if (!(seen >> (j * 8 + 2 * t + k) & 1u)) v = -INFINITY;
+              s[j][2 * hh + k] = v;
+              top = fmaxf(top, v);
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float base = top == -INFINITY ? 0.f : top - kLift;
+          keep[hh] = exp2_fast(m[hh] - base);
+          moved |= top != top_of[hh];
+          top_of[hh] = top;
+          m[hh] = top == -INFINITY ? -INFINITY : base;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float e = exp2_fast(s[j][2 * hh + k] - base);
+              s[j][2 * hh + k] = e;
+              sum += e;
+            }
+          l[hh] = l[hh] * keep[hh] + sum;
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int i2 = 0; i2 < DP / 8; ++i2)
+#pragma unroll
+            for (int k = 0; k < NR; ++k) o[i2][k] *= keep[k >> 1];
+        }
+        // ---- values
+#pragma unroll
+        for (int kt = 0; kt < NT / 2; ++kt) {
+          uint32_t pa[HALF ? 2 : 4];
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int hh = 0; hh < HR; ++hh) {
+              const float lo = s[2 * kt + half][2 * hh], hi = s[2 * kt + half][2 * hh + 1];
+              pa[HALF ? half : 2 * half + hh] = E4M3 ? pack_f16x2_rn(lo, hi) : pack_bf16x2_rn(lo, hi);
+            }
+#pragma unroll
+          for (int c = 0; c < C::kChunks; c += 2) {
+            uint32_t v4[4];
+            const int tr = kt * 16 + (lane & 15), cc = c + (lane >> 4);
+            ldsm_x4_t(vs0 + 16 * swz<C::kChunks>(tr, cc), v4[0], v4[1], v4[2], v4[3]);
+            if (!E4M3) {
+              if constexpr (HALF) {
+                mma_half<false>(o[c], pa[0], pa[1], v4[0], v4[1]);
+                mma_half<false>(o[c + 1], pa[0], pa[1], v4[2], v4[3]);
+              } else {
+                mma<false>(o[c], pa, v4[0], v4[1]);
+                mma<false>(o[c + 1], pa, v4[2], v4[3]);
+              }
+            } else {
+              // a 16-bit element is two channels of one token: bytes 0, 2 and 1, 3 pair two tokens' even and
+              // odd channels, which become two tiles of eight channels
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                  const uint32_t sel = odd ? 0x4431u : 0x4420u;
+                  const uint32_t b0 = e4m3x2_to_f16x2(__byte_perm(v4[2 * q], 0u, sel));
+                  const uint32_t b1 = e4m3x2_to_f16x2(__byte_perm(v4[2 * q + 1], 0u, sel));
+                  if constexpr (HALF) mma_half<true>(o[2 * (c + q) + odd], pa[0], pa[1], b0, b1);
+                  else mma<true>(o[2 * (c + q) + odd], pa, b0, b1);
+                }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      slot = slot + 1 == C::kStages ? 0 : slot + 1;
+    }
+    cp_async_wait<0>();
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, red[w]);
-    const float mn = fmaxf(m, top);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float keep = exp2f(m - base);
-    prob[tid] = row >= 0 ? exp2f(s - base) : 0.f;
-    m = mn;
-    l *= keep;
-    for (int i = 0; i < 4; ++i) acc[i] *= keep;
-    __syncthreads();
-    const int n = min(kThreads, hi - j0);
-    for (int t = 0; t < n; ++t) {
-      if (rows[t] < 0) continue;
-      l += prob[t];
-      for (int i = 0; i < 4; ++i) {
-        const int c = tid + i * kThreads;
-        if (c < dv) acc[i] = fmaf(prob[t], element<E4M3>(values, rows[t] + c), acc[i]);
+
+    // ---- join the warps: unnormalised accumulators through shared memory
+    float* buf = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int hh = 0; hh < HR; ++hh) {
+      float sum = l[hh];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int row = g + 8 * hh;
+      if (t == 0) {
+        part_m[warp][row] = m[hh];
+        part_l[warp][row] = sum;
+      }
+      float* dst = buf + (warp * kRows + row) * C::kPitch;
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        if (!E4M3) {
+          *reinterpret_cast<float2*>(dst + i * 8 + 2 * t) = make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
+        } else if ((i & 1) == 0) {
+          *reinterpret_cast<float4*>(dst + (i / 2) * 16 + 4 * t) =
+              make_float4(o[i][2 * hh], o[i + 1][2 * hh], o[i][2 * hh + 1], o[i + 1][2 * hh + 1]);
+        }
       }
     }
     __syncthreads();
+    const int c0 = cta_of(total, ctas, row0), c1 = cta_of(total, ctas, row0 + ntiles - 1);
+    const bool whole = c0 == c1;
+    float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * part_floats<DP>();
+    const int vecs = p.dim / 4;
+    for (int e = threadIdx.x; e < heads * vecs; e += kThreads) {
+      const int row = e / vecs, d = e % vecs * 4;
+      float top = part_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, part_m[w][row]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_fast(part_m[w][row] - base);
+        const float4 v = *reinterpret_cast<const float4*>(buf + (w * kRows + row) * C::kPitch + d);
+        sum = fmaf(f, part_l[w][row], sum);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (whole) {
+        const float inv = sum > 0.f ? p.v_scale / sum : 0.f;
+        const int64_t h = int64_t(b) * p.heads + head0 + row;
+        *reinterpret_cast<uint2*>(p.out + h * p.dim + d) =
+            make_uint2(pack_bf16x2_rn(acc.x * inv, acc.y * inv), pack_bf16x2_rn(acc.z * inv, acc.w * inv));
+        if (d == 0 && p.lse != nullptr) p.lse[h] = (top + log2f(sum)) * 0.69314718055994531f;
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + 2 * kRows + row * DP + d), acc);
+        if (d == 0) {
+          __stcg(part + row, top);
+          __stcg(part + kRows + row, sum);
+        }
+      }
+    }
+
+    // ---- join the CTAs of a row: the last one to arrive adds the parts in order
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const bool last = atomicAdd(counters + c0, 1) == c1 - c0;
+        if (last) counters[c0] = 0;
+        last_flag = last;
+      }
+      __syncthreads();
+      if (last_flag) {
+        __threadfence();
+        const int np = c1 - c0 + 1;
+        // part of CTA c0 + i: its last row for the first one, its first row for the others
+        auto part_at = [&](int i) { return parts + (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats<DP>(); };
+        float* weight = buf;                              // [np][kRows], then the rows' totals
+        __shared__ float row_top[kRows], row_sum[kRows];
+        for (int row = warp; row < heads; row += kWarps) {
+          float top = -INFINITY;
+          for (int i = lane; i < np; i += 32) top = fmaxf(top, __ldcg(part_at(i) + row));
+#pragma unroll
+          for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+          const float base = top == -INFINITY ? 0.f : top;
+          float sum = 0.f;
+          for (int i = lane; i < np; i += 32) {
+            const float f = exp2_fast(__ldcg(part_at(i) + row) - base);
+            weight[i * kRows + row] = f;
+            sum = fmaf(f, __ldcg(part_at(i) + kRows + row), sum);
+          }
+#pragma unroll
+          for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+          if (lane == 0) {
+            row_top[row] = top;
+            row_sum[row] = sum;
+          }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < heads * vecs; e += kThreads) {
+          const int row = e / vecs, d = e % vecs * 4;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int i = 0; i < np; ++i) {
+            const float f = weight[i * kRows + row];
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i) + 2 * kRows + row * DP + d));
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+          const float sum = row_sum[row], inv = sum > 0.f ? p.v_scale / sum : 0.f;
+          const int64_t h = int64_t(b) * p.heads + head0 + row;
+          *reinterpret_cast<uint2*>(p.out + h * p.dim + d) =
+              make_uint2(pack_bf16x2_rn(acc.x * inv, acc.y * inv), pack_bf16x2_rn(acc.z * inv, acc.w * inv));
+          if (d == 0 && p.lse != nullptr) p.lse[h] = (row_top[row] + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+    }
+    __syncthreads();                                      // the ring and the flags are free again
+    x = row0 + tile1;
   }
-  const float inv = l > 0.f ? p.v_scale / l : 0.f;
-  for (int i = 0; i < 4; ++i) {
-    const int c = tid + i * kThreads;
-    if (c < dv) p.out[(int64_t(b) * p.heads + h) * dv + c] = f32_to_bf16_rn(l > 0.f ? acc[i] * inv : 0.f);
+}
+
+template <int DP, bool E4M3, bool HALF>
+cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
+  using C = Cfg<DP, E4M3>;
+  const void* fn = reinterpret_cast<const void*>(attention_kernel<DP, E4M3, HALF>);
+  static bool attr_set[64] = {false};
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBufBytes);
+    if (e != cudaSuccess) return e;
+    attr_set[device] = true;
   }
-  if (tid == 0 && p.lse != nullptr) p.lse[int64_t(b) * p.heads + h] = (m + log2f(l)) * 0.69314718055994531f;
+  int grid = device_info(device).sm_count * (2 * C::kBufBytes <= 220 * 1024 ? 2 : 1);
+  if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
+  attention_kernel<DP, E4M3, HALF><<<grid, kThreads, C::kBufBytes, stream>>>(p, p.parts, p.counters);
+  note_launch();
+  return cudaGetLastError();
+}
+template <int DP>
+cudaError_t launch_dim(const AttnParams& p, bool e4m3, int device, cudaStream_t stream) {
+  const bool half = p.group <= 8;
+  if (e4m3) return half ? launch<DP, true, true>(p, device, stream) : launch<DP, true, false>(p, device, stream);
+  return half ? launch<DP, false, true>(p, device, stream) : launch<DP, false, false>(p, device, stream);
 }
 
 }  // namespace attn
 
-cudaError_t launch_attention(const AttnParams& p, int dtype, int, cudaStream_t stream) {
-  const dim3 grid(p.heads, p.batch);
-  if (dtype == MOE_W4A16_CACHE_E4M3) attn::attention_kernel<true><<<grid, attn::kThreads, 0, stream>>>(p, p.dim);
-  else attn::attention_kernel<false><<<grid, attn::kThreads, 0, stream>>>(p, p.dim);
-  note_launch();
-  return cudaGetLastError();
+size_t attention_part_bytes(int, int, int dim) {
+  const int floats = dim <= 64 ? attn::part_floats<64>() : dim <= 128 ? attn::part_floats<128>() : attn::part_floats<256>();
+  return size_t(kAttnMaxCtas) * 2 * floats * sizeof(float);
 }
 
-cudaError_t launch_latent_attention(const AttnParams& p, int, cudaStream_t stream) {
-  attn::attention_kernel<false><<<dim3(p.heads, p.batch), attn::kThreads, 0, stream>>>(p, kLatentValue);
-  note_launch();
-  return cudaGetLastError();
+cudaError_t launch_attention(const AttnParams& p, int dtype, int device, cudaStream_t stream) {
+  const bool e4m3 = dtype == MOE_W4A16_CACHE_E4M3;
+  if (p.dim <= 64) return attn::launch_dim<64>(p, e4m3, device, stream);
+  if (p.dim <= 128) return attn::launch_dim<128>(p, e4m3, device, stream);
+  return attn::launch_dim<256>(p, e4m3, device, stream);
 }
 
 }  // namespace moe

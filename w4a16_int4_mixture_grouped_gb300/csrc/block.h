@@ -40,7 +40,13 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   int* err;
+  int* counters;                       // [kAttnMaxCtas] arrivals of split rows' parts, zero between calls
+  float* parts;                        // FP32 parts of split rows, two to a CTA
 };
+// CTAs of an attention launch: two on each of the GPU's 152 SMs.
+constexpr int kAttnMaxCtas = 304;
+size_t attention_part_bytes(int heads, int kv_heads, int dim);
+size_t latent_part_bytes(int heads);
 
 // First and past-the-last seen token of query b; a length out of range is cut and recorded.
 __device__ __forceinline__ void seen_range(const AttnParams& p, int b, int& row, int& lo, int& hi) {

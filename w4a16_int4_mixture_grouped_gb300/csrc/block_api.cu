@@ -17,6 +17,9 @@ using namespace moe;
 
 namespace {
 
+// Arrival counters of the attention workspace, padded to 256 bytes.
+constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int) + 255) / 256 * 256;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool ws_fits(const void* ws, size_t bytes, size_t need) {
@@ -99,7 +102,7 @@ moe_w4a16_status attention_call(AttnParams& p, const moe_w4a16_pages* cache, con
   if (p.dim < 16 || p.dim % 16 != 0 || (!latent && p.dim > MOE_W4A16_MAX_HEAD_DIM)) return MOE_W4A16_ERR_UNSUPPORTED;
   moe_w4a16_status st = check_pages(cache, p.kv_heads, p.dim, latent);
   if (st != MOE_W4A16_OK) return st;
-  if (p.batch > 65535 || static_cast<int64_t>(p.batch) * p.heads >= (int64_t(1) << 31)) return MOE_W4A16_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p.batch) * p.heads >= (int64_t(1) << 31)) return MOE_W4A16_ERR_UNSUPPORTED;
   size_t need = 0;
   st = moe_w4a16_attention_workspace_size(p.heads, p.kv_heads, p.dim, &need);
   if (st != MOE_W4A16_OK) return st;
@@ -120,6 +123,8 @@ moe_w4a16_status attention_call(AttnParams& p, const moe_w4a16_pages* cache, con
   p.score_scale = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
   p.v_scale = cache->v_scale;
   p.err = static_cast<int*>(ws);
+  p.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + MOE_W4A16_WS_HEADER_BYTES);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_W4A16_WS_HEADER_BYTES + kAttnCounterBytes);
   int device = 0;
   MOE_CUDA_TRY(cudaGetDevice(&device));
   MOE_CUDA_TRY(latent ? launch_latent_attention(p, device, stream) : launch_attention(p, cache->dtype, device, stream));
@@ -136,7 +141,9 @@ moe_w4a16_status moe_w4a16_attention_workspace_size(int num_heads, int num_kv_he
   const bool latent = num_kv_heads == 1 && head_dim == MOE_W4A16_LATENT_DIM;
   if (head_dim < 16 || head_dim % 16 != 0 || (!latent && head_dim > MOE_W4A16_MAX_HEAD_DIM))
     return MOE_W4A16_ERR_UNSUPPORTED;
-  *bytes = MOE_W4A16_WS_HEADER_BYTES;
+  // header | arrival counters | parts of split rows
+  *bytes = MOE_W4A16_WS_HEADER_BYTES + kAttnCounterBytes +
+           (latent ? latent_part_bytes(num_heads) : attention_part_bytes(num_heads, num_kv_heads, head_dim));
   return MOE_W4A16_OK;
 }
 
