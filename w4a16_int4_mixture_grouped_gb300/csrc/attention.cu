@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   constexpr int HR = HALF ? 1 : 2;               // head rows of a thread (g, and g + 8)
   constexpr int NT = C::kTok / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ SeqCache cache;
+  __shared__ Share share;
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
   __shared__ int last_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -120,94 +120,25 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   const int chunks = (p.group + kRows - 1) / kRows;
   const int rows = p.kv_heads * chunks;          // work rows of a sequence
 
-  // total tiles, and the sequence at which this CTA's range begins
-  int64_t total = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kSeqCache) {
-    load_ranges(p, b0, &cache, kThreads);
-    total += int64_t(cached_tiles(&cache, C::kTile)) * rows;
-    // sequences that see nothing: zeros, spread over the CTAs
-    for (int i = 0; i < kSeqCache && b0 + i < p.batch; ++i) {
-      if (cache.s[i].hi > cache.s[i].lo || (b0 + i) % gridDim.x != blockIdx.x) continue;
-      const int64_t head0 = int64_t(b0 + i) * p.heads;
-      for (int64_t e = threadIdx.x; e < int64_t(p.heads) * p.dim / 8; e += kThreads)
-        reinterpret_cast<uint4*>(p.out + head0 * p.dim)[e] = make_uint4(0, 0, 0, 0);
-      if (p.lse != nullptr)
-        for (int h = threadIdx.x; h < p.heads; h += kThreads) p.lse[head0 + h] = -INFINITY;
-    }
-  }
-  if (total == 0) return;
-  const int ctas = static_cast<int>(min(int64_t(gridDim.x), total));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  int64_t x = cta_begin(total, ctas, blockIdx.x);
-  const int64_t x_end = cta_begin(total, ctas, blockIdx.x + 1);
-
-  // find sequence b with its first tile `first` on the line (the last chunk of ranges is still cached)
-  int cached = (p.batch - 1) / kSeqCache * kSeqCache, b = 0;
-  int64_t first = 0;
-  for (int b0 = 0;; b0 += kSeqCache) {
-    if (cached != b0) load_ranges(p, b0, &cache, kThreads);
-    cached = b0;
-    const int64_t n = int64_t(cached_tiles(&cache, C::kTile)) * rows;
-    if (x < first + n) {
-      b = b0;
-      break;
-    }
-    first += n;
-  }
-  {
-    // within the chunk: each lane takes four consecutive sequences
-    int n[kSeqCache / 32], sum = 0;
-#pragma unroll
-    for (int k = 0; k < kSeqCache / 32; ++k) {
-      const SeqRange r = cache.s[lane * (kSeqCache / 32) + k];
-      n[k] = tiles_of(r.lo, r.hi, C::kTile);
-      sum += n[k];
-    }
-    int pre = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
-    }
-    const int64_t after = first + int64_t(pre) * rows;
-    const int owner = __ffs(__ballot_sync(0xffffffffu, x < after)) - 1;
-    int64_t mine = after - int64_t(sum) * rows;
-    int bb = b + lane * (kSeqCache / 32);
-    for (int k = 0; k < kSeqCache / 32 && x >= mine + int64_t(n[k]) * rows; ++k) {
-      mine += int64_t(n[k]) * rows;
-      ++bb;
-    }
-    b = __shfl_sync(0xffffffffu, bb, owner);
-    first = __shfl_sync(0xffffffffu, mine, owner);
-  }
-
-  while (x < x_end) {
-    if (b >= cached + kSeqCache) {
-      cached += kSeqCache;
-      load_ranges(p, cached, &cache, kThreads);
-    }
-    const SeqRange sr = cache.s[b - cached];
-    const int ntiles = tiles_of(sr.lo, sr.hi, C::kTile);
-    if (x >= first + int64_t(ntiles) * rows) {
-      first += int64_t(ntiles) * rows;
-      ++b;
-      continue;
-    }
-    const int r = static_cast<int>((x - first) / ntiles);
-    const int64_t row0 = first + int64_t(r) * ntiles;
-    const int tile0 = static_cast<int>(x - row0);
-    const int tile1 = static_cast<int>(min(int64_t(ntiles), x_end - row0));
-    const int kvh = r / chunks, hc = r % chunks;
+  zero_empty<kThreads>(p, p.dim);
+  if (!find_share<kThreads>(p, rows, C::kTile, 1, &share)) return;
+  const int64_t total = share.total;
+  const int ctas = share.ctas;
+  PieceWalk walk;
+  walk.start(p, &share);
+  Piece pc;
+  while (walk.next(p, rows, C::kTile, pc)) {
+    const int kvh = pc.r / chunks, hc = pc.r % chunks;
     const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
     const int64_t head_off = int64_t(kvh) * p.head_stride;
-    const int32_t* table = p.t.tables + int64_t(sr.row) * p.t.table_stride;
-    const int tok0 = (sr.lo / C::kTile + tile0) * C::kTile + warp * C::kTok;   // this warp's first token
-    const int n = tile1 - tile0;
+    const int32_t* table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
+    const int tok0 = (pc.lo / C::kTile + pc.tile0) * C::kTile + warp * C::kTok;   // this warp's first token
+    const int n = pc.tile1 - pc.tile0, b = pc.b;
 
     // ---- copies of stage i: the page ids of the next stage are read one stage ahead
     auto entry_of = [&](int i) -> int {
       const int tok = tok0 + i * C::kTile + (lane & (C::kTok - 1));
-      if (i >= n || tok < sr.lo || tok >= sr.hi) return -1;
+      if (i >= n || tok < pc.lo || tok >= pc.hi) return -1;
       return table[tok / p.t.page_size];
     };
     int entry = entry_of(0);
@@ -482,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       }
     }
     __syncthreads();
-    const int c0 = cta_of(total, ctas, row0), c1 = cta_of(total, ctas, row0 + ntiles - 1);
+    const int c0 = cta_of(total, ctas, pc.row0), c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1);
     const bool whole = c0 == c1;
     float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * part_floats<DP>();
     const int vecs = p.dim / 4;
@@ -577,7 +508,6 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       }
     }
     __syncthreads();                                      // the ring and the flags are free again
-    x = row0 + tile1;
   }
 }
 

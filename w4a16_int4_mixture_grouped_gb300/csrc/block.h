@@ -45,6 +45,8 @@ struct AttnParams {
 };
 // CTAs of an attention launch: two on each of the GPU's 152 SMs.
 constexpr int kAttnMaxCtas = 304;
+constexpr int kLatentMaxCtas = 152;    // the latent kernel: one
+constexpr int kLatentMinTiles = 2;     // tiles a CTA of the latent kernel takes at least: a part costs as much as a tile
 size_t attention_part_bytes(int heads, int kv_heads, int dim);
 size_t latent_part_bytes(int heads);
 

@@ -1,93 +1,611 @@
-// Attention of one new token per sequence over a latent cache.
+// Attention of one new token per sequence over a latent cache: one row of 576 channels per token is
+// every head's key, its first 512 channels every head's value.
 //
-// Simple form: one CTA per (sequence, query head), tokens in strides of the CTA, a running
-// maximum and sum per thread joined at the end.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
+// With up to 64 heads on one row of 1152 bytes a token costs 2 * 64 * (576 + 512) flops for those
+// bytes, 121 a byte: at full HBM speed 0.8 PFLOP/s, beyond warp-level MMA. So both products run on
+// tcgen05, and both read the one copy of the tile in shared memory:
+//
+//   S^T [keys x heads]  = K [keys x 576] . Q^T       A = the tile, K-major
+//   O^T [512 x heads]  += V^T [512 x keys] . P^T      A = the same tile, M-major (no transposed copy)
+//
+//   * Tiles of 64 tokens, two in shared memory (2 x 72 KB) beside the 64 queries (72 KB): each is
+//     filled by a team of its own with cp.async (rows gathered by page; unseen slots zero-filled), so a tile
+//     is always in flight. The MMA's M is 128, so S^T has 64 rows of keys and 64 rows of whatever follows in
+//     shared memory, whose lanes nobody reads.
+//   * S^T is double-buffered in TMEM (2 x 64 columns), O^T takes 256 columns (four 128-channel tiles).
+//     Two issuing warps, so that the next tile's scores run beside this tile's softmax and values.
+//   * Softmax: the heads are columns, a lane is a key; two groups of four warps take 32 heads each. The
+//     base of the exponents only moves when a tile's maximum passes it by 2^8 (BF16 probabilities keep their
+//     relative precision, FP32 sums their range), so the accumulator in TMEM is seldom rescaled.
+//   * Work is shared out as in split.cuh; a row that crosses CTAs is written as FP32 parts, which a second
+//     kernel joins in order (64 heads x 512 channels are too much for one last CTA).
 #include <cuda_runtime.h>
 
 #include "block.h"
 #include "common.cuh"
+#include "split.cuh"
 
 namespace moe {
 namespace latent {
 
-constexpr int kThreads = 128;
+constexpr int kHeads = 64;                    // heads of a work row (MMA N)
+constexpr int kTile = 64;                     // tokens of a tile
+constexpr int kChunks = kLatentDim / 64;      // 128-byte column chunks of a row: 9
+constexpr int kChunkBytes64 = 64 * 128;       // 64 rows of one chunk, 128-byte swizzled
+constexpr int kTileBytes = kChunks * kChunkBytes64;      // 73,728
+constexpr int kValueTiles = kLatentValue / 128;          // M tiles of O^T: 4
 
-template <bool E4M3>
-__device__ __forceinline__ float element(const void* base, int64_t i) {
-  if (E4M3) return static_cast<float>(static_cast<const __nv_fp8_e4m3*>(base)[i]);
-  return bf16_to_f32(static_cast<const uint16_t*>(base)[i]);
+// warps: 0-7 softmax / rescale / epilogue, 8-11 tile loaders (two teams), 12 S issuer, 13 O issuer, 14-15 queries
+constexpr int kThreads = 512;
+constexpr int kGroups = 3;                    // chunk groups of a tile that the S issuer waits for
+
+constexpr int kKOff = 0;
+constexpr int kQOff = 2 * kTileBytes;
+constexpr int kPOff = kQOff + kTileBytes;
+constexpr int kBarOff = kPOff + kTile * 128;
+enum {
+  kBarFull = 0,                               // [2][kGroups] tile chunks loaded
+  kBarScore = kBarFull + 2 * kGroups,         // [2] S^T of a tile computed
+  kBarScoreFree = kBarScore + 2,              // [2] S^T read
+  kBarProb = kBarScoreFree + 2,               // P of a tile written, O^T rescaled if need be
+  kBarDone = kBarProb + 1,                    // [2] a tile's O^T product done: tile, P free, O^T stable
+  kBarQ = kBarDone + 2,                       // queries of a piece loaded
+  kBarQFree = kBarQ + 1,
+  kBarMax = kBarQFree + 1,                    // [2] the two column groups' exchanges
+  kBarDrain = kBarMax + 2,
+  kNumBars = kBarDrain + 2
+};
+constexpr int kMiscOff = kBarOff + kNumBars * 8;         // TMEM address, abort flag
+constexpr int kMaskOff = kMiscOff + 8;                   // [2] 64-bit masks of seen tokens
+constexpr int kMaxOff = kMaskOff + 16;                   // float [2][2][64] tile maxima by tile parity and key half
+constexpr int kSumOff = kMaxOff + 4 * kHeads * 4;        // float [2][64] sums by key half
+constexpr int kShareOff = (kSumOff + 2 * kHeads * 4 + 15) / 16 * 16;
+constexpr int kSmemBytes = kShareOff + static_cast<int>(sizeof(Share));
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kPOff % 1024 == 0 && kQOff % 1024 == 0 && kChunkBytes64 % 1024 == 0, "swizzled tiles");
+
+constexpr int kTmemCols = 512;
+constexpr int kScoreCol = 0;                  // S^T buffers at columns 0 and 64
+constexpr int kAccCol = 128;                  // O^T tile i at 128 + 64 i
+
+// A part of a row: base and sum of its 64 heads, then O^T unnormalised as [64][512].
+constexpr int kPartFloats = 2 * kHeads + kHeads * kLatentValue;
+// What a CTA left for the join: a row that starts in it and goes on in the next np - 1.
+struct Record {
+  int32_t np, b, head0, heads;
+};
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// DV channels of values per row (the latent form: 512 of 576); values at the key's own base when V is null.
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p, int dv) {
-  __shared__ float qs[kLatentDim], prob[kThreads], red[kThreads / 32];
-  __shared__ int64_t rows[kThreads];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  int seq, lo, hi;
-  seen_range(p, b, seq, lo, hi);
-  for (int c = tid; c < p.dim; c += kThreads) qs[c] = bf16_to_f32(p.q[b * p.q_stride + int64_t(h) * p.dim + c]);
+// Operand tiles are rows of 128 bytes in 128-byte swizzle, 8-row atoms of 1024 bytes. K-major (rows along
+// M or N, 64 channels of the reduction a row): atoms follow each other along the rows at 1024 bytes. M-major
+// (rows along the reduction, 64 channels of M or N a row): 8-row groups of the reduction at 1024 bytes, the next
+// 64 channels one chunk further.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead_bytes) {
+  return (static_cast<uint64_t>((addr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(lead_bytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// kind::f16, FP32 accumulator, BF16 operands, M = 128, N = 64; bits 15 / 16: A / B M-major.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kHeads >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+constexpr uint32_t kIdescScore = kIdesc;
+constexpr uint32_t kIdescValue = kIdesc | (1u << 15) | (1u << 16);
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Work rows of a sequence: blocks of up to 64 heads.
+__device__ __forceinline__ int head_blocks(int heads) { return (heads + kHeads - 1) / kHeads; }
+
+__global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p, Record* records) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bars = base + kBarOff;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
+  Share* share = reinterpret_cast<Share*>(smem + kShareOff);
+  const int rows = head_blocks(p.heads);
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  zero_empty<kThreads>(p, kLatentValue);
+  if (threadIdx.x == 0) records[blockIdx.x].np = 0;
+  if (!find_share<kThreads>(p, rows, kTile, kLatentMinTiles, share)) return;
+  if ((base & 1023u) != 0) {                 // the swizzle is a function of address bits
+    if (threadIdx.x == 0) set_error(p.err, MOE_W4A16_ERR_CUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(kBarFull + i), 64);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarScore + i), 1);
+      mbar_init(bar(kBarScoreFree + i), 4);
+      mbar_init(bar(kBarDone + i), 1);
+      mbar_init(bar(kBarMax + i), 4);
+      mbar_init(bar(kBarDrain + i), 1);
+    }
+    mbar_init(bar(kBarProb), 8);
+    mbar_init(bar(kBarQ), 64);
+    mbar_init(bar(kBarQFree), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + kMiscOff), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
   __syncthreads();
-  const void* values = p.v != nullptr ? p.v : p.k;
-  const int64_t head = int64_t(h / p.group) * p.head_stride;
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = lo; j0 < hi; j0 += kThreads) {
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    int64_t row = -1;
-    if (j < hi) {
-      const int page = p.t.tables[int64_t(seq) * p.t.table_stride + j / p.t.page_size];
-      if (page >= p.t.num_pages) set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
-      if (page >= 0 && page < p.t.num_pages) {
-        row = int64_t(page) * p.page_stride + int64_t(j % p.t.page_size) * p.token_stride + head;
-        float d = 0.f;
-        for (int c = 0; c < p.dim; ++c) d = fmaf(qs[c], element<E4M3>(p.k, row + c), d);
-        s = d * p.score_scale;
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kMiscOff);
+  const int64_t total = share->total;
+  const int ctas = share->ctas;
+  PieceWalk walk;
+  walk.start(p, share);
+  Piece pc;
+  auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.err, kWaitLimitNs); };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax, rescale, epilogue
+    const int q = warp & 3, group = warp >> 2;           // TMEM lane quarter, heads 32 group ..
+    const bool soft = q < 2;                             // lanes 0-63 hold the keys
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    float* maxima = reinterpret_cast<float*>(smem + kMaxOff);
+    const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(smem + kMaskOff);
+    uint32_t it = 0, exchanges = 0;                      // tiles, exchanges of this CTA so far
+    bool ok = true;
+    // one bounded exchange between the four warps of a column group
+    auto exchange = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMax + group));
+      const bool r = wait(kBarMax + group, exchanges & 1u);
+      ++exchanges;
+      return r;
+    };
+    while (ok && walk.next(p, rows, kTile, pc)) {
+      const int head0 = pc.r * kHeads, heads = min(kHeads, p.heads - head0);
+      const int mine = min(32, heads - 32 * group);      // heads of this column group (may be <= 0)
+      float top = -INFINITY;                             // lane h: base of head 32 group + h
+      float l[32];
+#pragma unroll
+      for (int h = 0; h < 32; ++h) l[h] = 0.f;
+      const int n = pc.tile1 - pc.tile0;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it & 1;
+        const uint32_t par = (it >> 1) & 1u;
+        uint32_t s[32];
+        if (soft) {
+          if (!(ok = wait(kBarScore + buf, par) && wait(kBarFull + buf * kGroups, par))) break;
+          tc_fence_after();
+          const bool seen = masks[buf * 2 + q] >> lane & 1u;
+          if (mine > 0) tmem_ld32(tmem + kScoreCol + buf * 64 + 32 * group + lanes, s);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarScoreFree + buf));
+          float best = -INFINITY;                        // lane h: this warp's maximum of head h
+#pragma unroll
+          for (int h = 0; h < 32; ++h) {
+            if (h >= mine) break;
+            const float v = seen ? __uint_as_float(s[h]) * p.score_scale : -INFINITY;
+            s[h] = __float_as_uint(v);
+            const float w = warp_max(v);
+            if (lane == h) best = w;
+          }
+          maxima[(buf * 2 + q) * kHeads + 32 * group + lane] = best;
+        }
+        if (!(ok = exchange())) break;
+        const float tile_top = fmaxf(maxima[buf * 2 * kHeads + 32 * group + lane],
+                                     maxima[(buf * 2 + 1) * kHeads + 32 * group + lane]);
+        const bool move = tile_top > top + 8.f;          // top = -inf at first: any seen score moves it
+        const float next = move ? tile_top : top;
+        const float keep = move ? exp2_fast(top - next) : 1.f;
+        const bool rescale = __any_sync(0xffffffffu, move);
+        top = next;
+        // the previous tile's product is done: O^T is stable, P and the tile after it are free
+        if (it != 0 && !(ok = wait(kBarDone + (buf ^ 1), ((it - 1) >> 1) & 1u))) break;
+        if (rescale && i > 0 && mine > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int mt = 0; mt < kValueTiles; ++mt) {
+            uint32_t o[32];
+            const uint32_t at = tmem + kAccCol + mt * 64 + 32 * group + lanes;
+            tmem_ld32(at, o);
+#pragma unroll
+            for (int h = 0; h < 32; ++h)
+              o[h] = __float_as_uint(__uint_as_float(o[h]) * __shfl_sync(0xffffffffu, keep, h));
+            tmem_st32(at, o);
+          }
+        }
+        if (soft) {
+          const float b0 = top == -INFINITY ? 0.f : top;
+          uint32_t packed[16];
+#pragma unroll
+          for (int h = 0; h < 32; h += 2) {
+            const float e0 = exp2_fast(__uint_as_float(s[h]) - __shfl_sync(0xffffffffu, b0, h));
+            const float e1 = exp2_fast(__uint_as_float(s[h + 1]) - __shfl_sync(0xffffffffu, b0, h + 1));
+            if (rescale) {
+              l[h] *= __shfl_sync(0xffffffffu, keep, h);
+              l[h + 1] *= __shfl_sync(0xffffffffu, keep, h + 1);
+            }
+            l[h] += h < mine ? e0 : 0.f;
+            l[h + 1] += h + 1 < mine ? e1 : 0.f;
+            packed[h / 2] = h < mine ? pack_bf16x2_rn(e0, h + 1 < mine ? e1 : 0.f) : 0u;
+          }
+          const int key = 32 * q + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(smem + kPOff + key * 128 + (((group * 4 + j) ^ (key & 7)) << 4)) =
+                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarProb));
+      }
+      if (!ok) break;
+
+      // ---- epilogue: the sums over keys, then this quarter's channels of O^T
+      float* sums = reinterpret_cast<float*>(smem + kSumOff);
+      if (soft) {
+        // 32 sums over 32 lanes: halve the heads a lane holds at each step; lane h ends with head h
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+          for (int h = 0; h < o; ++h) {
+            const bool hi = lane & o;
+            const float send = hi ? l[h] : l[h + o];
+            const float got = __shfl_xor_sync(0xffffffffu, send, o);
+            l[h] = (hi ? l[h + o] : l[h]) + got;
+          }
+        }
+        sums[q * kHeads + 32 * group + lane] = l[0];
+      }
+      if (!(ok = exchange())) break;
+      const float sum = sums[32 * group + lane] + sums[kHeads + 32 * group + lane];
+      if (!(ok = wait(kBarDone + ((it - 1) & 1), ((it - 1) >> 1) & 1u))) break;
+      tc_fence_after();
+      const int c0 = cta_of(total, ctas, pc.row0), c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1);
+      const int64_t out0 = (int64_t(pc.b) * p.heads + head0 + 32 * group);
+      const bool whole = c0 == c1;
+      float* part = p.parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * kPartFloats;
+      if (q == 0 && lane < mine) {
+        if (whole) {
+          if (p.lse != nullptr) p.lse[out0 + lane] = (top + log2f(sum)) * 0.69314718055994531f;
+        } else {
+          part[32 * group + lane] = top;
+          part[kHeads + 32 * group + lane] = sum;
+        }
+      }
+      if (!whole && static_cast<int>(blockIdx.x) == c0 && threadIdx.x == 0)
+        records[blockIdx.x] = Record{c1 - c0 + 1, pc.b, head0, heads};
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      if (mine > 0) {
+#pragma unroll 1
+        for (int mt = 0; mt < kValueTiles; ++mt) {
+          uint32_t o[32];
+          tmem_ld32(tmem + kAccCol + mt * 64 + 32 * group + lanes, o);
+          const int d = mt * 128 + 32 * q + lane;
+          if (whole) {
+#pragma unroll
+            for (int h = 0; h < 32; ++h) {
+              const float f = __shfl_sync(0xffffffffu, inv, h);
+              if (h < mine) p.out[(out0 + h) * kLatentValue + d] = f32_to_bf16_rn(__uint_as_float(o[h]) * f);
+            }
+          } else {
+            float* dst = part + 2 * kHeads + 32 * group * kLatentValue + d;
+#pragma unroll
+            for (int h = 0; h < 32; ++h)
+              if (h < mine) __stcg(dst + h * kLatentValue, __uint_as_float(o[h]));
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------- tile loaders
+    // Team 0 (warps 8, 9) fills buffer 0 with the even tiles, team 1 buffer 1 with the odd ones. A warp owns
+    // 32 of the tile's tokens: lane = token for the page look-up; copies of 8 lanes a row, 4 rows at a time.
+    const int team = (warp - 8) >> 1, half = (warp - 8) & 1;
+    uint32_t it = 0;
+    bool ok = true;
+    const uint8_t* src = static_cast<const uint8_t*>(p.k);
+    volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + kMaskOff);
+    while (ok && walk.next(p, rows, kTile, pc)) {
+      const int32_t* table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
+      const int n = pc.tile1 - pc.tile0;
+      auto entry_of = [&](int i) -> int {
+        const int tok = (pc.lo / kTile + pc.tile0 + i) * kTile + 32 * half + lane;
+        if (i >= n || tok < pc.lo || tok >= pc.hi) return -1;
+        return table[tok / p.t.page_size];
+      };
+      int i = static_cast<int>((it ^ team) & 1u);        // first tile of this team in the piece
+      int entry = entry_of(i);
+      for (; i < n; i += 2) {
+        const uint32_t g = it + i;                       // the tile's number in the CTA
+        const int tok = (pc.lo / kTile + pc.tile0 + i) * kTile + 32 * half + lane;
+        if (entry >= p.t.num_pages) {
+          set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
+          entry = -1;
+        }
+        int64_t off = -1;
+        if (entry >= 0) off = (int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride) * 2;
+        const uint32_t seen = __ballot_sync(0xffffffffu, off >= 0);
+        if (g >= 2 && !(ok = wait(kBarDone + team, ((g >> 1) - 1) & 1u))) break;
+        if (lane == 0) masks[team * 2 + half] = seen;
+        entry = entry_of(i + 2);
+        int64_t from[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
+        const uint32_t dst0 = base + kKOff + team * kTileBytes + half * 4096;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = k * 4 + (lane >> 3);
+            const bool have = from[k] >= 0;
+            cp_async16(dst0 + c * kChunkBytes64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                       src + (have ? from[k] + c * 128 + (lane & 7) * 16 : 0), have ? 16 : 0);
+          }
+          if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
+        }
+        static_assert(kGroups == 3, "waits below");
+        cp_async_wait<2>();
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kBarFull + team * kGroups));
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kBarFull + team * kGroups + 1));
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kBarFull + team * kGroups + 2));
+      }
+      it += n;
+    }
+    cp_async_wait<0>();
+  } else if (warp == 12) {
+    // ------------------------------------------------------------- S^T = K Q^T
+    uint32_t it = 0, piece = 0;
+    bool ok = true;
+    while (ok && walk.next(p, rows, kTile, pc)) {
+      if (!(ok = wait(kBarQ, piece & 1u))) break;
+      const int n = pc.tile1 - pc.tile0;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it & 1;
+        const uint32_t par = (it >> 1) & 1u;
+        if (!(ok = wait(kBarScoreFree + buf, par ^ 1u))) break;
+        const uint32_t d = tmem + kScoreCol + buf * 64;
+        for (int grp = 0; grp < kGroups; ++grp) {
+          if (!(ok = wait(kBarFull + buf * kGroups + grp, par))) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int cc = 0; cc < kChunks / kGroups; ++cc) {
+              const int c = grp * (kChunks / kGroups) + cc;
+              const uint64_t a = smem_desc(base + kKOff + buf * kTileBytes + c * kChunkBytes64, 16);
+              const uint64_t b = smem_desc(base + kQOff + c * kChunkBytes64, 16);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)                // 16 channels = 32 bytes a step
+                tc_mma(d, a + 2 * k, b + 2 * k, kIdescScore, c == 0 && k == 0 ? 0u : 1u);
+            }
+            if (grp == kGroups - 1) tc_commit(bar(kBarScore + buf));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (lane == 0) tc_commit(bar(kBarQFree));
+      __syncwarp();
+      ++piece;
+    }
+    if (lane == 0) {
+      tc_commit(bar(kBarDrain));
+      mbar_drain(bar(kBarDrain), 0);
+    }
+  } else if (warp == 13) {
+    // ------------------------------------------------------------- O^T += V^T P^T
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next(p, rows, kTile, pc)) {
+      const int n = pc.tile1 - pc.tile0;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it & 1;
+        if (!(ok = wait(kBarProb, it & 1u))) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int mt = 0; mt < kValueTiles; ++mt) {
+            const uint64_t a = smem_desc(base + kKOff + buf * kTileBytes + mt * 2 * kChunkBytes64, kChunkBytes64);
+            const uint64_t b = smem_desc(base + kPOff, kChunkBytes64);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)         // 16 tokens = two 1024-byte groups a step
+              tc_mma(tmem + kAccCol + mt * 64, a + k * 128, b + k * 128, kIdescValue, i == 0 && k == 0 ? 0u : 1u);
+          }
+          tc_commit(bar(kBarDone + buf));
+        }
+        __syncwarp();
       }
     }
-    rows[tid] = row;
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, red[w]);
-    const float mn = fmaxf(m, top);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float keep = exp2f(m - base);
-    prob[tid] = row >= 0 ? exp2f(s - base) : 0.f;
-    m = mn;
-    l *= keep;
-    for (int i = 0; i < 4; ++i) acc[i] *= keep;
-    __syncthreads();
-    const int n = min(kThreads, hi - j0);
-    for (int t = 0; t < n; ++t) {
-      if (rows[t] < 0) continue;
-      l += prob[t];
-      for (int i = 0; i < 4; ++i) {
-        const int c = tid + i * kThreads;
-        if (c < dv) acc[i] = fmaf(prob[t], element<E4M3>(values, rows[t] + c), acc[i]);
+    if (lane == 0) {
+      tc_commit(bar(kBarDrain + 1));
+      mbar_drain(bar(kBarDrain + 1), 0);
+    }
+  } else {
+    // ------------------------------------------------------------- queries of a piece
+    // Rows past the last head keep what they held: their columns of S^T and O^T are never read.
+    const int half = warp - 14;
+    uint32_t piece = 0;
+    bool ok = true;
+    while (ok && walk.next(p, rows, kTile, pc)) {
+      if (!(ok = wait(kBarQFree, (piece & 1u) ^ 1u))) break;
+      const int head0 = pc.r * kHeads, heads = min(kHeads, p.heads - head0);
+      const uint16_t* src = p.q + int64_t(pc.b) * p.q_stride + int64_t(head0) * kLatentDim;
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = half * 32 + k * 4 + (lane >> 3);
+          if (r < heads)
+            cp_async16(base + kQOff + c * kChunkBytes64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                       src + r * kLatentDim + c * 64 + (lane & 7) * 8, 16);
+        }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kBarQ));
+      ++piece;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the rows that cross CTAs: block (h, j) takes head h of the records c = j, j + gridDim.y, ...; its four
+// teams of 128 threads (4 channels each) take every fourth part, then add up in team order.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnParams p, const Record* records, int ctas) {
+  __shared__ float4 acc_s[4][128];
+  __shared__ float weight[kAttnMaxCtas];
+  __shared__ float top_s, sum_s;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int h = blockIdx.x, team = threadIdx.x >> 7, t = threadIdx.x & 127;
+  for (int c = blockIdx.y; c < ctas; c += gridDim.y) {
+    const Record r = records[c];
+    if (r.np <= 1 || h >= r.heads) continue;
+    auto part_at = [&](int i) { return p.parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * kPartFloats; };
+    if (threadIdx.x < 32) {
+      float top = -INFINITY;
+      for (int i = threadIdx.x; i < r.np; i += 32) top = fmaxf(top, __ldcg(part_at(i) + h));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float b0 = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      for (int i = threadIdx.x; i < r.np; i += 32) {
+        const float f = exp2_fast(__ldcg(part_at(i) + h) - b0);
+        weight[i] = f;
+        sum = fmaf(f, __ldcg(part_at(i) + kHeads + h), sum);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (threadIdx.x == 0) {
+        top_s = top;
+        sum_s = sum;
+      }
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = team; i < r.np; i += 4) {
+      const float f = weight[i];
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i) + 2 * kHeads + h * kLatentValue) + t);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    acc_s[team][t] = acc;
+    __syncthreads();
+    if (team == 0) {
+      for (int k = 1; k < 4; ++k) {
+        acc.x += acc_s[k][t].x;
+        acc.y += acc_s[k][t].y;
+        acc.z += acc_s[k][t].z;
+        acc.w += acc_s[k][t].w;
+      }
+      const float sum = sum_s, inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int64_t row = int64_t(r.b) * p.heads + r.head0 + h;
+      reinterpret_cast<uint2*>(p.out + row * kLatentValue)[t] =
+          make_uint2(pack_bf16x2_rn(acc.x * inv, acc.y * inv), pack_bf16x2_rn(acc.z * inv, acc.w * inv));
+      if (t == 0 && p.lse != nullptr) p.lse[row] = (top_s + log2f(sum)) * 0.69314718055994531f;
     }
     __syncthreads();
   }
-  const float inv = l > 0.f ? p.v_scale / l : 0.f;
-  for (int i = 0; i < 4; ++i) {
-    const int c = tid + i * kThreads;
-    if (c < dv) p.out[(int64_t(b) * p.heads + h) * dv + c] = f32_to_bf16_rn(l > 0.f ? acc[i] * inv : 0.f);
-  }
-  if (tid == 0 && p.lse != nullptr) p.lse[int64_t(b) * p.heads + h] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace latent
 
-size_t latent_part_bytes(int) { return 0; }
+using namespace latent;
 
-cudaError_t launch_latent_attention(const AttnParams& p, int, cudaStream_t stream) {
-  latent::attention_kernel<false><<<dim3(p.heads, p.batch), latent::kThreads, 0, stream>>>(p, kLatentValue);
-  note_launch();
-  return cudaGetLastError();
+size_t latent_part_bytes(int) {
+  return kAttnMaxCtas * sizeof(Record) + size_t(kLatentMaxCtas) * 2 * kPartFloats * sizeof(float);
+}
+
+cudaError_t launch_latent_attention(const AttnParams& p0, int device, cudaStream_t stream) {
+  static bool attr_set[64] = {false};
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[device]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_set[device] = true;
+  }
+  AttnParams p = p0;
+  Record* records = reinterpret_cast<Record*>(p.parts);
+  p.parts = reinterpret_cast<float*>(records + kAttnMaxCtas);
+  int grid = device_info(device).sm_count;
+  if (grid > kLatentMaxCtas) grid = kLatentMaxCtas;
+  latent_kernel<<<grid, kThreads, kSmemBytes, stream>>>(p, records);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.heads < kHeads ? p.heads : kHeads), 8);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_join_kernel, static_cast<const AttnParams&>(p), static_cast<const Record*>(records),
+                         grid);
+  note_launch(2);
+  return e;
 }
 
 }  // namespace moe
