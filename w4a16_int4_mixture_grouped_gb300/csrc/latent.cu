@@ -10,13 +10,15 @@
 //
 //   * Tiles of 64 tokens, two in shared memory (2 x 72 KB) beside the 64 queries (72 KB): each is
 //     filled by a team of its own with cp.async (rows gathered by page; unseen slots zero-filled), so a tile
-//     is always in flight. The MMA's M is 128, so S^T has 64 rows of keys and 64 rows of whatever follows in
-//     shared memory, whose lanes nobody reads.
-//   * S^T is double-buffered in TMEM (2 x 64 columns), O^T takes 256 columns (four 128-channel tiles).
-//     Two issuing warps, so that the next tile's scores run beside this tile's softmax and values.
-//   * Softmax: the heads are columns, a lane is a key; two groups of four warps take 32 heads each. The
-//     base of the exponents only moves when a tile's maximum passes it by 2^8 (BF16 probabilities keep their
-//     relative precision, FP32 sums their range), so the accumulator in TMEM is seldom rescaled.
+//     is always in flight.
+//   * S^T (M = 64: 16 lanes of each TMEM quarter) is double-buffered (2 x 64 columns), O^T takes 256 columns
+//     (four 128-channel tiles). Two issuing warps, so that the next tile's scores run beside this tile's
+//     softmax and values. Both products' operands come from shared memory: 4 KB a 64x64x16 MMA and 6 KB a
+//     128x64x16 one make 240 KB a tile, 1900 of the about 3250 cycles that a tile takes at HBM speed.
+//   * Softmax: the heads are columns, the lanes keys; two groups of four warps take 32 heads each, read in the
+//     MMA fragment layout (16 scores a thread). The base of the exponents only moves when a score passes it by
+//     2^8 (BF16 probabilities keep their relative precision, FP32 sums their range), so a tile costs no
+//     maximum over its keys, only a vote, and the accumulator in TMEM is seldom rescaled.
 //   * Work is shared out as in split.cuh; a row that crosses CTAs is written as FP32 parts, which a second
 //     kernel joins in order (64 heads x 512 channels are too much for one last CTA).
 #include <cuda_runtime.h>
@@ -57,9 +59,11 @@ enum {
 };
 constexpr int kMiscOff = kBarOff + kNumBars * 8;         // TMEM address, abort flag
 constexpr int kMaskOff = kMiscOff + 8;                   // [2] 64-bit masks of seen tokens
-constexpr int kMaxOff = kMaskOff + 16;                   // float [2][2][64] tile maxima by tile parity and key half
-constexpr int kSumOff = kMaxOff + 4 * kHeads * 4;        // float [2][64] sums by key half
-constexpr int kShareOff = (kSumOff + 2 * kHeads * 4 + 15) / 16 * 16;
+constexpr int kVoteOff = kMaskOff + 16;                  // int [2][2][4] votes by tile parity, group and quarter
+constexpr int kMaxOff = kVoteOff + 64;                   // float [4][64] maxima or sums by key quarter
+constexpr int kKeepOff = kMaxOff + 4 * kHeads * 4;       // float [64] factors of a rescale
+constexpr int kBaseOff = kKeepOff + kHeads * 4;          // float [64] bases at a row's end
+constexpr int kShareOff = (kBaseOff + kHeads * 4 + 15) / 16 * 16;
 constexpr int kSmemBytes = kShareOff + static_cast<int>(sizeof(Share));
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kPOff % 1024 == 0 && kQOff % 1024 == 0 && kChunkBytes64 % 1024 == 0, "swizzled tiles");
@@ -119,15 +123,20 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead_bytes
   return (static_cast<uint64_t>((addr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(lead_bytes >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-// kind::f16, FP32 accumulator, BF16 operands, M = 128, N = 64; bits 15 / 16: A / B M-major.
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kHeads >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-constexpr uint32_t kIdescScore = kIdesc;
-constexpr uint32_t kIdescValue = kIdesc | (1u << 15) | (1u << 16);
+// kind::f16, FP32 accumulator, BF16 operands, N = 64; bits 15 / 16: A / B M-major.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kHeads >> 3) << 17);
+constexpr uint32_t kIdescScore = kIdesc | (uint32_t(kTile >> 4) << 24);
+constexpr uint32_t kIdescValue = kIdesc | (uint32_t(128 >> 4) << 24) | (1u << 15) | (1u << 16);
 
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
+// 16 lanes x 32 columns in the MMA fragment layout: registers 4j, 4j+1 hold lane t/4, columns 8j + 2(t%4), +1
+// (thread t), registers 4j+2, 4j+3 the same of lane t/4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -160,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
     for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(kBarFull + i), 64);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarScore + i), 1);
-      mbar_init(bar(kBarScoreFree + i), 4);
+      mbar_init(bar(kBarScoreFree + i), 8);
       mbar_init(bar(kBarDone + i), 1);
       mbar_init(bar(kBarMax + i), 4);
       mbar_init(bar(kBarDrain + i), 1);
@@ -190,9 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
   if (warp < 8) {
     // ------------------------------------------------------------- softmax, rescale, epilogue
     const int q = warp & 3, group = warp >> 2;           // TMEM lane quarter, heads 32 group ..
-    const bool soft = q < 2;                             // lanes 0-63 hold the keys
+    const int r0 = lane >> 2, cc = lane & 3;             // this thread's keys 16 q + r0, + 8; heads 8 j + 2 cc, + 1
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    float* maxima = reinterpret_cast<float*>(smem + kMaxOff);
+    volatile int* votes = reinterpret_cast<volatile int*>(smem + kVoteOff);
+    float* maxima = reinterpret_cast<float*>(smem + kMaxOff) + 32 * group;      // [4][64]
+    float* keeps = reinterpret_cast<float*>(smem + kKeepOff) + 32 * group;
+    float* bases = reinterpret_cast<float*>(smem + kBaseOff) + 32 * group;
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(smem + kMaskOff);
     uint32_t it = 0, exchanges = 0;                      // tiles, exchanges of this CTA so far
     bool ok = true;
@@ -207,77 +219,100 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
     while (ok && walk.next(p, rows, kTile, pc)) {
       const int head0 = pc.r * kHeads, heads = min(kHeads, p.heads - head0);
       const int mine = min(32, heads - 32 * group);      // heads of this column group (may be <= 0)
-      float top = -INFINITY;                             // lane h: base of head 32 group + h
-      float l[32];
+      float at[8], l[8];                                 // bases and sums of heads 8 j + 2 cc + e at 2 j + e
 #pragma unroll
-      for (int h = 0; h < 32; ++h) l[h] = 0.f;
+      for (int h = 0; h < 8; ++h) {
+        at[h] = -INFINITY;
+        l[h] = 0.f;
+      }
       const int n = pc.tile1 - pc.tile0;
       for (int i = 0; i < n; ++i, ++it) {
         const int buf = it & 1;
         const uint32_t par = (it >> 1) & 1u;
-        uint32_t s[32];
-        if (soft) {
-          if (!(ok = wait(kBarScore + buf, par) && wait(kBarFull + buf * kGroups, par))) break;
-          tc_fence_after();
-          const bool seen = masks[buf * 2 + q] >> lane & 1u;
-          if (mine > 0) tmem_ld32(tmem + kScoreCol + buf * 64 + 32 * group + lanes, s);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarScoreFree + buf));
-          float best = -INFINITY;                        // lane h: this warp's maximum of head h
+        uint32_t s[16];
+        if (!(ok = wait(kBarScore + buf, par) && wait(kBarFull + buf * kGroups, par))) break;
+        tc_fence_after();
+        const uint32_t seen = masks[buf * 2 + (q >> 1)] >> (16 * (q & 1)) & 0xffffu;
+        tmem_ld_frag(tmem + kScoreCol + buf * 64 + 32 * group + lanes, s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarScoreFree + buf));
+        bool over = false;
+        if (seen != 0xffffu) {
+          const bool a = seen >> r0 & 1u, b = seen >> (r0 + 8) & 1u;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) {
-            if (h >= mine) break;
-            const float v = seen ? __uint_as_float(s[h]) * p.score_scale : -INFINITY;
-            s[h] = __float_as_uint(v);
-            const float w = warp_max(v);
-            if (lane == h) best = w;
+          for (int k = 0; k < 16; ++k) {
+            const bool in = (k & 2) ? b : a;
+            const float v = in ? __uint_as_float(s[k]) * p.score_scale : -INFINITY;
+            s[k] = __float_as_uint(v);
+            over |= v > at[(k >> 2) * 2 + (k & 1)] + 8.f;
           }
-          maxima[(buf * 2 + q) * kHeads + 32 * group + lane] = best;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float v = __uint_as_float(s[k]) * p.score_scale;
+            s[k] = __float_as_uint(v);
+            over |= v > at[(k >> 2) * 2 + (k & 1)] + 8.f;   // at = -inf at first: any seen score
+          }
         }
+        over = __any_sync(0xffffffffu, over);
+        if (lane == 0) votes[(buf * 2 + group) * 4 + q] = over;
         if (!(ok = exchange())) break;
-        const float tile_top = fmaxf(maxima[buf * 2 * kHeads + 32 * group + lane],
-                                     maxima[(buf * 2 + 1) * kHeads + 32 * group + lane]);
-        const bool move = tile_top > top + 8.f;          // top = -inf at first: any seen score moves it
-        const float next = move ? tile_top : top;
-        const float keep = move ? exp2_fast(top - next) : 1.f;
-        const bool rescale = __any_sync(0xffffffffu, move);
-        top = next;
+        over = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) over |= votes[(buf * 2 + group) * 4 + k] != 0;
+        if (over) {
+          // new bases: the maximum over the tile's keys where it passes the old one
+          float best[8];
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            best[h] = fmaxf(__uint_as_float(s[(h >> 1) * 4 + (h & 1)]), __uint_as_float(s[(h >> 1) * 4 + 2 + (h & 1)]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], o));
+            if (r0 == 0) maxima[q * kHeads + (h >> 1) * 8 + 2 * cc + (h & 1)] = best[h];
+          }
+          if (!(ok = exchange())) break;
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const int head = (h >> 1) * 8 + 2 * cc + (h & 1);
+            float top = at[h];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, maxima[k * kHeads + head]);
+            const float keep = top == at[h] ? 1.f : exp2_fast(at[h] - top);
+            at[h] = top;
+            l[h] *= keep;
+            if (q == 0 && r0 == 0) keeps[head] = keep;
+          }
+          if (!(ok = exchange())) break;
+        }
         // the previous tile's product is done: O^T is stable, P and the tile after it are free
         if (it != 0 && !(ok = wait(kBarDone + (buf ^ 1), ((it - 1) >> 1) & 1u))) break;
-        if (rescale && i > 0 && mine > 0) {
+        if (over && i > 0 && mine > 0) {
           tc_fence_after();
 #pragma unroll 1
           for (int mt = 0; mt < kValueTiles; ++mt) {
             uint32_t o[32];
-            const uint32_t at = tmem + kAccCol + mt * 64 + 32 * group + lanes;
-            tmem_ld32(at, o);
+            const uint32_t acc = tmem + kAccCol + mt * 64 + 32 * group + lanes;
+            tmem_ld32(acc, o);
 #pragma unroll
-            for (int h = 0; h < 32; ++h)
-              o[h] = __float_as_uint(__uint_as_float(o[h]) * __shfl_sync(0xffffffffu, keep, h));
-            tmem_st32(at, o);
+            for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * keeps[h]);
+            tmem_st32(acc, o);
           }
         }
-        if (soft) {
-          const float b0 = top == -INFINITY ? 0.f : top;
-          uint32_t packed[16];
+        {
+          uint8_t* row = smem + kPOff + (16 * q + r0) * 128 + cc * 4;    // rows r0 and r0 + 8: the same swizzle
 #pragma unroll
-          for (int h = 0; h < 32; h += 2) {
-            const float e0 = exp2_fast(__uint_as_float(s[h]) - __shfl_sync(0xffffffffu, b0, h));
-            const float e1 = exp2_fast(__uint_as_float(s[h + 1]) - __shfl_sync(0xffffffffu, b0, h + 1));
-            if (rescale) {
-              l[h] *= __shfl_sync(0xffffffffu, keep, h);
-              l[h + 1] *= __shfl_sync(0xffffffffu, keep, h + 1);
-            }
-            l[h] += h < mine ? e0 : 0.f;
-            l[h + 1] += h + 1 < mine ? e1 : 0.f;
-            packed[h / 2] = h < mine ? pack_bf16x2_rn(e0, h + 1 < mine ? e1 : 0.f) : 0u;
+          for (int j = 0; j < 4; ++j) {
+            const float b0 = at[2 * j] == -INFINITY ? 0.f : at[2 * j], b1 = at[2 * j + 1] == -INFINITY ? 0.f : at[2 * j + 1];
+            const float e0 = exp2_fast(__uint_as_float(s[4 * j]) - b0), e1 = exp2_fast(__uint_as_float(s[4 * j + 1]) - b1);
+            const float e2 = exp2_fast(__uint_as_float(s[4 * j + 2]) - b0),
+                        e3 = exp2_fast(__uint_as_float(s[4 * j + 3]) - b1);
+            l[2 * j] += e0 + e2;
+            l[2 * j + 1] += e1 + e3;
+            const int chunk = ((group * 4 + j) ^ r0) << 4;
+            *reinterpret_cast<uint32_t*>(row + chunk) = pack_bf16x2_rn(e0, e1);
+            *reinterpret_cast<uint32_t*>(row + 8 * 128 + chunk) = pack_bf16x2_rn(e2, e3);
           }
-          const int key = 32 * q + lane;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(smem + kPOff + key * 128 + (((group * 4 + j) ^ (key & 7)) << 4)) =
-                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -287,23 +322,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
       if (!ok) break;
 
       // ---- epilogue: the sums over keys, then this quarter's channels of O^T
-      float* sums = reinterpret_cast<float*>(smem + kSumOff);
-      if (soft) {
-        // 32 sums over 32 lanes: halve the heads a lane holds at each step; lane h ends with head h
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+      for (int h = 0; h < 8; ++h) {
 #pragma unroll
-          for (int h = 0; h < o; ++h) {
-            const bool hi = lane & o;
-            const float send = hi ? l[h] : l[h + o];
-            const float got = __shfl_xor_sync(0xffffffffu, send, o);
-            l[h] = (hi ? l[h + o] : l[h]) + got;
-          }
+        for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        if (r0 == 0) {
+          const int head = (h >> 1) * 8 + 2 * cc + (h & 1);
+          maxima[q * kHeads + head] = l[h];
+          if (q == 0) bases[head] = at[h];
         }
-        sums[q * kHeads + 32 * group + lane] = l[0];
       }
       if (!(ok = exchange())) break;
-      const float sum = sums[32 * group + lane] + sums[kHeads + 32 * group + lane];
+      const float top = bases[lane];                     // lane h: head 32 group + h
+      const float sum = maxima[lane] + maxima[kHeads + lane] + maxima[2 * kHeads + lane] + maxima[3 * kHeads + lane];
       if (!(ok = wait(kBarDone + ((it - 1) & 1), ((it - 1) >> 1) & 1u))) break;
       tc_fence_after();
       const int c0 = cta_of(total, ctas, pc.row0), c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1);
@@ -473,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
     }
   } else {
     // ------------------------------------------------------------- queries of a piece
-    // Rows past the last head keep what they held: their columns of S^T and O^T are never read.
+    // Rows past the last head are zeros.
     const int half = warp - 14;
     uint32_t piece = 0;
     bool ok = true;
@@ -485,9 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = half * 32 + k * 4 + (lane >> 3);
-          if (r < heads)
-            cp_async16(base + kQOff + c * kChunkBytes64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                       src + r * kLatentDim + c * 64 + (lane & 7) * 8, 16);
+          cp_async16(base + kQOff + c * kChunkBytes64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                     r < heads ? src + r * kLatentDim + c * 64 + (lane & 7) * 8 : src, r < heads ? 16 : 0);
         }
       cp_async_commit();
       cp_async_wait<0>();
