@@ -11,10 +11,12 @@
 //   * Tiles of 64 tokens, two in shared memory (2 x 72 KB) beside the 64 queries (72 KB): each is
 //     filled by a team of its own with cp.async (rows gathered by page; unseen slots zero-filled), so a tile
 //     is always in flight.
-//   * S^T (M = 64: 16 lanes of each TMEM quarter) is double-buffered (2 x 64 columns), O^T takes 256 columns
-//     (four 128-channel tiles). Two issuing warps, so that the next tile's scores run beside this tile's
-//     softmax and values. Both products' operands come from shared memory: 4 KB a 64x64x16 MMA and 6 KB a
-//     128x64x16 one make 240 KB a tile, 1900 of the about 3250 cycles that a tile takes at HBM speed.
+//   * S^T (M = 64: 16 lanes of each TMEM quarter) is double-buffered, O^T takes 256 columns (four 128-channel
+//     tiles). The next tile's scores run beside this tile's softmax and values. A thread issues an MMA every 60
+//     to 75 cycles whatever its size, 52 of them a tile, so each product has two issuing warps: S^T in two
+//     accumulators (even and odd chunks of the reduction) that the softmax adds up, O^T two channel tiles each.
+//     Both products' operands come from shared memory: 4 KB a 64x64x16 MMA and 6 KB a 128x64x16 one make
+//     240 KB a tile, 1900 of the about 3250 cycles that a tile takes at HBM speed.
 //   * Softmax: the heads are columns, the lanes keys; two groups of four warps take 32 heads each, read in the
 //     MMA fragment layout (16 scores a thread). The base of the exponents only moves when a score passes it by
 //     2^8 (BF16 probabilities keep their relative precision, FP32 sums their range), so a tile costs no
@@ -37,7 +39,7 @@ constexpr int kChunkBytes64 = 64 * 128;       // 64 rows of one chunk, 128-byte 
 constexpr int kTileBytes = kChunks * kChunkBytes64;      // 73,728
 constexpr int kValueTiles = kLatentValue / 128;          // M tiles of O^T: 4
 
-// warps: 0-7 softmax / rescale / epilogue, 8-11 tile loaders (two teams), 12 S issuer, 13 O issuer, 14-15 queries
+// warps: 0-7 softmax / rescale / epilogue, 8-11 tile loaders (two teams), 12-13 queries and S^T, 14-15 O^T
 constexpr int kThreads = 512;
 constexpr int kGroups = 3;                    // chunk groups of a tile that the S issuer waits for
 
@@ -69,8 +71,8 @@ static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kPOff % 1024 == 0 && kQOff % 1024 == 0 && kChunkBytes64 % 1024 == 0, "swizzled tiles");
 
 constexpr int kTmemCols = 512;
-constexpr int kScoreCol = 0;                  // S^T buffers at columns 0 and 64
-constexpr int kAccCol = 128;                  // O^T tile i at 128 + 64 i
+constexpr int kScoreCol = 0;                  // S^T buffer b, accumulator a at 128 b + 64 a
+constexpr int kAccCol = 256;                  // O^T tile i at 256 + 64 i
 
 // A part of a row: base and sum of its 64 heads, then O^T unnormalised as [64][512].
 constexpr int kPartFloats = 2 * kHeads + kHeads * kLatentValue;
@@ -136,6 +138,11 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
+}
+// Both accumulators of a score buffer.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16], uint32_t (&r2)[16]) {
+  tmem_ld_frag(addr, r);
+  tmem_ld_frag(addr + 64, r2);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -168,15 +175,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(kBarFull + i), 64);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarScore + i), 1);
+      mbar_init(bar(kBarScore + i), 2);
       mbar_init(bar(kBarScoreFree + i), 8);
-      mbar_init(bar(kBarDone + i), 1);
+      mbar_init(bar(kBarDone + i), 2);
       mbar_init(bar(kBarMax + i), 4);
-      mbar_init(bar(kBarDrain + i), 1);
+      mbar_init(bar(kBarDrain + i), 2);
     }
     mbar_init(bar(kBarProb), 8);
     mbar_init(bar(kBarQ), 64);
-    mbar_init(bar(kBarQFree), 1);
+    mbar_init(bar(kBarQFree), 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -233,7 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
         if (!(ok = wait(kBarScore + buf, par) && wait(kBarFull + buf * kGroups, par))) break;
         tc_fence_after();
         const uint32_t seen = masks[buf * 2 + (q >> 1)] >> (16 * (q & 1)) & 0xffffu;
-        tmem_ld_frag(tmem + kScoreCol + buf * 64 + 32 * group + lanes, s);
+        {
+          uint32_t s2[16];
+          tmem_ld_frag(tmem + kScoreCol + buf * 128 + 32 * group + lanes, s, s2);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) + __uint_as_float(s2[k]));
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarScoreFree + buf));
@@ -406,20 +418,35 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
         if (g >= 2 && !(ok = wait(kBarDone + team, ((g >> 1) - 1) & 1u))) break;
         if (lane == 0) masks[team * 2 + half] = seen;
         entry = entry_of(i + 2);
-        int64_t from[8];
+        const uint8_t* from[8];
+        uint32_t to[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
-        const uint32_t dst0 = base + kKOff + team * kTileBytes + half * 4096;
+        for (int k = 0; k < 8; ++k) {
+          const int64_t o = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
+          from[k] = src + (o >= 0 ? o + (lane & 7) * 16 : 0);
+          const int r = k * 4 + (lane >> 3);
+          to[k] = base + kKOff + team * kTileBytes + half * 4096 + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+        }
+        if (seen == 0xffffffffu) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = k * 4 + (lane >> 3);
-            const bool have = from[k] >= 0;
-            cp_async16(dst0 + c * kChunkBytes64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                       src + (have ? from[k] + c * 128 + (lane & 7) * 16 : 0), have ? 16 : 0);
+            for (int k = 0; k < 8; ++k)
+              asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to[k] + c * kChunkBytes64),
+                           "l"(from[k] + c * 128)
+                           : "memory");
+            if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
           }
-          if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const bool have = seen >> (k * 4 + (lane >> 3)) & 1u;
+              cp_async16(to[k] + c * kChunkBytes64, have ? from[k] + c * 128 : src, have ? 16 : 0);
+            }
+            if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
+          }
         }
         static_assert(kGroups == 3, "waits below");
         cp_async_wait<2>();
@@ -435,78 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
       it += n;
     }
     cp_async_wait<0>();
-  } else if (warp == 12) {
-    // ------------------------------------------------------------- S^T = K Q^T
+  } else if (warp < 14) {
+    // ------------------------------------------------------------- queries of a piece, S^T = K Q^T
+    // Query rows past the last head are zeros. Issuer 0 takes the even chunks, issuer 1 the odd ones.
+    const int half = warp - 12;
     uint32_t it = 0, piece = 0;
-    bool ok = true;
-    while (ok && walk.next(p, rows, kTile, pc)) {
-      if (!(ok = wait(kBarQ, piece & 1u))) break;
-      const int n = pc.tile1 - pc.tile0;
-      for (int i = 0; i < n; ++i, ++it) {
-        const int buf = it & 1;
-        const uint32_t par = (it >> 1) & 1u;
-        if (!(ok = wait(kBarScoreFree + buf, par ^ 1u))) break;
-        const uint32_t d = tmem + kScoreCol + buf * 64;
-        for (int grp = 0; grp < kGroups; ++grp) {
-          if (!(ok = wait(kBarFull + buf * kGroups + grp, par))) break;
-          tc_fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int cc = 0; cc < kChunks / kGroups; ++cc) {
-              const int c = grp * (kChunks / kGroups) + cc;
-              const uint64_t a = smem_desc(base + kKOff + buf * kTileBytes + c * kChunkBytes64, 16);
-              const uint64_t b = smem_desc(base + kQOff + c * kChunkBytes64, 16);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)                // 16 channels = 32 bytes a step
-                tc_mma(d, a + 2 * k, b + 2 * k, kIdescScore, c == 0 && k == 0 ? 0u : 1u);
-            }
-            if (grp == kGroups - 1) tc_commit(bar(kBarScore + buf));
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-      }
-      if (lane == 0) tc_commit(bar(kBarQFree));
-      __syncwarp();
-      ++piece;
-    }
-    if (lane == 0) {
-      tc_commit(bar(kBarDrain));
-      mbar_drain(bar(kBarDrain), 0);
-    }
-  } else if (warp == 13) {
-    // ------------------------------------------------------------- O^T += V^T P^T
-    uint32_t it = 0;
-    bool ok = true;
-    while (ok && walk.next(p, rows, kTile, pc)) {
-      const int n = pc.tile1 - pc.tile0;
-      for (int i = 0; i < n; ++i, ++it) {
-        const int buf = it & 1;
-        if (!(ok = wait(kBarProb, it & 1u))) break;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int mt = 0; mt < kValueTiles; ++mt) {
-            const uint64_t a = smem_desc(base + kKOff + buf * kTileBytes + mt * 2 * kChunkBytes64, kChunkBytes64);
-            const uint64_t b = smem_desc(base + kPOff, kChunkBytes64);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)         // 16 tokens = two 1024-byte groups a step
-              tc_mma(tmem + kAccCol + mt * 64, a + k * 128, b + k * 128, kIdescValue, i == 0 && k == 0 ? 0u : 1u);
-          }
-          tc_commit(bar(kBarDone + buf));
-        }
-        __syncwarp();
-      }
-    }
-    if (lane == 0) {
-      tc_commit(bar(kBarDrain + 1));
-      mbar_drain(bar(kBarDrain + 1), 0);
-    }
-  } else {
-    // ------------------------------------------------------------- queries of a piece
-    // Rows past the last head are zeros.
-    const int half = warp - 14;
-    uint32_t piece = 0;
     bool ok = true;
     while (ok && walk.next(p, rows, kTile, pc)) {
       if (!(ok = wait(kBarQFree, (piece & 1u) ^ 1u))) break;
@@ -523,7 +483,73 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
       cp_async_wait<0>();
       fence_proxy_async_smem();
       mbar_arrive(bar(kBarQ));
+      if (!(ok = wait(kBarQ, piece & 1u))) break;
+      const int n = pc.tile1 - pc.tile0;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it & 1;
+        const uint32_t par = (it >> 1) & 1u;
+        if (!(ok = wait(kBarScoreFree + buf, par ^ 1u))) break;
+        const uint32_t d = tmem + kScoreCol + buf * 128 + half * 64;
+#pragma unroll
+        for (int grp = 0; grp < kGroups; ++grp) {
+          if (ok) ok = wait(kBarFull + buf * kGroups + grp, par);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int cc = 0; cc < kChunks / kGroups; ++cc) {
+              const int c = grp * (kChunks / kGroups) + cc;
+              if ((c & 1) != half) continue;
+              const uint64_t a = smem_desc(base + kKOff + buf * kTileBytes + c * kChunkBytes64, 16);
+              const uint64_t b = smem_desc(base + kQOff + c * kChunkBytes64, 16);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)                // 16 channels = 32 bytes a step
+                tc_mma(d, a + 2 * k, b + 2 * k, kIdescScore, c < 2 && k == 0 ? 0u : 1u);
+            }
+            if (grp == kGroups - 1) tc_commit(bar(kBarScore + buf));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (lane == 0) tc_commit(bar(kBarQFree));
+      __syncwarp();
       ++piece;
+    }
+    cp_async_wait<0>();
+    if (lane == 0) {
+      tc_commit(bar(kBarDrain));
+      mbar_drain(bar(kBarDrain), 0);
+    }
+  } else {
+    // ------------------------------------------------------------- O^T += V^T P^T, two channel tiles an issuer
+    const int half = warp - 14;
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next(p, rows, kTile, pc)) {
+      const int n = pc.tile1 - pc.tile0;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it & 1;
+        if (!(ok = wait(kBarProb, it & 1u))) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int m = 0; m < kValueTiles / 2; ++m) {
+            const int mt = half * (kValueTiles / 2) + m;
+            const uint64_t a = smem_desc(base + kKOff + buf * kTileBytes + mt * 2 * kChunkBytes64, kChunkBytes64);
+            const uint64_t b = smem_desc(base + kPOff, kChunkBytes64);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)         // 16 tokens = two 1024-byte groups a step
+              tc_mma(tmem + kAccCol + mt * 64, a + k * 128, b + k * 128, kIdescValue, i == 0 && k == 0 ? 0u : 1u);
+          }
+          tc_commit(bar(kBarDone + buf));
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      tc_commit(bar(kBarDrain + 1));
+      mbar_drain(bar(kBarDrain + 1), 0);
     }
   }
 
