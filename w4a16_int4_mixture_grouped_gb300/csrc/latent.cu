@@ -145,6 +145,10 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16], u
   tmem_ld_frag(addr + 64, r2);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// Bytes (a multiple of 16, from a 16-byte boundary) on their way from HBM to L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -417,7 +421,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
         const uint32_t seen = __ballot_sync(0xffffffffu, off >= 0);
         if (g >= 2 && !(ok = wait(kBarDone + team, ((g >> 1) - 1) & 1u))) break;
         if (lane == 0) masks[team * 2 + half] = seen;
-        entry = entry_of(i + 2);
         const uint8_t* from[8];
         uint32_t to[8];
 #pragma unroll
@@ -448,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
             if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
           }
         }
+        entry = entry_of(i + 2);
         static_assert(kGroups == 3, "waits below");
         cp_async_wait<2>();
         fence_proxy_async_smem();
@@ -458,6 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
         cp_async_wait<0>();
         fence_proxy_async_smem();
         mbar_arrive(bar(kBarFull + team * kGroups + 2));
+        // this team's next tile on its way to L2 while this one is worked on (an instruction a row: slow to issue,
+        // so behind the arrivals)
+        if (entry >= 0 && entry < p.t.num_pages)
+          prefetch_l2(src + (int64_t(entry) * p.page_stride + int64_t((tok + 2 * kTile) % p.t.page_size) * p.token_stride) * 2,
+                      kLatentDim * 2);
       }
       it += n;
     }
@@ -561,65 +570,98 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
   }
 }
 
-// Joins the rows that cross CTAs: block (h, j) takes head h of the records c = j, j + gridDim.y, ...; its four
-// teams of 128 threads (4 channels each) take every fourth part, then add up in team order.
-constexpr int kJoinThreads = 512;
+// Joins the rows that cross CTAs. Every block lists the split rows (records with more than one part); an item
+// is (row, head), 512 channels. Many items: a warp each; few: a block each, its warps taking every eighth part.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kLaneVecs = kLatentValue / 4 / 32;          // float4 of a lane: 4
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnParams p, const Record* records, int ctas) {
-  __shared__ float4 acc_s[4][128];
-  __shared__ float weight[kAttnMaxCtas];
-  __shared__ float top_s, sum_s;
+  __shared__ int list[kAttnMaxCtas];
+  __shared__ float4 acc_s[kJoinWarps][kLatentValue / 4];
+  __shared__ int count_s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int h = blockIdx.x, team = threadIdx.x >> 7, t = threadIdx.x & 127;
-  for (int c = blockIdx.y; c < ctas; c += gridDim.y) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int count = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const bool split = c0 + lane < ctas && __ldcg(&records[c0 + lane].np) > 1;
+      const uint32_t m = __ballot_sync(0xffffffffu, split);
+      if (split) list[count + __popc(m & ((1u << lane) - 1u))] = c0 + lane;
+      count += __popc(m);
+    }
+    if (lane == 0) count_s = count;
+  }
+  __syncthreads();
+  const int heads = min(kHeads, p.heads);
+  const int64_t items = int64_t(count_s) * heads;
+  const bool by_warp = items > int64_t(gridDim.x) * 2;
+  const int64_t first = by_warp ? int64_t(blockIdx.x) * kJoinWarps + warp : blockIdx.x;
+  const int64_t step = by_warp ? int64_t(gridDim.x) * kJoinWarps : gridDim.x;
+  const int part0 = by_warp ? 0 : warp, parts_step = by_warp ? 1 : kJoinWarps;
+  for (int64_t item = first; item < items; item += step) {
+    const int c = list[item / heads], h = static_cast<int>(item % heads);
     const Record r = records[c];
-    if (r.np <= 1 || h >= r.heads) continue;
+    if (h >= r.heads) continue;                           // (a block by itself: all of its warps alike)
     auto part_at = [&](int i) { return p.parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * kPartFloats; };
-    if (threadIdx.x < 32) {
-      float top = -INFINITY;
-      for (int i = threadIdx.x; i < r.np; i += 32) top = fmaxf(top, __ldcg(part_at(i) + h));
+    float top = -INFINITY;
+    for (int i = lane; i < r.np; i += 32) top = fmaxf(top, __ldcg(part_at(i) + h));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float b0 = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      for (int i = threadIdx.x; i < r.np; i += 32) {
-        const float f = exp2_fast(__ldcg(part_at(i) + h) - b0);
-        weight[i] = f;
-        sum = fmaf(f, __ldcg(part_at(i) + kHeads + h), sum);
-      }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float b0 = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 acc[kLaneVecs];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (threadIdx.x == 0) {
-        top_s = top;
-        sum_s = sum;
+    for (int k = 0; k < kLaneVecs; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < r.np; i0 += 32) {
+      // lane i: the weight of part i0 + i
+      float f = 0.f;
+      if (i0 + lane < r.np) {
+        f = exp2_fast(__ldcg(part_at(i0 + lane) + h) - b0);
+        sum = fmaf(f, __ldcg(part_at(i0 + lane) + kHeads + h), sum);
+      }
+      const int n = min(32, r.np - i0);
+#pragma unroll 4
+      for (int i = part0; i < n; i += parts_step) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        const float4* src = reinterpret_cast<const float4*>(part_at(i0 + i) + 2 * kHeads + h * kLatentValue) + lane;
+#pragma unroll
+        for (int k = 0; k < kLaneVecs; ++k) {
+          const float4 v = __ldcg(src + 32 * k);
+          acc[k].x = fmaf(w, v.x, acc[k].x);
+          acc[k].y = fmaf(w, v.y, acc[k].y);
+          acc[k].z = fmaf(w, v.z, acc[k].z);
+          acc[k].w = fmaf(w, v.w, acc[k].w);
+        }
       }
     }
-    __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = team; i < r.np; i += 4) {
-      const float f = weight[i];
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i) + 2 * kHeads + h * kLatentValue) + t);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
-    acc_s[team][t] = acc;
-    __syncthreads();
-    if (team == 0) {
-      for (int k = 1; k < 4; ++k) {
-        acc.x += acc_s[k][t].x;
-        acc.y += acc_s[k][t].y;
-        acc.z += acc_s[k][t].z;
-        acc.w += acc_s[k][t].w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (!by_warp) {
+      // the warps' sums, added in their order
+#pragma unroll
+      for (int k = 0; k < kLaneVecs; ++k) acc_s[warp][32 * k + lane] = acc[k];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int k = 0; k < kLaneVecs; ++k)
+          for (int w = 1; w < kJoinWarps; ++w) {
+            const float4 v = acc_s[w][32 * k + lane];
+            acc[k].x += v.x;
+            acc[k].y += v.y;
+            acc[k].z += v.z;
+            acc[k].w += v.w;
+          }
       }
-      const float sum = sum_s, inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int64_t row = int64_t(r.b) * p.heads + r.head0 + h;
-      reinterpret_cast<uint2*>(p.out + row * kLatentValue)[t] =
-          make_uint2(pack_bf16x2_rn(acc.x * inv, acc.y * inv), pack_bf16x2_rn(acc.z * inv, acc.w * inv));
-      if (t == 0 && p.lse != nullptr) p.lse[row] = (top_s + log2f(sum)) * 0.69314718055994531f;
+      __syncthreads();
+      if (warp != 0) continue;
     }
-    __syncthreads();
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t row = int64_t(r.b) * p.heads + r.head0 + h;
+#pragma unroll
+    for (int k = 0; k < kLaneVecs; ++k)
+      reinterpret_cast<uint2*>(p.out + row * kLatentValue)[32 * k + lane] =
+          make_uint2(pack_bf16x2_rn(acc[k].x * inv, acc[k].y * inv), pack_bf16x2_rn(acc[k].z * inv, acc[k].w * inv));
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = (top + log2f(sum)) * 0.69314718055994531f;
   }
 }
 
@@ -650,7 +692,7 @@ cudaError_t launch_latent_attention(const AttnParams& p0, int device, cudaStream
   if (e != cudaSuccess) return e;
   // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.heads < kHeads ? p.heads : kHeads), 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * 4));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
