@@ -375,10 +375,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
           tmem_ld32(tmem + kAccCol + mt * 64 + 32 * group + lanes, o);
           const int d = mt * 128 + 32 * q + lane;
           if (whole) {
+            // lane pairs trade values so that each stores two channels of one head: the even lane of the first,
+            // the odd lane of the second of two heads
 #pragma unroll
-            for (int h = 0; h < 32; ++h) {
-              const float f = __shfl_sync(0xffffffffu, inv, h);
-              if (h < mine) p.out[(out0 + h) * kLatentValue + d] = f32_to_bf16_rn(__uint_as_float(o[h]) * f);
+            for (int h = 0; h < 32; h += 2) {
+              const float v0 = __uint_as_float(o[h]) * __shfl_sync(0xffffffffu, inv, h);
+              const float v1 = __uint_as_float(o[h + 1]) * __shfl_sync(0xffffffffu, inv, h + 1);
+              const bool odd = lane & 1;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+              const int head = h + (odd ? 1 : 0);
+              if (head < mine)
+                *reinterpret_cast<uint32_t*>(p.out + (out0 + head) * kLatentValue + (d & ~1)) =
+                    odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
             }
           } else {
             float* dst = part + 2 * kHeads + 32 * group * kLatentValue + d;
@@ -481,13 +489,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
       if (!(ok = wait(kBarQFree, (piece & 1u) ^ 1u))) break;
       const int head0 = pc.r * kHeads, heads = min(kHeads, p.heads - head0);
       const uint16_t* src = p.q + int64_t(pc.b) * p.q_stride + int64_t(head0) * kLatentDim;
-      for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = half * 32 + k * 4 + (lane >> 3);
-          cp_async16(base + kQOff + c * kChunkBytes64 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                     r < heads ? src + r * kLatentDim + c * 64 + (lane & 7) * 8 : src, r < heads ? 16 : 0);
-        }
+      for (int k = 0; k < 8; ++k) {
+        const int r = half * 32 + k * 4 + (lane >> 3);
+        const uint32_t to = base + kQOff + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+        const uint16_t* from = src + (r < heads ? r * kLatentDim + (lane & 7) * 8 : 0);
+        const uint32_t bytes = r < heads ? 16 : 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) cp_async16(to + c * kChunkBytes64, from + (bytes ? c * 64 : 0), bytes);
+      }
       cp_async_commit();
       cp_async_wait<0>();
       fence_proxy_async_smem();
