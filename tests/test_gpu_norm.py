@@ -54,6 +54,24 @@ def test_rows(rows):
     check(bf16(rng, rows, 512), bf16(rng, rows, 512), bf16(rng, 512), bf16(rng, 512), None)
 
 
+@pytest.mark.parametrize("n", [1032, 2048, 2056, 7168, 8192, 8200, 16384])
+@pytest.mark.parametrize("res32", [False, True])
+@pytest.mark.parametrize("gate", [None, "channel", "token", "sequence"])
+def test_many_long_rows(n, res32, gate):
+    rng = np.random.default_rng(n + res32)
+    t = 1300 if n < 8000 else 1240
+    h = bf16(rng, t, n, scale=2.0)
+    g = {None: None, "channel": bf16(rng, n), "token": bf16(rng, t, n), "sequence": bf16(rng, 20, n)}[gate]
+    check(bf16(rng, t, n), h.float() if res32 else h, bf16(rng, n), bf16(rng, n), g)
+
+
+@pytest.mark.parametrize("post,pre", [(False, False), (False, True), (True, False)])
+def test_many_long_rows_without_a_norm(post, pre):
+    rng = np.random.default_rng(post + 2 * pre)
+    t, n = 1300, 1544
+    check(bf16(rng, t, n), bf16(rng, t, n), bf16(rng, n) if post else None, bf16(rng, n) if pre else None, None)
+
+
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("pre", [False, True])
 @pytest.mark.parametrize("gate", [None, "channel", "sequence", "token"])
