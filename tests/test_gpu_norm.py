@@ -65,6 +65,23 @@ def test_many_long_rows(n, res32, gate):
     check(bf16(rng, t, n), h.float() if res32 else h, bf16(rng, n), bf16(rng, n), g)
 
 
+@pytest.mark.parametrize("n", [1, 3, 8, 57, 63, 64, 65, 121, 250, 256, 257, 505, 512, 513, 1021, 1026, 4100, 8185, 8191, 16377])
+@pytest.mark.parametrize("res32", [False, True])
+def test_widths_of_many_rows(n, res32):
+    """Rows that start at every alignment; neighbours untouched (a guard column on each side of the outputs)."""
+    rng = np.random.default_rng(n + res32)
+    t = 701
+    h = bf16(rng, t, n, scale=2.0)
+    h = h.float() if res32 else h
+    x, w1, w2 = bf16(rng, t, n), bf16(rng, n), bf16(rng, n)
+    out, y = check(x, h, w1, w2, bf16(rng, n))
+    flat_h = torch.full((t * n + 16,), 7.0, dtype=h.dtype, device=DEV)
+    flat_y = torch.full((t * n + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+    check(x, h, w1, w2, None, out=flat_h[8:8 + t * n].view(t, n), y=flat_y[8:8 + t * n].view(t, n))
+    for f in (flat_h, flat_y):
+        assert (f[:8] == 7).all() and (f[8 + t * n:] == 7).all()
+
+
 @pytest.mark.parametrize("post,pre", [(False, False), (False, True), (True, False)])
 def test_many_long_rows_without_a_norm(post, pre):
     rng = np.random.default_rng(post + 2 * pre)

@@ -134,6 +134,8 @@ struct NormParams {
   uint16_t* y;
   int64_t y_stride;
 };
-cudaError_t launch_block_norm(const NormParams& p, bool res32, bool vec, int device, cudaStream_t stream);
+// width: columns of one access (8, 4, 2 or 1) that every row of every tensor allows; shift: rows that start anywhere, but
+// all tensors' alike, from 16-byte aligned first rows.
+cudaError_t launch_block_norm(const NormParams& p, bool res32, int width, bool shift, int device, cudaStream_t stream);
 
 }  // namespace moe

@@ -343,14 +343,25 @@ moe_w4a16_status moe_w4a16_block_norm(const uint16_t* x, int64_t x_stride, const
     return MOE_W4A16_ERR_INVALID_ARG;
   const bool res32 = residual_dtype == MOE_W4A16_RESIDUAL_F32;
   const auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
-  // element alignment of every tensor; the vector path needs 16 bytes and strides of 8 elements
+  // element alignment of every tensor, then the widest access that all rows of all of them allow: 2 bytes a column
+  // for BF16, 4 (up to 16 in all) for an FP32 residual
   const uintptr_t res = bits(h) | bits(h_out), rest = bits(x) | bits(gate) | bits(w_post) | bits(w_pre) | bits(y);
   if ((res & (res32 ? 3u : 1u)) != 0 || (rest & 1u) != 0) return MOE_W4A16_ERR_INVALID_ARG;
-  int64_t strides = n | h_stride;
-  if (x != nullptr) strides |= x_stride;
-  if (h_out != nullptr) strides |= h_out_stride;
-  if (y != nullptr) strides |= y_stride;
-  const bool vec = ((res | rest) & 15u) == 0 && strides % 8 == 0;
+  int64_t columns = n;
+  if (rows > 1) {
+    columns |= h_stride;
+    if (x != nullptr) columns |= x_stride;
+    if (h_out != nullptr) columns |= h_out_stride;
+    if (y != nullptr) columns |= y_stride;
+  }
+  int width = 8;
+  while (width > 1 && (columns % width != 0 || (rest & (2u * width - 1u)) != 0 ||
+                       (res & (res32 ? (width > 4 ? 15u : 4u * width - 1u) : 2u * width - 1u)) != 0))
+    width /= 2;
+  // rows that start at any column, but all tensors' alike
+  const auto alike = [&](const void* t, int64_t stride) { return t == nullptr || rows == 1 || (stride - h_stride) % 8 == 0; };
+  const bool shift = width < 8 && ((res | bits(x) | bits(y)) & 15u) == 0 && alike(x, x_stride) &&
+                     alike(h_out, h_out_stride) && alike(y, y_stride);
   NormParams p{};
   p.x = x;
   p.x_stride = x_stride;
@@ -371,7 +382,7 @@ moe_w4a16_status moe_w4a16_block_norm(const uint16_t* x, int64_t x_stride, const
   p.y_stride = y_stride;
   int device = 0;
   MOE_CUDA_TRY(cudaGetDevice(&device));
-  MOE_CUDA_TRY(launch_block_norm(p, res32, vec, device, reinterpret_cast<cudaStream_t>(stream)));
+  MOE_CUDA_TRY(launch_block_norm(p, res32, width, shift, device, reinterpret_cast<cudaStream_t>(stream)));
   return MOE_W4A16_OK;
 }
 
