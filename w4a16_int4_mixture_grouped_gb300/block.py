@@ -29,6 +29,7 @@ LATENT_DIM, LATENT_VALUE_DIM = 576, 512
 MAX_HEAD_DIM, MAX_PAGE_SIZE, MAX_NORM_WIDTH = 256, 4096, 32768
 
 _CACHE_DTYPES = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3}
+_RESIDUALS = {torch.bfloat16: RESIDUAL_BF16, torch.float32: RESIDUAL_F32}
 _BF16 = torch.bfloat16
 _I32 = torch.int32
 
@@ -68,25 +69,32 @@ for _name, _args in _SIGNATURES.items():
     _FN[_name] = _fn
 
 
-def _call(name: str, dev: torch.device, *args) -> None:
-    """The C entry point on dev's current stream (made current for the launch where it is not)."""
-    if torch.cuda.current_device() == dev.index:
-        status = _FN[name](*args, torch.cuda.current_stream(dev).cuda_stream)
+# The current stream's handle without a Stream object around it: a tenth of a decode call's host time otherwise.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
+
+
+def _call(name: str, index: int, *args) -> None:
+    """The C entry point on the current stream of device `index` (made current for the launch where it is not)."""
+    if _current_device() == index:
+        status = _FN[name](*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = _FN[name](*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            status = _FN[name](*args, _raw_stream(index))
     if status != 0:
         raise MoeW4A16Error(status, name)
 
 
-def _need(t: torch.Tensor, name: str, dtype, dim: int, dev: Optional[torch.device] = None) -> torch.Tensor:
-    """A CUDA tensor of that type and rank whose last dimension is dense."""
+def _need(t: torch.Tensor, name: str, dtype, dim: int, index: Optional[int] = None) -> torch.Tensor:
+    """A tensor of that type and rank on CUDA device `index` (None: any) whose last dimension is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if not t.is_cuda:
+    where = t.get_device()
+    if where < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if index is not None and where != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.dim() != dim:
@@ -96,13 +104,13 @@ def _need(t: torch.Tensor, name: str, dtype, dim: int, dev: Optional[torch.devic
     return t
 
 
-def _vector(t: Optional[torch.Tensor], name: str, n: int, dev: torch.device, dtype=_I32) -> Optional[int]:
+def _vector(t: Optional[torch.Tensor], name: str, n: int, index: int, dtype=_I32) -> Optional[int]:
     """Address of a dense 1-D tensor of n elements (None for None)."""
     if t is None:
         return None
-    _need(t, name, dtype, 1, dev)
-    if t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    _need(t, name, dtype, 1, index)
+    if t.size(0) != n:
+        raise ValueError(f"{name} has {t.size(0)} elements, expected {n}")
     return t.data_ptr()
 
 
@@ -113,61 +121,51 @@ def _rows_dense(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _outer_stride(t: torch.Tensor) -> int:
-    """Stride of the first dimension (of a single row: the row's own length)."""
-    return t.stride(0) if t.size(0) > 1 else t[0].numel()
+def _outer_stride(t: torch.Tensor, row: int) -> int:
+    """Stride of the first dimension (of at most one row: the row's own length)."""
+    return t.stride(0) if t.size(0) > 1 else row
 
 
-def _table(tables: torch.Tensor, dev: torch.device) -> Tuple[int, int, int, int]:
+def _table(tables: torch.Tensor, index: int) -> Tuple[int, int, int, int]:
     """(address, row stride, max_pages, num_seqs)."""
-    _need(tables, "tables", _I32, 2, dev)
+    _need(tables, "tables", _I32, 2, index)
     s, m = tables.shape
     return tables.data_ptr(), (tables.stride(0) if s > 1 else m), m, s
 
 
-def _pages(k: torch.Tensor, v: Optional[torch.Tensor], dev: torch.device, k_scale: float, v_scale: float) -> Pages:
-    rank = 4 if v is not None else 3
-    _need(k, "k_pages", None, rank, dev)
-    if k.dtype not in _CACHE_DTYPES:
+def _pages(k: torch.Tensor, v: Optional[torch.Tensor], index: int, k_scale: float, v_scale: float) -> Pages:
+    _need(k, "k_pages", None, 4 if v is not None else 3, index)
+    kind = _CACHE_DTYPES.get(k.dtype)
+    if kind is None:
         raise TypeError(f"pages have dtype {k.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
-    st = k.stride()
-    if v is not None:
-        _need(v, "v_pages", k.dtype, 4, dev)
-        if v.shape != k.shape or v.stride() != st:
-            raise ValueError("k_pages and v_pages must have the same shape and strides")
-    c = Pages()
-    c.k = k.data_ptr()
-    c.v = v.data_ptr() if v is not None else None
-    c.dtype = _CACHE_DTYPES[k.dtype]
-    c.num_pages, c.page_size = k.shape[0], k.shape[1]
-    c.page_stride, c.token_stride = st[0], st[1]
-    c.head_stride = st[2] if v is not None else k.shape[2]
-    c.k_scale, c.v_scale = k_scale, v_scale
-    return c
+    shape, st = k.shape, k.stride()
+    if v is None:
+        return Pages(k.data_ptr(), None, kind, shape[0], shape[1], 0, st[0], st[1], shape[2], k_scale, v_scale)
+    _need(v, "v_pages", k.dtype, 4, index)
+    if v.shape != shape or v.stride() != st:
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    return Pages(k.data_ptr(), v.data_ptr(), kind, shape[0], shape[1], 0, st[0], st[1], st[2], k_scale, v_scale)
 
 
 def _pool(pool: torch.Tensor) -> Pool:
     """pool [planes, num_pages, ...], each page dense."""
     if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
         raise ValueError("pool must be a CUDA tensor")
-    if pool.dim() < 3:
+    shape, st = pool.shape, pool.stride()
+    if len(shape) < 3:
         raise ValueError("pool must be [planes, num_pages, ...]")
-    size = pool.element_size()
     dense = 1
-    for n, s in zip(reversed(pool.shape[2:]), reversed(pool.stride()[2:])):
+    for n, s in zip(reversed(shape[2:]), reversed(st[2:])):
         if n > 1 and s != dense:
             raise ValueError("pool: each page must be dense")
         dense *= n
-    p = Pool()
-    p.base = pool.data_ptr()
-    p.num_planes, p.num_pages = pool.shape[0], pool.shape[1]
-    p.plane_stride, p.page_stride, p.page_bytes = pool.stride(0) * size, pool.stride(1) * size, dense * size
-    return p
+    size = pool.element_size()
+    return Pool(pool.data_ptr(), shape[0], shape[1], st[0] * size, st[1] * size, dense * size)
 
 
-def _ws(ws: torch.Tensor, dev: torch.device) -> Tuple[int, int]:
-    _need(ws, "ws", torch.uint8, 1, dev)
-    return ws.data_ptr(), ws.numel()
+def _ws(ws: torch.Tensor, index: int) -> Tuple[int, int]:
+    _need(ws, "ws", torch.uint8, 1, index)
+    return ws.data_ptr(), ws.size(0)
 
 
 def _alloc_ws(nbytes: int, device) -> torch.Tensor:
@@ -196,18 +194,17 @@ def attention_workspace(batch: int, num_heads: int, num_kv_heads: int, head_dim:
     return _alloc_ws(attention_workspace_size(num_heads, num_kv_heads, head_dim), device)
 
 
-def _attention_out(q, width, out, lse):
-    b, h = q.shape[0], q.shape[1]
+def _attention_out(q, b, h, width, index, out, lse):
     if out is None:
-        out = q.new_empty((b, h, width))
+        out = torch.empty((b, h, width), dtype=_BF16, device=q.device)
     else:
-        _need(out, "out", _BF16, 3, q.device)
+        _need(out, "out", _BF16, 3, index)
         if out.shape != (b, h, width) or not out.is_contiguous():
             raise ValueError(f"out must be contiguous [{b}, {h}, {width}]")
     if lse is None:
         lse = torch.empty((b, h), dtype=torch.float32, device=q.device)
     else:
-        _need(lse, "lse", torch.float32, 2, q.device)
+        _need(lse, "lse", torch.float32, 2, index)
         if lse.shape != (b, h) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{b}, {h}]")
     return out, lse
@@ -223,16 +220,19 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     scale defaults to D ** -0.5; window counts the newest tokens seen (0: all); seq_ids [B] names the row of
     tables and lens of each query (default: row b)."""
     _rows_dense(_need(q, "q", _BF16, 3), "q")
-    dev = q.device
+    index = q.get_device()
     b, h, d = q.shape
-    c = _pages(k_pages, v_pages, dev, k_scale, v_scale)
-    if v_pages is None or k_pages.shape[3] != d:
+    if v_pages is None:
+        raise ValueError("v_pages is missing (a latent cache: latent_attention)")
+    c = _pages(k_pages, v_pages, index, k_scale, v_scale)
+    heads, dim = k_pages.shape[2:]
+    if dim != d:
         raise ValueError(f"pages must hold keys and values of {d} channels")
-    ta, ts, mp, ns = _table(tables, dev)
-    out, lse = _attention_out(q, d, out, lse)
-    wa, wn = _ws(ws, dev)
-    _call("paged_attention", dev, q.data_ptr(), _outer_stride(q) if b else h * d, b, h, k_pages.shape[2], d,
-          ctypes.byref(c), ta, ts, mp, _vector(lens, "lens", ns, dev), _vector(seq_ids, "seq_ids", b, dev), ns,
+    ta, ts, mp, ns = _table(tables, index)
+    out, lse = _attention_out(q, b, h, d, index, out, lse)
+    wa, wn = _ws(ws, index)
+    _call("paged_attention", index, q.data_ptr(), _outer_stride(q, h * d), b, h, heads, d, c, ta, ts, mp,
+          _vector(lens, "lens", ns, index), _vector(seq_ids, "seq_ids", b, index), ns,
           d ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), wa, wn)
     return out, lse
 
@@ -243,16 +243,16 @@ def latent_attention(q: torch.Tensor, pages: torch.Tensor, tables: torch.Tensor,
                      lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The same over a latent cache: q [B, H, 576], pages [P, S, 576] -> (out bf16 [B, H, 512], lse [B, H])."""
     _rows_dense(_need(q, "q", _BF16, 3), "q")
-    dev = q.device
+    index = q.get_device()
     b, h, d = q.shape
-    c = _pages(pages, None, dev, 1.0, 1.0)
-    if d != LATENT_DIM or pages.shape[2] != LATENT_DIM:
+    c = _pages(pages, None, index, 1.0, 1.0)
+    if d != LATENT_DIM or pages.size(2) != LATENT_DIM:
         raise ValueError(f"q and pages must have {LATENT_DIM} channels")
-    ta, ts, mp, ns = _table(tables, dev)
-    out, lse = _attention_out(q, LATENT_VALUE_DIM, out, lse)
-    wa, wn = _ws(ws, dev)
-    _call("latent_attention", dev, q.data_ptr(), _outer_stride(q) if b else h * d, b, h, ctypes.byref(c), ta, ts, mp,
-          _vector(lens, "lens", ns, dev), _vector(seq_ids, "seq_ids", b, dev), ns, scale, window, out.data_ptr(),
+    ta, ts, mp, ns = _table(tables, index)
+    out, lse = _attention_out(q, b, h, LATENT_VALUE_DIM, index, out, lse)
+    wa, wn = _ws(ws, index)
+    _call("latent_attention", index, q.data_ptr(), _outer_stride(q, h * d), b, h, c, ta, ts, mp,
+          _vector(lens, "lens", ns, index), _vector(seq_ids, "seq_ids", b, index), ns, scale, window, out.data_ptr(),
           lse.data_ptr(), wa, wn)
     return out, lse
 
@@ -269,22 +269,22 @@ def cache_append(k: torch.Tensor, k_pages: torch.Tensor, tables: torch.Tensor, s
     if (v is None) != latent:
         raise ValueError("v and v_pages go together")
     _rows_dense(_need(k, "k", _BF16, 2 if latent else 3), "k")
-    dev = k.device
-    c = _pages(k_pages, v_pages, dev, k_scale, v_scale)
+    index = k.get_device()
+    c = _pages(k_pages, v_pages, index, k_scale, v_scale)
     if tuple(k_pages.shape[2:]) != tuple(k.shape[1:]):
         raise ValueError(f"rows are {tuple(k.shape[1:])}, pages hold {tuple(k_pages.shape[2:])}")
     n = k.shape[0]
     heads, dim = (1, k.shape[1]) if latent else k.shape[1:]
     if not latent:
-        _rows_dense(_need(v, "v", _BF16, 3, dev), "v")
+        _rows_dense(_need(v, "v", _BF16, 3, index), "v")
         if v.shape != k.shape:
             raise ValueError("k and v must have the same shape")
-    ta, ts, mp, ns = _table(tables, dev)
-    wa, wn = _ws(ws, dev)
-    _call("cache_append", dev, k.data_ptr(), _outer_stride(k) if n else heads * dim,
-          None if latent else v.data_ptr(), 0 if latent else (_outer_stride(v) if n else heads * dim), n, heads, dim,
-          ctypes.byref(c), ta, ts, mp, ns, _vector(seq_ids, "seq_ids", n, dev),
-          _vector(positions, "positions", n, dev), wa, wn)
+    ta, ts, mp, ns = _table(tables, index)
+    wa, wn = _ws(ws, index)
+    _call("cache_append", index, k.data_ptr(), _outer_stride(k, heads * dim),
+          None if latent else v.data_ptr(), 0 if latent else _outer_stride(v, heads * dim), n, heads, dim,
+          c, ta, ts, mp, ns, _vector(seq_ids, "seq_ids", n, index),
+          _vector(positions, "positions", n, index), wa, wn)
 
 
 def cache_workspace_size(num_pages: int, count: int) -> int:
@@ -307,15 +307,15 @@ def cache_extend(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, s
     """Grows the sequences by counts tokens (default one each), taking free pages; -> positions [n], each
     sequence's old length, -1 where it did not fit."""
     _need(refs, "refs", _I32, 1)
-    dev = refs.device
-    n = seq_ids.numel()
-    ta, ts, mp, ns = _table(tables, dev)
+    index = refs.get_device()
+    n = seq_ids.size(0)
+    ta, ts, mp, ns = _table(tables, index)
     if out is None:
-        out = torch.empty(n, dtype=_I32, device=dev)
-    wa, wn = _ws(ws, dev)
-    _call("cache_extend", dev, refs.data_ptr(), refs.numel(), ta, ts, mp, _vector(lens, "lens", ns, dev), ns,
-          _vector(seq_ids, "seq_ids", n, dev), _vector(counts, "counts", n, dev), n, page_size,
-          _vector(out, "out", n, dev), wa, wn)
+        out = torch.empty(n, dtype=_I32, device=refs.device)
+    wa, wn = _ws(ws, index)
+    _call("cache_extend", index, refs.data_ptr(), refs.size(0), ta, ts, mp, _vector(lens, "lens", ns, index), ns,
+          _vector(seq_ids, "seq_ids", n, index), _vector(counts, "counts", n, index), n, page_size,
+          _vector(out, "out", n, index), wa, wn)
     return out
 
 
@@ -324,34 +324,34 @@ def cache_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, len
     """Makes each (empty) children[i] a copy of parents[i]: full pages shared, a partly filled last page of pool
     [planes, num_pages, ...] copied in every plane."""
     p = _pool(pool)
-    dev = pool.device
-    n = parents.numel()
-    ta, ts, mp, ns = _table(tables, dev)
-    wa, wn = _ws(ws, dev)
-    _call("cache_fork", dev, ctypes.byref(p), _vector(refs, "refs", p.num_pages, dev), ta, ts, mp,
-          _vector(lens, "lens", ns, dev), ns, _vector(parents, "parents", n, dev),
-          _vector(children, "children", n, dev), n, page_size, wa, wn)
+    index = pool.get_device()
+    n = parents.size(0)
+    ta, ts, mp, ns = _table(tables, index)
+    wa, wn = _ws(ws, index)
+    _call("cache_fork", index, p, _vector(refs, "refs", p.num_pages, index), ta, ts, mp,
+          _vector(lens, "lens", ns, index), ns, _vector(parents, "parents", n, index),
+          _vector(children, "children", n, index), n, page_size, wa, wn)
 
 
 def cache_free(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, seq_ids: torch.Tensor, page_size: int,
                ws: torch.Tensor, keep: Optional[torch.Tensor] = None) -> None:
     """Frees the sequences' pages; with keep [n], only those wholly before the newest keep[i] tokens."""
     _need(refs, "refs", _I32, 1)
-    dev = refs.device
-    n = seq_ids.numel()
-    ta, ts, mp, ns = _table(tables, dev)
-    wa, wn = _ws(ws, dev)
-    _call("cache_free", dev, refs.data_ptr(), refs.numel(), ta, ts, mp, _vector(lens, "lens", ns, dev), ns,
-          _vector(seq_ids, "seq_ids", n, dev), _vector(keep, "keep", n, dev), n, page_size, wa, wn)
+    index = refs.get_device()
+    n = seq_ids.size(0)
+    ta, ts, mp, ns = _table(tables, index)
+    wa, wn = _ws(ws, index)
+    _call("cache_free", index, refs.data_ptr(), refs.size(0), ta, ts, mp, _vector(lens, "lens", ns, index), ns,
+          _vector(seq_ids, "seq_ids", n, index), _vector(keep, "keep", n, index), n, page_size, wa, wn)
 
 
 def cache_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor) -> None:
     """pool[:, dst[i]] = pool[:, src[i]]; no destination is a source or another destination."""
     p = _pool(pool)
-    dev = pool.device
-    n = src.numel()
-    wa, wn = _ws(ws, dev)
-    _call("cache_copy", dev, ctypes.byref(p), _vector(src, "src", n, dev), _vector(dst, "dst", n, dev), n, wa, wn)
+    index = pool.get_device()
+    n = src.size(0)
+    wa, wn = _ws(ws, index)
+    _call("cache_copy", index, p, _vector(src, "src", n, index), _vector(dst, "dst", n, index), n, wa, wn)
 
 
 def cache_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, ws: torch.Tensor,
@@ -360,20 +360,20 @@ def cache_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, 
 
     The new counts and tables are new tensors unless refs_out / tables_out (which may be refs / tables) are given."""
     p = _pool(pool)
-    dev = pool.device
-    ra = _vector(refs, "refs", p.num_pages, dev)
-    ta, ts, mp, ns = _table(tables, dev)
+    index = pool.get_device()
+    ra = _vector(refs, "refs", p.num_pages, index)
+    ta, ts, mp, ns = _table(tables, index)
     if refs_out is None:
-        refs_out = torch.empty(p.num_pages, dtype=_I32, device=dev)
+        refs_out = torch.empty(p.num_pages, dtype=_I32, device=refs.device)
     if tables_out is None:
-        tables_out = torch.empty_strided(tables.shape, (ts, 1), dtype=_I32, device=dev)
-    to, tos, _, _ = _table(tables_out, dev)
+        tables_out = torch.empty_strided(tables.shape, (ts, 1), dtype=_I32, device=refs.device)
+    to, tos, _, _ = _table(tables_out, index)
     if tables_out.shape != tables.shape or tos != ts:
         raise ValueError("tables_out must have the shape and strides of tables")
-    page_map = torch.empty(p.num_pages, dtype=_I32, device=dev)
-    num_live = torch.empty(1, dtype=_I32, device=dev)
-    wa, wn = _ws(ws, dev)
-    _call("cache_compact", dev, ctypes.byref(p), ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", p.num_pages, dev),
+    page_map = torch.empty(p.num_pages, dtype=_I32, device=refs.device)
+    num_live = torch.empty(1, dtype=_I32, device=refs.device)
+    wa, wn = _ws(ws, index)
+    _call("cache_compact", index, p, ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", p.num_pages, index),
           to, page_map.data_ptr(), num_live.data_ptr(), wa, wn)
     return refs_out, tables_out, page_map, num_live
 
@@ -394,44 +394,37 @@ def block_norm(x: Optional[torch.Tensor], residual: torch.Tensor, w_post: Option
     changes it), residual bf16 or float32 [T, n]; without w_post x enters as it is, without w_pre y is None.
     gate bf16 [n], or [G, n] with G dividing T (row t takes gate row t // (T // G)). out may be residual."""
     _need(residual, "residual", None, 2)
-    dev = residual.device
-    if residual.dtype is _BF16:
-        kind = RESIDUAL_BF16
-    elif residual.dtype is torch.float32:
-        kind = RESIDUAL_F32
-    else:
+    index, kind = residual.get_device(), _RESIDUALS.get(residual.dtype)
+    if kind is None:
         raise TypeError(f"residual has dtype {residual.dtype}, expected torch.bfloat16 or torch.float32")
-    t, n = residual.shape
-    if x is not None and _need(x, "x", _BF16, 2, dev).shape != residual.shape:
-        raise ValueError("x and residual must have the same shape")
+    shape = residual.shape
+    t, n = shape
+    xa = xs = ga = oa = os_ = ya = ys = None
+    if x is not None:
+        if _need(x, "x", _BF16, 2, index).shape != shape:
+            raise ValueError("x and residual must have the same shape")
+        xa, xs = x.data_ptr(), _outer_stride(x, n)
     gate_rows = 1
     if gate is not None:
-        _need(gate, "gate", _BF16, gate.dim(), dev)
-        if gate.dim() not in (1, 2) or gate.shape[-1] != n or not gate.is_contiguous():
+        if _need(gate, "gate", _BF16, gate.dim(), index).shape[-1] != n or gate.dim() > 2 or not gate.is_contiguous():
             raise ValueError(f"gate must be contiguous [{n}] or [G, {n}]")
-        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
-    same = x is None and residual_scale == 1.0 and out is None       # the residual passes through unchanged
-    if same:
-        out = None
-    elif out is None:
-        out = torch.empty((t, n), dtype=residual.dtype, device=dev)
-    elif _need(out, "out", residual.dtype, 2, dev).shape != residual.shape:
-        raise ValueError("out and residual must have the same shape")
-    if w_pre is None:
-        if y is not None:
-            raise ValueError("y needs w_pre")
-    elif y is None:
-        y = torch.empty((t, n), dtype=_BF16, device=dev)
-    elif _need(y, "y", _BF16, 2, dev).shape != residual.shape:
-        raise ValueError("y and residual must have the same shape")
-
-    def stride(a):
-        return 0 if a is None else (a.stride(0) if t > 1 else n)
-
-    def ptr(a):
-        return None if a is None else a.data_ptr()
-
-    _call("block_norm", dev, ptr(x), stride(x), residual.data_ptr(), stride(residual), kind, ptr(gate), gate_rows,
-          _vector(w_post, "w_post", n, dev, _BF16), _vector(w_pre, "w_pre", n, dev, _BF16), t, n, eps, residual_scale,
-          block_scale, ptr(out), stride(out), ptr(y), stride(y))
-    return (residual if same else out), y
+        ga, gate_rows = gate.data_ptr(), gate.size(0) if gate.dim() == 2 else 1
+    h = residual
+    if x is not None or residual_scale != 1.0 or out is not None:    # else the residual passes through unchanged
+        if out is None:
+            out = torch.empty(shape, dtype=residual.dtype, device=residual.device)
+        elif _need(out, "out", residual.dtype, 2, index).shape != shape:
+            raise ValueError("out and residual must have the same shape")
+        h, oa, os_ = out, out.data_ptr(), _outer_stride(out, n)
+    if w_pre is not None:
+        if y is None:
+            y = torch.empty(shape, dtype=_BF16, device=residual.device)
+        elif _need(y, "y", _BF16, 2, index).shape != shape:
+            raise ValueError("y and residual must have the same shape")
+        ya, ys = y.data_ptr(), _outer_stride(y, n)
+    elif y is not None:
+        raise ValueError("y needs w_pre")
+    _call("block_norm", index, xa, xs or 0, residual.data_ptr(), _outer_stride(residual, n), kind, ga, gate_rows,
+          _vector(w_post, "w_post", n, index, _BF16), _vector(w_pre, "w_pre", n, index, _BF16), t, n, eps,
+          residual_scale, block_scale, oa, os_ or 0, ya, ys or 0)
+    return h, y
