@@ -38,6 +38,7 @@ struct Cfg {
   static constexpr int kChunks = kRowBytes / 16;
   // tokens of a warp's stage: 8 KB of keys and values (16 KB for 256 BF16 channels)
   static constexpr int kTok = DP * kElem <= 128 ? 32 : 16;
+  static constexpr uint32_t kAll = kTok == 32 ? 0xffffffffu : (1u << (kTok & 31)) - 1u;   // all of them seen
   static constexpr int kStageBytes = 2 * kTok * kRowBytes;
   static constexpr int kStages = kStageBytes <= 4096 ? 6 : 3;
   static constexpr int kTile = kWarps * kTok;
@@ -105,6 +106,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <int DP>
 constexpr int part_floats() { return 2 * kRows + kRows * DP; }
 
+// 16 bytes that are there (cp_async16's zero-filling form costs more instructions).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int DP, bool E4M3, bool HALF>
 __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p, float* parts, int* counters) {
   using C = Cfg<DP, E4M3>;
@@ -118,17 +124,26 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
   const int chunks = (p.group + kRows - 1) / kRows;
-  const int rows = p.kv_heads * chunks;          // work rows of a sequence
+  // The work rows of a sequence (cache heads x blocks of 16 query heads): `lanes` of them go side by side, CTA
+  // lane + lanes * i taking the i-th share of the tokens of row `lane`; the others follow each other on the line.
+  const int lanes = p.lanes, lane_row = blockIdx.x % lanes, rows = p.kv_heads * chunks / lanes;
 
   zero_empty<kThreads>(p, p.dim);
-  if (!find_share<kThreads>(p, rows, C::kTile, 1, &share)) return;
+  if (!find_share<kThreads>(p, blockIdx.x / lanes, gridDim.x / lanes, rows, C::kTile, 1, &share)) return;
   const int64_t total = share.total;
   const int ctas = share.ctas;
+  // a stage's tokens never straddle a page, and every chunk of their rows holds channels
+  const bool one_run = p.t.page_size % C::kTok == 0 && p.dim == DP;
+  // scores enter the exponentials as |scale| s, the queries negated where the scale is negative
+  // (zeroed where it is zero, so that the factor itself is never zero: an unseen token's -infinity stays one)
+  const uint32_t negate = p.score_scale < 0.f ? 0x80008000u : 0u;
+  const float abs_scale = p.score_scale == 0.f ? 1.f : fmaxf(fabsf(p.score_scale), 1.2e-38f);
+  const bool flat = p.score_scale == 0.f;
   PieceWalk walk;
   walk.start(p, &share);
   Piece pc;
   while (walk.next(p, rows, C::kTile, pc)) {
-    const int kvh = pc.r / chunks, hc = pc.r % chunks;
+    const int r = pc.r * lanes + lane_row, kvh = r / chunks, hc = r % chunks;
     const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
     const int64_t head_off = int64_t(kvh) * p.head_stride;
     const int32_t* table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
@@ -154,19 +169,38 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         int64_t off = -1;
         if (entry >= 0)
           off = int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride + head_off;
-        seen = __ballot_sync(0xffffffffu, off >= 0);
+        seen = __ballot_sync(0xffffffffu, off >= 0) & C::kAll;
         if (seen != 0) {
           const uint32_t kd = ring + slot * C::kStageBytes, vd = kd + C::kTok * C::kRowBytes;
           const uint8_t* kb = static_cast<const uint8_t*>(p.k);
           const uint8_t* vb = static_cast<const uint8_t*>(p.v);
+          constexpr int kCopies = C::kTok * C::kChunks / 32;
+          const auto key_at = [](int tr, int c) { return 16 * (E4M3 ? swz_key8<C::kChunks>(tr, c) : swz<C::kChunks>(tr, c)); };
+          if (seen == C::kAll && one_run) {
+            // the stage's tokens lie behind each other in one page: lane's row and chunk advance by whole rows
+            const int64_t o = (__shfl_sync(0xffffffffu, off, 0) + int64_t(lane / C::kChunks) * p.token_stride) * C::kElem +
+                              lane % C::kChunks * 16;
+            const uint8_t* ks = kb + o;
+            const uint8_t* vs = vb + o;
+            const int64_t step = int64_t(32 / C::kChunks) * p.token_stride * C::kElem;
 #pragma unroll
-          for (int j = 0; j < C::kTok * C::kChunks / 32; ++j) {
-            const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
-            const int64_t o = __shfl_sync(0xffffffffu, off, tr);
-            const bool ok = o >= 0 && c * 16 < p.dim * C::kElem;
-            const int64_t at = ok ? o * C::kElem + c * 16 : 0;
-            cp_async16(kd + 16 * (E4M3 ? swz_key8<C::kChunks>(tr, c) : swz<C::kChunks>(tr, c)), kb + at, ok ? 16 : 0);
-            cp_async16(vd + 16 * swz<C::kChunks>(tr, c), vb + at, ok ? 16 : 0);
+            for (int j = 0; j < kCopies; ++j) {
+              const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
+              copy16(kd + key_at(tr, c), ks);
+              copy16(vd + 16 * swz<C::kChunks>(tr, c), vs);
+              ks += step;
+              vs += step;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j) {
+              const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
+              const int64_t o = __shfl_sync(0xffffffffu, off, tr);
+              const bool ok = o >= 0 && c * 16 < p.dim * C::kElem;
+              const int64_t at = ok ? o * C::kElem + c * 16 : 0;
+              cp_async16(kd + key_at(tr, c), kb + at, ok ? 16 : 0);
+              cp_async16(vd + 16 * swz<C::kChunks>(tr, c), vb + at, ok ? 16 : 0);
+            }
           }
         }
         entry = entry_of(i + 1);
@@ -185,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     for (int hh = 0; hh < HR; ++hh) {
       const int row = g + 8 * hh;
       const uint16_t* src = p.q + int64_t(b) * p.q_stride + int64_t(head0 + row) * p.dim;
-      qscale[hh] = p.score_scale;
+      qscale[hh] = abs_scale;
       if (!E4M3) {
         // (row, k 2t..2t+1) and (row, k 2t+8..2t+9) of each 16-channel step
 #pragma unroll
@@ -194,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           for (int half = 0; half < 2; ++half) {
             const int d = ks * 16 + half * 8 + 2 * t;
             qa[ks][HALF ? half : 2 * half + hh] =
-                row < heads && d < p.dim ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
+                row < heads && d < p.dim && !flat ? *reinterpret_cast<const uint32_t*>(src + d) ^ negate : 0u;
           }
       } else {
         // the channels in the order in which a lane reads 8-bit keys: step s of a 64-channel block
@@ -204,7 +238,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const int d = (ks >> 2) * 64 + 16 * t + 4 * (ks & 3);
-          raw[ks] = row < heads && d < p.dim ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0u, 0u);
+          raw[ks] = row < heads && d < p.dim && !flat ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0u, 0u);
+          raw[ks].x ^= negate;
+          raw[ks].y ^= negate;
           const uint32_t w[2] = {raw[ks].x, raw[ks].y};
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -219,8 +255,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         e = max(e, -126);
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
         const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
-        qscale[hh] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23) *
-                     __uint_as_float(static_cast<uint32_t>(127 + (e - e / 2)) << 23);
+        qscale[hh] = fmaxf(abs_scale * __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23) *
+                               __uint_as_float(static_cast<uint32_t>(127 + (e - e / 2)) << 23),
+                           1.2e-38f);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t w[2] = {raw[ks].x, raw[ks].y};
@@ -303,24 +340,24 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
               }
             }
         }
-        // ---- running softmax (in units of log 2)
+        // ---- running softmax, exponents in units of log 2: scale s - m
+        if (seen != C::kAll) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < NR; ++k)
+              if (!(seen >> (j * 8 + 2 * t + (k & 1)) & 1u)) s[j][k] = -INFINITY;
+        }
         bool moved = false;
         float keep[HR];
 #pragma unroll
         for (int hh = 0; hh < HR; ++hh) {
           float top = top_of[hh];
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float v = s[j][2 * hh + k] * qscale[hh];
-              if (!(seen >> (j * 8 + 2 * t + k) & 1u)) v = -INFINITY;
-              s[j][2 * hh + k] = v;
-              top = fmaxf(top, v);
-            }
+          for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[j][2 * hh], s[j][2 * hh + 1]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float base = top == -INFINITY ? 0.f : top - kLift;
+          const float base = top == -INFINITY ? 0.f : top * qscale[hh] - kLift;
           keep[hh] = exp2_fast(m[hh] - base);
           moved |= top != top_of[hh];
           top_of[hh] = top;
@@ -330,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float e = exp2_fast(s[j][2 * hh + k] - base);
+              const float e = exp2_fast(fmaf(s[j][2 * hh + k], qscale[hh], -base));
               s[j][2 * hh + k] = e;
               sum += e;
             }
@@ -413,7 +450,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       }
     }
     __syncthreads();
-    const int c0 = cta_of(total, ctas, pc.row0), c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1);
+    // first and last CTA of the row, as blocks of the grid
+    const int c0 = cta_of(total, ctas, pc.row0) * lanes + lane_row;
+    const int c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1) * lanes + lane_row;
     const bool whole = c0 == c1;
     float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * part_floats<DP>();
     const int vecs = p.dim / 4;
@@ -455,16 +494,16 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        const bool last = atomicAdd(counters + c0, 1) == c1 - c0;
+        const bool last = atomicAdd(counters + c0, 1) == (c1 - c0) / lanes;
         if (last) counters[c0] = 0;
         last_flag = last;
       }
       __syncthreads();
       if (last_flag) {
         __threadfence();
-        const int np = c1 - c0 + 1;
+        const int np = (c1 - c0) / lanes + 1;
         // part of CTA c0 + i: its last row for the first one, its first row for the others
-        auto part_at = [&](int i) { return parts + (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats<DP>(); };
+        auto part_at = [&](int i) { return parts + (int64_t(c0 + i * lanes) * 2 + (i == 0 ? 1 : 0)) * part_floats<DP>(); };
         float* weight = buf;                              // [np][kRows], then the rows' totals
         __shared__ float row_top[kRows], row_sum[kRows];
         for (int row = warp; row < heads; row += kWarps) {
@@ -524,7 +563,13 @@ cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   }
   int grid = device_info(device).sm_count * (2 * C::kBufBytes <= 220 * 1024 ? 2 : 1);
   if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
-  attention_kernel<DP, E4M3, HALF><<<grid, kThreads, C::kBufBytes, stream>>>(p, p.parts, p.counters);
+  // All rows of a sequence side by side where that idles at most one CTA in twenty: the heads of a token lie next to
+  // each other in the usual cache, and read at about the same time they share DRAM pages (a row of one head is
+  // 128 bytes in an E4M3 cache of 128 channels).
+  AttnParams q = p;
+  const int rows = p.kv_heads * ((p.group + kRows - 1) / kRows);
+  q.lanes = rows <= grid && grid / rows * rows * 20 >= grid * 19 ? rows : 1;
+  attention_kernel<DP, E4M3, HALF><<<grid / q.lanes * q.lanes, kThreads, C::kBufBytes, stream>>>(q, p.parts, p.counters);
   note_launch();
   return cudaGetLastError();
 }

@@ -37,6 +37,7 @@ struct AttnParams {
   float score_scale;                   // scale * k_scale * log2(e): scores in units of log 2
   float v_scale;
   int window;
+  int lanes;                           // grouped form: work rows of a sequence that go side by side
   uint16_t* out;
   float* lse;
   int* err;

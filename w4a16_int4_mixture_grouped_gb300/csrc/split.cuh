@@ -28,10 +28,11 @@ struct Share {
   int sums[32];
 };
 
-// Fills *sh for this CTA (every thread calls it; shares of at least min_tiles tiles where there are
-// fewer than that for every CTA). False: no work for it.
+// Fills *sh for CTA `cta` of `grid` (every thread calls it; shares of at least min_tiles tiles where there
+// are fewer than that for every CTA). False: no work for it.
 template <int THREADS>
-__device__ __forceinline__ bool find_share(const AttnParams& p, int rows, int tile, int min_tiles, Share* sh) {
+__device__ __forceinline__ bool find_share(const AttnParams& p, int cta, int grid, int rows, int tile, int min_tiles,
+                                           Share* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t line = 0;                                   // tiles of the sequences before the chunk
   for (int pass = 0; pass < 2; ++pass) {
@@ -64,12 +65,12 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int rows, int ti
       if (pass == 0 && b0 + THREADS >= p.batch) {
         if (threadIdx.x == 0) {
           int64_t ctas = line / min_tiles;
-          ctas = ctas < 1 ? 1 : ctas > gridDim.x ? gridDim.x : ctas;
-          const bool work = line > 0 && blockIdx.x < ctas;
+          ctas = ctas < 1 ? 1 : ctas > grid ? grid : ctas;
+          const bool work = line > 0 && cta < ctas;
           sh->total = line;
           sh->ctas = static_cast<int>(ctas);
-          sh->x = work ? cta_begin(line, static_cast<int>(ctas), blockIdx.x) : 0;
-          sh->x_end = work ? cta_begin(line, static_cast<int>(ctas), blockIdx.x + 1) : 0;
+          sh->x = work ? cta_begin(line, static_cast<int>(ctas), cta) : 0;
+          sh->x_end = work ? cta_begin(line, static_cast<int>(ctas), cta + 1) : 0;
         }
         __syncthreads();
         if (sh->x >= sh->x_end) return false;
