@@ -8,9 +8,9 @@
 //   S^T [keys x heads]  = K [keys x 576] . Q^T       A = the tile, K-major
 //   O^T [512 x heads]  += V^T [512 x keys] . P^T      A = the same tile, M-major (no transposed copy)
 //
-//   * Tiles of 64 tokens, two in shared memory (2 x 72 KB) beside the 64 queries (72 KB): each is
-//     filled by a team of its own with cp.async (rows gathered by page; unseen slots zero-filled), so a tile
-//     is always in flight.
+//   * Tiles of 64 tokens, two in shared memory (2 x 72 KB) beside the 64 queries (72 KB), filled with cp.async
+//     (rows gathered by page; unseen slots zero-filled); the tile two ahead is prefetched into L2, so that HBM does
+//     not wait for a free buffer.
 //   * S^T (M = 64: 16 lanes of each TMEM quarter) is double-buffered, O^T takes 256 columns (four 128-channel
 //     tiles). The next tile's scores run beside this tile's softmax and values. A thread issues an MMA every 60
 //     to 75 cycles whatever its size, 52 of them a tile, so each product has two issuing warps: S^T in two
@@ -39,7 +39,7 @@ constexpr int kChunkBytes64 = 64 * 128;       // 64 rows of one chunk, 128-byte 
 constexpr int kTileBytes = kChunks * kChunkBytes64;      // 73,728
 constexpr int kValueTiles = kLatentValue / 128;          // M tiles of O^T: 4
 
-// warps: 0-7 softmax / rescale / epilogue, 8-11 tile loaders (two teams), 12-13 queries and S^T, 14-15 O^T
+// warps: 0-7 softmax / rescale / epilogue, 8-11 tile loaders, 12-13 queries and S^T, 14-15 O^T
 constexpr int kThreads = 512;
 constexpr int kGroups = 3;                    // chunk groups of a tile that the S issuer waits for
 
@@ -55,14 +55,12 @@ enum {
   kBarDone = kBarProb + 1,                    // [2] a tile's O^T product done: tile, P free, O^T stable
   kBarQ = kBarDone + 2,                       // queries of a piece loaded
   kBarQFree = kBarQ + 1,
-  kBarMax = kBarQFree + 1,                    // [2] the two column groups' exchanges
-  kBarDrain = kBarMax + 2,
+  kBarDrain = kBarQFree + 1,
   kNumBars = kBarDrain + 2
 };
 constexpr int kMiscOff = kBarOff + kNumBars * 8;         // TMEM address, abort flag
-constexpr int kMaskOff = kMiscOff + 8;                   // [2] 64-bit masks of seen tokens
-constexpr int kVoteOff = kMaskOff + 16;                  // int [2][2][4] votes by tile parity, group and quarter
-constexpr int kMaxOff = kVoteOff + 64;                   // float [4][64] maxima or sums by key quarter
+constexpr int kMaskOff = kMiscOff + 8;                   // [2][4] masks of 16 tokens seen
+constexpr int kMaxOff = kMaskOff + 32;                   // float [4][64] maxima or sums by key quarter
 constexpr int kKeepOff = kMaxOff + 4 * kHeads * 4;       // float [64] factors of a rescale
 constexpr int kBaseOff = kKeepOff + kHeads * 4;          // float [64] bases at a row's end
 constexpr int kShareOff = (kBaseOff + kHeads * 4 + 15) / 16 * 16;
@@ -177,12 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(kBarFull + i), 64);
+    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(kBarFull + i), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarScore + i), 2);
       mbar_init(bar(kBarScoreFree + i), 8);
       mbar_init(bar(kBarDone + i), 2);
-      mbar_init(bar(kBarMax + i), 4);
       mbar_init(bar(kBarDrain + i), 2);
     }
     mbar_init(bar(kBarProb), 8);
@@ -212,22 +209,29 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
     const int q = warp & 3, group = warp >> 2;           // TMEM lane quarter, heads 32 group ..
     const int r0 = lane >> 2, cc = lane & 3;             // this thread's keys 16 q + r0, + 8; heads 8 j + 2 cc, + 1
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    volatile int* votes = reinterpret_cast<volatile int*>(smem + kVoteOff);
     float* maxima = reinterpret_cast<float*>(smem + kMaxOff) + 32 * group;      // [4][64]
     float* keeps = reinterpret_cast<float*>(smem + kKeepOff) + 32 * group;
     float* bases = reinterpret_cast<float*>(smem + kBaseOff) + 32 * group;
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(smem + kMaskOff);
-    uint32_t it = 0, exchanges = 0;                      // tiles, exchanges of this CTA so far
-    bool ok = true;
-    // one bounded exchange between the four warps of a column group
-    auto exchange = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMax + group));
-      const bool r = wait(kBarMax + group, exchanges & 1u);
-      ++exchanges;
-      return r;
+    uint32_t it = 0;                                     // tiles of this CTA so far
+    bool dead = false;                                   // a wait gave up
+    auto wait_or_die = [&](int i, uint32_t parity) {
+      if (!dead) dead = !wait(i, parity);
     };
-    while (ok && walk.next(p, rows, kTile, pc)) {
+    // The four warps of a column group meet at a hardware barrier, which also ORs their votes. After a wait that gave
+    // up they go on (with nothing to show for it) rather than leave, so that all of them reach every barrier.
+    auto any_of_group = [&](bool vote) {
+      int r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
+          "selp.b32 %0, 1, 0, q;\n\t}"
+          : "=r"(r)
+          : "r"(static_cast<int>(vote)), "r"(1 + group)
+          : "memory");
+      return r != 0;
+    };
+    auto group_sync = [&]() { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); };
+    while (walk.next(p, rows, kTile, pc)) {
       const int head0 = pc.r * kHeads, heads = min(kHeads, p.heads - head0);
       const int mine = min(32, heads - 32 * group);      // heads of this column group (may be <= 0)
       float at[8], l[8];                                 // bases and sums of heads 8 j + 2 cc + e at 2 j + e
@@ -241,9 +245,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
         const int buf = it & 1;
         const uint32_t par = (it >> 1) & 1u;
         uint32_t s[16];
-        if (!(ok = wait(kBarScore + buf, par) && wait(kBarFull + buf * kGroups, par))) break;
+        wait_or_die(kBarFull + buf * kGroups, par);
+        wait_or_die(kBarScore + buf, par);
         tc_fence_after();
-        const uint32_t seen = masks[buf * 2 + (q >> 1)] >> (16 * (q & 1)) & 0xffffu;
+        const uint32_t seen = masks[buf * 4 + q];             // 16 bits
         {
           uint32_t s2[16];
           tmem_ld_frag(tmem + kScoreCol + buf * 128 + 32 * group + lanes, s, s2);
@@ -271,12 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
             over |= v > at[(k >> 2) * 2 + (k & 1)] + 8.f;   // at = -inf at first: any seen score
           }
         }
-        over = __any_sync(0xffffffffu, over);
-        if (lane == 0) votes[(buf * 2 + group) * 4 + q] = over;
-        if (!(ok = exchange())) break;
-        over = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) over |= votes[(buf * 2 + group) * 4 + k] != 0;
+        over = any_of_group(over);
         if (over) {
           // new bases: the maximum over the tile's keys where it passes the old one
           float best[8];
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
             for (int o = 4; o < 32; o <<= 1) best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], o));
             if (r0 == 0) maxima[q * kHeads + (h >> 1) * 8 + 2 * cc + (h & 1)] = best[h];
           }
-          if (!(ok = exchange())) break;
+          group_sync();
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
             const int head = (h >> 1) * 8 + 2 * cc + (h & 1);
@@ -299,35 +299,45 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
             l[h] *= keep;
             if (q == 0 && r0 == 0) keeps[head] = keep;
           }
-          if (!(ok = exchange())) break;
-        }
-        // the previous tile's product is done: O^T is stable, P and the tile after it are free
-        if (it != 0 && !(ok = wait(kBarDone + (buf ^ 1), ((it - 1) >> 1) & 1u))) break;
-        if (over && i > 0 && mine > 0) {
-          tc_fence_after();
+          group_sync();
+          if (i > 0) {
+            // O^T is stable once the previous tile's product is done
+            wait_or_die(kBarDone + (buf ^ 1), ((it - 1) >> 1) & 1u);
+            tc_fence_after();
+            if (mine > 0) {
 #pragma unroll 1
-          for (int mt = 0; mt < kValueTiles; ++mt) {
-            uint32_t o[32];
-            const uint32_t acc = tmem + kAccCol + mt * 64 + 32 * group + lanes;
-            tmem_ld32(acc, o);
+              for (int mt = 0; mt < kValueTiles; ++mt) {
+                uint32_t o[32];
+                const uint32_t acc = tmem + kAccCol + mt * 64 + 32 * group + lanes;
+                tmem_ld32(acc, o);
 #pragma unroll
-            for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * keeps[h]);
-            tmem_st32(acc, o);
+                for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * keeps[h]);
+                tmem_st32(acc, o);
+              }
+            }
           }
         }
+        uint32_t packed[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float b0 = at[2 * j] == -INFINITY ? 0.f : at[2 * j], b1 = at[2 * j + 1] == -INFINITY ? 0.f : at[2 * j + 1];
+          const float e0 = exp2_fast(__uint_as_float(s[4 * j]) - b0), e1 = exp2_fast(__uint_as_float(s[4 * j + 1]) - b1);
+          const float e2 = exp2_fast(__uint_as_float(s[4 * j + 2]) - b0),
+                      e3 = exp2_fast(__uint_as_float(s[4 * j + 3]) - b1);
+          l[2 * j] += e0 + e2;
+          l[2 * j + 1] += e1 + e3;
+          packed[2 * j] = pack_bf16x2_rn(e0, e1);
+          packed[2 * j + 1] = pack_bf16x2_rn(e2, e3);
+        }
+        // the previous tile's product is done: P is free
+        if (it != 0) wait_or_die(kBarDone + (buf ^ 1), ((it - 1) >> 1) & 1u);
         {
           uint8_t* row = smem + kPOff + (16 * q + r0) * 128 + cc * 4;    // rows r0 and r0 + 8: the same swizzle
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float b0 = at[2 * j] == -INFINITY ? 0.f : at[2 * j], b1 = at[2 * j + 1] == -INFINITY ? 0.f : at[2 * j + 1];
-            const float e0 = exp2_fast(__uint_as_float(s[4 * j]) - b0), e1 = exp2_fast(__uint_as_float(s[4 * j + 1]) - b1);
-            const float e2 = exp2_fast(__uint_as_float(s[4 * j + 2]) - b0),
-                        e3 = exp2_fast(__uint_as_float(s[4 * j + 3]) - b1);
-            l[2 * j] += e0 + e2;
-            l[2 * j + 1] += e1 + e3;
             const int chunk = ((group * 4 + j) ^ r0) << 4;
-            *reinterpret_cast<uint32_t*>(row + chunk) = pack_bf16x2_rn(e0, e1);
-            *reinterpret_cast<uint32_t*>(row + 8 * 128 + chunk) = pack_bf16x2_rn(e2, e3);
+            *reinterpret_cast<uint32_t*>(row + chunk) = packed[2 * j];
+            *reinterpret_cast<uint32_t*>(row + 8 * 128 + chunk) = packed[2 * j + 1];
           }
           fence_proxy_async_smem();
         }
@@ -335,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarProb));
       }
-      if (!ok) break;
 
       // ---- epilogue: the sums over keys, then this quarter's channels of O^T
 #pragma unroll
@@ -348,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
           if (q == 0) bases[head] = at[h];
         }
       }
-      if (!(ok = exchange())) break;
+      group_sync();
       const float top = bases[lane];                     // lane h: head 32 group + h
       const float sum = maxima[lane] + maxima[kHeads + lane] + maxima[2 * kHeads + lane] + maxima[3 * kHeads + lane];
-      if (!(ok = wait(kBarDone + ((it - 1) & 1), ((it - 1) >> 1) & 1u))) break;
+      wait_or_die(kBarDone + ((it - 1) & 1), ((it - 1) >> 1) & 1u);
       tc_fence_after();
       const int c0 = cta_of(total, ctas, pc.row0), c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1);
       const int64_t out0 = (int64_t(pc.b) * p.heads + head0 + 32 * group);
@@ -400,50 +409,66 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------- tile loaders
-    // Team 0 (warps 8, 9) fills buffer 0 with the even tiles, team 1 buffer 1 with the odd ones. A warp owns
-    // 32 of the tile's tokens: lane = token for the page look-up; copies of 8 lanes a row, 4 rows at a time.
-    const int team = (warp - 8) >> 1, half = (warp - 8) & 1;
+    // A warp owns 16 of a tile's tokens: lane & 15 = token for the page look-up; copies of 8 lanes a row, 4 rows at
+    // a time.
+    const int quarter = warp - 8;
     uint32_t it = 0;
     bool ok = true;
     const uint8_t* src = static_cast<const uint8_t*>(p.k);
     volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + kMaskOff);
+    uint32_t to[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = k * 4 + (lane >> 3);
+      to[k] = base + kKOff + (quarter * 16 + r) * 128 + (((lane & 7) ^ (r & 7)) << 4);
+    }
     while (ok && walk.next(p, rows, kTile, pc)) {
       const int32_t* table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
       const int n = pc.tile1 - pc.tile0;
+      const int tok0 = (pc.lo / kTile + pc.tile0) * kTile + 16 * quarter + (lane & 15);
       auto entry_of = [&](int i) -> int {
-        const int tok = (pc.lo / kTile + pc.tile0 + i) * kTile + 32 * half + lane;
+        const int tok = tok0 + i * kTile;
         if (i >= n || tok < pc.lo || tok >= pc.hi) return -1;
         return table[tok / p.t.page_size];
       };
-      int i = static_cast<int>((it ^ team) & 1u);        // first tile of this team in the piece
-      int entry = entry_of(i);
-      for (; i < n; i += 2) {
-        const uint32_t g = it + i;                       // the tile's number in the CTA
-        const int tok = (pc.lo / kTile + pc.tile0 + i) * kTile + 32 * half + lane;
+      // byte offset of this lane's token in tile i, -1 where it is not seen
+      auto offset_of = [&](int entry, int i) -> int64_t {
+        if (entry < 0) return -1;
         if (entry >= p.t.num_pages) {
           set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
-          entry = -1;
+          return -1;
         }
-        int64_t off = -1;
-        if (entry >= 0) off = (int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride) * 2;
-        const uint32_t seen = __ballot_sync(0xffffffffu, off >= 0);
-        if (g >= 2 && !(ok = wait(kBarDone + team, ((g >> 1) - 1) & 1u))) break;
-        if (lane == 0) masks[team * 2 + half] = seen;
-        const uint8_t* from[8];
-        uint32_t to[8];
+        return (int64_t(entry) * p.page_stride + int64_t((tok0 + i * kTile) % p.t.page_size) * p.token_stride) * 2;
+      };
+      // a tile two ahead on its way to L2: one request where its rows lie behind each other, else one a row (60
+      // cycles each, so behind the arrivals)
+      auto prefetch = [&](int64_t off) {
+        const int64_t first = __shfl_sync(0xffffffffu, off, 0);
+        if (__all_sync(0xffffffffu, first >= 0 && off == first + (lane & 15) * (kLatentDim * 2))) {
+          if (lane == 0) prefetch_l2(src + first, 16 * kLatentDim * 2);
+        } else if (off >= 0 && lane < 16) {
+          prefetch_l2(src + off, kLatentDim * 2);
+        }
+      };
+      int64_t off = offset_of(entry_of(0), 0), off1 = offset_of(entry_of(1), 1);
+      for (int i = 0; i < n; ++i, ++it) {
+        const int buf = it & 1;
+        const uint32_t seen = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
+        const uint8_t* from[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           const int64_t o = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
           from[k] = src + (o >= 0 ? o + (lane & 7) * 16 : 0);
-          const int r = k * 4 + (lane >> 3);
-          to[k] = base + kKOff + team * kTileBytes + half * 4096 + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
         }
-        if (seen == 0xffffffffu) {
+        if (it >= 2 && !(ok = wait(kBarDone + buf, ((it >> 1) - 1) & 1u))) break;
+        if (lane == 0) masks[buf * 4 + quarter] = seen;
+        const uint32_t shift = buf * kTileBytes;
+        if (seen == 0xffffu) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to[k] + c * kChunkBytes64),
+            for (int k = 0; k < 4; ++k)
+              asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to[k] + shift + c * kChunkBytes64),
                            "l"(from[k] + c * 128)
                            : "memory");
             if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
@@ -452,31 +477,30 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
 #pragma unroll 1
           for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
               const bool have = seen >> (k * 4 + (lane >> 3)) & 1u;
-              cp_async16(to[k] + c * kChunkBytes64, have ? from[k] + c * 128 : src, have ? 16 : 0);
+              cp_async16(to[k] + shift + c * kChunkBytes64, have ? from[k] + c * 128 : src, have ? 16 : 0);
             }
             if (c % (kChunks / kGroups) == kChunks / kGroups - 1) cp_async_commit();
           }
         }
-        entry = entry_of(i + 2);
+        const int entry = entry_of(i + 2);
+        auto landed = [&](int grp) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarFull + buf * kGroups + grp));
+        };
         static_assert(kGroups == 3, "waits below");
         cp_async_wait<2>();
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kBarFull + team * kGroups));
+        landed(0);
         cp_async_wait<1>();
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kBarFull + team * kGroups + 1));
+        landed(1);
         cp_async_wait<0>();
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kBarFull + team * kGroups + 2));
-        // this team's next tile on its way to L2 while this one is worked on (an instruction a row: slow to issue,
-        // so behind the arrivals)
-        if (entry >= 0 && entry < p.t.num_pages)
-          prefetch_l2(src + (int64_t(entry) * p.page_stride + int64_t((tok + 2 * kTile) % p.t.page_size) * p.token_stride) * 2,
-                      kLatentDim * 2);
+        landed(2);
+        off = off1;
+        off1 = offset_of(entry, i + 2);
+        prefetch(off1);
       }
-      it += n;
     }
     cp_async_wait<0>();
   } else if (warp < 14) {
