@@ -610,17 +610,20 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kLaneVecs = kLatentValue / 4 / 32;          // float4 of a lane: 4
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnParams p, const Record* records, int ctas) {
-  __shared__ int list[kAttnMaxCtas];
+  __shared__ int list[kLatentMaxCtas];
   __shared__ float4 acc_s[kJoinWarps][kLatentValue / 4];
   __shared__ int count_s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
-    int count = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const bool split = c0 + lane < ctas && __ldcg(&records[c0 + lane].np) > 1;
-      const uint32_t m = __ballot_sync(0xffffffffu, split);
-      if (split) list[count + __popc(m & ((1u << lane) - 1u))] = c0 + lane;
+    constexpr int kLoads = (kLatentMaxCtas + 31) / 32;     // all in flight together
+    int np[kLoads], count = 0;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) np[k] = 32 * k + lane < ctas ? __ldcg(&records[32 * k + lane].np) : 0;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const uint32_t m = __ballot_sync(0xffffffffu, np[k] > 1);
+      if (np[k] > 1) list[count + __popc(m & ((1u << lane) - 1u))] = 32 * k + lane;
       count += __popc(m);
     }
     if (lane == 0) count_s = count;
@@ -726,7 +729,7 @@ cudaError_t launch_latent_attention(const AttnParams& p0, int device, cudaStream
   if (e != cudaSuccess) return e;
   // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid * 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * 8));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
