@@ -1,4 +1,5 @@
-"""MoE FFN forward built from the C-ABI calls (sequencing and buffers only).
+"""MoE FFN forward, and a decoder layer's decode step around it, built from the C-ABI calls (sequencing and buffers
+only).
 
 The hot path of one MoE layer: routing layout -> gate_up GEMM with fused
 SwiGLU -> down GEMM with fused weighted top-k combine. Every step is a call
@@ -8,6 +9,11 @@ orders the calls on the current stream.
 Indexed layout: the gate_up GEMM writes SwiGLU(h) in sorted_ids slot order
 (FLAG_OUT_SORTED), so the down GEMM reads its rows consecutively
 (FLAG_A_SORTED) and combines them back per token.
+
+DecoderLayer is the decode step of one layer: attention over a PagedCache, the
+MoE FFN, and the norms between them and the residual stream. Its dense
+projections (queries, keys and values, output, router) are plain library
+products.
 """
 
 from __future__ import annotations
@@ -17,8 +23,9 @@ from typing import Optional
 import torch
 
 from . import (FLAG_A_SORTED, FLAG_COMBINE, FLAG_OUT_SORTED, FLAG_SPLIT, FLAG_SWIGLU, KERNEL_SPLIT, LAYOUT_CONTIGUOUS,
-               LAYOUT_INDEXED, MODE_GATE_UP, MODE_PLAIN, PreparedWeight, align, align_size, contiguous,
-               contiguous_layout, gather_rows, gather_sorted, indexed, plan, workspace)
+               LAYOUT_INDEXED, LATENT_DIM, LATENT_VALUE_DIM, MODE_GATE_UP, MODE_PLAIN, PreparedWeight, align, align_size,
+               block_norm, contiguous, contiguous_layout, gather_rows, gather_sorted, indexed, plan, workspace)
+from .cache import PagedCache
 
 CONTIGUOUS_SEGMENT = 128
 DECODE_MAX_BLOCK_M = 32    # indexed calls with block_m above this run the tcgen05 kernel
@@ -112,3 +119,46 @@ class MoEFFN:
         route = self.route(topk_ids)
         h = self.gate_up(self.gate_up_input(a, route), route)
         return self.down(h, route, topk_weights, out)
+
+
+class DecoderLayer:
+    """One layer's decode step over a PagedCache: attention, MoE FFN, and the norms before and after both.
+
+    w_qkv bf16 [hidden, (Hq + 2 Hkv) * D] (latent: [hidden, Hq * 576 + 576], queries in the latent space, then the
+    row to cache), w_o bf16 [Hq * D, hidden] (latent: [Hq * 512, hidden]), w_router bf16 [hidden, E]; norms bf16
+    [hidden]: after attention, before the FFN, after the FFN (each None: that norm is left out; the one before the FFN is
+    needed). A position encoding is the caller's: rotate inside `project`."""
+
+    def __init__(self, cache: PagedCache, layer: int, ffn: MoEFFN, num_heads: int, w_qkv: torch.Tensor, w_o: torch.Tensor,
+                 w_router: torch.Tensor, norm_ffn: torch.Tensor, norm_post_attn: Optional[torch.Tensor] = None,
+                 norm_post_ffn: Optional[torch.Tensor] = None, eps: float = 1e-6, window: int = 0):
+        self.cache, self.layer, self.ffn, self.heads = cache, layer, ffn, num_heads
+        self.w_qkv, self.w_o, self.w_router = w_qkv, w_o, w_router
+        self.norm_ffn, self.norm_post_attn, self.norm_post_ffn = norm_ffn, norm_post_attn, norm_post_ffn
+        self.eps, self.window = eps, window
+        if cache.latent:
+            self.kv_heads, self.dim, self.scale = 1, LATENT_DIM, (LATENT_VALUE_DIM // 4 + 64) ** -0.5
+        else:
+            self.kv_heads, self.dim = cache.pool.shape[3:]
+            self.scale = self.dim ** -0.5
+
+    def project(self, y: torch.Tensor, positions: torch.Tensor):
+        """(q [B, Hq, D], k, v) of the new tokens; slices of one product."""
+        x = (y @ self.w_qkv).view(y.shape[0], -1, self.dim)
+        q = x[:, :self.heads]
+        if self.cache.latent:
+            return q, x[:, self.heads], None
+        return q, x[:, self.heads:self.heads + self.kv_heads], x[:, self.heads + self.kv_heads:]
+
+    def forward(self, residual: torch.Tensor, y: torch.Tensor, seq_ids: torch.Tensor, positions: torch.Tensor,
+                next_norm: Optional[torch.Tensor] = None):
+        """residual [B, hidden] and its norm y for this layer -> (residual, y normed by next_norm, or None)."""
+        q, k, v = self.project(y, positions)
+        self.cache.append(self.layer, k, v, seq_ids, positions)
+        o = self.cache.attend(self.layer, q, seq_ids, self.scale, self.window)
+        residual, y = block_norm(o.view(y.shape[0], -1) @ self.w_o, residual, w_post=self.norm_post_attn,
+                                 w_pre=self.norm_ffn, eps=self.eps)
+        top = torch.topk(torch.softmax((y @ self.w_router).float(), -1), self.ffn.top_k)
+        weights = (top.values / top.values.sum(-1, keepdim=True)).contiguous()
+        f = self.ffn.forward(y, top.indices.to(torch.int32), weights)
+        return block_norm(f, residual, w_post=self.norm_post_ffn, w_pre=next_norm, eps=self.eps)
