@@ -75,19 +75,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = torch.cuda.current_device
 
 
-def _call(name: str, index: int, *args) -> None:
+def _run(name: str, index: int, fn, *args) -> None:
     """The C entry point on the current stream of device `index` (made current for the launch where it is not)."""
     if _current_device() == index:
-        status = _FN[name](*args, _raw_stream(index))
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = _FN[name](*args, _raw_stream(index))
-    if status != 0:
+            status = fn(*args, _raw_stream(index))
+    if status:
         raise MoeW4A16Error(status, name)
 
 
 def _need(t: torch.Tensor, name: str, dtype, dim: int, index: Optional[int] = None) -> torch.Tensor:
     """A tensor of that type and rank on CUDA device `index` (None: any) whose last dimension is dense."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == dim and t.stride(-1) == 1 and t.get_device() == index:
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     where = t.get_device()
@@ -104,12 +106,9 @@ def _need(t: torch.Tensor, name: str, dtype, dim: int, index: Optional[int] = No
     return t
 
 
-def _vector(t: Optional[torch.Tensor], name: str, n: int, index: int, dtype=_I32) -> Optional[int]:
-    """Address of a dense 1-D tensor of n elements (None for None)."""
-    if t is None:
-        return None
-    _need(t, name, dtype, 1, index)
-    if t.size(0) != n:
+def _vector(t: torch.Tensor, name: str, n: int, index: int, dtype=_I32) -> int:
+    """Address of a dense 1-D tensor of n elements."""
+    if _need(t, name, dtype, 1, index).size(0) != n:
         raise ValueError(f"{name} has {t.size(0)} elements, expected {n}")
     return t.data_ptr()
 
@@ -119,11 +118,6 @@ def _rows_dense(t: torch.Tensor, name: str) -> torch.Tensor:
     if t.dim() == 3 and t.size(1) > 1 and t.stride(1) != t.size(2):
         raise ValueError(f"{name}: heads must be dense")
     return t
-
-
-def _outer_stride(t: torch.Tensor, row: int) -> int:
-    """Stride of the first dimension (of at most one row: the row's own length)."""
-    return t.stride(0) if t.size(0) > 1 else row
 
 
 def _table(tables: torch.Tensor, index: int) -> Tuple[int, int, int, int]:
@@ -231,8 +225,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     ta, ts, mp, ns = _table(tables, index)
     out, lse = _attention_out(q, b, h, d, index, out, lse)
     wa, wn = _ws(ws, index)
-    _call("paged_attention", index, q.data_ptr(), _outer_stride(q, h * d), b, h, heads, d, c, ta, ts, mp,
-          _vector(lens, "lens", ns, index), _vector(seq_ids, "seq_ids", b, index), ns,
+    _run("paged_attention", index, _FN["paged_attention"], q.data_ptr(), q.stride(0) if b > 1 else h * d, b, h, heads, d, c, ta, ts, mp,
+          _vector(lens, "lens", ns, index), None if seq_ids is None else _vector(seq_ids, "seq_ids", b, index), ns,
           d ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), wa, wn)
     return out, lse
 
@@ -251,8 +245,8 @@ def latent_attention(q: torch.Tensor, pages: torch.Tensor, tables: torch.Tensor,
     ta, ts, mp, ns = _table(tables, index)
     out, lse = _attention_out(q, b, h, LATENT_VALUE_DIM, index, out, lse)
     wa, wn = _ws(ws, index)
-    _call("latent_attention", index, q.data_ptr(), _outer_stride(q, h * d), b, h, c, ta, ts, mp,
-          _vector(lens, "lens", ns, index), _vector(seq_ids, "seq_ids", b, index), ns, scale, window, out.data_ptr(),
+    _run("latent_attention", index, _FN["latent_attention"], q.data_ptr(), q.stride(0) if b > 1 else h * d, b, h, c, ta, ts, mp,
+          _vector(lens, "lens", ns, index), None if seq_ids is None else _vector(seq_ids, "seq_ids", b, index), ns, scale, window, out.data_ptr(),
           lse.data_ptr(), wa, wn)
     return out, lse
 
@@ -281,8 +275,8 @@ def cache_append(k: torch.Tensor, k_pages: torch.Tensor, tables: torch.Tensor, s
             raise ValueError("k and v must have the same shape")
     ta, ts, mp, ns = _table(tables, index)
     wa, wn = _ws(ws, index)
-    _call("cache_append", index, k.data_ptr(), _outer_stride(k, heads * dim),
-          None if latent else v.data_ptr(), 0 if latent else _outer_stride(v, heads * dim), n, heads, dim,
+    _run("cache_append", index, _FN["cache_append"], k.data_ptr(), k.stride(0) if n > 1 else heads * dim,
+          None if latent else v.data_ptr(), 0 if latent else (v.stride(0) if n > 1 else heads * dim), n, heads, dim,
           c, ta, ts, mp, ns, _vector(seq_ids, "seq_ids", n, index),
           _vector(positions, "positions", n, index), wa, wn)
 
@@ -313,8 +307,8 @@ def cache_extend(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, s
     if out is None:
         out = torch.empty(n, dtype=_I32, device=refs.device)
     wa, wn = _ws(ws, index)
-    _call("cache_extend", index, refs.data_ptr(), refs.size(0), ta, ts, mp, _vector(lens, "lens", ns, index), ns,
-          _vector(seq_ids, "seq_ids", n, index), _vector(counts, "counts", n, index), n, page_size,
+    _run("cache_extend", index, _FN["cache_extend"], refs.data_ptr(), refs.size(0), ta, ts, mp, _vector(lens, "lens", ns, index), ns,
+          _vector(seq_ids, "seq_ids", n, index), None if counts is None else _vector(counts, "counts", n, index), n, page_size,
           _vector(out, "out", n, index), wa, wn)
     return out
 
@@ -328,7 +322,7 @@ def cache_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, len
     n = parents.size(0)
     ta, ts, mp, ns = _table(tables, index)
     wa, wn = _ws(ws, index)
-    _call("cache_fork", index, p, _vector(refs, "refs", p.num_pages, index), ta, ts, mp,
+    _run("cache_fork", index, _FN["cache_fork"], p, _vector(refs, "refs", p.num_pages, index), ta, ts, mp,
           _vector(lens, "lens", ns, index), ns, _vector(parents, "parents", n, index),
           _vector(children, "children", n, index), n, page_size, wa, wn)
 
@@ -341,8 +335,8 @@ def cache_free(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, seq
     n = seq_ids.size(0)
     ta, ts, mp, ns = _table(tables, index)
     wa, wn = _ws(ws, index)
-    _call("cache_free", index, refs.data_ptr(), refs.size(0), ta, ts, mp, _vector(lens, "lens", ns, index), ns,
-          _vector(seq_ids, "seq_ids", n, index), _vector(keep, "keep", n, index), n, page_size, wa, wn)
+    _run("cache_free", index, _FN["cache_free"], refs.data_ptr(), refs.size(0), ta, ts, mp, _vector(lens, "lens", ns, index), ns,
+          _vector(seq_ids, "seq_ids", n, index), None if keep is None else _vector(keep, "keep", n, index), n, page_size, wa, wn)
 
 
 def cache_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor) -> None:
@@ -351,7 +345,7 @@ def cache_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, ws: tor
     index = pool.get_device()
     n = src.size(0)
     wa, wn = _ws(ws, index)
-    _call("cache_copy", index, p, _vector(src, "src", n, index), _vector(dst, "dst", n, index), n, wa, wn)
+    _run("cache_copy", index, _FN["cache_copy"], p, _vector(src, "src", n, index), _vector(dst, "dst", n, index), n, wa, wn)
 
 
 def cache_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, ws: torch.Tensor,
@@ -373,7 +367,7 @@ def cache_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, 
     page_map = torch.empty(p.num_pages, dtype=_I32, device=refs.device)
     num_live = torch.empty(1, dtype=_I32, device=refs.device)
     wa, wn = _ws(ws, index)
-    _call("cache_compact", index, p, ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", p.num_pages, index),
+    _run("cache_compact", index, _FN["cache_compact"], p, ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", p.num_pages, index),
           to, page_map.data_ptr(), num_live.data_ptr(), wa, wn)
     return refs_out, tables_out, page_map, num_live
 
@@ -393,38 +387,50 @@ def block_norm(x: Optional[torch.Tensor], residual: torch.Tensor, w_post: Option
     x bf16 [T, n] (None: the norm before the first block; h' is then the residual itself unless residual_scale
     changes it), residual bf16 or float32 [T, n]; without w_post x enters as it is, without w_pre y is None.
     gate bf16 [n], or [G, n] with G dividing T (row t takes gate row t // (T // G)). out may be residual."""
-    _need(residual, "residual", None, 2)
-    index, kind = residual.get_device(), _RESIDUALS.get(residual.dtype)
+    kind = _RESIDUALS.get(residual.dtype) if isinstance(residual, torch.Tensor) else None
     if kind is None:
-        raise TypeError(f"residual has dtype {residual.dtype}, expected torch.bfloat16 or torch.float32")
-    shape = residual.shape
+        raise TypeError(f"residual must be a torch.bfloat16 or torch.float32 tensor, got {getattr(residual, 'dtype', residual)}")
+    _need(residual, "residual", residual.dtype, 2)
+    index, shape = residual.get_device(), residual.shape
     t, n = shape
-    xa = xs = ga = oa = os_ = ya = ys = None
+    xa = ga = oa = ya = wa = wb = None
+    xs = os_ = ys = n
+    gate_rows = 1
     if x is not None:
         if _need(x, "x", _BF16, 2, index).shape != shape:
             raise ValueError("x and residual must have the same shape")
-        xa, xs = x.data_ptr(), _outer_stride(x, n)
-    gate_rows = 1
+        xa = x.data_ptr()
     if gate is not None:
         if _need(gate, "gate", _BF16, gate.dim(), index).shape[-1] != n or gate.dim() > 2 or not gate.is_contiguous():
             raise ValueError(f"gate must be contiguous [{n}] or [G, {n}]")
         ga, gate_rows = gate.data_ptr(), gate.size(0) if gate.dim() == 2 else 1
+    if w_post is not None:
+        wa = _vector(w_post, "w_post", n, index, _BF16)
     h = residual
     if x is not None or residual_scale != 1.0 or out is not None:    # else the residual passes through unchanged
         if out is None:
-            out = torch.empty(shape, dtype=residual.dtype, device=residual.device)
+            out = torch.empty_like(residual)
         elif _need(out, "out", residual.dtype, 2, index).shape != shape:
             raise ValueError("out and residual must have the same shape")
-        h, oa, os_ = out, out.data_ptr(), _outer_stride(out, n)
+        h, oa = out, out.data_ptr()
     if w_pre is not None:
+        wb = _vector(w_pre, "w_pre", n, index, _BF16)
         if y is None:
-            y = torch.empty(shape, dtype=_BF16, device=residual.device)
+            y = torch.empty_like(residual) if kind == RESIDUAL_BF16 else torch.empty(shape, dtype=_BF16, device=residual.device)
         elif _need(y, "y", _BF16, 2, index).shape != shape:
             raise ValueError("y and residual must have the same shape")
-        ya, ys = y.data_ptr(), _outer_stride(y, n)
+        ya = y.data_ptr()
     elif y is not None:
         raise ValueError("y needs w_pre")
-    _call("block_norm", index, xa, xs or 0, residual.data_ptr(), _outer_stride(residual, n), kind, ga, gate_rows,
-          _vector(w_post, "w_post", n, index, _BF16), _vector(w_pre, "w_pre", n, index, _BF16), t, n, eps,
-          residual_scale, block_scale, oa, os_ or 0, ya, ys or 0)
+    hs = n
+    if t > 1:
+        hs = residual.stride(0)
+        if xa is not None:
+            xs = x.stride(0)
+        if oa is not None:
+            os_ = out.stride(0)
+        if ya is not None:
+            ys = y.stride(0)
+    _run("block_norm", index, _FN["block_norm"], xa, xs, residual.data_ptr(), hs, kind, ga, gate_rows, wa, wb, t, n, eps,
+         residual_scale, block_scale, oa, os_, ya, ys)
     return h, y
