@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnPar
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       const uint32_t m = __ballot_sync(0xffffffffu, np[k] > 1);
-      if (np[k] > 1) list[count + __popc(m & ((1u << lane) - 1u))] = 32 * k + lane;
+      if (np[k] > 1) list[count + __popc(m & ((1u << lane) - 1u))] = 32 * k + lane + (np[k] << 16);
       count += __popc(m);
     }
     if (lane == 0) count_s = count;
@@ -636,31 +636,36 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnPar
   const int64_t step = by_warp ? int64_t(gridDim.x) * kJoinWarps : gridDim.x;
   const int part0 = by_warp ? 0 : warp, parts_step = by_warp ? 1 : kJoinWarps;
   for (int64_t item = first; item < items; item += step) {
-    const int c = list[item / heads], h = static_cast<int>(item % heads);
-    const Record r = records[c];
-    if (h >= r.heads) continue;                           // (a block by itself: all of its warps alike)
+    const int entry = list[item / heads], c = entry & 0xffff, np = entry >> 16, h = static_cast<int>(item % heads);
+    const Record r = records[c];                          // (needed last; the parts' loads do not wait for it)
     auto part_at = [&](int i) { return p.parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * kPartFloats; };
-    float top = -INFINITY;
-    for (int i = lane; i < r.np; i += 32) top = fmaxf(top, __ldcg(part_at(i) + h));
+    // lane i: base and sum of part i, i + 32, ... (a row has at most kLatentMaxCtas)
+    constexpr int kRounds = (kLatentMaxCtas + 31) / 32;
+    float top = -INFINITY, sum = 0.f, m[kRounds], l[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int i = 32 * k + lane;
+      m[k] = i < np ? __ldcg(part_at(i) + h) : -INFINITY;
+      l[k] = i < np ? __ldcg(part_at(i) + kHeads + h) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) top = fmaxf(top, m[k]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float b0 = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
     float4 acc[kLaneVecs];
 #pragma unroll
     for (int k = 0; k < kLaneVecs; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < r.np; i0 += 32) {
-      // lane i: the weight of part i0 + i
-      float f = 0.f;
-      if (i0 + lane < r.np) {
-        f = exp2_fast(__ldcg(part_at(i0 + lane) + h) - b0);
-        sum = fmaf(f, __ldcg(part_at(i0 + lane) + kHeads + h), sum);
-      }
-      const int n = min(32, r.np - i0);
+#pragma unroll
+    for (int rd = 0; rd < kRounds; ++rd) {
+      if (32 * rd >= np) break;
+      const float f = exp2_fast(m[rd] - b0);
+      sum = fmaf(f, l[rd], sum);
+      const int n = min(32, np - 32 * rd);
 #pragma unroll 4
       for (int i = part0; i < n; i += parts_step) {
         const float w = __shfl_sync(0xffffffffu, f, i);
-        const float4* src = reinterpret_cast<const float4*>(part_at(i0 + i) + 2 * kHeads + h * kLatentValue) + lane;
+        const float4* src = reinterpret_cast<const float4*>(part_at(32 * rd + i) + 2 * kHeads + h * kLatentValue) + lane;
 #pragma unroll
         for (int k = 0; k < kLaneVecs; ++k) {
           const float4 v = __ldcg(src + 32 * k);
@@ -692,6 +697,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnPar
       __syncthreads();
       if (warp != 0) continue;
     }
+    if (h >= r.heads) continue;                           // (a last block of heads: its other parts were never written)
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int64_t row = int64_t(r.b) * p.heads + r.head0 + h;
 #pragma unroll
