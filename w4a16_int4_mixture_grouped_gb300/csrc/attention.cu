@@ -43,9 +43,9 @@ struct Cfg {
   static constexpr int kStages = kStageBytes <= 4096 ? 6 : 3;
   static constexpr int kTile = kWarps * kTok;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kPitch = DP + 4;                                  // floats of a joined row
-  static constexpr int kJoinBytes = kWarps * kRows * kPitch * 4;
-  static constexpr int kBufBytes = kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes;
+  // the warps' accumulators are joined 8 rows and up to 128 channels at a time, beside the ring
+  static constexpr int kJoinCols = DP < 128 ? DP : 128;
+  static constexpr int kSmemBytes = kRingBytes + kWarps * 8 * kJoinCols * 4;
 };
 
 // Position of 16-byte chunk c of token row r: rows r .. r+7 at one chunk (ldmatrix) fall on eight
@@ -121,6 +121,13 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   __shared__ Share share;
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
   __shared__ int last_flag;
+  // the pieces that a warp's copies have reached and its work has not finished
+  struct Ahead {
+    int64_t row0;
+    int b, r, n, ntiles;
+  };
+  constexpr int kAhead = C::kStages + 1;
+  __shared__ Ahead pieces[kWarps][kAhead];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
   const int chunks = (p.group + kRows - 1) / kRows;
@@ -139,77 +146,103 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   const uint32_t negate = p.score_scale < 0.f ? 0x80008000u : 0u;
   const float abs_scale = p.score_scale == 0.f ? 1.f : fmaxf(fabsf(p.score_scale), 1.2e-38f);
   const bool flat = p.score_scale == 0.f;
-  PieceWalk walk;
-  walk.start(p, &share);
-  Piece pc;
-  while (walk.next(p, rows, C::kTile, pc)) {
-    const int r = pc.r * lanes + lane_row, kvh = r / chunks, hc = r % chunks;
-    const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
-    const int64_t head_off = int64_t(kvh) * p.head_stride;
-    const int32_t* table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
-    const int tok0 = (pc.lo / C::kTile + pc.tile0) * C::kTile + warp * C::kTok;   // this warp's first token
-    const int n = pc.tile1 - pc.tile0, b = pc.b;
-
-    // ---- copies of stage i: the page ids of the next stage are read one stage ahead
-    auto entry_of = [&](int i) -> int {
-      const int tok = tok0 + i * C::kTile + (lane & (C::kTok - 1));
-      if (i >= n || tok < pc.lo || tok >= pc.hi) return -1;
-      return table[tok / p.t.page_size];
-    };
-    int entry = entry_of(0);
-    uint32_t masks[C::kStages];                   // seen tokens of the stages in flight
-    auto issue = [&](int i, int slot) -> uint32_t {
-      uint32_t seen = 0;
-      if (i < n) {
-        const int tok = tok0 + i * C::kTile + (lane & (C::kTok - 1));
-        if (entry >= p.t.num_pages) {
-          set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
-          entry = -1;
-        }
-        int64_t off = -1;
-        if (entry >= 0)
-          off = int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride + head_off;
-        seen = __ballot_sync(0xffffffffu, off >= 0) & C::kAll;
-        if (seen != 0) {
-          const uint32_t kd = ring + slot * C::kStageBytes, vd = kd + C::kTok * C::kRowBytes;
-          const uint8_t* kb = static_cast<const uint8_t*>(p.k);
-          const uint8_t* vb = static_cast<const uint8_t*>(p.v);
-          constexpr int kCopies = C::kTok * C::kChunks / 32;
-          const auto key_at = [](int tr, int c) { return 16 * (E4M3 ? swz_key8<C::kChunks>(tr, c) : swz<C::kChunks>(tr, c)); };
-          if (seen == C::kAll && one_run) {
-            // the stage's tokens lie behind each other in one page: lane's row and chunk advance by whole rows
-            const int64_t o = (__shfl_sync(0xffffffffu, off, 0) + int64_t(lane / C::kChunks) * p.token_stride) * C::kElem +
-                              lane % C::kChunks * 16;
-            const uint8_t* ks = kb + o;
-            const uint8_t* vs = vb + o;
-            const int64_t step = int64_t(32 / C::kChunks) * p.token_stride * C::kElem;
+  // ---- copies run ahead of the work by kStages - 1 stages, across the pieces of the share: a walk of their own
+  PieceWalk ahead;
+  ahead.start(p, &share);
+  int ahead_tok = 0, ahead_left = 0, ahead_lo = 0, ahead_hi = 0, entry = -1;   // of the warp's next stage
+  int64_t ahead_head = 0;
+  const int32_t* ahead_table = nullptr;
+  // this lane's page in the next stage, read a stage early
+  auto next_entry = [&]() {
+    const int tok = ahead_tok + (lane & (C::kTok - 1));
+    entry = tok >= ahead_lo && tok < ahead_hi ? ahead_table[tok / p.t.page_size] : -1;
+  };
+  int found = 0, found_slot = 0;
+  auto next_piece = [&]() {
+    Piece pc;
+    if (!ahead.next(p, rows, C::kTile, pc)) return;
+    if (lane == 0) pieces[warp][found_slot] = {pc.row0, pc.b, pc.r, pc.tile1 - pc.tile0, pc.ntiles};
+    ++found;
+    found_slot = found_slot + 1 == kAhead ? 0 : found_slot + 1;
+    const int r = pc.r * lanes + lane_row, kvh = r / chunks, head0 = kvh * p.group + r % chunks * kRows;
+    ahead_table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
+    ahead_head = int64_t(kvh) * p.head_stride;
+    ahead_tok = (pc.lo / C::kTile + pc.tile0) * C::kTile + warp * C::kTok;
+    ahead_left = pc.tile1 - pc.tile0;
+    ahead_lo = pc.lo;
+    ahead_hi = pc.hi;
+    next_entry();
+    // its queries to L2 (warp 0: one line a lane; up to 16 heads x 256 channels are two)
+    if (warp == 0) {
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(p.q + int64_t(pc.b) * p.q_stride + int64_t(head0) * p.dim);
+      const int bytes = min(kRows, p.group - r % chunks * kRows) * p.dim * 2;
+      for (int i = lane * 128; i < bytes; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+    }
+  };
+  auto issue = [&](int slot) -> uint32_t {
+    uint32_t seen = 0;
+    if (ahead_left > 0) {
+      const int tok = ahead_tok + (lane & (C::kTok - 1));
+      if (entry >= p.t.num_pages) {
+        set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
+        entry = -1;
+      }
+      int64_t off = -1;
+      if (entry >= 0)
+        off = int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride + ahead_head;
+      seen = __ballot_sync(0xffffffffu, off >= 0) & C::kAll;
+      if (seen != 0) {
+        const uint32_t kd = ring + slot * C::kStageBytes, vd = kd + C::kTok * C::kRowBytes;
+        const uint8_t* kb = static_cast<const uint8_t*>(p.k);
+        const uint8_t* vb = static_cast<const uint8_t*>(p.v);
+        constexpr int kCopies = C::kTok * C::kChunks / 32;
+        const auto key_at = [](int tr, int c) { return 16 * (E4M3 ? swz_key8<C::kChunks>(tr, c) : swz<C::kChunks>(tr, c)); };
+        if (seen == C::kAll && one_run) {
+          // the stage's tokens lie behind each other in one page: lane's row and chunk advance by whole rows
+          const int64_t o = (__shfl_sync(0xffffffffu, off, 0) + int64_t(lane / C::kChunks) * p.token_stride) * C::kElem +
+                            lane % C::kChunks * 16;
+          const uint8_t* ks = kb + o;
+          const uint8_t* vs = vb + o;
+          const int64_t step = int64_t(32 / C::kChunks) * p.token_stride * C::kElem;
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j) {
-              const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
-              copy16(kd + key_at(tr, c), ks);
-              copy16(vd + 16 * swz<C::kChunks>(tr, c), vs);
-              ks += step;
-              vs += step;
-            }
-          } else {
+          for (int j = 0; j < kCopies; ++j) {
+            const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
+            copy16(kd + key_at(tr, c), ks);
+            copy16(vd + 16 * swz<C::kChunks>(tr, c), vs);
+            ks += step;
+            vs += step;
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j) {
-              const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
-              const int64_t o = __shfl_sync(0xffffffffu, off, tr);
-              const bool ok = o >= 0 && c * 16 < p.dim * C::kElem;
-              const int64_t at = ok ? o * C::kElem + c * 16 : 0;
-              cp_async16(kd + key_at(tr, c), kb + at, ok ? 16 : 0);
-              cp_async16(vd + 16 * swz<C::kChunks>(tr, c), vb + at, ok ? 16 : 0);
-            }
+          for (int j = 0; j < kCopies; ++j) {
+            const int idx = j * 32 + lane, tr = idx / C::kChunks, c = idx % C::kChunks;
+            const int64_t o = __shfl_sync(0xffffffffu, off, tr);
+            const bool ok = o >= 0 && c * 16 < p.dim * C::kElem;
+            const int64_t at = ok ? o * C::kElem + c * 16 : 0;
+            cp_async16(kd + key_at(tr, c), kb + at, ok ? 16 : 0);
+            cp_async16(vd + 16 * swz<C::kChunks>(tr, c), vb + at, ok ? 16 : 0);
           }
         }
-        entry = entry_of(i + 1);
       }
-      cp_async_commit();
-      return seen;
-    };
+      ahead_tok += C::kTile;
+      if (--ahead_left > 0) next_entry();
+      else next_piece();
+    }
+    cp_async_commit();
+    return seen;
+  };
+  next_piece();
+  uint32_t masks[C::kStages];                     // seen tokens of the stages in flight
 #pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s) masks[s] = issue(s, s);
+  for (int s = 0; s < C::kStages - 1; ++s) masks[s] = issue(s);
+  int slot = 0;
+
+  for (int done = 0, done_slot = 0; done < found; ++done, done_slot = done_slot + 1 == kAhead ? 0 : done_slot + 1) {
+    __syncwarp();
+    const Ahead& pc = pieces[warp][done_slot];
+    const int r = pc.r * lanes + lane_row, kvh = r / chunks, hc = r % chunks;
+    const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
+    const int n = pc.n, b = pc.b;
 
     // ---- queries as MMA A fragments
     constexpr int KS = DP / 16;
@@ -285,12 +318,10 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
 #pragma unroll
       for (int k = 0; k < NR; ++k) o[i][k] = 0.f;
 
-    int slot = 0;
     for (int i = 0; i < n; ++i) {
       {
-        const int ahead = i + C::kStages - 1;
         const int to = slot == 0 ? C::kStages - 1 : slot - 1;
-        const uint32_t seen = issue(ahead, to);
+        const uint32_t seen = issue(to);
 #pragma unroll
         for (int s = 0; s < C::kStages; ++s)
           if (s == to) masks[s] = seen;
@@ -423,69 +454,76 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       __syncwarp();
       slot = slot + 1 == C::kStages ? 0 : slot + 1;
     }
-    cp_async_wait<0>();
-    __syncthreads();
-
-    // ---- join the warps: unnormalised accumulators through shared memory
-    float* buf = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int hh = 0; hh < HR; ++hh) {
-      float sum = l[hh];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int row = g + 8 * hh;
-      if (t == 0) {
-        part_m[warp][row] = m[hh];
-        part_l[warp][row] = sum;
-      }
-      float* dst = buf + (warp * kRows + row) * C::kPitch;
-#pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
-        if (!E4M3) {
-          *reinterpret_cast<float2*>(dst + i * 8 + 2 * t) = make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
-        } else if ((i & 1) == 0) {
-          *reinterpret_cast<float4*>(dst + (i / 2) * 16 + 4 * t) =
-              make_float4(o[i][2 * hh], o[i + 1][2 * hh], o[i][2 * hh + 1], o[i + 1][2 * hh + 1]);
-        }
-      }
-    }
-    __syncthreads();
+    // ---- join the warps: unnormalised accumulators through shared memory, beside the copies in flight. Row `row` of
+    // 8, block i of 8 channels at ((row * blocks + (i ^ row)) * 8: a fragment's rows fall on different banks.
+    constexpr int kBlocks = C::kJoinCols / 8;
+    float* buf = reinterpret_cast<float*>(smem + C::kRingBytes);
     // first and last CTA of the row, as blocks of the grid
     const int c0 = cta_of(total, ctas, pc.row0) * lanes + lane_row;
     const int c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1) * lanes + lane_row;
     const bool whole = c0 == c1;
     float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * part_floats<DP>();
     const int vecs = p.dim / 4;
-    for (int e = threadIdx.x; e < heads * vecs; e += kThreads) {
-      const int row = e / vecs, d = e % vecs * 4;
-      float top = part_m[0][row];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, part_m[w][row]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(part_m[w][row] - base);
-        const float4 v = *reinterpret_cast<const float4*>(buf + (w * kRows + row) * C::kPitch + d);
-        sum = fmaf(f, part_l[w][row], sum);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+    for (int hh = 0; hh < HR; ++hh) {
+      float sum = l[hh];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (t == 0) {
+        part_m[warp][g + 8 * hh] = m[hh];
+        part_l[warp][g + 8 * hh] = sum;
       }
-      if (whole) {
-        const float inv = sum > 0.f ? p.v_scale / sum : 0.f;
-        const int64_t h = int64_t(b) * p.heads + head0 + row;
-        *reinterpret_cast<uint2*>(p.out + h * p.dim + d) =
-            make_uint2(pack_bf16x2_rn(acc.x * inv, acc.y * inv), pack_bf16x2_rn(acc.z * inv, acc.w * inv));
-        if (d == 0 && p.lse != nullptr) p.lse[h] = (top + log2f(sum)) * 0.69314718055994531f;
-      } else {
-        __stcg(reinterpret_cast<float4*>(part + 2 * kRows + row * DP + d), acc);
-        if (d == 0) {
-          __stcg(part + row, top);
-          __stcg(part + kRows + row, sum);
+#pragma unroll
+      for (int cb = 0; cb < DP / C::kJoinCols; ++cb) {
+        float* dst = buf + (warp * 8 + g) * C::kJoinCols;
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j) {
+          const int i = cb * kBlocks + j;
+          if (!E4M3) {
+            *reinterpret_cast<float2*>(dst + (j ^ (g & (kBlocks - 1))) * 8 + 2 * t) = make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
+          } else if ((i & 1) == 0) {
+            // channels 16 (i / 2) + 4 t ..: the half of a pair of blocks that t / 2 names
+            *reinterpret_cast<float4*>(dst + ((j + (t >> 1)) ^ (g & (kBlocks - 1))) * 8 + 4 * (t & 1)) =
+                make_float4(o[i][2 * hh], o[i + 1][2 * hh], o[i][2 * hh + 1], o[i + 1][2 * hh + 1]);
+          }
         }
+        __syncthreads();
+        const int here = min(8, heads - 8 * hh);           // rows of this half (may be <= 0)
+        const int cols = min(C::kJoinCols, p.dim - cb * C::kJoinCols) / 4;
+        for (int e = threadIdx.x; e < here * cols; e += kThreads) {
+          const int row8 = e / cols, row = 8 * hh + row8, dc = e % cols * 4, d = cb * C::kJoinCols + dc;
+          float top = part_m[0][row];
+#pragma unroll
+          for (int w = 1; w < kWarps; ++w) top = fmaxf(top, part_m[w][row]);
+          const float base = top == -INFINITY ? 0.f : top;
+          float sum2 = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2_fast(part_m[w][row] - base);
+            const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + row8) * C::kJoinCols +
+                                                              ((dc >> 3) ^ (row8 & (kBlocks - 1))) * 8 + (dc & 7));
+            sum2 = fmaf(f, part_l[w][row], sum2);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+          if (whole) {
+            const float inv = sum2 > 0.f ? p.v_scale / sum2 : 0.f;
+            const int64_t h = int64_t(b) * p.heads + head0 + row;
+            *reinterpret_cast<uint2*>(p.out + h * p.dim + d) =
+                make_uint2(pack_bf16x2_rn(acc.x * inv, acc.y * inv), pack_bf16x2_rn(acc.z * inv, acc.w * inv));
+            if (d == 0 && p.lse != nullptr) p.lse[h] = (top + log2f(sum2)) * 0.69314718055994531f;
+          } else {
+            __stcg(reinterpret_cast<float4*>(part + 2 * kRows + row * DP + d), acc);
+            if (d == 0) {
+              __stcg(part + row, top);
+              __stcg(part + kRows + row, sum2);
+            }
+          }
+        }
+        __syncthreads();                                   // the buffer is free again
       }
     }
 
@@ -504,8 +542,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         const int np = (c1 - c0) / lanes + 1;
         // part of CTA c0 + i: its last row for the first one, its first row for the others
         auto part_at = [&](int i) { return parts + (int64_t(c0 + i * lanes) * 2 + (i == 0 ? 1 : 0)) * part_floats<DP>(); };
-        float* weight = buf;                              // [np][kRows], then the rows' totals
-        __shared__ float row_top[kRows], row_sum[kRows];
+        float* row_top = part_m[0];                       // read by nobody any more
+        float* row_sum = part_l[0];
         for (int row = warp; row < heads; row += kWarps) {
           float top = -INFINITY;
           for (int i = lane; i < np; i += 32) top = fmaxf(top, __ldcg(part_at(i) + row));
@@ -515,7 +553,6 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           float sum = 0.f;
           for (int i = lane; i < np; i += 32) {
             const float f = exp2_fast(__ldcg(part_at(i) + row) - base);
-            weight[i * kRows + row] = f;
             sum = fmaf(f, __ldcg(part_at(i) + kRows + row), sum);
           }
 #pragma unroll
@@ -529,9 +566,10 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         for (int e = threadIdx.x; e < heads * vecs; e += kThreads) {
           const int row = e / vecs, d = e % vecs * 4;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float base = row_top[row] == -INFINITY ? 0.f : row_top[row];
 #pragma unroll 8
           for (int i = 0; i < np; ++i) {
-            const float f = weight[i * kRows + row];
+            const float f = exp2_fast(__ldcg(part_at(i) + row) - base);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i) + 2 * kRows + row * DP + d));
             acc.x = fmaf(f, v.x, acc.x);
             acc.y = fmaf(f, v.y, acc.y);
@@ -546,8 +584,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         }
       }
     }
-    __syncthreads();                                      // the ring and the flags are free again
+    if (!whole) __syncthreads();                          // the flag and the totals are free again
   }
+  cp_async_wait<0>();
 }
 
 template <int DP, bool E4M3, bool HALF>
@@ -557,11 +596,11 @@ cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   static bool attr_set[64] = {false};
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[device]) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBufBytes);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set[device] = true;
   }
-  int grid = device_info(device).sm_count * (2 * C::kBufBytes <= 220 * 1024 ? 2 : 1);
+  int grid = device_info(device).sm_count * (2 * (C::kSmemBytes + 2048) <= 228 * 1024 ? 2 : 1);
   if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
   // All rows of a sequence side by side where that idles at most one CTA in twenty: the heads of a token lie next to
   // each other in the usual cache, and read at about the same time they share DRAM pages (a row of one head is
@@ -569,7 +608,7 @@ cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   AttnParams q = p;
   const int rows = p.kv_heads * ((p.group + kRows - 1) / kRows);
   q.lanes = rows <= grid && grid / rows * rows * 20 >= grid * 19 ? rows : 1;
-  attention_kernel<DP, E4M3, HALF><<<grid / q.lanes * q.lanes, kThreads, C::kBufBytes, stream>>>(q, p.parts, p.counters);
+  attention_kernel<DP, E4M3, HALF><<<grid / q.lanes * q.lanes, kThreads, C::kSmemBytes, stream>>>(q, p.parts, p.counters);
   note_launch();
   return cudaGetLastError();
 }
@@ -577,8 +616,12 @@ template <int DP>
 cudaError_t launch_dim(const AttnParams& p, bool e4m3, int device, cudaStream_t stream) {
   // groups of up to 8 heads leave half of the MMA's rows out and need half the accumulators (with 256 8-bit channels
   // that form spills registers: 2.6 TB/s against 5.1 of the full one)
-  const bool half = p.group <= 8 && !(DP == 256 && e4m3);
-  if (e4m3) return half ? launch<DP, true, true>(p, device, stream) : launch<DP, true, false>(p, device, stream);
+  const bool half = p.group <= 8;
+  if constexpr (DP == 256) {
+    if (e4m3) return launch<DP, true, false>(p, device, stream);
+  } else {
+    if (e4m3) return half ? launch<DP, true, true>(p, device, stream) : launch<DP, true, false>(p, device, stream);
+  }
   return half ? launch<DP, false, true>(p, device, stream) : launch<DP, false, false>(p, device, stream);
 }
 

@@ -25,7 +25,7 @@ __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
 struct Share {
   int64_t total, x, x_end, first;
   int ctas, b;
-  int sums[32];
+  int sums[16];
 };
 
 // Fills *sh for CTA `cta` of `grid` (every thread calls it; shares of at least min_tiles tiles where there
