@@ -2,22 +2,29 @@
 //
 // For each sequence and cache head: scores s = q K^T of the up to 16 query heads that share it, a
 // softmax over the seen tokens with a running maximum and sum, and o = p V. Every key and value is
-// read once; at 4 flops a byte and query head the bound is HBM, so the kernel is built around
-// keeping copies in flight:
+// read once; at one flop a byte and query head (E4M3: two) the bound is HBM, so the kernel is built
+// around keeping copies in flight:
 //
 //   * One CTA of four warps takes an equal share of all tiles of all sequences (split.cuh), whatever
 //     the lengths; rows that cross a CTA's range are joined by the last CTA to arrive, in order, from
 //     FP32 parts. One launch, no host knowledge of the lengths.
 //   * Within a tile each warp owns its own tokens: its own ring of shared-memory stages filled by
 //     its own cp.async, its own maximum, sum and accumulator. No barrier in the loop; the four
-//     warps are joined once per row.
+//     warps are joined once per row, in a buffer beside the ring, while the next rows' stages are on their way
+//     (4096 rows of 128 tokens: 540 us against 756 with the ring drained at a row's end).
+//   * Two CTAs an SM with 96 KB of stages between them: 24 KB a warp keep HBM busy. Three or four CTAs with shorter
+//     rings are slower (230 to 445 us where two take 194).
 //   * The query heads of a cache head are the 16 rows of m16n8k16 MMAs (rows 8-15 are left out where
 //     the group has at most 8 heads), so a key or value is loaded from shared memory once for all heads.
-//     Warp-level MMA reaches: a 16-row MMA per 256 bytes is a tenth of its rate at full HBM speed.
+//     Warp-level MMA reaches: at full HBM speed its pipe is 19% busy (E4M3: 34%).
 //   * Unseen slots (past the end, before the window, freed pages) are not read: their rows are
 //     zero-filled and their scores are -infinity, so nothing in them reaches the result.
 //   * The probabilities enter the value product as BF16 (E4M3 pages: FP16, keys and values converted
 //     exactly, queries scaled by a power of two per row). Their sum is taken in FP32 before that rounding.
+//
+// 96 sequences of up to 8191 tokens, 8 cache heads x 8 query heads x 128 channels, BF16: 329 us, 6.5 TB/s, 96% of a plain
+// copy. 8 sequences of up to 131072 tokens, E4M3: 197 us, 6.0 TB/s: converting 8-bit elements takes the issue slots that
+// copies would use (64 channels: 4.4 TB/s; 256: 4.8, where registers spill as well).
 #include <cuda_runtime.h>
 
 #include "block.h"

@@ -41,7 +41,7 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return lanes_sum<32>(lane < warps ? red[lane] : 0.f);
 }
 
-// E consecutive elements by one access (FP32: of at most 16 bytes), from an address aligned to it.
+// E (1, 2 or 8) consecutive elements by one access (FP32: of at most 16 bytes), from an address aligned to it.
 template <int E>
 struct Pack {
   float v[E];
@@ -62,9 +62,6 @@ __device__ __forceinline__ Pack<E> load_bf16(const uint16_t* p) {
   if (E == 8) {
     const uint4 w = *reinterpret_cast<const uint4*>(p);
     a[0] = w.x, a[1] = w.y, a[2] = w.z, a[3] = w.w;
-  } else if (E == 4) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    a[0] = w.x, a[1] = w.y;
   } else if (E == 2) {
     a[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
@@ -77,7 +74,7 @@ __device__ __forceinline__ Pack<E> load_bf16(const uint16_t* p) {
 template <int E>
 __device__ __forceinline__ Pack<E> load_f32(const float* p) {
   Pack<E> r;
-  if (E >= 4) {
+  if (E == 8) {
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
       const float4 a = reinterpret_cast<const float4*>(p)[i];
@@ -101,7 +98,6 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const Pack<E>& x) {
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) w[i] = pack_bf16x2_rn(x.v[(2 * i) % E], x.v[(2 * i + 1) % E]);
   if (E == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  else if (E == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 template <int E>
@@ -111,7 +107,7 @@ __device__ __forceinline__ void store_f32(float* p, const Pack<E>& x) {
     asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x.v[0]), "f"(x.v[1 % E]),
                  "f"(x.v[2 % E]), "f"(x.v[3 % E]), "f"(x.v[4 % E]), "f"(x.v[5 % E]), "f"(x.v[6 % E]), "f"(x.v[7 % E])
                  : "memory");
-  } else if (E >= 4) {
+  } else if (E == 8) {
 #pragma unroll
     for (int i = 0; i < E / 4; ++i)
       reinterpret_cast<float4*>(p)[i] =
@@ -424,7 +420,7 @@ void launch(const NormParams& p, int sm_count, cudaStream_t stream) {
     return launch_cta<RES32, E, 5, SHIFT>(p, packs, stream);       // (up to 4097 packs)
   } else {
     if (packs <= 8192) return launch_cta<RES32, E, 8, SHIFT>(p, packs, stream);
-    if constexpr (E < 4) return launch_cta<RES32, E, 32, SHIFT>(p, packs, stream);
+    return launch_cta<RES32, E, 32, SHIFT>(p, packs, stream);
   }
 }
 
