@@ -11,7 +11,7 @@
 //   * Within a tile each warp owns its own tokens: its own ring of shared-memory stages filled by
 //     its own cp.async, its own maximum, sum and accumulator. No barrier in the loop; the four
 //     warps are joined once per row, in a buffer beside the ring, while the next rows' stages are on their way
-//     (4096 rows of 128 tokens: 540 us against 756 with the ring drained at a row's end).
+//     (4096 rows of 128 tokens: 495 us against 756 with the ring drained at a row's end).
 //   * Two CTAs an SM with 96 KB of stages between them: 24 KB a warp keep HBM busy. Three or four CTAs with shorter
 //     rings are slower (230 to 445 us where two take 194).
 //   * The query heads of a cache head are the 16 rows of m16n8k16 MMAs (rows 8-15 are left out where
@@ -238,7 +238,35 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     cp_async_commit();
     return seen;
   };
+  // A piece's queries. BF16: (row, k 2t..2t+1) and (row, k 2t+8..2t+9) of each 16-channel step. E4M3: the channels in
+  // the order in which a lane reads 8-bit keys: step s of a 64-channel block takes channels 16 t + 4 s .. + 3 of lane t.
+  // BF16 up to 128 channels asks for them while the piece before is being joined (4096 rows of 128 tokens: 540 -> 495 us);
+  // with 256 channels registers are wanting, and E4M3, bound by its conversions, gains nothing (486 us both ways) and
+  // loses registers in its loop (a long row 196 -> 200 us).
+  constexpr int KS = DP / 16;
+  constexpr bool kEarly = !E4M3 && DP <= 128;
+  uint2 raw[KS][HR];
+  auto load_queries = [&](const Ahead& pc) {
+    const int r = pc.r * lanes + lane_row, head0 = r / chunks * p.group + r % chunks * kRows;
+    const int heads = min(kRows, p.group - r % chunks * kRows);
+#pragma unroll
+    for (int hh = 0; hh < HR; ++hh) {
+      const int row = g + 8 * hh;
+      const uint16_t* src = p.q + int64_t(pc.b) * p.q_stride + int64_t(head0 + row) * p.dim;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int d = E4M3 ? (ks >> 2) * 64 + 16 * t + 4 * (ks & 3) : ks * 16 + 2 * t;
+        raw[ks][hh] = make_uint2(0u, 0u);
+        if (row < heads && d < p.dim && !flat) {
+          if (E4M3) raw[ks][hh] = *reinterpret_cast<const uint2*>(src + d);
+          else raw[ks][hh] = make_uint2(*reinterpret_cast<const uint32_t*>(src + d), *reinterpret_cast<const uint32_t*>(src + d + 8));
+        }
+      }
+    }
+  };
   next_piece();
+  __syncwarp();
+  if (kEarly) load_queries(pieces[warp][0]);      // (a CTA that gets here has a piece)
   uint32_t masks[C::kStages];                     // seen tokens of the stages in flight
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) masks[s] = issue(s);
@@ -252,36 +280,24 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     const int n = pc.n, b = pc.b;
 
     // ---- queries as MMA A fragments
-    constexpr int KS = DP / 16;
+    if (!kEarly) load_queries(pc);
     uint32_t qa[KS][HALF ? 2 : 4];
     float qscale[HR];
 #pragma unroll
     for (int hh = 0; hh < HR; ++hh) {
-      const int row = g + 8 * hh;
-      const uint16_t* src = p.q + int64_t(b) * p.q_stride + int64_t(head0 + row) * p.dim;
       qscale[hh] = abs_scale;
       if (!E4M3) {
-        // (row, k 2t..2t+1) and (row, k 2t+8..2t+9) of each 16-channel step
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int d = ks * 16 + half * 8 + 2 * t;
-            qa[ks][HALF ? half : 2 * half + hh] =
-                row < heads && d < p.dim && !flat ? *reinterpret_cast<const uint32_t*>(src + d) ^ negate : 0u;
-          }
+        for (int ks = 0; ks < KS; ++ks) {
+          qa[ks][HALF ? 0 : hh] = raw[ks][hh].x ^ negate;
+          qa[ks][HALF ? 1 : 2 + hh] = raw[ks][hh].y ^ negate;
+        }
       } else {
-        // the channels in the order in which a lane reads 8-bit keys: step s of a 64-channel block
-        // takes channels 16 t + 4 s .. + 3 of lane t. Scaled into the FP16 range by a power of two.
-        uint2 raw[KS];
+        // scaled into the FP16 range by a power of two
         float top = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const int d = (ks >> 2) * 64 + 16 * t + 4 * (ks & 3);
-          raw[ks] = row < heads && d < p.dim && !flat ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0u, 0u);
-          raw[ks].x ^= negate;
-          raw[ks].y ^= negate;
-          const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+          const uint32_t w[2] = {raw[ks][hh].x, raw[ks][hh].y};
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             top = fmaxf(top, fmaxf(fabsf(bf16_to_f32(static_cast<uint16_t>(w[j]))),
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
                            1.2e-38f);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t w[2] = {raw[ks].x, raw[ks].y};
+          const uint32_t w[2] = {raw[ks][hh].x ^ negate, raw[ks][hh].y ^ negate};
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             qa[ks][HALF ? half : 2 * half + hh] =
@@ -460,6 +476,10 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       }
       __syncwarp();
       slot = slot + 1 == C::kStages ? 0 : slot + 1;
+    }
+    if (kEarly && done + 1 < found) {
+      __syncwarp();
+      load_queries(pieces[warp][done_slot + 1 == kAhead ? 0 : done_slot + 1]);
     }
     // ---- join the warps: unnormalised accumulators through shared memory, beside the copies in flight. Row `row` of
     // 8, block i of 8 channels at ((row * blocks + (i ^ row)) * 8: a fragment's rows fall on different banks.
