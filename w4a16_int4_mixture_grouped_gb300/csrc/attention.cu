@@ -11,20 +11,24 @@
 //   * Within a tile each warp owns its own tokens: its own ring of shared-memory stages filled by
 //     its own cp.async, its own maximum, sum and accumulator. No barrier in the loop; the four
 //     warps are joined once per row, in a buffer beside the ring, while the next rows' stages are on their way
-//     (4096 rows of 128 tokens: 495 us against 756 with the ring drained at a row's end).
+//     (4096 rows of 128 tokens: 488 us against 756 with the ring drained at a row's end).
 //   * Two CTAs an SM with 96 KB of stages between them: 24 KB a warp keep HBM busy. Three or four CTAs with shorter
 //     rings are slower (230 to 445 us where two take 194).
-//   * The query heads of a cache head are the 16 rows of m16n8k16 MMAs (rows 8-15 are left out where
-//     the group has at most 8 heads), so a key or value is loaded from shared memory once for all heads.
-//     Warp-level MMA reaches: at full HBM speed its pipe is 19% busy (E4M3: 34%).
+//   * The query heads of a cache head share its keys and values as loaded from shared memory, by warp-level MMA
+//     (m16n8k16; at full HBM speed its pipe is a fifth to a third busy). Groups of up to 8 heads are its 8 columns, tokens
+//     (scores) and channels (output) its 16 rows; larger groups are the 16 rows, 16 heads at a time. With 8 heads in 16
+//     rows, half of them idle, twice the MMAs and registers cost E4M3 much (256 channels 223 us against 173, 128: 183
+//     against 174, 64: 244 against 224) and BF16 a little (128 channels 328 against 324).
 //   * Unseen slots (past the end, before the window, freed pages) are not read: their rows are
 //     zero-filled and their scores are -infinity, so nothing in them reaches the result.
 //   * The probabilities enter the value product as BF16 (E4M3 pages: FP16, keys and values converted
 //     exactly, queries scaled by a power of two per row). Their sum is taken in FP32 before that rounding.
 //
-// 96 sequences of up to 8191 tokens, 8 cache heads x 8 query heads x 128 channels, BF16: 329 us, 6.5 TB/s, 96% of a plain
-// copy. 8 sequences of up to 131072 tokens, E4M3: 197 us, 6.0 TB/s: converting 8-bit elements takes the issue slots that
-// copies would use (64 channels: 4.4 TB/s; 256: 4.8, where registers spill as well).
+// 96 sequences of up to 8191 tokens, 8 cache heads x 8 query heads x 128 channels, BF16: 324 us, 6.6 TB/s, 98% of a plain
+// copy. 8 sequences of up to 131072 tokens, E4M3: 191 us, 6.1 TB/s. What E4M3 still lacks there goes to the conversions
+// of its elements (64 channels: 4.8 TB/s, with as much softmax a token for half the bytes; groups of 16 heads 5.8 TB/s,
+// with 256 channels 4.6, where registers spill). Rows of 128 tokens: 4.4 TB/s BF16, 2.3 E4M3, bound by each row's start
+// and join.
 #include <cuda_runtime.h>
 
 #include "block.h"
@@ -84,14 +88,11 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
   else
     mma_16816(d, a, b0, b1);
 }
-// Rows 0-7 alone: the other rows of A are zero, their results dropped.
-template <bool F16>
-__device__ __forceinline__ void mma_half(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-  float x[4] = {d[0], d[1], 0.f, 0.f};
-  const uint32_t a[4] = {a0, 0u, a2, 0u};
-  mma<F16>(x, a, b0, b1);
-  d[0] = x[0];
-  d[1] = x[1];
+// The transpose of an 8x8 matrix of 16-bit elements, a row's pair of columns a register.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
   uint32_t r;
@@ -118,12 +119,12 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-template <int DP, bool E4M3, bool HALF>
+template <int DP, bool E4M3, bool EIGHT>
 __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p, float* parts, int* counters) {
   using C = Cfg<DP, E4M3>;
-  constexpr int NR = HALF ? 2 : 4;               // accumulator registers of an MMA that are used
-  constexpr int HR = HALF ? 1 : 2;               // head rows of a thread (g, and g + 8)
-  constexpr int NT = C::kTok / 8;
+  constexpr int QR = EIGHT ? 1 : 2;              // query rows of a lane (g, and g + 8)
+  constexpr int ST = EIGHT ? C::kTok / 16 : C::kTok / 8;     // score tiles: 16 tokens x 8 heads, or 16 heads x 8 tokens
+  constexpr int OT = EIGHT ? DP / 16 : DP / 8;               // output tiles: 16 channels x 8 heads, or 16 heads x 8 channels
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Share share;
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
@@ -245,12 +246,12 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   // loses registers in its loop (a long row 196 -> 200 us).
   constexpr int KS = DP / 16;
   constexpr bool kEarly = !E4M3 && DP <= 128;
-  uint2 raw[KS][HR];
+  uint2 raw[KS][QR];
   auto load_queries = [&](const Ahead& pc) {
     const int r = pc.r * lanes + lane_row, head0 = r / chunks * p.group + r % chunks * kRows;
     const int heads = min(kRows, p.group - r % chunks * kRows);
 #pragma unroll
-    for (int hh = 0; hh < HR; ++hh) {
+    for (int hh = 0; hh < QR; ++hh) {
       const int row = g + 8 * hh;
       const uint16_t* src = p.q + int64_t(pc.b) * p.q_stride + int64_t(head0 + row) * p.dim;
 #pragma unroll
@@ -279,18 +280,18 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
     const int n = pc.n, b = pc.b;
 
-    // ---- queries as MMA A fragments
+    // ---- queries as MMA fragments: A (16 rows), or B (8 columns: the same elements as rows 0-7 of A)
     if (!kEarly) load_queries(pc);
-    uint32_t qa[KS][HALF ? 2 : 4];
-    float qscale[HR];
+    uint32_t qa[KS][2 * QR];
+    float qscale[2];
 #pragma unroll
-    for (int hh = 0; hh < HR; ++hh) {
+    for (int hh = 0; hh < QR; ++hh) {
       qscale[hh] = abs_scale;
       if (!E4M3) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          qa[ks][HALF ? 0 : hh] = raw[ks][hh].x ^ negate;
-          qa[ks][HALF ? 1 : 2 + hh] = raw[ks][hh].y ^ negate;
+          qa[ks][hh] = raw[ks][hh].x ^ negate;
+          qa[ks][QR + hh] = raw[ks][hh].y ^ negate;
         }
       } else {
         // scaled into the FP16 range by a power of two
@@ -319,27 +320,37 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           const uint32_t w[2] = {raw[ks][hh].x ^ negate, raw[ks][hh].y ^ negate};
 #pragma unroll
           for (int half = 0; half < 2; ++half)
-            qa[ks][HALF ? half : 2 * half + hh] =
+            qa[ks][QR * half + hh] =
                 pack_f16x2_rn(bf16_to_f32(static_cast<uint16_t>(w[half])) * down * down2,
                               bf16_to_f32(static_cast<uint16_t>(w[half] >> 16)) * down * down2);
         }
       }
     }
 
-    // m: what the exponents are taken against, the maximum seen so far (E4M3: 15 below it, so that FP16
-    // probabilities reach 2^15 and lose nothing down to 2^-39 of the largest)
-    constexpr float kLift = E4M3 ? 15.f : 0.f;
-    float top_of[HR], m[HR], l[HR], o[DP / 8][NR];
+    // statistics of a lane's two heads: g, g + 8, or with heads as columns 2 t, 2 t + 1
+    if (EIGHT && E4M3) {
+      const float of_g = qscale[0];
+      qscale[0] = __shfl_sync(0xffffffffu, of_g, 8 * t);
+      qscale[1] = __shfl_sync(0xffffffffu, of_g, 8 * t + 4);
+    } else if (EIGHT) {
+      qscale[1] = abs_scale;
+    }
+    // m: what the exponents are taken against. 16 heads: the maximum seen so far (E4M3: 15 below it, so that FP16
+    // probabilities reach 2^15 and lose nothing down to 2^-39 of the largest). Up to 8 heads, where a maximum over the
+    // tokens crosses eight lanes: a maximum that only moves when a score passes it by 2^kSlack (E4M3: FP16
+    // probabilities of 2^kLift to 2^15, which lose nothing down to 2^-32 of the largest).
+    constexpr float kLift = !E4M3 ? 0.f : EIGHT ? 8.f : 15.f, kSlack = E4M3 ? 7.f : 8.f;
+    float top_of[2], m[2], l[2], o[OT][4];
 #pragma unroll
-    for (int hh = 0; hh < HR; ++hh) {
+    for (int hh = 0; hh < 2; ++hh) {
       top_of[hh] = -INFINITY;
       m[hh] = -INFINITY;
       l[hh] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
+    for (int i = 0; i < OT; ++i)
 #pragma unroll
-      for (int k = 0; k < NR; ++k) o[i][k] = 0.f;
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 
     for (int i = 0; i < n; ++i) {
       {
@@ -357,119 +368,207 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         if (s == slot) seen = masks[s];
       if (seen != 0) {
         const uint32_t ks0 = ring + slot * C::kStageBytes, vs0 = ks0 + C::kTok * C::kRowBytes;
-        // ---- scores
-        float s[NT][NR];
+        float s[ST][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < ST; ++j)
 #pragma unroll
-          for (int k = 0; k < NR; ++k) s[j][k] = 0.f;
-        if (!E4M3) {
+          for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
+        if constexpr (EIGHT) {
+          // ---- scores, tokens x heads
+          if (!E4M3) {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int j = 0; j < NT; j += 2) {
-              uint32_t b4[4];
-              const int tr = j * 8 + (lane & 7) + ((lane >> 4) << 3), c = ks * 2 + ((lane >> 3) & 1);
-              ldsm_x4(ks0 + 16 * swz<C::kChunks>(tr, c), b4[0], b4[1], b4[2], b4[3]);
-              if constexpr (HALF) {
-                mma_half<false>(s[j], qa[ks][0], qa[ks][1], b4[0], b4[1]);
-                mma_half<false>(s[j + 1], qa[ks][0], qa[ks][1], b4[2], b4[3]);
+              for (int j = 0; j < ST; ++j) {
+                uint32_t a4[4];
+                const int tr = j * 16 + (lane & 15), c = ks * 2 + (lane >> 4);
+                ldsm_x4(ks0 + 16 * swz<C::kChunks>(tr, c), a4[0], a4[1], a4[2], a4[3]);
+                mma<false>(s[j], a4, qa[ks][0], qa[ks][1]);
+              }
+          } else {
+#pragma unroll
+            for (int kb = 0; kb < DP / 64; ++kb)
+#pragma unroll
+              for (int j = 0; j < ST; ++j) {
+                const uint4 x4 = lds128(ks0 + 16 * swz_key8<C::kChunks>(j * 16 + g, kb * 4 + t));
+                const uint4 y4 = lds128(ks0 + 16 * swz_key8<C::kChunks>(j * 16 + 8 + g, kb * 4 + t));
+                const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+                for (int st = 0; st < 4; ++st) {
+                  const uint32_t a4[4] = {e4m3x2_to_f16x2(x[st] & 0xffffu), e4m3x2_to_f16x2(y[st] & 0xffffu),
+                                          e4m3x2_to_f16x2(x[st] >> 16), e4m3x2_to_f16x2(y[st] >> 16)};
+                  mma<true>(s[j], a4, qa[kb * 4 + st][0], qa[kb * 4 + st][1]);
+                }
+              }
+          }
+          // ---- running softmax, exponents in units of log 2: scale s - m
+          if (seen != C::kAll) {
+#pragma unroll
+            for (int j = 0; j < ST; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (!(seen >> (j * 16 + (k >> 1) * 8 + g) & 1u)) s[j][k] = -INFINITY;
+          }
+          bool over = false;                               // (m of -infinity: any seen score)
+#pragma unroll
+          for (int j = 0; j < ST; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) over |= fmaf(s[j][k], qscale[k & 1], -m[k & 1]) > kLift + kSlack;
+          if (__any_sync(0xffffffffu, over)) {
+            float keep[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < ST; ++j) top = fmaxf(top, fmaxf(s[j][e], s[j][2 + e]));
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              const float base = top * qscale[e] - kLift;
+              keep[e] = 1.f;
+              if (base > m[e]) {
+                keep[e] = exp2_fast(m[e] - base);
+                m[e] = base;
+              }
+              l[e] *= keep[e];
+            }
+#pragma unroll
+            for (int i2 = 0; i2 < OT; ++i2)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i2][k] *= keep[k & 1];
+          }
+          const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+          for (int j = 0; j < ST; ++j) {
+            // ---- probabilities as the 16 x 8 operand: its columns are heads, a register two tokens
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              s[j][k] = exp2_fast(fmaf(s[j][k], qscale[k & 1], -base[k & 1]));
+              l[k & 1] += s[j][k];
+            }
+            const uint32_t p0 = transpose8(E4M3 ? pack_f16x2_rn(s[j][0], s[j][1]) : pack_bf16x2_rn(s[j][0], s[j][1]));
+            const uint32_t p1 = transpose8(E4M3 ? pack_f16x2_rn(s[j][2], s[j][3]) : pack_bf16x2_rn(s[j][2], s[j][3]));
+            // ---- values, channels x tokens
+#pragma unroll
+            for (int c = 0; c < C::kChunks; c += 2) {
+              uint32_t v4[4];
+              if (!E4M3) {
+                const int tr = j * 16 + (lane & 7) + ((lane >> 4) << 3), cc = c + ((lane >> 3) & 1);
+                ldsm_x4_t(vs0 + 16 * swz<C::kChunks>(tr, cc), v4[0], v4[1], v4[2], v4[3]);
+                mma<false>(o[c / 2], v4, p0, p1);
               } else {
+                // a 16-bit element is two channels of one token: bytes 0, 2 and 1, 3 pair two tokens' even and odd
+                // channels, rows g and g + 8 of the tile
+                const int tr = j * 16 + (lane & 15), cc = c + (lane >> 4);
+                ldsm_x4_t(vs0 + 16 * swz<C::kChunks>(tr, cc), v4[0], v4[1], v4[2], v4[3]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const uint32_t a4[4] = {e4m3x2_to_f16x2(__byte_perm(v4[2 * q], 0u, 0x4420u)),
+                                          e4m3x2_to_f16x2(__byte_perm(v4[2 * q], 0u, 0x4431u)),
+                                          e4m3x2_to_f16x2(__byte_perm(v4[2 * q + 1], 0u, 0x4420u)),
+                                          e4m3x2_to_f16x2(__byte_perm(v4[2 * q + 1], 0u, 0x4431u))};
+                  mma<true>(o[c + q], a4, p0, p1);
+                }
+              }
+            }
+          }
+        } else {
+          // ---- scores
+          if (!E4M3) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int j = 0; j < ST; j += 2) {
+                uint32_t b4[4];
+                const int tr = j * 8 + (lane & 7) + ((lane >> 4) << 3), c = ks * 2 + ((lane >> 3) & 1);
+                ldsm_x4(ks0 + 16 * swz<C::kChunks>(tr, c), b4[0], b4[1], b4[2], b4[3]);
                 mma<false>(s[j], qa[ks], b4[0], b4[1]);
                 mma<false>(s[j + 1], qa[ks], b4[2], b4[3]);
               }
-            }
-        } else {
+          } else {
 #pragma unroll
-          for (int kb = 0; kb < DP / 64; ++kb)
+            for (int kb = 0; kb < DP / 64; ++kb)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const uint4 w4 = lds128(ks0 + 16 * swz_key8<C::kChunks>(j * 8 + g, kb * 4 + t));
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+              for (int j = 0; j < ST; ++j) {
+                const uint4 w4 = lds128(ks0 + 16 * swz_key8<C::kChunks>(j * 8 + g, kb * 4 + t));
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-              for (int st = 0; st < 4; ++st) {
-                const uint32_t b0 = e4m3x2_to_f16x2(w[st] & 0xffffu), b1 = e4m3x2_to_f16x2(w[st] >> 16);
-                if constexpr (HALF) mma_half<true>(s[j], qa[kb * 4 + st][0], qa[kb * 4 + st][1], b0, b1);
-                else mma<true>(s[j], qa[kb * 4 + st], b0, b1);
+                for (int st = 0; st < 4; ++st) {
+                  const uint32_t b0 = e4m3x2_to_f16x2(w[st] & 0xffffu), b1 = e4m3x2_to_f16x2(w[st] >> 16);
+                  mma<true>(s[j], qa[kb * 4 + st], b0, b1);
+                }
               }
-            }
-        }
-        // ---- running softmax, exponents in units of log 2: scale s - m
-        if (seen != C::kAll) {
+          }
+          // ---- running softmax, exponents in units of log 2: scale s - m
+          if (seen != C::kAll) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < ST; ++j)
 #pragma unroll
-            for (int k = 0; k < NR; ++k)
-              if (!(seen >> (j * 8 + 2 * t + (k & 1)) & 1u)) s[j][k] = -INFINITY;
-        }
-        bool moved = false;
-        float keep[HR];
+              for (int k = 0; k < 4; ++k)
+                if (!(seen >> (j * 8 + 2 * t + (k & 1)) & 1u)) s[j][k] = -INFINITY;
+          }
+          bool moved = false;
+          float keep[2];
 #pragma unroll
-        for (int hh = 0; hh < HR; ++hh) {
-          float top = top_of[hh];
+          for (int hh = 0; hh < 2; ++hh) {
+            float top = top_of[hh];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[j][2 * hh], s[j][2 * hh + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float base = top == -INFINITY ? 0.f : top * qscale[hh] - kLift;
-          keep[hh] = exp2_fast(m[hh] - base);
-          moved |= top != top_of[hh];
-          top_of[hh] = top;
-          m[hh] = top == -INFINITY ? -INFINITY : base;
-          float sum = 0.f;
+            for (int j = 0; j < ST; ++j) top = fmaxf(top, fmaxf(s[j][2 * hh], s[j][2 * hh + 1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float base = top == -INFINITY ? 0.f : top * qscale[hh] - kLift;
+            keep[hh] = exp2_fast(m[hh] - base);
+            moved |= top != top_of[hh];
+            top_of[hh] = top;
+            m[hh] = top == -INFINITY ? -INFINITY : base;
+            float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < ST; ++j)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float e = exp2_fast(fmaf(s[j][2 * hh + k], qscale[hh], -base));
-              s[j][2 * hh + k] = e;
-              sum += e;
-            }
-          l[hh] = l[hh] * keep[hh] + sum;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
+              for (int k = 0; k < 2; ++k) {
+                const float e = exp2_fast(fmaf(s[j][2 * hh + k], qscale[hh], -base));
+                s[j][2 * hh + k] = e;
+                sum += e;
+              }
+            l[hh] = l[hh] * keep[hh] + sum;
+          }
+          if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int i2 = 0; i2 < DP / 8; ++i2)
+            for (int i2 = 0; i2 < OT; ++i2)
 #pragma unroll
-            for (int k = 0; k < NR; ++k) o[i2][k] *= keep[k >> 1];
-        }
-        // ---- values
+              for (int k = 0; k < 4; ++k) o[i2][k] *= keep[k >> 1];
+          }
+          // ---- values
 #pragma unroll
-        for (int kt = 0; kt < NT / 2; ++kt) {
-          uint32_t pa[HALF ? 2 : 4];
+          for (int kt = 0; kt < ST / 2; ++kt) {
+            uint32_t pa[4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int hh = 0; hh < HR; ++hh) {
-              const float lo = s[2 * kt + half][2 * hh], hi = s[2 * kt + half][2 * hh + 1];
-              pa[HALF ? half : 2 * half + hh] = E4M3 ? pack_f16x2_rn(lo, hi) : pack_bf16x2_rn(lo, hi);
-            }
+              for (int hh = 0; hh < 2; ++hh) {
+                const float lo = s[2 * kt + half][2 * hh], hi = s[2 * kt + half][2 * hh + 1];
+                pa[2 * half + hh] = E4M3 ? pack_f16x2_rn(lo, hi) : pack_bf16x2_rn(lo, hi);
+              }
 #pragma unroll
-          for (int c = 0; c < C::kChunks; c += 2) {
-            uint32_t v4[4];
-            const int tr = kt * 16 + (lane & 15), cc = c + (lane >> 4);
-            ldsm_x4_t(vs0 + 16 * swz<C::kChunks>(tr, cc), v4[0], v4[1], v4[2], v4[3]);
-            if (!E4M3) {
-              if constexpr (HALF) {
-                mma_half<false>(o[c], pa[0], pa[1], v4[0], v4[1]);
-                mma_half<false>(o[c + 1], pa[0], pa[1], v4[2], v4[3]);
-              } else {
+            for (int c = 0; c < C::kChunks; c += 2) {
+              uint32_t v4[4];
+              const int tr = kt * 16 + (lane & 15), cc = c + (lane >> 4);
+              ldsm_x4_t(vs0 + 16 * swz<C::kChunks>(tr, cc), v4[0], v4[1], v4[2], v4[3]);
+              if (!E4M3) {
                 mma<false>(o[c], pa, v4[0], v4[1]);
                 mma<false>(o[c + 1], pa, v4[2], v4[3]);
+              } else {
+                // a 16-bit element is two channels of one token: bytes 0, 2 and 1, 3 pair two tokens' even and
+                // odd channels, which become two tiles of eight channels
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                  for (int odd = 0; odd < 2; ++odd) {
+                    const uint32_t sel = odd ? 0x4431u : 0x4420u;
+                    const uint32_t b0 = e4m3x2_to_f16x2(__byte_perm(v4[2 * q], 0u, sel));
+                    const uint32_t b1 = e4m3x2_to_f16x2(__byte_perm(v4[2 * q + 1], 0u, sel));
+                    mma<true>(o[2 * (c + q) + odd], pa, b0, b1);
+                  }
               }
-            } else {
-              // a 16-bit element is two channels of one token: bytes 0, 2 and 1, 3 pair two tokens' even and
-              // odd channels, which become two tiles of eight channels
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                  const uint32_t sel = odd ? 0x4431u : 0x4420u;
-                  const uint32_t b0 = e4m3x2_to_f16x2(__byte_perm(v4[2 * q], 0u, sel));
-                  const uint32_t b1 = e4m3x2_to_f16x2(__byte_perm(v4[2 * q + 1], 0u, sel));
-                  if constexpr (HALF) mma_half<true>(o[2 * (c + q) + odd], pa[0], pa[1], b0, b1);
-                  else mma<true>(o[2 * (c + q) + odd], pa, b0, b1);
-                }
             }
           }
         }
@@ -482,8 +581,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       load_queries(pieces[warp][done_slot + 1 == kAhead ? 0 : done_slot + 1]);
     }
     // ---- join the warps: unnormalised accumulators through shared memory, beside the copies in flight. Row `row` of
-    // 8, block i of 8 channels at ((row * blocks + (i ^ row)) * 8: a fragment's rows fall on different banks.
+    // 8, block i of 8 channels at (row * blocks + at_block(row, i)) * 8: a fragment's rows fall on different banks.
     constexpr int kBlocks = C::kJoinCols / 8;
+    auto at_block = [](int row, int i) { return i ^ (EIGHT ? row >> 1 : row & (kBlocks - 1)); };
     float* buf = reinterpret_cast<float*>(smem + C::kRingBytes);
     // first and last CTA of the row, as blocks of the grid
     const int c0 = cta_of(total, ctas, pc.row0) * lanes + lane_row;
@@ -492,26 +592,46 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * part_floats<DP>();
     const int vecs = p.dim / 4;
 #pragma unroll
-    for (int hh = 0; hh < HR; ++hh) {
+    for (int hh = 0; hh < 2; ++hh) {
       float sum = l[hh];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t == 0) {
-        part_m[warp][g + 8 * hh] = m[hh];
-        part_l[warp][g + 8 * hh] = sum;
+#pragma unroll
+      for (int x = EIGHT ? 4 : 1; x < (EIGHT ? 32 : 4); x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      if (EIGHT ? g == 0 : t == 0) {
+        part_m[warp][EIGHT ? 2 * t + hh : g + 8 * hh] = m[hh];
+        part_l[warp][EIGHT ? 2 * t + hh : g + 8 * hh] = sum;
       }
+    }
+#pragma unroll
+    for (int hh = 0; hh < QR; ++hh) {
 #pragma unroll
       for (int cb = 0; cb < DP / C::kJoinCols; ++cb) {
-        float* dst = buf + (warp * 8 + g) * C::kJoinCols;
+        if constexpr (EIGHT) {
+          // tile i: heads 2 t, 2 t + 1, channels 16 i + g, + 8 (E4M3: 16 i + 2 g, + 1)
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-          const int i = cb * kBlocks + j;
-          if (!E4M3) {
-            *reinterpret_cast<float2*>(dst + (j ^ (g & (kBlocks - 1))) * 8 + 2 * t) = make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
-          } else if ((i & 1) == 0) {
-            // channels 16 (i / 2) + 4 t ..: the half of a pair of blocks that t / 2 names
-            *reinterpret_cast<float4*>(dst + ((j + (t >> 1)) ^ (g & (kBlocks - 1))) * 8 + 4 * (t & 1)) =
-                make_float4(o[i][2 * hh], o[i + 1][2 * hh], o[i][2 * hh + 1], o[i + 1][2 * hh + 1]);
+          for (int j = 0; j < kBlocks; j += 2)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = 2 * t + e, i = (cb * kBlocks + j) / 2;
+              float* dst = buf + (warp * 8 + row) * C::kJoinCols;
+              if (!E4M3) {
+                dst[at_block(row, j) * 8 + g] = o[i][e];
+                dst[at_block(row, j + 1) * 8 + g] = o[i][2 + e];
+              } else {
+                *reinterpret_cast<float2*>(dst + at_block(row, j + (g >> 2)) * 8 + 2 * (g & 3)) = make_float2(o[i][e], o[i][2 + e]);
+              }
+            }
+        } else {
+          float* dst = buf + (warp * 8 + g) * C::kJoinCols;
+#pragma unroll
+          for (int j = 0; j < kBlocks; ++j) {
+            const int i = cb * kBlocks + j;
+            if (!E4M3) {
+              *reinterpret_cast<float2*>(dst + at_block(g, j) * 8 + 2 * t) = make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
+            } else if ((i & 1) == 0) {
+              // channels 16 (i / 2) + 4 t ..: the half of a pair of blocks that t / 2 names
+              *reinterpret_cast<float4*>(dst + at_block(g, j + (t >> 1)) * 8 + 4 * (t & 1)) =
+                  make_float4(o[i][2 * hh], o[i + 1][2 * hh], o[i][2 * hh + 1], o[i + 1][2 * hh + 1]);
+            }
           }
         }
         __syncthreads();
@@ -529,7 +649,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           for (int w = 0; w < kWarps; ++w) {
             const float f = exp2_fast(part_m[w][row] - base);
             const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + row8) * C::kJoinCols +
-                                                              ((dc >> 3) ^ (row8 & (kBlocks - 1))) * 8 + (dc & 7));
+                                                              at_block(row8, dc >> 3) * 8 + (dc & 7));
             sum2 = fmaf(f, part_l[w][row], sum2);
             acc.x = fmaf(f, v.x, acc.x);
             acc.y = fmaf(f, v.y, acc.y);
@@ -616,10 +736,10 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   cp_async_wait<0>();
 }
 
-template <int DP, bool E4M3, bool HALF>
+template <int DP, bool E4M3, bool EIGHT>
 cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   using C = Cfg<DP, E4M3>;
-  const void* fn = reinterpret_cast<const void*>(attention_kernel<DP, E4M3, HALF>);
+  const void* fn = reinterpret_cast<const void*>(attention_kernel<DP, E4M3, EIGHT>);
   static bool attr_set[64] = {false};
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[device]) {
@@ -635,21 +755,15 @@ cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   AttnParams q = p;
   const int rows = p.kv_heads * ((p.group + kRows - 1) / kRows);
   q.lanes = rows <= grid && grid / rows * rows * 20 >= grid * 19 ? rows : 1;
-  attention_kernel<DP, E4M3, HALF><<<grid / q.lanes * q.lanes, kThreads, C::kSmemBytes, stream>>>(q, p.parts, p.counters);
+  attention_kernel<DP, E4M3, EIGHT><<<grid / q.lanes * q.lanes, kThreads, C::kSmemBytes, stream>>>(q, p.parts, p.counters);
   note_launch();
   return cudaGetLastError();
 }
 template <int DP>
 cudaError_t launch_dim(const AttnParams& p, bool e4m3, int device, cudaStream_t stream) {
-  // groups of up to 8 heads leave half of the MMA's rows out and need half the accumulators (with 256 8-bit channels
-  // that form spills registers: 2.6 TB/s against 5.1 of the full one)
-  const bool half = p.group <= 8;
-  if constexpr (DP == 256) {
-    if (e4m3) return launch<DP, true, false>(p, device, stream);
-  } else {
-    if (e4m3) return half ? launch<DP, true, true>(p, device, stream) : launch<DP, true, false>(p, device, stream);
-  }
-  return half ? launch<DP, false, true>(p, device, stream) : launch<DP, false, false>(p, device, stream);
+  const bool eight = p.group <= 8;
+  if (e4m3) return eight ? launch<DP, true, true>(p, device, stream) : launch<DP, true, false>(p, device, stream);
+  return eight ? launch<DP, false, true>(p, device, stream) : launch<DP, false, false>(p, device, stream);
 }
 
 }  // namespace attn
