@@ -141,6 +141,17 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   const int chunks = (p.group + kRows - 1) / kRows;
   // The work rows of a sequence (cache heads x blocks of 16 query heads): `lanes` of them go side by side, CTA
   // lane + lanes * i taking the i-th share of the tokens of row `lane`; the others follow each other on the line.
+  // (Divisions are by far the longest instruction sequences of a short row: shifts or nothing in the usual cases.)
+  const int page_shift = (p.t.page_size & (p.t.page_size - 1)) == 0 ? 31 - __clz(p.t.page_size) : -1;
+  auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / p.t.page_size; };
+  auto head_of = [&](int r, int& block) {              // cache head and block of 16 query heads of work row r
+    if (chunks == 1) {
+      block = 0;
+      return r;
+    }
+    block = r % chunks;
+    return r / chunks;
+  };
   const int lanes = p.lanes, lane_row = blockIdx.x % lanes, rows = p.kv_heads * chunks / lanes;
 
   zero_empty<kThreads>(p, p.dim);
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   // this lane's page in the next stage, read a stage early
   auto next_entry = [&]() {
     const int tok = ahead_tok + (lane & (C::kTok - 1));
-    entry = tok >= ahead_lo && tok < ahead_hi ? ahead_table[tok / p.t.page_size] : -1;
+    entry = tok >= ahead_lo && tok < ahead_hi ? ahead_table[page_of(tok)] : -1;
   };
   int found = 0, found_slot = 0;
   auto next_piece = [&]() {
@@ -172,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     if (lane == 0) pieces[warp][found_slot] = {pc.row0, pc.b, pc.r, pc.tile1 - pc.tile0, pc.ntiles};
     ++found;
     found_slot = found_slot + 1 == kAhead ? 0 : found_slot + 1;
-    const int r = pc.r * lanes + lane_row, kvh = r / chunks, head0 = kvh * p.group + r % chunks * kRows;
+    int block;
+    const int kvh = head_of(pc.r * lanes + lane_row, block), head0 = kvh * p.group + block * kRows;
     ahead_table = p.t.tables + int64_t(pc.seq) * p.t.table_stride;
     ahead_head = int64_t(kvh) * p.head_stride;
     ahead_tok = (pc.lo / C::kTile + pc.tile0) * C::kTile + warp * C::kTok;
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     // its queries to L2 (warp 0: one line a lane; up to 16 heads x 256 channels are two)
     if (warp == 0) {
       const uint8_t* q = reinterpret_cast<const uint8_t*>(p.q + int64_t(pc.b) * p.q_stride + int64_t(head0) * p.dim);
-      const int bytes = min(kRows, p.group - r % chunks * kRows) * p.dim * 2;
+      const int bytes = min(kRows, p.group - block * kRows) * p.dim * 2;
       for (int i = lane * 128; i < bytes; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
     }
   };
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       }
       int64_t off = -1;
       if (entry >= 0)
-        off = int64_t(entry) * p.page_stride + int64_t(tok % p.t.page_size) * p.token_stride + ahead_head;
+        off = int64_t(entry) * p.page_stride + int64_t(tok - page_of(tok) * p.t.page_size) * p.token_stride + ahead_head;
       seen = __ballot_sync(0xffffffffu, off >= 0) & C::kAll;
       if (seen != 0) {
         const uint32_t kd = ring + slot * C::kStageBytes, vd = kd + C::kTok * C::kRowBytes;
@@ -241,15 +253,15 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   };
   // A piece's queries. BF16: (row, k 2t..2t+1) and (row, k 2t+8..2t+9) of each 16-channel step. E4M3: the channels in
   // the order in which a lane reads 8-bit keys: step s of a 64-channel block takes channels 16 t + 4 s .. + 3 of lane t.
-  // BF16 up to 128 channels asks for them while the piece before is being joined (4096 rows of 128 tokens: 540 -> 495 us);
-  // with 256 channels registers are wanting, and E4M3, bound by its conversions, gains nothing (486 us both ways) and
-  // loses registers in its loop (a long row 196 -> 200 us).
+  // Up to 128 channels they are asked for while the piece before is being joined (4096 rows of 128 tokens: BF16 540 ->
+  // 495 us, E4M3 465 -> 430); with 256, and 16 heads of E4M3, registers are wanting (186 us for a long row against 191).
   constexpr int KS = DP / 16;
-  constexpr bool kEarly = !E4M3 && DP <= 128;
+  constexpr bool kEarly = DP <= 128 && (EIGHT || !E4M3);
   uint2 raw[KS][QR];
   auto load_queries = [&](const Ahead& pc) {
-    const int r = pc.r * lanes + lane_row, head0 = r / chunks * p.group + r % chunks * kRows;
-    const int heads = min(kRows, p.group - r % chunks * kRows);
+    int block;
+    const int head0 = head_of(pc.r * lanes + lane_row, block) * p.group + block * kRows;
+    const int heads = min(kRows, p.group - block * kRows);
 #pragma unroll
     for (int hh = 0; hh < QR; ++hh) {
       const int row = g + 8 * hh;
@@ -276,8 +288,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   for (int done = 0, done_slot = 0; done < found; ++done, done_slot = done_slot + 1 == kAhead ? 0 : done_slot + 1) {
     __syncwarp();
     const Ahead& pc = pieces[warp][done_slot];
-    const int r = pc.r * lanes + lane_row, kvh = r / chunks, hc = r % chunks;
-    const int head0 = kvh * p.group + hc * kRows, heads = min(kRows, p.group - hc * kRows);
+    int block;
+    const int head0 = head_of(pc.r * lanes + lane_row, block) * p.group + block * kRows;
+    const int heads = min(kRows, p.group - block * kRows);
     const int n = pc.n, b = pc.b;
 
     // ---- queries as MMA fragments: A (16 rows), or B (8 columns: the same elements as rows 0-7 of A)
@@ -586,9 +599,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
     auto at_block = [](int row, int i) { return i ^ (EIGHT ? row >> 1 : row & (kBlocks - 1)); };
     float* buf = reinterpret_cast<float*>(smem + C::kRingBytes);
     // first and last CTA of the row, as blocks of the grid
-    const int c0 = cta_of(total, ctas, pc.row0) * lanes + lane_row;
-    const int c1 = cta_of(total, ctas, pc.row0 + pc.ntiles - 1) * lanes + lane_row;
-    const bool whole = c0 == c1;
+    const bool whole = n == pc.ntiles;
+    const int c0 = whole ? 0 : cta_of(total, ctas, pc.row0) * lanes + lane_row;
+    const int c1 = whole ? 0 : cta_of(total, ctas, pc.row0 + pc.ntiles - 1) * lanes + lane_row;
     float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * part_floats<DP>();
     const int vecs = p.dim / 4;
 #pragma unroll
@@ -636,9 +649,11 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
         }
         __syncthreads();
         const int here = min(8, heads - 8 * hh);           // rows of this half (may be <= 0)
-        const int cols = min(C::kJoinCols, p.dim - cb * C::kJoinCols) / 4;
-        for (int e = threadIdx.x; e < here * cols; e += kThreads) {
-          const int row8 = e / cols, row = 8 * hh + row8, dc = e % cols * 4, d = cb * C::kJoinCols + dc;
+        constexpr int kVecs = C::kJoinCols / 4;
+#pragma unroll 2
+        for (int e = threadIdx.x; e < 8 * kVecs; e += kThreads) {
+          const int row8 = e / kVecs, row = 8 * hh + row8, dc = e % kVecs * 4, d = cb * C::kJoinCols + dc;
+          if (row8 >= here || d >= p.dim) continue;
           float top = part_m[0][row];
 #pragma unroll
           for (int w = 1; w < kWarps; ++w) top = fmaxf(top, part_m[w][row]);
