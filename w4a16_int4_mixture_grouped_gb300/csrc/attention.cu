@@ -11,7 +11,7 @@
 //   * Within a tile each warp owns its own tokens: its own ring of shared-memory stages filled by
 //     its own cp.async, its own maximum, sum and accumulator. No barrier in the loop; the four
 //     warps are joined once per row, in a buffer beside the ring, while the next rows' stages are on their way
-//     (4096 rows of 128 tokens: 488 us against 756 with the ring drained at a row's end).
+//     (4096 rows of 128 tokens: 481 us against 756 with the ring drained at a row's end).
 //   * Two CTAs an SM with 96 KB of stages between them: 24 KB a warp keep HBM busy. Three or four CTAs with shorter
 //     rings are slower (230 to 445 us where two take 194).
 //   * The query heads of a cache head share its keys and values as loaded from shared memory, by warp-level MMA
@@ -25,10 +25,11 @@
 //     exactly, queries scaled by a power of two per row). Their sum is taken in FP32 before that rounding.
 //
 // 96 sequences of up to 8191 tokens, 8 cache heads x 8 query heads x 128 channels, BF16: 324 us, 6.6 TB/s, 98% of a plain
-// copy. 8 sequences of up to 131072 tokens, E4M3: 191 us, 6.1 TB/s. What E4M3 still lacks there goes to the conversions
-// of its elements (64 channels: 4.8 TB/s, with as much softmax a token for half the bytes; groups of 16 heads 5.8 TB/s,
-// with 256 channels 4.6, where registers spill). Rows of 128 tokens: 4.4 TB/s BF16, 2.3 E4M3, bound by each row's start
-// and join.
+// copy. 8 sequences of up to 131072 tokens, E4M3: 192 us, 6.1 TB/s. What E4M3 still lacks there goes to the conversions
+// of its elements (64 channels: 5.7 TB/s, with as much softmax a token for half the bytes; groups of 16 heads 6.0 TB/s,
+// with 256 channels 4.9, where registers spill). Rows of 128 tokens: 4.5 TB/s BF16, 2.8 E4M3, bound by each row's start
+// and join. Rows of 80 or 96 BF16 channels: 4.9 to 5.7 TB/s; heads' rows that share DRAM bursts are read by CTAs that drift
+// apart.
 #include <cuda_runtime.h>
 
 #include "block.h"
