@@ -199,6 +199,25 @@ def test_scores_far_apart_and_scales():
         check(q, k, v, tables, lens, page, scale=scale)
 
 
+@pytest.mark.parametrize("group", [3, 8, 16])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_scores_that_rise_and_fall(group, e4m3):
+    """Scores that climb by a little from token to token, up to 2^40 of the first probabilities, and come down again:
+    whatever the exponents are taken against has to follow."""
+    rng = np.random.default_rng(31)
+    page, n, dim = 16, 1500, 64
+    tables, total = tables_for(rng, [n, n], page)
+    k, v = make_pages(rng, total, page, 1, dim, e4m3)
+    q = queries(rng, 2, group, dim)
+    steps = np.concatenate([np.linspace(0.0, 1.0, 900), np.linspace(1.0, 0.2, n - 900)])
+    for b in range(2):
+        one = q[b, 0].float() / q[b, 0].float().norm()
+        for j in range(n):
+            k[tables[b, j // page], j % page, 0] = (one * float(steps[j]) * 28.0).to(k.dtype)
+    q[:] = q[:, :1] / q[:, :1].float().norm(dim=-1, keepdim=True).to(torch.bfloat16)
+    check(q, k, v, tables, [n, n], page, scale=1.0)
+
+
 def test_wide_range_of_queries_over_an_8_bit_cache():
     """Queries far above and below the FP16 range: each row is scaled by its own power of two."""
     rng = np.random.default_rng(9)

@@ -15,7 +15,7 @@
 //   * Two CTAs an SM with 96 KB of stages between them: 24 KB a warp keep HBM busy. Three or four CTAs with shorter
 //     rings are slower (230 to 445 us where two take 194).
 //   * The query heads of a cache head share its keys and values as loaded from shared memory, by warp-level MMA
-//     (m16n8k16; at full HBM speed its pipe is a fifth to a third busy). Groups of up to 8 heads are its 8 columns, tokens
+//     (m16n8k16; at full HBM speed its pipe is 10% busy, E4M3 18%). Groups of up to 8 heads are its 8 columns, tokens
 //     (scores) and channels (output) its 16 rows; larger groups are the 16 rows, 16 heads at a time. With 8 heads in 16
 //     rows, half of them idle, twice the MMAs and registers cost E4M3 much (256 channels 223 us against 173, 128: 183
 //     against 174, 64: 244 against 224) and BF16 a little (128 channels 328 against 324).
