@@ -17,6 +17,7 @@ refs int32 [num_pages] how many tables hold a page.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -47,7 +48,11 @@ class Pool(ctypes.Structure):
 
 
 _P, _I, _L, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-_PAGES, _POOL = ctypes.POINTER(Pages), ctypes.POINTER(Pool)
+# The structures of a call go over as their bytes (packing them is half as long as filling a ctypes structure).
+_PAGES = _POOL = ctypes.c_void_p
+_pack_pages = struct.Struct("@PPiiiiqqqff").pack
+_pack_pool = struct.Struct("@Piiqqq").pack
+assert struct.calcsize("@PPiiiiqqqff") == ctypes.sizeof(Pages) and struct.calcsize("@Piiqqq") == ctypes.sizeof(Pool)
 _SIGNATURES = {
     "attention_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
     "paged_attention": [_P, _L, _I, _I, _I, _I, _PAGES, _P, _L, _I, _P, _P, _I, _F, _I, _P, _P, _P, _SZ, _P],
@@ -72,7 +77,7 @@ for _name, _args in _SIGNATURES.items():
 # The current stream's handle without a Stream object around it: a tenth of a decode call's host time otherwise.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = torch.cuda.current_device
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(name: str, index: int, fn, *args) -> None:
@@ -88,7 +93,8 @@ def _run(name: str, index: int, fn, *args) -> None:
 
 def _need(t: torch.Tensor, name: str, dtype, dim: int, index: Optional[int] = None) -> torch.Tensor:
     """A tensor of that type and rank on CUDA device `index` (None: any) whose last dimension is dense."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == dim and t.stride(-1) == 1 and t.get_device() == index:
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == dim and t.get_device() == index
+            and (t.is_contiguous() or t.stride(-1) == 1)):
         return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
@@ -127,22 +133,24 @@ def _table(tables: torch.Tensor, index: int) -> Tuple[int, int, int, int]:
     return tables.data_ptr(), (tables.stride(0) if s > 1 else m), m, s
 
 
-def _pages(k: torch.Tensor, v: Optional[torch.Tensor], index: int, k_scale: float, v_scale: float) -> Pages:
-    _need(k, "k_pages", None, 4 if v is not None else 3, index)
-    kind = _CACHE_DTYPES.get(k.dtype)
+def _pages(k: torch.Tensor, v: Optional[torch.Tensor], index: int, k_scale: float, v_scale: float) -> bytes:
+    """A moe_w4a16_pages of k and v (None: a latent cache)."""
+    dtype = k.dtype if isinstance(k, torch.Tensor) else None
+    _need(k, "k_pages", dtype, 4 if v is not None else 3, index)
+    kind = _CACHE_DTYPES.get(dtype)
     if kind is None:
-        raise TypeError(f"pages have dtype {k.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
+        raise TypeError(f"pages have dtype {dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
     shape, st = k.shape, k.stride()
     if v is None:
-        return Pages(k.data_ptr(), None, kind, shape[0], shape[1], 0, st[0], st[1], shape[2], k_scale, v_scale)
-    _need(v, "v_pages", k.dtype, 4, index)
+        return _pack_pages(k.data_ptr(), 0, kind, shape[0], shape[1], 0, st[0], st[1], shape[2], k_scale, v_scale)
+    _need(v, "v_pages", dtype, 4, index)
     if v.shape != shape or v.stride() != st:
         raise ValueError("k_pages and v_pages must have the same shape and strides")
-    return Pages(k.data_ptr(), v.data_ptr(), kind, shape[0], shape[1], 0, st[0], st[1], st[2], k_scale, v_scale)
+    return _pack_pages(k.data_ptr(), v.data_ptr(), kind, shape[0], shape[1], 0, st[0], st[1], st[2], k_scale, v_scale)
 
 
-def _pool(pool: torch.Tensor) -> Pool:
-    """pool [planes, num_pages, ...], each page dense."""
+def _pool(pool: torch.Tensor) -> Tuple[bytes, int]:
+    """(moe_w4a16_pool, num_pages) of pool [planes, num_pages, ...], each page dense."""
     if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
         raise ValueError("pool must be a CUDA tensor")
     shape, st = pool.shape, pool.stride()
@@ -154,7 +162,7 @@ def _pool(pool: torch.Tensor) -> Pool:
             raise ValueError("pool: each page must be dense")
         dense *= n
     size = pool.element_size()
-    return Pool(pool.data_ptr(), shape[0], shape[1], st[0] * size, st[1] * size, dense * size)
+    return _pack_pool(pool.data_ptr(), shape[0], shape[1], st[0] * size, st[1] * size, dense * size), shape[1]
 
 
 def _ws(ws: torch.Tensor, index: int) -> Tuple[int, int]:
@@ -317,12 +325,12 @@ def cache_fork(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, len
                children: torch.Tensor, page_size: int, ws: torch.Tensor) -> None:
     """Makes each (empty) children[i] a copy of parents[i]: full pages shared, a partly filled last page of pool
     [planes, num_pages, ...] copied in every plane."""
-    p = _pool(pool)
+    p, pages = _pool(pool)
     index = pool.get_device()
     n = parents.size(0)
     ta, ts, mp, ns = _table(tables, index)
     wa, wn = _ws(ws, index)
-    _run("cache_fork", index, _FN["cache_fork"], p, _vector(refs, "refs", p.num_pages, index), ta, ts, mp,
+    _run("cache_fork", index, _FN["cache_fork"], p, _vector(refs, "refs", pages, index), ta, ts, mp,
           _vector(lens, "lens", ns, index), ns, _vector(parents, "parents", n, index),
           _vector(children, "children", n, index), n, page_size, wa, wn)
 
@@ -341,7 +349,7 @@ def cache_free(refs: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, seq
 
 def cache_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor) -> None:
     """pool[:, dst[i]] = pool[:, src[i]]; no destination is a source or another destination."""
-    p = _pool(pool)
+    p, _ = _pool(pool)
     index = pool.get_device()
     n = src.size(0)
     wa, wn = _ws(ws, index)
@@ -353,21 +361,21 @@ def cache_compact(pool: torch.Tensor, refs: torch.Tensor, tables: torch.Tensor, 
     """Moves the pages in use to the front of the pool -> (refs, tables, page_map [num_pages], num_live [1]).
 
     The new counts and tables are new tensors unless refs_out / tables_out (which may be refs / tables) are given."""
-    p = _pool(pool)
+    p, pages = _pool(pool)
     index = pool.get_device()
-    ra = _vector(refs, "refs", p.num_pages, index)
+    ra = _vector(refs, "refs", pages, index)
     ta, ts, mp, ns = _table(tables, index)
     if refs_out is None:
-        refs_out = torch.empty(p.num_pages, dtype=_I32, device=refs.device)
+        refs_out = torch.empty(pages, dtype=_I32, device=refs.device)
     if tables_out is None:
         tables_out = torch.empty_strided(tables.shape, (ts, 1), dtype=_I32, device=refs.device)
     to, tos, _, _ = _table(tables_out, index)
     if tables_out.shape != tables.shape or tos != ts:
         raise ValueError("tables_out must have the shape and strides of tables")
-    page_map = torch.empty(p.num_pages, dtype=_I32, device=refs.device)
+    page_map = torch.empty(pages, dtype=_I32, device=refs.device)
     num_live = torch.empty(1, dtype=_I32, device=refs.device)
     wa, wn = _ws(ws, index)
-    _run("cache_compact", index, _FN["cache_compact"], p, ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", p.num_pages, index),
+    _run("cache_compact", index, _FN["cache_compact"], p, ra, ta, ts, mp, ns, _vector(refs_out, "refs_out", pages, index),
           to, page_map.data_ptr(), num_live.data_ptr(), wa, wn)
     return refs_out, tables_out, page_map, num_live
 
