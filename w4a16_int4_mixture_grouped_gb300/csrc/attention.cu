@@ -156,7 +156,17 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
   const int lanes = p.lanes, lane_row = blockIdx.x % lanes, rows = p.kv_heads * chunks / lanes;
 
   zero_empty<kThreads>(p, p.dim);
-  if (!find_share<kThreads>(p, blockIdx.x / lanes, gridDim.x / lanes, rows, C::kTile, 1, &share)) return;
+  // A part of a split row costs its join about 0.13 us a vector that a thread adds up, a tile 0.8 us, and a split as such
+  // 2.5 us: rows of up to three tiles stay whole, and few rows are cut into about 2.8 sqrt(tiles / vectors) parts, no more.
+  // (One sequence, 8 heads a cache head: 20000 tokens of one cache head 51 -> 20 us against a part for every CTA, 8192
+  // tokens of 8 cache heads 20 -> 17, 100 tokens 8.3 -> 6.0. With 4 or 5.6 in place of 2.8 long rows take 2 to 18% longer.)
+  const int items = (min(kRows, p.group) * p.dim + 511) / 512;
+  const auto ctas_of = [items](int64_t tiles, int longest) -> int64_t {
+    if (longest <= 3) return tiles / max(longest, 1);
+    const int64_t most = static_cast<int64_t>(static_cast<float>(tiles) * 2.8f * rsqrtf(static_cast<float>(longest) * items)) + 1;
+    return tiles <= most ? tiles : (tiles + (tiles + most - 1) / most - 1) / ((tiles + most - 1) / most);
+  };
+  if (!find_share<kThreads>(p, blockIdx.x / lanes, gridDim.x / lanes, rows, C::kTile, ctas_of, &share)) return;
   const int64_t total = share.total;
   const int ctas = share.ctas;
   // a stage's tokens never straddle a page, and every chunk of their rows holds channels
@@ -730,14 +740,25 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           const int row = e / vecs, d = e % vecs * 4;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           const float base = row_top[row] == -INFINITY ? 0.f : row_top[row];
-#pragma unroll 8
-          for (int i = 0; i < np; ++i) {
-            const float f = exp2_fast(__ldcg(part_at(i) + row) - base);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i) + 2 * kRows + row * DP + d));
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
+          // (always kFlight parts in flight: a loop's remainder would wait for each of its parts)
+          constexpr int kFlight = 8;
+          for (int i0 = 0; i0 < np; i0 += kFlight) {
+            float f[kFlight];
+            float4 v[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+              const float* from = part_at(min(i0 + i, np - 1));
+              f[i] = __ldcg(from + row);
+              v[i] = __ldcg(reinterpret_cast<const float4*>(from + 2 * kRows + row * DP + d));
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+              const float w = i0 + i < np ? exp2_fast(f[i] - base) : 0.f;
+              acc.x = fmaf(w, v[i].x, acc.x);
+              acc.y = fmaf(w, v[i].y, acc.y);
+              acc.z = fmaf(w, v[i].z, acc.z);
+              acc.w = fmaf(w, v[i].w, acc.w);
+            }
           }
           const float sum = row_sum[row], inv = sum > 0.f ? p.v_scale / sum : 0.f;
           const int64_t h = int64_t(b) * p.heads + head0 + row;
@@ -765,12 +786,14 @@ cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   }
   int grid = device_info(device).sm_count * (2 * (C::kSmemBytes + 2048) <= 228 * 1024 ? 2 : 1);
   if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
-  // All rows of a sequence side by side where that idles at most one CTA in twenty: the heads of a token lie next to
-  // each other in the usual cache, and read at about the same time they share DRAM pages (a row of one head is
-  // 128 bytes in an E4M3 cache of 128 channels).
+  // As many rows of a sequence side by side as divide them and idle at most one CTA in four: the heads of a token lie
+  // next to each other in the usual cache, and read at about the same time they share DRAM pages. (64 sequences of 4096
+  // tokens against one row after another: 64 heads of 64 E4M3 channels 645 -> 421 us, 56 of 128 578 -> 543, 64 of 128 BF16
+  // channels, where a sixth of the CTAs idles, 1219 -> 1185.)
   AttnParams q = p;
   const int rows = p.kv_heads * ((p.group + kRows - 1) / kRows);
-  q.lanes = rows <= grid && grid / rows * rows * 20 >= grid * 19 ? rows : 1;
+  for (q.lanes = rows < grid ? rows : grid; rows % q.lanes != 0 || grid / q.lanes * q.lanes * 4 < grid * 3; --q.lanes) {
+  }
   attention_kernel<DP, E4M3, EIGHT><<<grid / q.lanes * q.lanes, kThreads, C::kSmemBytes, stream>>>(q, p.parts, p.counters);
   note_launch();
   return cudaGetLastError();

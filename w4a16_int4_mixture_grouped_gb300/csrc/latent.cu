@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
   asm volatile("griddepcontrol.launch_dependents;");
   zero_empty<kThreads>(p, kLatentValue);
   if (threadIdx.x == 0) records[blockIdx.x].np = 0;
-  if (!find_share<kThreads>(p, blockIdx.x, gridDim.x, rows, kTile, kLatentMinTiles, share)) return;
+  const auto min_tiles = [](int64_t tiles, int) { return tiles / kLatentMinTiles; };
+  if (!find_share<kThreads>(p, blockIdx.x, gridDim.x, rows, kTile, min_tiles, share)) return;
   if ((base & 1023u) != 0) {                 // the swizzle is a function of address bits
     if (threadIdx.x == 0) set_error(p.err, MOE_W4A16_ERR_CUDA);
     return;

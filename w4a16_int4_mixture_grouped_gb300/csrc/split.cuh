@@ -26,14 +26,16 @@ struct Share {
   int64_t total, x, x_end, first;
   int ctas, b;
   int sums[16];
+  int longest;
 };
 
-// Fills *sh for CTA `cta` of `grid` (every thread calls it; shares of at least min_tiles tiles where there
-// are fewer than that for every CTA). False: no work for it.
-template <int THREADS>
-__device__ __forceinline__ bool find_share(const AttnParams& p, int cta, int grid, int rows, int tile, int min_tiles,
-                                           Share* sh) {
+// Fills *sh for CTA `cta` of `grid` (every thread calls it). ctas_of(tiles, longest) says into how many shares that many
+// tiles go, of which the longest row has `longest`, where there are fewer than CTAs or than a split is worth.
+// False: no work for it.
+template <int THREADS, typename F>
+__device__ __forceinline__ bool find_share(const AttnParams& p, int cta, int grid, int rows, int tile, F ctas_of, Share* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) sh->longest = 0;
   int64_t line = 0;                                   // tiles of the sequences before the chunk
   for (int pass = 0; pass < 2; ++pass) {
     line = 0;
@@ -51,8 +53,10 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, int gri
         const int y = __shfl_up_sync(0xffffffffu, pre, o);
         if (lane >= o) pre += y;
       }
+      const int most = __reduce_max_sync(0xffffffffu, n);
       __syncthreads();
       if (lane == 31) sh->sums[warp] = pre;
+      if (lane == 0) atomicMax(&sh->longest, most);
       __syncthreads();
       int64_t before = 0, all = 0;
 #pragma unroll
@@ -64,7 +68,7 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, int gri
       line += all * rows;
       if (pass == 0 && b0 + THREADS >= p.batch) {
         if (threadIdx.x == 0) {
-          int64_t ctas = line / min_tiles;
+          int64_t ctas = ctas_of(line, sh->longest);
           ctas = ctas < 1 ? 1 : ctas > grid ? grid : ctas;
           const bool work = line > 0 && cta < ctas;
           sh->total = line;
