@@ -64,6 +64,41 @@ def test_extend(page, pages):
     assert tight or pages > 40
 
 
+@pytest.mark.parametrize("offset", [0, 1])
+def test_free_pages_far_into_a_large_pool(offset):
+    """Free pages here and there behind thousands in use, counts at an address that 16 bytes do not divide; then compacted."""
+    rng = np.random.default_rng(17)
+    page, seqs, pages = 2, 50, 20011
+    lens = [int(x) for x in rng.integers(700, 760, seqs)]
+    refs, tables, ln = state(rng, pages, seqs, 600, lens, page)
+    spare = np.setdiff1d(np.arange(pages), tables[tables >= 0])
+    refs[spare] = 1                                                     # in use by others, all but a few
+    refs[rng.permutation(spare[spare > 9000])[:40]] = 0
+    store = torch.zeros(pages + 4, dtype=torch.int32, device=DEV)
+    dr = store[offset:offset + pages]
+    dr.copy_(torch.from_numpy(refs))
+    dt, dl = dev(tables), dev(ln)
+    ws = M.cache_workspace(pages, seqs)
+    for _ in range(3):
+        ids = rng.permutation(seqs)[:30].astype(np.int32)
+        pos = M.cache_extend(dr, dt, dl, dev(ids), page, ws)
+        want = R.extend(refs, tables, ln, ids, [1] * len(ids), page)
+        assert np.array_equal(pos.cpu().numpy(), want)
+        assert np.array_equal(dr.cpu().numpy(), refs) and np.array_equal(dt.cpu().numpy(), tables)
+    drop = rng.permutation(pages)[:9000]
+    drop = drop[~np.isin(drop, tables[tables >= 0])]
+    refs[drop] = 0
+    dr.copy_(torch.from_numpy(refs))
+    pool = pool_of(rng, 1, pages, 8)
+    dp = on(pool)
+    new_refs, new_tables, page_map, live = M.cache_compact(dp, dr, dt, ws)
+    want_refs, want_tables, want_map, want_live = R.compact(pool, refs, tables)
+    assert int(live.item()) == want_live
+    assert np.array_equal(page_map.cpu().numpy(), want_map) and np.array_equal(new_refs.cpu().numpy(), want_refs)
+    assert np.array_equal(new_tables.cpu().numpy(), want_tables)
+    assert np.array_equal(dp.cpu().numpy(), pool)
+
+
 def test_extend_more_entries_than_a_block_and_bad_ids():
     rng = np.random.default_rng(1)
     page, seqs, pages = 4, 3000, 4000

@@ -68,15 +68,29 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
   return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// Lists the lowest `need` free pages, ascending; returns how many there are (at most `need`).
+// Lists the lowest `need` free pages, ascending; returns how many there are (at most `need`). Eight pages a thread and
+// step (a read and a prefix sum, about 1.5 us): behind 16384 pages in use, growing and freeing 256 sequences takes 7.1 us, behind
+// 131072 19.7 (a page a thread: 13.5 and 73).
 __device__ __forceinline__ int list_free(const int32_t* refs, int num_pages, int need, int32_t* out, int* warp_sums) {
+  constexpr int kEach = 8;
+  const bool wide = (reinterpret_cast<uintptr_t>(refs) & 15u) == 0;
   int found = 0;
-  for (int p0 = 0; p0 < num_pages && found < need; p0 += kPlanThreads) {
-    const int p = p0 + threadIdx.x;
-    const int is_free = p < num_pages && refs[p] <= 0;
+  for (int p0 = 0; p0 < num_pages && found < need; p0 += kPlanThreads * kEach) {
+    const int p = p0 + threadIdx.x * kEach;
+    int r[kEach];
+    if (wide && p + kEach <= num_pages) {
+      const int4 a = reinterpret_cast<const int4*>(refs + p)[0], b = reinterpret_cast<const int4*>(refs + p)[1];
+      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) r[k] = p + k < num_pages ? refs[p + k] : 1;
+    }
+    uint32_t is_free = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) is_free |= (r[k] <= 0 ? 1u : 0u) << k;
     int total;
-    const int at = found + block_prefix(is_free, warp_sums, total);
-    if (is_free && at < need) out[at] = p;
+    int at = found + block_prefix(__popc(is_free), warp_sums, total);
+    for (; is_free != 0 && at < need; is_free &= is_free - 1) out[at++] = p + __ffs(is_free) - 1;
     found += total;
   }
   __syncthreads();
