@@ -33,7 +33,11 @@
  *     decode kernel's unit hand-out counters). Zero it once after allocation
  *     (moe_w4a16_workspace_init); every call leaves its counters at zero, but a
  *     call that recorded a device error may not, so zero it again after one.
- *     Calls that share a workspace must be ordered on one stream.
+ *     Calls that share a workspace must be ordered on one stream. Indexed GEMM
+ *     calls with block_m <= 32 and masked ones keep their counters at one place:
+ *     they may share a workspace whatever their shapes. A GEMM call with
+ *     block_m > 32 or of the contiguous layout keeps other data there, so it
+ *     shares one only with calls like itself (or zero it in between).
  */
 #ifndef MOE_W4A16_H_
 #define MOE_W4A16_H_
@@ -291,8 +295,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_plan(int layout, int num_tokens, int to
  * GEMM reads consecutive rows; for MOE_W4A16_FLAG_COMBINE an arrival counter
  * per (token, 256 output channels, slice) and a bf16 [num_tokens*top_k, n]
  * staging buffer for the routed rows; for calls that may run the decode kernel
- * (indexed block_m <= 32, masked), the FP32 partial tiles and counters of the
- * units it cuts into k-ranges: the last min(units, 304) units of a call with
+ * (indexed block_m <= 32, masked), the counters (behind the header, whatever
+ * the shape) and FP32 partial tiles of the units it cuts into k-ranges: the last min(units, 304) units of a call with
  * at most 2048 (row block, 256-channel) units (304 units x 4 parts: 19.9 MB for
  * block_m <= 16, 39.9 MB for 32-row blocks and masked calls); with
  * MOE_W4A16_FLAG_SPLIT also the table of the tcgen05 kernel's blocks (int4

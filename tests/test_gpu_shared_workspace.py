@@ -1,0 +1,44 @@
+"""One workspace for calls of different shapes and kinds, one after the other on a stream."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from gpu_util import (assert_close, bits_to_dev, dev_to_bits, distinct_topk, i32_to_dev, prepare_dev, random_acts,
+                      random_weights)
+
+pytestmark = pytest.mark.gpu
+
+M = pytest.importorskip("w4a16_int4_mixture_grouped_gb300") if torch.cuda.is_available() else None
+DEV = torch.device("cuda", 0) if torch.cuda.is_available() else None
+
+
+def test_gemm_calls_whose_regions_differ():
+    """A combining call stages its routed rows where a plain call of a workspace of its own size has other things; both
+    cut their last units into parts that a counter joins."""
+    rng = np.random.default_rng(1900)
+    e, kd, n, bm = 16, 256, 2048, 16
+    qw, sc = random_weights(rng, e, n, kd)
+    pw = prepare_dev(qw, sc, 1, DEV)
+    flags = M.FLAG_COMBINE | M.FLAG_A_PER_ROW
+    t1, k1 = 1000, 8
+    ws = M.workspace(M.LAYOUT_INDEXED, t1, k1, e, n, kd, bm, flags, DEV)
+    assert ws.numel() > M.workspace_size(M.LAYOUT_INDEXED, 24, 2, e, n, kd, bm, 0)
+    ids1 = distinct_topk(rng, t1, e, k1)
+    a1 = bits_to_dev(random_acts(rng, t1 * k1, kd), DEV)
+    w1 = torch.from_numpy(rng.uniform(0, 1, size=(t1, k1)).astype(np.float32)).to(DEV)
+    ids2 = distinct_topk(rng, 24, e, 2)
+    a2 = random_acts(rng, 24, kd)
+    want = O.indexed_gemm(a2, ids2, lambda x: (qw[x], sc[x]), n)
+    first = None
+    for _ in range(2):
+        s_ids, e_ids, npp, _ = M.align(i32_to_dev(ids1, DEV), e, bm, ws)
+        big = M.indexed(a1, pw, s_ids, e_ids, npp, t1, k1, bm, ws, flags=flags, topk_weights=w1)
+        s_ids, e_ids, npp, _ = M.align(i32_to_dev(ids2, DEV), e, bm, ws)
+        out = torch.full((48, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+        M.indexed(bits_to_dev(a2, DEV), pw, s_ids, e_ids, npp, 24, 2, bm, ws, out=out)
+        assert M.get_device_error(ws) == 0
+        assert_close(dev_to_bits(out), want, "a small call after a large one")
+        first = big if first is None else first
+        assert torch.equal(big, first)

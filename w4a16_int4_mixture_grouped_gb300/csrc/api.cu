@@ -192,8 +192,10 @@ moe_w4a16_status moe_w4a16_align_size(int num_tokens, int top_k, int num_experts
   return MOE_W4A16_OK;
 }
 
-// Workspace of a GEMM call: [header 256 B][gathered activations][combine counters][combine staging]
-// [contiguous: merged row-block table].
+// Workspace of a GEMM call: [header 256 B][cut units' arrival counters][gathered activations][combine counters]
+// [combine staging][contiguous: merged row-block table][cut units' partial tiles][indexed split: tables].
+// The cut units' counters have to be zero between calls, so they lie where no call that has them puts anything
+// else, whatever its shape: such calls may share a workspace. (The combine counters are zeroed by each call.)
 // Header: int32 0 = device error word; int32 16, 17 = the decode kernel's unit hand-out counters.
 constexpr int kGrabWord = 16;
 struct WsLayout {
@@ -227,6 +229,11 @@ static moe_w4a16_status ws_layout(int layout, int num_tokens, int top_k, int num
     return MOE_W4A16_ERR_INVALID_ARG;
   if (layout < MOE_W4A16_LAYOUT_INDEXED || layout > MOE_W4A16_LAYOUT_MASKED) return MOE_W4A16_ERR_INVALID_ARG;
   size_t off = MOE_W4A16_WS_HEADER_BYTES;
+  const int rows = cut_rows(layout, block_m);
+  if (rows != 0) {
+    L->cutc_off = off;
+    off += align_up(kCutCounterBytes, 256);
+  }
   if (gathers_activations(layout, block_m, flags)) {
     size_t ms, mb;
     moe_w4a16_status st = moe_w4a16_align_size(num_tokens, top_k, num_experts, block_m, &ms, &mb);
@@ -254,12 +261,10 @@ static moe_w4a16_status ws_layout(int layout, int num_tokens, int top_k, int num
     L->cb_off = off;
     off += align_up((static_cast<size_t>(L->cb_segs) + 1) * 16, 256);
   }
-  if (const int rows = cut_rows(layout, block_m)) {
+  if (rows != 0) {
     L->cut_off = off;
     L->cut_bytes = cut_partial_bytes(rows);
     off += L->cut_bytes;
-    L->cutc_off = off;
-    off += align_up(kCutCounterBytes, 256);
   }
   if (layout == MOE_W4A16_LAYOUT_INDEXED && (flags & MOE_W4A16_FLAG_SPLIT)) {
     const int64_t cap = split_table_cap(static_cast<int64_t>(num_tokens) * top_k);
