@@ -474,7 +474,10 @@ typedef struct moe_w4a16_pages {
   float k_scale, v_scale; /* E4M3: an element stands for element * scale; BF16: 1 */
 } moe_w4a16_pages;
 
-/* Workspace bytes of the two attention calls for num_heads query heads over
+/* The attention, cache_* and page calls may share a workspace of the largest of their sizes (ordered on one stream), but
+ * not with a GEMM call, which keeps data where the attention calls' counters have to be zero, and the other way round.
+ *
+ * Workspace bytes of the two attention calls for num_heads query heads over
  * num_kv_heads cache heads of head_dim channels (latent: 1 head of
  * MOE_W4A16_LATENT_DIM). Independent of batch and lengths. Zero it once
  * (moe_w4a16_workspace_init); every call leaves its counters at zero. */

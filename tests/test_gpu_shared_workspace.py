@@ -42,3 +42,50 @@ def test_gemm_calls_whose_regions_differ():
         assert_close(dev_to_bits(out), want, "a small call after a large one")
         first = big if first is None else first
         assert torch.equal(big, first)
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+def test_page_calls_and_attention_on_one_workspace():
+    """Grouped attention joins its split rows by counters in the workspace; the page calls keep lists there, the latent
+    form its parts."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    page, pages, seqs, width, heads, dim = 16, 2048, 128, 600, 8, 64
+    pool = torch.randn((2, pages, page, 1, dim), generator=g, device=DEV).to(torch.bfloat16)
+    latent = torch.randn((pages, page, 576), generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.randn((2, heads, dim), generator=g, device=DEV).to(torch.bfloat16)
+    ql = torch.randn((2, heads, 576), generator=g, device=DEV).to(torch.bfloat16)
+    long = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)[:2 * width].view(2, width).contiguous()
+    lens = i32([width * page, width * page - 37])
+
+    def grouped(ws):
+        return M.paged_attention(q, pool[0], pool[1], long, lens, ws)
+
+    def one_latent(ws):
+        return M.latent_attention(ql, latent, long, lens, ws, 0.05)
+
+    def page_calls(ws):
+        refs = torch.zeros(pages, dtype=torch.int32, device=DEV)
+        tables = torch.full((2 * seqs, 8), -1, dtype=torch.int32, device=DEV)
+        n = torch.zeros(2 * seqs, dtype=torch.int32, device=DEV)
+        first, second = torch.arange(seqs, dtype=torch.int32, device=DEV), torch.arange(seqs, 2 * seqs, dtype=torch.int32, device=DEV)
+        work = pool.clone()
+        pos = M.cache_extend(refs, tables, n, first, page, ws, counts=torch.full_like(first, 70))
+        M.cache_append(q[:1, :1], work[0], tables, first[:1], pos[:1], ws, v=q[1:, :1], v_pages=work[1])
+        M.cache_fork(work, refs, tables, n, first, second, page, ws)
+        M.cache_free(refs, tables, n, first[::3].contiguous(), page, ws)
+        moved = M.cache_compact(work, refs, tables, ws)
+        return (pos, work, refs, tables, n) + moved
+
+    calls = [grouped, one_latent, page_calls]
+    own = [M.attention_workspace(2, heads, 1, dim), M.attention_workspace(2, heads, 1, 576), M.cache_workspace(pages, seqs)]
+    want = [call(ws) for call, ws in zip(calls, own)]
+    assert [M.get_device_error(ws) for ws in own] == [0, 0, 0]
+    ws = torch.zeros(max(x.numel() for x in own), dtype=torch.uint8, device=DEV)
+    for order in ((2, 0, 1, 0), (1, 0, 2, 0), (2, 1, 2, 0, 0)):
+        for i in order:
+            for got, ref in zip(calls[i](ws), want[i]):
+                assert torch.equal(got, ref)
+    assert M.get_device_error(ws) == 0

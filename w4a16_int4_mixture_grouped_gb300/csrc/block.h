@@ -46,6 +46,10 @@ struct AttnParams {
 };
 // CTAs of an attention launch: two on each of the GPU's 152 SMs.
 constexpr int kAttnMaxCtas = 304;
+// Arrival counters of grouped attention, behind the 256-byte header of the workspace. They have to be zero between calls,
+// so no other call on cache or attention puts anything there: all of them may share a workspace.
+constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int) + 255) / 256 * 256;
+constexpr size_t kBlockWsOffset = MOE_W4A16_WS_HEADER_BYTES + kAttnCounterBytes;   // what a call need not leave at zero
 constexpr int kLatentMaxCtas = 152;    // the latent kernel: one
 constexpr int kLatentMinTiles = 2;     // tiles a CTA of the latent kernel takes at least: a part costs as much as a tile
 size_t attention_part_bytes(int heads, int kv_heads, int dim);
@@ -91,7 +95,7 @@ struct PoolView {
   int planes, num_pages;
   int64_t plane_stride, page_stride, page_bytes;
 };
-// Workspace of the page calls after the 256-byte header, in int32 words: [0] number of copies, then
+// Workspace of the page calls from kBlockWsOffset on, in int32 words: [0] number of copies, then
 // per entry {source, destination} of a copy, {pages of its table row, granted}, then one word per page.
 constexpr size_t kCacheWsPairs = 16;
 inline size_t cache_ws_words(int num_pages, int count) {

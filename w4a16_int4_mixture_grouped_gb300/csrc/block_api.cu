@@ -17,9 +17,6 @@ using namespace moe;
 
 namespace {
 
-// Arrival counters of the attention workspace, padded to 256 bytes.
-constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int) + 255) / 256 * 256;
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool ws_fits(const void* ws, size_t bytes, size_t need) {
@@ -88,7 +85,7 @@ moe_w4a16_status page_ops(int32_t* refs, int num_pages, int32_t* tables, int64_t
   o->lens = lens;
   o->refs = refs;
   o->count = count;
-  o->scratch = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + MOE_W4A16_WS_HEADER_BYTES);
+  o->scratch = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kBlockWsOffset);
   o->entries = count > num_pages ? count : num_pages;
   o->err = static_cast<int*>(ws);
   return MOE_W4A16_OK;
@@ -124,7 +121,7 @@ moe_w4a16_status attention_call(AttnParams& p, const moe_w4a16_pages* cache, con
   p.v_scale = cache->v_scale;
   p.err = static_cast<int*>(ws);
   p.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + MOE_W4A16_WS_HEADER_BYTES);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_W4A16_WS_HEADER_BYTES + kAttnCounterBytes);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kBlockWsOffset);
   int device = 0;
   MOE_CUDA_TRY(cudaGetDevice(&device));
   MOE_CUDA_TRY(latent ? launch_latent_attention(p, device, stream) : launch_attention(p, cache->dtype, device, stream));
@@ -142,8 +139,7 @@ moe_w4a16_status moe_w4a16_attention_workspace_size(int num_heads, int num_kv_he
   if (head_dim < 16 || head_dim % 16 != 0 || (!latent && head_dim > MOE_W4A16_MAX_HEAD_DIM))
     return MOE_W4A16_ERR_UNSUPPORTED;
   // header | arrival counters | parts of split rows
-  *bytes = MOE_W4A16_WS_HEADER_BYTES + kAttnCounterBytes +
-           (latent ? latent_part_bytes(num_heads) : attention_part_bytes(num_heads, num_kv_heads, head_dim));
+  *bytes = kBlockWsOffset + (latent ? latent_part_bytes(num_heads) : attention_part_bytes(num_heads, num_kv_heads, head_dim));
   return MOE_W4A16_OK;
 }
 
@@ -236,7 +232,8 @@ moe_w4a16_status moe_w4a16_cache_append(const uint16_t* k, int64_t k_stride, con
 moe_w4a16_status moe_w4a16_cache_workspace_size(int num_pages, int count, size_t* bytes) {
   if (bytes == nullptr || num_pages < 0 || count < 0 || count > (1 << 28) || num_pages > (1 << 28))
     return MOE_W4A16_ERR_INVALID_ARG;
-  *bytes = MOE_W4A16_WS_HEADER_BYTES + cache_ws_words(num_pages, count) * sizeof(int32_t);
+  // header | the attention calls' counters, left alone | scratch
+  *bytes = kBlockWsOffset + cache_ws_words(num_pages, count) * sizeof(int32_t);
   return MOE_W4A16_OK;
 }
 
