@@ -37,7 +37,9 @@
  *     calls with block_m <= 32 and masked ones keep their counters at one place:
  *     they may share a workspace whatever their shapes. A GEMM call with
  *     block_m > 32 or of the contiguous layout keeps other data there, so it
- *     shares one only with calls like itself (or zero it in between).
+ *     shares one only with calls like itself (or zero it in between). A call
+ *     that finds a counter which cannot be right records
+ *     MOE_W4A16_ERR_WORKSPACE; part of its output may then not be written.
  */
 #ifndef MOE_W4A16_H_
 #define MOE_W4A16_H_
@@ -62,7 +64,7 @@ typedef enum moe_w4a16_status {
   MOE_W4A16_ERR_INVALID_ARG = 1,    /* null pointer, bad size, inconsistent flags */
   MOE_W4A16_ERR_UNSUPPORTED = 2,    /* quantisation scheme or shape outside what the kernels handle */
   MOE_W4A16_ERR_MODE_MISMATCH = 3,  /* prepared weight's recorded mode/version does not fit the call */
-  MOE_W4A16_ERR_WORKSPACE = 4,      /* workspace missing or too small */
+  MOE_W4A16_ERR_WORKSPACE = 4,      /* workspace missing or too small; device: its counters were not left at zero */
   MOE_W4A16_ERR_CAPACITY = 5,       /* device: an expert holds more rows than the masked budget */
   MOE_W4A16_ERR_DEVICE_TIMEOUT = 6, /* device: a pipeline wait gave up */
   MOE_W4A16_ERR_CUDA = 7,           /* a CUDA runtime call failed */

@@ -89,3 +89,34 @@ def test_page_calls_and_attention_on_one_workspace():
             for got, ref in zip(calls[i](ws), want[i]):
                 assert torch.equal(got, ref)
     assert M.get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("fill", [0x3F, 0xFF])
+def test_counters_that_other_data_lies_on_are_recorded(fill):
+    """A workspace that a call of another kind has used: reported, and right again once it is zeroed."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k = torch.randn((200, 16, 1, 64), generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.randn((1, 8, 64), generator=g, device=DEV).to(torch.bfloat16)
+    table, lens = torch.arange(200, dtype=torch.int32, device=DEV)[None], i32([3200])
+    ws = M.attention_workspace(1, 8, 1, 64)
+    want = M.paged_attention(q, k, k, table, lens, ws)
+    ws[M.WS_HEADER_BYTES:] = fill
+    M.paged_attention(q, k, k, table, lens, ws)
+    assert M.get_device_error(ws) == 4
+    M.workspace_init(ws)
+    got = M.paged_attention(q, k, k, table, lens, ws)
+    assert M.get_device_error(ws) == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    rng = np.random.default_rng(3)
+    e, t, kd, n = 4, 16, 256, 512
+    qw, sc = random_weights(rng, e, n, kd)
+    pw, a = prepare_dev(qw, sc, 1, DEV), bits_to_dev(random_acts(rng, t, kd), DEV)
+    ws = M.workspace(M.LAYOUT_INDEXED, t, 2, e, n, kd, 16, 0, DEV)
+    s_ids, e_ids, npp, _ = M.align(i32_to_dev(distinct_topk(rng, t, e, 2), DEV), e, 16, ws)
+    want = M.indexed(a, pw, s_ids, e_ids, npp, t, 2, 16, ws)
+    assert M.get_device_error(ws) == 0
+    ws[M.WS_HEADER_BYTES:] = fill
+    M.indexed(a, pw, s_ids, e_ids, npp, t, 2, 16, ws)
+    assert M.get_device_error(ws) == 4
+    M.workspace_init(ws)
+    assert torch.equal(M.indexed(a, pw, s_ids, e_ids, npp, t, 2, 16, ws), want) and M.get_device_error(ws) == 0

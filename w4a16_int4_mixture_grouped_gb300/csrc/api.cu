@@ -102,7 +102,7 @@ const char* moe_w4a16_status_string(moe_w4a16_status s) {
     case MOE_W4A16_ERR_INVALID_ARG: return "invalid argument";
     case MOE_W4A16_ERR_UNSUPPORTED: return "unsupported quantisation scheme or shape";
     case MOE_W4A16_ERR_MODE_MISMATCH: return "prepared weight mode/version does not fit this call";
-    case MOE_W4A16_ERR_WORKSPACE: return "workspace missing or too small";
+    case MOE_W4A16_ERR_WORKSPACE: return "workspace missing or too small, or (device) its counters not left at zero";
     case MOE_W4A16_ERR_CAPACITY: return "an expert exceeds the masked row budget";
     case MOE_W4A16_ERR_DEVICE_TIMEOUT: return "a device pipeline wait timed out";
     case MOE_W4A16_ERR_CUDA: return "CUDA runtime error";

@@ -707,8 +707,10 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        const bool last = atomicAdd(counters + c0, 1) == (c1 - c0) / lanes;
+        const int before = atomicAdd(counters + c0, 1), others = (c1 - c0) / lanes;
+        const bool last = before == others;
         if (last) counters[c0] = 0;
+        if (before < 0 || before > others) set_error(p.err, MOE_W4A16_ERR_WORKSPACE);   // not a zeroed workspace's
         last_flag = last;
       }
       __syncthreads();

@@ -229,7 +229,11 @@ __device__ __forceinline__ bool part_fixup(const GemmParams& p, int su, int part
   __threadfence();
   __syncwarp();
   int last = 0;
-  if (lane == 0) last = atomicAdd(p.sk_counters + su * kConsumerWarps + warp, 1) == parts - 1;
+  if (lane == 0) {
+    const int before = atomicAdd(p.sk_counters + su * kConsumerWarps + warp, 1);
+    last = before == parts - 1;
+    if (before < 0 || before >= parts) set_error(p.err, MOE_W4A16_ERR_WORKSPACE);   // not a zeroed workspace's
+  }
   last = __shfl_sync(0xffffffffu, last, 0);
   if (!last) return false;
   __threadfence();
