@@ -316,13 +316,13 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_workspace_init(void* ws, size_t ws_byte
 MOE_W4A16_API moe_w4a16_status moe_w4a16_get_device_error(const void* ws, moe_w4a16_stream_t stream, int32_t* code);
 
 /* Diagnostics and tests: sets, for the current device, the limit after which a
- * GEMM kernel's pipeline wait gives up (default MOE_W4A16_WAIT_LIMIT_NS, about
+ * pipeline wait of a GEMM or the latent attention kernel gives up (default MOE_W4A16_WAIT_LIMIT_NS, about
  * two seconds; larger values are INVALID_ARG). A wait that runs out records
  * MOE_W4A16_ERR_DEVICE_TIMEOUT in the workspace error word; the kernel then
  * stops its CTA's pipeline, lets copies already in flight land (those drains
  * keep the default limit), releases its tensor memory and returns. Below 20 us
  * the waits poll without suspending, so with a limit of 0 the first wait for
- * data that has not arrived yet gives up at once. Applies to the GEMM calls
+ * data that has not arrived yet gives up at once. Applies to the calls
  * made after it on that device, from any thread, until set again. Recover from
  * the error with moe_w4a16_workspace_init on the workspace (counters may be
  * left non-zero). */

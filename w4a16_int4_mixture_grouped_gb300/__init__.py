@@ -264,7 +264,7 @@ WAIT_LIMIT_NS = 2_000_000_000   # default limit of a device pipeline wait
 
 
 def set_wait_limit_ns(ns: int, device=None) -> None:
-    """Diagnostics and tests: the limit after which a GEMM kernel's pipeline wait gives up, on `device`
+    """Diagnostics and tests: the limit after which a pipeline wait of a GEMM or the latent attention kernel gives up, on `device`
     (default WAIT_LIMIT_NS; 0 makes the first wait for data not yet arrived give up at once)."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):

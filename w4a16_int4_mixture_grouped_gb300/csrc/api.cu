@@ -17,7 +17,7 @@ namespace moe {
 
 static std::atomic<uint64_t> g_launches{0};
 
-// Wait limit of the GEMM launches per device (moe_w4a16_set_wait_limit_ns).
+// Wait limit of the GEMM and latent attention launches per device (moe_w4a16_set_wait_limit_ns).
 constexpr int kMaxWaitDevices = 64;
 static std::atomic<uint64_t> g_wait_ns[kMaxWaitDevices] = {};
 static std::atomic<bool> g_wait_set{false};

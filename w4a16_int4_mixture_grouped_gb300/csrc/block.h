@@ -41,6 +41,7 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   int* err;
+  uint64_t wait_ns;                    // latent form: limit of a pipeline wait
   int* counters;                       // [kAttnMaxCtas] arrivals of split rows' parts, zero between calls
   float* parts;                        // FP32 parts of split rows, two to a CTA
 };

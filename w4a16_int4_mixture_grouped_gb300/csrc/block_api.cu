@@ -124,6 +124,7 @@ moe_w4a16_status attention_call(AttnParams& p, const moe_w4a16_pages* cache, con
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kBlockWsOffset);
   int device = 0;
   MOE_CUDA_TRY(cudaGetDevice(&device));
+  p.wait_ns = wait_limit_ns(device);
   MOE_CUDA_TRY(latent ? launch_latent_attention(p, device, stream) : launch_attention(p, cache->dtype, device, stream));
   return MOE_W4A16_OK;
 }

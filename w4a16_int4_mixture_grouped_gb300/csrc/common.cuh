@@ -58,7 +58,7 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 }
 
 // Upper bound of any single pipeline wait, unless the host lowered it for a launch
-// (GemmParams::wait_ns; diagnostics and tests through moe_w4a16_set_wait_limit_ns). A wait
+// (GemmParams::wait_ns, AttnParams::wait_ns; diagnostics and tests through moe_w4a16_set_wait_limit_ns). A wait
 // that runs out records MOE_W4A16_ERR_DEVICE_TIMEOUT, raises the CTA's abort flag and returns
 // false. The drains of copies still in flight after an abort always use kWaitLimitNs.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

@@ -160,6 +160,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // Work rows of a sequence: blocks of up to 64 heads.
 __device__ __forceinline__ int head_blocks(int heads) { return (heads + kHeads - 1) / kHeads; }
 
+// DIAG: the diagnostic instantiation, whose waits take the launch's own limit (moe_w4a16_set_wait_limit_ns).
+template <bool DIAG>
 __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p, Record* records) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
   PieceWalk walk;
   walk.start(p, share);
   Piece pc;
-  auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.err, kWaitLimitNs); };
+  auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.err, DIAG ? p.wait_ns : kWaitLimitNs); };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax, rescale, epilogue
@@ -721,22 +723,28 @@ size_t latent_part_bytes(int) {
   return kLatentMaxCtas * sizeof(Record) + size_t(kLatentMaxCtas) * 2 * kPartFloats * sizeof(float);
 }
 
-cudaError_t launch_latent_attention(const AttnParams& p0, int device, cudaStream_t stream) {
+template <bool DIAG>
+static cudaError_t launch(const AttnParams& p, Record* records, int grid, int device, cudaStream_t stream) {
   static bool attr_set[64] = {false};
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[device]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        cudaFuncSetAttribute(latent_kernel<DIAG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set[device] = true;
   }
+  latent_kernel<DIAG><<<grid, kThreads, kSmemBytes, stream>>>(p, records);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_latent_attention(const AttnParams& p0, int device, cudaStream_t stream) {
   AttnParams p = p0;
   Record* records = reinterpret_cast<Record*>(p.parts);
   p.parts = reinterpret_cast<float*>(records + kLatentMaxCtas);
   int grid = device_info(device).sm_count;
   if (grid > kLatentMaxCtas) grid = kLatentMaxCtas;
-  latent_kernel<<<grid, kThreads, kSmemBytes, stream>>>(p, records);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = p.wait_ns == kWaitLimitNs ? launch<false>(p, records, grid, device, stream)
+                                            : launch<true>(p, records, grid, device, stream);
   if (e != cudaSuccess) return e;
   // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
   cudaLaunchConfig_t cfg{};
