@@ -190,3 +190,23 @@ def test_refusals():
     assert status(lambda: M.block_norm(x, h, w_pre=w, eps=-1.0)) == "ERR_INVALID_ARG"
     big = torch.zeros((1, 32769), dtype=torch.bfloat16, device=DEV)
     assert status(lambda: M.block_norm(big, big)) == "ERR_UNSUPPORTED"
+
+
+@pytest.mark.parametrize("n", [1024, 1021, 509, 3, 8185, 12289])
+@pytest.mark.parametrize("rows", [5, 701])
+@pytest.mark.parametrize("where", ["w_post", "gate"])
+def test_an_infinite_factor_of_an_edge_column(n, rows, where):
+    """h' is infinite in that column alone, so its norm makes every other column of y zero: what lies past a row's ends
+    takes no part, whatever the edge column's factor is."""
+    rng = np.random.default_rng(n)
+    x, h = bf16(rng, rows, n), bf16(rng, rows, n)
+    f = {k: bf16(rng, n, scale=0.1, shift=1.0) for k in ("w_post", "gate", "w_pre")}
+    for at in (0, n - 1):
+        x[:, at] = 1.0
+        plain, _ = M.block_norm(x, h, **f)
+        bad = {k: v.clone() for k, v in f.items()}
+        bad[where][at] = float("inf")
+        got, y = M.block_norm(x, h, **bad)
+        keep = [c for c in range(n) if c != at]
+        assert torch.equal(got[:, keep], plain[:, keep]) and torch.isinf(got[:, at]).all()
+        assert (y[:, keep] == 0).all() and torch.isnan(y[:, at]).all()

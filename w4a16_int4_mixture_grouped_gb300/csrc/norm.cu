@@ -134,11 +134,12 @@ __device__ __forceinline__ Pack<8> load_edge(const float* row, int c, int n) {
   for (int i = 0; i < 8; ++i) r.v[i] = c + i >= 0 && c + i < n ? row[c + i] : 0.f;
   return r;
 }
-// Eight columns of a weight row at any alignment.
+// Eight columns of a weight row at any alignment; zero outside the row (an edge column's factor, infinite perhaps, must
+// not reach the zeros beside it: their product enters the row's sum).
 __device__ __forceinline__ Pack<8> load_any(const uint16_t* row, int c, int n) {
   Pack<8> r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = bf16_to_f32(__ldg(row + min(max(c + i, 0), n - 1)));
+  for (int i = 0; i < 8; ++i) r.v[i] = c + i >= 0 && c + i < n ? bf16_to_f32(__ldg(row + c + i)) : 0.f;
   return r;
 }
 
