@@ -493,8 +493,10 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_attention_workspace_size(int num_heads,
  *   out = v_scale * sum_j exp(s[j] - m) V_j / l,  lse = m + ln l,  m = max s, l = sum_j exp(s[j] - m);
  *   nothing seen: out = 0, lse = -infinity.
  * Scores, maxima, sums and outputs are FP32 (the products take the probabilities
- * rounded to BF16, or to FP16 over E4M3 pages); the output is rounded once. What lies
- * in unseen slots, NaN included, does not reach the result.
+ * rounded to BF16, or to FP16 over E4M3 pages); the output is rounded once. Over E4M3
+ * pages the queries of a head are taken into FP16 by a power of two: exact, but for
+ * channels below 2^-32 of the head's largest, which lose bits and below 2^-40 count as
+ * zero. What lies in unseen slots, NaN included, does not reach the result.
  *   q    bf16 [batch, num_heads, head_dim], q_stride elements between sequences; 16-byte aligned
  *   head_dim  a multiple of 16, at most MOE_W4A16_MAX_HEAD_DIM (else UNSUPPORTED)
  *   seq_ids  int32 [batch]: the row of tables and lens of each query (NULL: query b reads row b)

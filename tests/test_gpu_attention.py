@@ -233,6 +233,23 @@ def test_wide_range_of_queries_over_an_8_bit_cache():
     check(q[2:], k, v, tables[2:], lens[2:], page)
 
 
+@pytest.mark.parametrize("group", [4, 16])
+def test_channels_far_apart_within_a_query_over_an_8_bit_cache(group):
+    """One channel of each query far above the others and met by keys of zero, so that the small ones decide: they keep
+    their bits down to 2^-32 of the largest."""
+    rng = np.random.default_rng(41)
+    page, n, dim = 16, 200, 64
+    for power in (10, 17, 24, 30):
+        tables, total = tables_for(rng, [n, n], page)
+        k, v = make_pages(rng, total, page, 1, dim, True)
+        k.view(torch.uint8)[..., 5] = 0
+        q = queries(rng, 2, group, dim, 0.3)
+        small = q.float().abs() < 0.25               # within 2^-2 of each other: the row's span is the power's
+        q[small] = 0.25
+        q[..., 5] = 2.0 ** power
+        check(q, k, v, tables, [n, n], page, scale=0.125)
+
+
 def test_offsets_past_32_bits():
     """Pages more than 2^31 elements into a pool."""
     page, hkv, dim = 64, 8, 128
