@@ -269,6 +269,27 @@ def test_offsets_past_32_bits():
     check(q, small[0], small[1], np.array([[0, 1, 2]], dtype=np.int32), [170], page)
 
 
+@pytest.mark.parametrize("dim,e4m3", [(64, False), (128, True), (128, False)])
+def test_a_length_at_the_end_of_32_bits(dim, e4m3):
+    """The longest table of pages of 64 tokens, its last columns alone with pages: a window that ends 2^31 - 64 tokens in
+    sees what a short sequence of the same last tokens does."""
+    page, window, hkv, heads = 64, 100, 1, 4
+    rng = np.random.default_rng(62)
+    k, v = make_pages(rng, 4, page, hkv, dim, e4m3)
+    q = queries(rng, 2, heads, dim)
+    width = (1 << 25) - 1
+    tables = torch.full((1, width), -1, dtype=torch.int32, device=DEV)              # 134 MB
+    tables[0, -3:] = torch.tensor([2, 0, 3], dtype=torch.int32, device=DEV)
+    ids = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = M.attention_workspace(1, heads, hkv, dim)
+    for short in (192, 181, 131):                                                   # tokens of the last three pages
+        lens = torch.tensor([(width - 3) * page + short], dtype=torch.int32, device=DEV)
+        got = M.paged_attention(q[:1], k, v, tables, lens, ws, window=window, seq_ids=ids)
+        assert M.get_device_error(ws) == 0
+        want = check(q[:1], k, v, np.array([[2, 0, 3]], dtype=np.int32), [short], page, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_another_stream_and_a_graph():
     rng = np.random.default_rng(11)
     page, lens = 16, [333, 40]

@@ -256,9 +256,12 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
           }
         }
       }
-      ahead_tok += C::kTile;
-      if (--ahead_left > 0) next_entry();
-      else next_piece();
+      if (--ahead_left > 0) {
+        ahead_tok += C::kTile;
+        next_entry();
+      } else {
+        next_piece();
+      }
     }
     cp_async_commit();
     return seen;

@@ -434,8 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const AttnParams p,
       const int n = pc.tile1 - pc.tile0;
       const int tok0 = (pc.lo / kTile + pc.tile0) * kTile + 16 * quarter + (lane & 15);
       auto entry_of = [&](int i) -> int {
+        if (i >= n) return -1;
         const int tok = tok0 + i * kTile;
-        if (i >= n || tok < pc.lo || tok >= pc.hi) return -1;
+        if (tok < pc.lo || tok >= pc.hi) return -1;
         return table[tok / p.t.page_size];
       };
       // byte offset of this lane's token in tile i, -1 where it is not seen

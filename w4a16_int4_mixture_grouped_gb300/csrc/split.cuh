@@ -10,7 +10,7 @@
 namespace moe {
 
 __device__ __forceinline__ int tiles_of(int lo, int hi, int tile) {
-  return hi > lo ? (hi + tile - 1) / tile - lo / tile : 0;
+  return hi > lo ? (hi - 1) / tile + 1 - lo / tile : 0;     // (hi + tile - 1 may pass 2^31)
 }
 
 // First tile of CTA c, and the CTA of tile x.
