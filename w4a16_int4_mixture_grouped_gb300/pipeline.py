@@ -13,7 +13,7 @@ Indexed layout: the gate_up GEMM writes SwiGLU(h) in sorted_ids slot order
 DecoderLayer is the decode step of one layer: attention over a PagedCache, the
 MoE FFN, and the norms between them and the residual stream. Its dense
 projections (queries, keys and values, output, router) are plain library
-products.
+products, the router's softmax and top-k torch operators.
 """
 
 from __future__ import annotations
@@ -23,11 +23,12 @@ from typing import Optional
 import torch
 
 from . import (FLAG_A_SORTED, FLAG_COMBINE, FLAG_OUT_SORTED, FLAG_SPLIT, FLAG_SWIGLU, KERNEL_SPLIT, LAYOUT_CONTIGUOUS,
-               LAYOUT_INDEXED, LATENT_DIM, LATENT_VALUE_DIM, MODE_GATE_UP, MODE_PLAIN, PreparedWeight, align, align_size,
+               LAYOUT_INDEXED, LATENT_DIM, MODE_GATE_UP, MODE_PLAIN, PreparedWeight, align, align_size,
                block_norm, contiguous, contiguous_layout, gather_rows, gather_sorted, indexed, plan, workspace)
 from .cache import PagedCache
 
 CONTIGUOUS_SEGMENT = 128
+LATENT_HEAD_DIM = 192      # channels of a query head before the latent space (128 and 64 of position) unless a scale says otherwise
 DECODE_MAX_BLOCK_M = 32    # indexed calls with block_m above this run the tcgen05 kernel
 
 
@@ -127,20 +128,25 @@ class DecoderLayer:
     w_qkv bf16 [hidden, (Hq + 2 Hkv) * D] (latent: [hidden, Hq * 576 + 576], queries in the latent space, then the
     row to cache), w_o bf16 [Hq * D, hidden] (latent: [Hq * 512, hidden]), w_router bf16 [hidden, E]; norms bf16
     [hidden]: after attention, before the FFN, after the FFN (each None: that norm is left out; the one before the FFN is
-    needed). A position encoding is the caller's: rotate inside `project`."""
+    needed). scale multiplies the scores: default D ** -0.5; a latent cache's rows do not say how wide the heads were
+    before they were taken into the latent space, so give that width ** -0.5 unless it is LATENT_HEAD_DIM. A position
+    encoding is the caller's: rotate inside `project`."""
 
     def __init__(self, cache: PagedCache, layer: int, ffn: MoEFFN, num_heads: int, w_qkv: torch.Tensor, w_o: torch.Tensor,
                  w_router: torch.Tensor, norm_ffn: torch.Tensor, norm_post_attn: Optional[torch.Tensor] = None,
-                 norm_post_ffn: Optional[torch.Tensor] = None, eps: float = 1e-6, window: int = 0):
+                 norm_post_ffn: Optional[torch.Tensor] = None, eps: float = 1e-6, window: int = 0,
+                 scale: Optional[float] = None):
         self.cache, self.layer, self.ffn, self.heads = cache, layer, ffn, num_heads
         self.w_qkv, self.w_o, self.w_router = w_qkv, w_o, w_router
         self.norm_ffn, self.norm_post_attn, self.norm_post_ffn = norm_ffn, norm_post_attn, norm_post_ffn
         self.eps, self.window = eps, window
         if cache.latent:
-            self.kv_heads, self.dim, self.scale = 1, LATENT_DIM, (LATENT_VALUE_DIM // 4 + 64) ** -0.5
+            self.kv_heads, self.dim = 1, LATENT_DIM
+            default = LATENT_HEAD_DIM ** -0.5
         else:
             self.kv_heads, self.dim = cache.pool.shape[3:]
-            self.scale = self.dim ** -0.5
+            default = self.dim ** -0.5
+        self.scale = default if scale is None else scale
 
     def project(self, y: torch.Tensor, positions: torch.Tensor):
         """(q [B, Hq, D], k, v) of the new tokens; slices of one product."""
