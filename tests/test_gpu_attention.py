@@ -290,6 +290,58 @@ def test_a_length_at_the_end_of_32_bits(dim, e4m3):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("group", [4, 16])
+@pytest.mark.parametrize("what", ["query", "key", "value", "infinite key"])
+def test_a_number_that_is_none_stays_where_it_is_seen(what, group, e4m3):
+    """A NaN query channel reaches its own head, a NaN key the heads of its cache head and sequence, a NaN value their
+    channel. A key that is infinite against a query makes its token's score -infinity or the head's result no number."""
+    if what == "infinite key" and e4m3:
+        pytest.skip("no infinities in the type")
+    rng = np.random.default_rng(61)
+    page, lens, hkv, dim = 16, [300, 300, 50], 2, 64
+    tables, total = tables_for(rng, lens, page)
+    k, v = make_pages(rng, total, page, hkv, dim, e4m3)
+    q = queries(rng, 3, hkv * group, dim)
+    q[:, :, 9] = torch.where(torch.arange(hkv * group, device=DEV) % 2 == 0, 1.0, -1.0).to(torch.bfloat16)
+    tok = (int(tables[1, 4]), 9)
+    nan = np.zeros((3, hkv * group, dim), dtype=bool)
+    first = slice(group, 2 * group)                          # the heads of cache head 1
+    clean_k = k.clone()
+    if what == "query":
+        q0 = q.clone()
+        q[1, 3, 20] = math.nan
+        nan[1, 3] = True
+    elif what == "value":
+        (v.view(torch.uint8) if e4m3 else v)[tok[0], tok[1], 1, 33] = 0x7F if e4m3 else math.nan
+        nan[1, first, 33] = True
+    elif what == "key":
+        (k.view(torch.uint8) if e4m3 else k)[tok[0], tok[1], 1, 9] = 0x7F if e4m3 else math.nan
+        nan[1, first] = True
+    else:
+        k[tok[0], tok[1], 1, 9] = math.inf                   # heads with a negative channel there: the token is not seen
+        nan[1, group:2 * group:2] = True
+    ws = M.attention_workspace(3, hkv * group, hkv, dim)
+    out, lse = M.paged_attention(q, k, v, torch.from_numpy(tables).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), ws)
+    assert M.get_device_error(ws) == 0
+    kn, vn = f64(clean_k), np.nan_to_num(f64(v))
+    qn = f64(q0 if what == "query" else q)
+    ref, bound, rl, lb = R.attention(qn, lambda p, t: kn[p, t], lambda p, t: vn[p, t], group, tables, lens, page, total,
+                                     dim ** -0.5, 0)
+    if what == "infinite key":                               # the other heads of that cache head without the token
+        unseen = tables.copy()
+        keep = [j for j in range(300) if j != 4 * page + 9]
+        k2, v2 = kn[unseen[1][np.array(keep) // page], np.array(keep) % page, 1], vn[unseen[1][np.array(keep) // page], np.array(keep) % page, 1]
+        for h in range(group + 1, 2 * group, 2):
+            s = k2 @ qn[1, h] * dim ** -0.5
+            w = np.exp(s - s.max())
+            ref[1, h], rl[1, h] = w @ v2 / w.sum(), s.max() + np.log(w.sum())
+    got, gl = f64(out), f64(lse)
+    assert np.isnan(got[nan]).all() and (np.abs(got - ref)[~nan] <= bound[~nan]).all()
+    rows = nan.all(2)
+    assert np.isnan(gl[rows]).all() and (np.abs(gl - rl)[~rows] <= lb[~rows]).all()
+
+
 def test_another_stream_and_a_graph():
     rng = np.random.default_rng(11)
     page, lens = 16, [333, 40]
