@@ -607,7 +607,7 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_compact(const moe_w4a16_pool* poo
  *   gate   bf16 [gate_rows, n] dense or NULL; gate_rows divides rows, row t takes gate row
  *          t / (rows / gate_rows): one for all tokens, one per sequence, one per token
  *   w_post, w_pre  bf16 [n]; w_pre and y both or neither; x NULL needs gate and w_post NULL
- *   n      1 .. MOE_W4A16_MAX_NORM_WIDTH; strides in elements between rows, any (the wider the power of two,
+ *   n      1 .. MOE_W4A16_MAX_NORM_WIDTH; strides in elements between rows, any from n on (the wider the power of two,
  *          up to 8, that divides n and the strides, with pointers aligned alike, the wider the accesses) */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_block_norm(const uint16_t* x, int64_t x_stride, const void* h, int64_t h_stride,
                                                     int residual_dtype, const uint16_t* gate, int gate_rows,

@@ -1,9 +1,9 @@
 // Attention of one new token per sequence over a paged cache, grouped heads.
 //
-// For each sequence and cache head: scores s = q K^T of the up to 16 query heads that share it, a
-// softmax over the seen tokens with a running maximum and sum, and o = p V. Every key and value is
-// read once; at one flop a byte and query head (E4M3: two) the bound is HBM, so the kernel is built
-// around keeping copies in flight:
+// For each sequence and cache head: scores s = q K^T of the query heads that share it, a softmax over the seen
+// tokens with a running maximum and sum, and o = p V. Every key and value is read once (by groups above 16 heads once
+// for each block of 16); at one flop a byte and query head (E4M3: two) the bound is HBM, so the kernel is built around
+// keeping copies in flight:
 //
 //   * One CTA of four warps takes an equal share of all tiles of all sequences (split.cuh), whatever
 //     the lengths; rows that cross a CTA's range are joined by the last CTA to arrive, in order, from
@@ -12,8 +12,8 @@
 //     its own cp.async, its own maximum, sum and accumulator. No barrier in the loop; the four
 //     warps are joined once per row, in a buffer beside the ring, while the next rows' stages are on their way
 //     (4096 rows of 128 tokens: 481 us against 756 with the ring drained at a row's end).
-//   * Two CTAs an SM with 96 KB of stages between them: 24 KB a warp keep HBM busy. Three or four CTAs with shorter
-//     rings are slower (230 to 445 us where two take 194).
+//   * Two CTAs an SM with 96 KB of stages each, 24 KB a warp, keep HBM busy (256 BF16 channels: one CTA with 192 KB). Three
+//     or four CTAs with shorter rings are slower (230 to 445 us where two take 194).
 //   * The query heads of a cache head share its keys and values as loaded from shared memory, by warp-level MMA
 //     (m16n8k16; at full HBM speed its pipe is 10% busy, E4M3 18%). Groups of up to 8 heads are its 8 columns, tokens
 //     (scores) and channels (output) its 16 rows; larger groups are the 16 rows, 16 heads at a time. With 8 heads in 16
@@ -27,10 +27,10 @@
 //
 // 96 sequences of up to 8191 tokens, 8 cache heads x 8 query heads x 128 channels, BF16: 324 us, 6.6 TB/s, 98% of a plain
 // copy. 8 sequences of up to 131072 tokens, E4M3: 192 us, 6.1 TB/s. What E4M3 still lacks there goes to the conversions
-// of its elements (64 channels: 5.7 TB/s, with as much softmax a token for half the bytes; groups of 16 heads 6.0 TB/s,
-// with 256 channels 4.9, where registers spill). Rows of 128 tokens: 4.5 TB/s BF16, 2.8 E4M3, bound by each row's start
-// and join. Rows of 80 or 96 BF16 channels: 4.9 to 5.7 TB/s; heads' rows that share DRAM bursts are read by CTAs that drift
-// apart.
+// of its elements (64 channels: 5.7 TB/s, with as much softmax a token for half the bytes; groups of 16 heads 6.0 TB/s).
+// With 256 channels and 16 heads registers spill, 40 bytes BF16 (6.1 TB/s, 6.7 with 8 heads) and 32 E4M3 (4.8, 6.0). Rows
+// of 128 tokens: 4.5 TB/s BF16, 2.8 E4M3, bound by each row's start and join. Rows of 80 or 96 BF16 channels: 4.9 to 5.7
+// TB/s; heads' rows that share DRAM bursts are read by CTAs that drift apart.
 #include <cuda_runtime.h>
 
 #include "block.h"
@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
 
   zero_empty<kThreads>(p, p.dim);
   // A part of a split row costs its join about 0.13 us a vector that a thread adds up, a tile 0.8 us, and a split as such
-  // 2.5 us: rows of up to three tiles stay whole, and few rows are cut into about 2.8 sqrt(tiles / vectors) parts, no more.
+  // 2.5 us: where no row has more than three tiles each share is as long as the longest row, so that few rows are cut (those
+  // that a share's end falls into), and a few longer rows are cut into about 2.8 sqrt(tiles / vectors) parts, no more.
   // (One sequence, 8 heads a cache head: 20000 tokens of one cache head 51 -> 20 us against a part for every CTA, 8192
   // tokens of 8 cache heads 20 -> 17, 100 tokens 8.3 -> 6.0. With 4 or 5.6 in place of 2.8 long rows take 2 to 18% longer.)
   const int items = (min(kRows, p.group) * p.dim + 511) / 512;
@@ -365,11 +366,11 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnParams p,
       qscale[1] = abs_scale;
     }
     // m: what the exponents are taken against. 16 heads: the maximum seen so far (E4M3: 15 below it, so that FP16
-    // probabilities reach 2^15 and lose nothing down to 2^-39 of the largest). Up to 8 heads, where a maximum over the
-    // tokens crosses eight lanes: a maximum that is only taken when a score passes it by 2^kSlack. BF16: by anything, so
-    // that the largest probability is 1 and not rounded (error of 96 ragged sequences 0.0008 against 0.0009 with a slack
-    // of 2^8, for 0.3% of the time). E4M3: FP16 probabilities of 2^kLift to 2^15, which lose nothing down to 2^-32 of the
-    // largest.
+    // probabilities reach 2^15, keep their bits down to 2^-29 of the largest and end at 2^-39 of it). Up to 8 heads, where
+    // a maximum over the tokens crosses eight lanes: a maximum that is only taken when a score passes it by 2^kSlack. BF16:
+    // by anything, so that the largest probability is 1 and not rounded (error of 96 ragged sequences 0.0008 against 0.0009
+    // with a slack of 2^8, for 0.3% of the time). E4M3: FP16 probabilities of 2^kLift to 2^15, which keep their bits down to
+    // 2^-22 of the largest or further, and end at 2^-32 of it or below.
     constexpr float kLift = !E4M3 ? 0.f : EIGHT ? 8.f : 15.f, kSlack = E4M3 ? 7.f : 0.f;
     float top_of[2], m[2], l[2], o[OT][4];
 #pragma unroll

@@ -8,6 +8,9 @@
 //   S^T [keys x heads]  = K [keys x 576] . Q^T       A = the tile, K-major
 //   O^T [512 x heads]  += V^T [512 x keys] . P^T      A = the same tile, M-major (no transposed copy)
 //
+// Sequences with more than 64 heads are read once for each block of 64, one block after the other: over 128 sequences of
+// 2048 to 8192 tokens 128 heads take 265 us where 64 take 154.
+//
 //   * Tiles of 64 tokens, two in shared memory (2 x 72 KB) beside the 64 queries (72 KB), filled with cp.async
 //     (rows gathered by page; unseen slots zero-filled); the tile two ahead is prefetched into L2, so that HBM does
 //     not wait for a free buffer.

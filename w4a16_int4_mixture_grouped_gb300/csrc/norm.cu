@@ -8,13 +8,18 @@
 //   * Short rows (up to 64 packs): 8, 16 or 32 lanes a row, sums by shuffles alone.
 //   * Longer rows: a CTA a row, one barrier a sum (every warp adds up the warps' sums itself). Few rows: all that a
 //     row needs, weights and gate included, is requested before the first sum.
-//   * Many long rows: two packs of 8 columns a thread in at most 42 registers, weights read (from L1) where they are
-//     used, so that three CTAs share an SM and one's loads run beside the others' sums. 8192 x 7168 with an FP32
-//     residual: 109 us, 6.46 TB/s (a plain copy of as many bytes: 108.7 us). At 64 registers and two CTAs it takes
-//     133 us; one CTA an SM that walks through rows with four of them in flight in shared memory, by cp.async or by
-//     bulk copies, 125 us.
+//   * Many long rows: two packs of 8 columns a thread in 40 registers (FP32 residual: 40 bytes spilled), weights read
+//     (from L1) where they are used, so that three CTAs share an SM and one's loads run beside the others' sums.
+//     8192 x 7168 with an FP32 residual: 109 us, 6.46 TB/s (a plain copy of as many bytes: 108.7 us). At 64 registers
+//     and two CTAs it takes 133 us; one CTA an SM that walks through rows with four of them in flight in shared
+//     memory, by cp.async or by bulk copies, 125 us.
 //   * Packs of 8 columns, 16 bytes of BF16. Rows of any width do with them too where all tensors' rows start alike
 //     (contiguous tensors): only the packs at a row's two ends go column by column. Otherwise packs of 2 or 1.
+//
+// Slower forms, by the bytes that they need: odd widths, whose weights are read a column at a time (8192 x 7167: 2.7 TB/s BF16
+// residual, 4.2 FP32; 8192 x 1021: 2.5); rows wider than 16384 columns, whose packs spill (728 to 2856 bytes of stores a
+// thread; 4096 x 20000: 2.1 and 2.6 TB/s, 2048 x 32768: 2.0 and 2.4); rows that start at different alignments (8192 x 7167:
+// 1.2, 2048 x 20001: 0.8).
 #include <cuda_runtime.h>
 
 #include "block.h"
