@@ -136,6 +136,7 @@ enum { MOE_W4A16_RESIDUAL_BF16 = 0, MOE_W4A16_RESIDUAL_F32 = 1 };
 #define MOE_W4A16_MAX_HEAD_DIM 256                 /* head_dim of moe_w4a16_paged_attention: 16, 32, ... 256 */
 #define MOE_W4A16_MAX_PAGE_SIZE 4096               /* tokens of a cache page */
 #define MOE_W4A16_MAX_NORM_WIDTH 32768             /* row length of moe_w4a16_block_norm */
+#define MOE_W4A16_MAX_ROTARY_DIM 1024              /* channels of a head that moe_w4a16_rotary turns */
 
 /* Host-side description of a prepared weight, filled by moe_w4a16_prepare and
  * passed by address to every GEMM call (host pointer). */
@@ -595,6 +596,88 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_compact(const moe_w4a16_pool* poo
                                                        int num_seqs, int32_t* refs_out, int32_t* tables_out,
                                                        int32_t* page_map, int32_t* num_live, void* ws, size_t ws_bytes,
                                                        moe_w4a16_stream_t stream);
+
+/* Workspace bytes of moe_w4a16_paged_chunk_attention, independent of batch, chunks and lengths; another attention,
+ * cache_* or page call may share it (see above). */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_workspace_size(int num_heads, int num_kv_heads, int head_dim,
+                                                                    size_t* bytes);
+
+/* Attention of a chunk of new tokens per sequence over a paged cache, grouped heads, causal: a prompt or a piece of
+ * one, drafts to verify, or both beside sequences that decode. The chunk of sequence b is the rows starts[b] <= t <
+ * starts[b + 1] of q, n of them; its keys and values are in the cache already, as the last n of the sequence's lens
+ * tokens. Row t stands at position p = lens - n + (t - starts[b]) and sees the tokens j, max(0, p - window + 1) <= j <= p
+ * (window 0: all up to p), whose table entry is a page. Scores, outputs, unseen slots and what is refused or recorded
+ * are those of moe_w4a16_paged_attention; a row that sees nothing (a chunk longer than its sequence, freed pages) gives
+ * zeros and -infinity. Rows before starts[0] and from starts[batch] on are left as they were.
+ *   q        bf16 [num_tokens, num_heads, head_dim], q_stride elements between tokens; 16-byte aligned
+ *   starts   int32 [batch + 1], ascending, 0 .. num_tokens; a chunk that does not lie within them is skipped and recorded as
+ *            MOE_W4A16_ERR_BAD_INDEX
+ *   seq_ids  int32 [batch]: the row of tables and lens of each chunk (NULL: chunk b reads row b)
+ *   out      bf16 [num_tokens, num_heads, head_dim] dense; lse float [num_tokens, num_heads] or NULL */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_attention(
+    const uint16_t* q, int64_t q_stride, int num_tokens, const int32_t* starts, int batch, int num_heads,
+    int num_kv_heads, int head_dim, const moe_w4a16_pages* cache, const int32_t* tables, int64_t table_stride,
+    int max_pages, const int32_t* lens, const int32_t* seq_ids, int num_seqs, float scale, int window, uint16_t* out,
+    float* lse, void* ws, size_t ws_bytes, moe_w4a16_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotation of positions. Of a head's channels, `dim` from `offset` on turn in pairs: at position p pair i becomes
+ *   a' = magnitude * (a cos w - b sin w),  b' = magnitude * (a sin w + b cos w),  w = p * f_i,
+ * with (a, b) the channels offset + i and offset + i + dim / 2, or, interleaved, offset + 2i and offset + 2i + 1. The
+ * other channels are copied. A frequency f_i (radians a token, in double precision) is kept in 1/2^64 of a turn, and
+ * p * f_i modulo a turn is taken in whole numbers, so that far positions (negative ones turn back) lose nothing beyond the
+ * frequency's own 2^-53; sines, cosines and products are FP32, the result is rounded once.
+ * ------------------------------------------------------------------------- */
+
+/* Frequencies for contexts longer than the trained one (`trained_length` tokens), by a factor >= 1, in double
+ * precision: with g_i = theta^(-2i/dim) and n_i = trained_length * g_i / 2 pi turns within that length,
+ *   NONE    g_i
+ *   LINEAR  g_i / factor
+ *   BASE    (theta * factor^(dim / (dim - 2)))^(-2i/dim): the slowest pair turns `factor` times slower, the first as before
+ *   TURNS   s g_i + (1 - s) g_i / factor, s = (n_i - low) / (high - low) cut to 0 .. 1
+ *   INDEX   the same with 1 - s = (i - i_high) / max(i_low - i_high, 0.001) cut to 0 .. 1, i_high = floor and i_low = ceil of
+ *           dim ln(trained_length / (2 pi n)) / (2 ln theta) at n = high and low, cut to 0 .. dim - 1
+ *   GIVEN   given[i]
+ * LINEAR and BASE take factor; TURNS and INDEX also trained_length and 0 < low < high (INDEX: theta != 1). Host only:
+ * turns[dim / 2] is host memory, to be copied to the device by the caller. */
+enum { MOE_W4A16_ROTARY_NONE = 0, MOE_W4A16_ROTARY_LINEAR = 1, MOE_W4A16_ROTARY_BASE = 2, MOE_W4A16_ROTARY_TURNS = 3,
+       MOE_W4A16_ROTARY_INDEX = 4, MOE_W4A16_ROTARY_GIVEN = 5 };
+MOE_W4A16_API moe_w4a16_status moe_w4a16_rotary_frequencies(int dim, double theta, int scaling, double factor,
+                                                            int trained_length, double low, double high,
+                                                            const double* given, uint64_t* turns);
+
+typedef struct moe_w4a16_rotary_desc {
+  const uint64_t* turns;  /* device, [dim / 2], 8-byte aligned */
+  int32_t dim;            /* channels that turn: even, 2 .. MOE_W4A16_MAX_ROTARY_DIM */
+  int32_t offset;         /* the first of them */
+  int32_t interleaved;    /* 0: pairs dim / 2 apart, 1: side by side */
+  float magnitude;
+} moe_w4a16_rotary_desc;
+
+/* out = x turned by its positions.
+ *   x, out   bf16 [num_tokens, num_heads, head_dim] with any strides (elements) between tokens and between heads; out may be
+ *            x (the same address and strides: turned in place), else the two do not overlap. Rows of out do not overlap.
+ *            The wider the power of two, up to 8, that divides head_dim, offset, dim / 2 (interleaved: dim) and the strides, with
+ *            pointers aligned alike, the wider the accesses.
+ *   positions int32 [num_tokens] */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_rotary(const uint16_t* x, int64_t x_stride, int64_t x_head_stride,
+                                                const int32_t* positions, int num_tokens, int num_heads, int head_dim,
+                                                const moe_w4a16_rotary_desc* rotary, uint16_t* out, int64_t out_stride,
+                                                int64_t out_head_stride, moe_w4a16_stream_t stream);
+
+/* moe_w4a16_cache_append with the rotation on the way, in one launch: k is turned by its position, then written (E4M3: the
+ * element nearest to the turned key / k_scale, without a rounding to BF16 between); v is written as it is; q, turned by the
+ * same positions, goes to q_out. Query rows are turned whatever becomes of their key: a negative position turns back.
+ *   q, q_out bf16 [num_tokens, num_q_heads, head_dim], strides between tokens, 16-byte aligned; both NULL: keys and values
+ *            alone. q_out may be q; it does not overlap k or v.
+ *   rotary   offset and dim multiples of 8, dim of 16 unless interleaved (else UNSUPPORTED); offset + dim <= head_dim
+ * Other arguments as for moe_w4a16_cache_append. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_append_rotary(
+    const uint16_t* q, int64_t q_stride, int num_q_heads, uint16_t* q_out, int64_t q_out_stride, const uint16_t* k,
+    int64_t k_stride, const uint16_t* v, int64_t v_stride, int num_tokens, int num_heads, int head_dim,
+    const moe_w4a16_rotary_desc* rotary, const moe_w4a16_pages* cache, const int32_t* tables, int64_t table_stride,
+    int max_pages, int num_seqs, const int32_t* seq_ids, const int32_t* positions, void* ws, size_t ws_bytes,
+    moe_w4a16_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Norms around a block (attention or FFN) on the residual stream, in one pass:

@@ -484,5 +484,8 @@ def masked(a3: torch.Tensor, masked_m: torch.Tensor, expected_m: int, pw: Prepar
 
 from .block import (CACHE_BF16, CACHE_E4M3, LATENT_DIM, LATENT_VALUE_DIM, MAX_HEAD_DIM, MAX_NORM_WIDTH,  # noqa: E402,F401
                     MAX_PAGE_SIZE, RESIDUAL_BF16, RESIDUAL_F32, attention_workspace, attention_workspace_size,
-                    block_norm, cache_append, cache_compact, cache_copy, cache_extend, cache_fork, cache_free,
-                    cache_workspace, cache_workspace_size, latent_attention, paged_attention)
+                    block_norm, cache_append, cache_append_rotary, cache_compact, cache_copy, cache_extend, cache_fork,
+                    cache_free, cache_workspace, cache_workspace_size, latent_attention, paged_attention,
+                    paged_chunk_attention, paged_chunk_workspace, paged_chunk_workspace_size)
+from .positions import (MAX_ROTARY_DIM, ROTARY_BASE, ROTARY_GIVEN, ROTARY_INDEX, ROTARY_LINEAR, ROTARY_NONE,  # noqa: E402,F401
+                        ROTARY_TURNS, Rotary, rotary, rotary_frequencies)

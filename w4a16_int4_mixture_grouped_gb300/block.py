@@ -64,6 +64,9 @@ _SIGNATURES = {
     "cache_free": [_P, _I, _P, _L, _I, _P, _I, _P, _P, _I, _I, _P, _SZ, _P],
     "cache_copy": [_POOL, _P, _P, _I, _P, _SZ, _P],
     "cache_compact": [_POOL, _P, _P, _L, _I, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "paged_chunk_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
+    "paged_chunk_attention": [_P, _L, _I, _P, _I, _I, _I, _I, _PAGES, _P, _L, _I, _P, _P, _I, _F, _I, _P, _P, _P, _SZ, _P],
+    "cache_append_rotary": [_P, _L, _I, _P, _L, _P, _L, _P, _L, _I, _I, _I, _P, _PAGES, _P, _L, _I, _I, _P, _P, _P, _SZ, _P],
     "block_norm": [_P, _L, _P, _L, _I, _P, _I, _P, _P, _I, _I, _F, _F, _F, _P, _L, _P, _L, _P],
 }
 _FN = {}
@@ -107,7 +110,7 @@ def _need(t: torch.Tensor, name: str, dtype, dim: int, index: Optional[int] = No
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
-    if t.stride(-1) != 1 and t.size(-1) > 1:
+    if t.stride(-1) != 1 and t.size(-1) > 1 and t.numel():
         raise ValueError(f"{name}: the last dimension must be dense")
     return t
 
@@ -259,6 +262,52 @@ def latent_attention(q: torch.Tensor, pages: torch.Tensor, tables: torch.Tensor,
     return out, lse
 
 
+def paged_chunk_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    out = _SZ(0)
+    status = _FN["paged_chunk_workspace_size"](num_heads, num_kv_heads, head_dim, ctypes.byref(out))
+    if status != 0:
+        raise MoeW4A16Error(status, "paged_chunk_workspace_size")
+    return int(out.value)
+
+
+def paged_chunk_workspace(num_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """Allocates (through torch) and zeroes a workspace for paged_chunk_attention, whatever the batch and lengths."""
+    return _alloc_ws(paged_chunk_workspace_size(num_heads, num_kv_heads, head_dim), device)
+
+
+def paged_chunk_attention(q: torch.Tensor, starts: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                          tables: torch.Tensor, lens: torch.Tensor, ws: torch.Tensor, scale: Optional[float] = None,
+                          window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                          seq_ids: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """A chunk of new tokens per sequence over its pages, causal: q [T, H, D] -> (out bf16 [T, H, D], lse float [T, H]).
+
+    Rows starts[b] .. starts[b + 1] - 1 of q (starts int32 [B + 1]) are the last tokens of the sequence that row
+    seq_ids[b] (default: b) of tables and lens describes, their keys and values appended already. A row sees the tokens
+    up to its own, with a window the newest `window` of them. Rows of no chunk are left as they were (as they come from
+    the allocator, where out and lse are not given)."""
+    _rows_dense(_need(q, "q", _BF16, 3), "q")
+    index = q.get_device()
+    t, h, d = q.shape
+    if v_pages is None:
+        raise ValueError("v_pages is missing")
+    c = _pages(k_pages, v_pages, index, k_scale, v_scale)
+    heads, dim = k_pages.shape[2:]
+    if dim != d:
+        raise ValueError(f"pages must hold keys and values of {d} channels")
+    b = _need(starts, "starts", _I32, 1, index).size(0) - 1
+    if b < 0:
+        raise ValueError("starts has no element")
+    ta, ts, mp, ns = _table(tables, index)
+    out, lse = _attention_out(q, t, h, d, index, out, lse)
+    wa, wn = _ws(ws, index)
+    _run("paged_chunk_attention", index, _FN["paged_chunk_attention"], q.data_ptr(), q.stride(0) if t > 1 else h * d, t,
+         starts.data_ptr(), b, h, heads, d, c, ta, ts, mp, _vector(lens, "lens", ns, index),
+         None if seq_ids is None else _vector(seq_ids, "seq_ids", b, index), ns, d ** -0.5 if scale is None else scale, window,
+         out.data_ptr(), lse.data_ptr(), wa, wn)
+    return out, lse
+
+
 # ---------------------------------------------------------------------------
 # cache
 # ---------------------------------------------------------------------------
@@ -287,6 +336,52 @@ def cache_append(k: torch.Tensor, k_pages: torch.Tensor, tables: torch.Tensor, s
           None if latent else v.data_ptr(), 0 if latent else (v.stride(0) if n > 1 else heads * dim), n, heads, dim,
           c, ta, ts, mp, ns, _vector(seq_ids, "seq_ids", n, index),
           _vector(positions, "positions", n, index), wa, wn)
+
+
+def cache_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, k_pages: torch.Tensor, tables: torch.Tensor,
+                        seq_ids: torch.Tensor, positions: torch.Tensor, rotary, ws: torch.Tensor,
+                        v: Optional[torch.Tensor] = None, v_pages: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+                        v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """cache_append of keys turned by their positions (a Rotary's) on the way, and the same rotation of the queries
+    q [T, Hq, dim] (or None) -> q_out, a new dense tensor unless given (it may be q). Every query row is turned, whatever
+    becomes of its key."""
+    latent = v_pages is None
+    if (v is None) != latent:
+        raise ValueError("v and v_pages go together")
+    _rows_dense(_need(k, "k", _BF16, 2 if latent else 3), "k")
+    index = k.get_device()
+    c = _pages(k_pages, v_pages, index, k_scale, v_scale)
+    if k_pages.shape[2:] != k.shape[1:]:
+        raise ValueError(f"rows are {tuple(k.shape[1:])}, pages hold {tuple(k_pages.shape[2:])}")
+    n = k.shape[0]
+    heads, dim = (1, k.shape[1]) if latent else k.shape[1:]
+    width = heads * dim
+    va = vs = 0
+    if not latent:
+        _rows_dense(_need(v, "v", _BF16, 3, index), "v")
+        if v.shape != k.shape:
+            raise ValueError("k and v must have the same shape")
+        va, vs = v.data_ptr(), v.stride(0) if n > 1 else width
+    qa = oa = qh = qs = os_ = 0
+    if q is not None:
+        _rows_dense(_need(q, "q", _BF16, 3, index), "q")
+        qn, qh, qd = q.shape
+        if qn != n or qd != dim:
+            raise ValueError(f"q must be [{n}, heads, {dim}]")
+        if q_out is None:
+            q_out = torch.empty((n, qh, dim), dtype=_BF16, device=q.device)
+        elif _rows_dense(_need(q_out, "q_out", _BF16, 3, index), "q_out").shape != q.shape:
+            raise ValueError("q_out and q must have the same shape")
+        qa, oa = q.data_ptr(), q_out.data_ptr()
+        qs, os_ = (q.stride(0), q_out.stride(0)) if n > 1 else (qh * dim, qh * dim)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    ta, ts, mp, ns = _table(tables, index)
+    wa, wn = _ws(ws, index)
+    _run("cache_append_rotary", index, _FN["cache_append_rotary"], qa, qs, qh, oa, os_, k.data_ptr(),
+         k.stride(0) if n > 1 else width, va, vs, n, heads, dim, rotary.desc(index), c, ta, ts, mp, ns,
+         _vector(seq_ids, "seq_ids", n, index), _vector(positions, "positions", n, index), wa, wn)
+    return q_out
 
 
 def cache_workspace_size(num_pages: int, count: int) -> int:

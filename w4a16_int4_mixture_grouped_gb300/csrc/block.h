@@ -91,6 +91,91 @@ struct AppendParams {
 };
 cudaError_t launch_cache_append(const AppendParams& p, int dtype, cudaStream_t stream);
 
+// Attention of a chunk of new tokens a sequence.
+struct ChunkParams {
+  const uint16_t* q;
+  int64_t q_stride;
+  int tokens;
+  const int32_t* starts;               // [batch + 1]
+  int batch, heads, kv_heads, group;
+  int dim;
+  const void* k;
+  const void* v;
+  int64_t page_stride, token_stride, head_stride;   // elements
+  TableView t;
+  const int32_t* lens;
+  const int32_t* seq_ids;
+  float score_scale;                   // scale * k_scale * log2(e)
+  float v_scale;
+  int window;
+  uint16_t* out;
+  float* lse;
+  int* err;
+  uint64_t wait_ns;
+  void* scratch;                       // chunk_scratch_bytes
+};
+size_t chunk_scratch_bytes(int heads, int kv_heads, int dim);
+
+// A sequence's chunk: n rows of q from first on, at positions base .. base + n - 1 of table row `row`.
+struct ChunkRange {
+  int row, first, n, base;
+};
+__device__ __forceinline__ ChunkRange chunk_range(const ChunkParams& p, int b) {
+  ChunkRange c{-1, 0, 0, 0};
+  const int from = p.starts[b], to = p.starts[b + 1];
+  const int row = p.seq_ids != nullptr ? p.seq_ids[b] : b;
+  if (from < 0 || to > p.tokens || from > to) {
+    atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
+    return c;
+  }
+  c.first = from;
+  c.n = to - from;
+  if (row < 0 || row >= p.t.num_seqs) {
+    if (c.n > 0) atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
+    c.base = -c.n;                     // its rows see nothing
+    return c;
+  }
+  c.row = row;
+  const int cap = p.t.max_pages * p.t.page_size;
+  int len = p.lens[row];
+  if (len < 0 || len > cap) {
+    atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
+    len = len < 0 ? 0 : cap;
+  }
+  c.base = len - c.n;
+  return c;
+}
+cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int device, cudaStream_t stream);
+
+// A rotation (moe_w4a16_rotary_desc) as the kernels take it.
+struct RotaryView {
+  const uint64_t* turns;
+  int dim, offset;
+  int interleaved;
+  float magnitude;
+};
+struct RotaryParams {
+  const uint16_t* x;
+  int64_t x_stride, x_head_stride;
+  const int32_t* positions;
+  int tokens, heads, dim;
+  RotaryView r;
+  uint16_t* out;
+  int64_t out_stride, out_head_stride;
+};
+// width: elements of one access (8, 4, 2 or 1) that every head of x and out, and the rotated part, allow.
+cudaError_t launch_rotary(const RotaryParams& p, int width, int device, cudaStream_t stream);
+struct AppendRotaryParams {
+  AppendParams a;
+  const uint16_t* q;                   // or null
+  int64_t q_stride;
+  uint16_t* q_out;
+  int64_t q_out_stride;
+  int q_heads;
+  RotaryView r;
+};
+cudaError_t launch_cache_append_rotary(const AppendRotaryParams& p, int dtype, int device, cudaStream_t stream);
+
 struct PoolView {
   uint8_t* base;
   int planes, num_pages;

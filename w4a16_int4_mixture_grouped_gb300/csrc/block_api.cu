@@ -129,6 +129,57 @@ moe_w4a16_status attention_call(AttnParams& p, const moe_w4a16_pages* cache, con
   return MOE_W4A16_OK;
 }
 
+// The arguments that both append calls take; p.tokens of 0: nothing to do.
+moe_w4a16_status append_params(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, int num_tokens,
+                               int num_heads, int head_dim, const moe_w4a16_pages* cache, const int32_t* tables,
+                               int64_t table_stride, int max_pages, int num_seqs, const int32_t* seq_ids,
+                               const int32_t* positions, void* ws, size_t ws_bytes, AppendParams* out) {
+  if (num_tokens < 0 || num_heads < 1 || head_dim < 8 || head_dim > (1 << 16) || num_heads > (1 << 12))
+    return MOE_W4A16_ERR_INVALID_ARG;
+  if (cache == nullptr) return MOE_W4A16_ERR_INVALID_ARG;
+  const bool latent = cache->v == nullptr;
+  moe_w4a16_status st = check_pages(cache, num_heads, head_dim, latent);
+  if (st != MOE_W4A16_OK) return st;
+  if (!table_ok(tables, table_stride, max_pages, cache->page_size, num_seqs)) return MOE_W4A16_ERR_INVALID_ARG;
+  if (!ws_fits(ws, ws_bytes, MOE_W4A16_WS_HEADER_BYTES)) return MOE_W4A16_ERR_WORKSPACE;
+  const int64_t width = static_cast<int64_t>(num_heads) * head_dim;
+  if ((v == nullptr) != latent && num_tokens > 0) return MOE_W4A16_ERR_INVALID_ARG;
+  if (k_stride < width || k_stride % 8 != 0 || (!latent && (v_stride < width || v_stride % 8 != 0)))
+    return MOE_W4A16_ERR_INVALID_ARG;
+  AppendParams& p = *out;
+  p.tokens = num_tokens;
+  if (num_tokens == 0) return MOE_W4A16_OK;
+  if (k == nullptr || seq_ids == nullptr || positions == nullptr || !aligned16(k) || !aligned16(v))
+    return MOE_W4A16_ERR_INVALID_ARG;
+  p.src[0] = k;
+  p.src[1] = v;
+  p.src_stride[0] = k_stride;
+  p.src_stride[1] = v_stride;
+  p.pages[0] = cache->k;
+  p.pages[1] = cache->v;
+  p.scale[0] = cache->k_scale;
+  p.scale[1] = cache->v_scale;
+  p.heads = num_heads;
+  p.dim = head_dim;
+  p.page_stride = cache->page_stride;
+  p.token_stride = cache->token_stride;
+  p.head_stride = cache->head_stride;
+  p.t = table_view(tables, table_stride, max_pages, cache->page_size, cache->num_pages, num_seqs);
+  p.seq_ids = seq_ids;
+  p.positions = positions;
+  p.err = static_cast<int*>(ws);
+  return MOE_W4A16_OK;
+}
+
+bool rotary_ok(const moe_w4a16_rotary_desc* r, int head_dim) {
+  return r != nullptr && r->turns != nullptr && (reinterpret_cast<uintptr_t>(r->turns) & 7u) == 0 && r->dim >= 2 &&
+         r->dim % 2 == 0 && r->dim <= MOE_W4A16_MAX_ROTARY_DIM && r->offset >= 0 && r->offset <= head_dim - r->dim &&
+         (r->interleaved == 0 || r->interleaved == 1) && std::isfinite(r->magnitude);
+}
+RotaryView rotary_view(const moe_w4a16_rotary_desc* r) {
+  return RotaryView{r->turns, r->dim, r->offset, r->interleaved, r->magnitude};
+}
+
 }  // namespace
 
 extern "C" {
@@ -192,41 +243,195 @@ moe_w4a16_status moe_w4a16_cache_append(const uint16_t* k, int64_t k_stride, con
                                         const int32_t* tables, int64_t table_stride, int max_pages, int num_seqs,
                                         const int32_t* seq_ids, const int32_t* positions, void* ws, size_t ws_bytes,
                                         moe_w4a16_stream_t stream) {
-  if (num_tokens < 0 || num_heads < 1 || head_dim < 8 || head_dim > (1 << 16) || num_heads > (1 << 12))
-    return MOE_W4A16_ERR_INVALID_ARG;
-  if (cache == nullptr) return MOE_W4A16_ERR_INVALID_ARG;
-  const bool latent = cache->v == nullptr;
-  moe_w4a16_status st = check_pages(cache, num_heads, head_dim, latent);
+  AppendParams p{};
+  const moe_w4a16_status st = append_params(k, k_stride, v, v_stride, num_tokens, num_heads, head_dim, cache, tables,
+                                            table_stride, max_pages, num_seqs, seq_ids, positions, ws, ws_bytes, &p);
+  if (st != MOE_W4A16_OK || p.tokens == 0) return st;
+  MOE_CUDA_TRY(launch_cache_append(p, cache->dtype, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_W4A16_OK;
+}
+
+moe_w4a16_status moe_w4a16_cache_append_rotary(
+    const uint16_t* q, int64_t q_stride, int num_q_heads, uint16_t* q_out, int64_t q_out_stride, const uint16_t* k,
+    int64_t k_stride, const uint16_t* v, int64_t v_stride, int num_tokens, int num_heads, int head_dim,
+    const moe_w4a16_rotary_desc* rotary, const moe_w4a16_pages* cache, const int32_t* tables, int64_t table_stride,
+    int max_pages, int num_seqs, const int32_t* seq_ids, const int32_t* positions, void* ws, size_t ws_bytes,
+    moe_w4a16_stream_t stream) {
+  AppendRotaryParams p{};
+  const moe_w4a16_status st =
+      append_params(k, k_stride, v, v_stride, num_tokens, num_heads, head_dim, cache, tables, table_stride, max_pages,
+                    num_seqs, seq_ids, positions, ws, ws_bytes, &p.a);
   if (st != MOE_W4A16_OK) return st;
-  if (!table_ok(tables, table_stride, max_pages, cache->page_size, num_seqs)) return MOE_W4A16_ERR_INVALID_ARG;
-  if (!ws_fits(ws, ws_bytes, MOE_W4A16_WS_HEADER_BYTES)) return MOE_W4A16_ERR_WORKSPACE;
-  const int64_t width = static_cast<int64_t>(num_heads) * head_dim;
-  if ((v == nullptr) != latent && num_tokens > 0) return MOE_W4A16_ERR_INVALID_ARG;
-  if (k_stride < width || k_stride % 8 != 0 || (!latent && (v_stride < width || v_stride % 8 != 0)))
+  if (!rotary_ok(rotary, head_dim)) return MOE_W4A16_ERR_INVALID_ARG;
+  if (rotary->offset % 8 != 0 || rotary->dim % (rotary->interleaved ? 8 : 16) != 0) return MOE_W4A16_ERR_UNSUPPORTED;
+  if (q != nullptr || q_out != nullptr) {
+    const int64_t width = static_cast<int64_t>(num_q_heads) * head_dim;
+    if (num_q_heads < 1 || num_q_heads > (1 << 16) || q_stride < width || q_out_stride < width || q_stride % 8 != 0 ||
+        q_out_stride % 8 != 0 || (num_tokens > 0 && (q == nullptr || q_out == nullptr)) || !aligned16(q) || !aligned16(q_out))
+      return MOE_W4A16_ERR_INVALID_ARG;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.q_out = q_out;
+    p.q_out_stride = q_out_stride;
+    p.q_heads = num_q_heads;
+  }
+  if (num_tokens == 0) return MOE_W4A16_OK;
+  p.r = rotary_view(rotary);
+  int device = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&device));
+  MOE_CUDA_TRY(launch_cache_append_rotary(p, cache->dtype, device, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_W4A16_OK;
+}
+
+moe_w4a16_status moe_w4a16_rotary_frequencies(int dim, double theta, int scaling, double factor, int trained_length,
+                                              double low, double high, const double* given, uint64_t* turns) {
+  if (turns == nullptr || dim < 2 || dim % 2 != 0 || dim > MOE_W4A16_MAX_ROTARY_DIM) return MOE_W4A16_ERR_INVALID_ARG;
+  if (scaling < MOE_W4A16_ROTARY_NONE || scaling > MOE_W4A16_ROTARY_GIVEN) return MOE_W4A16_ERR_INVALID_ARG;
+  const bool bands = scaling == MOE_W4A16_ROTARY_TURNS || scaling == MOE_W4A16_ROTARY_INDEX;
+  const bool scaled = bands || scaling == MOE_W4A16_ROTARY_LINEAR || scaling == MOE_W4A16_ROTARY_BASE;
+  if (scaling == MOE_W4A16_ROTARY_GIVEN ? given == nullptr : !(theta > 0) || !std::isfinite(theta))
+    return MOE_W4A16_ERR_INVALID_ARG;
+  if (scaled && (!(factor >= 1) || !std::isfinite(factor))) return MOE_W4A16_ERR_INVALID_ARG;
+  if (bands && (trained_length < 1 || !(low > 0) || !(high > low) || !std::isfinite(high))) return MOE_W4A16_ERR_INVALID_ARG;
+  if (scaling == MOE_W4A16_ROTARY_INDEX && theta == 1) return MOE_W4A16_ERR_INVALID_ARG;
+  if (scaling == MOE_W4A16_ROTARY_BASE && dim == 2 && factor != 1) return MOE_W4A16_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  if (scaling == MOE_W4A16_ROTARY_BASE && factor != 1) theta *= std::pow(factor, dim / (dim - 2.0));
+  double edge[2] = {0, 0};                                    // INDEX: the pairs that turn `high` and `low` times
+  if (scaling == MOE_W4A16_ROTARY_INDEX) {
+    const double most = dim - 1;
+    edge[0] = std::floor(dim * std::log(trained_length / (two_pi * high)) / (2 * std::log(theta)));
+    edge[1] = std::ceil(dim * std::log(trained_length / (two_pi * low)) / (2 * std::log(theta)));
+    for (double& e : edge) e = e < 0 ? 0 : e > most ? most : e;
+  }
+  for (int i = 0; i < dim / 2; ++i) {
+    double f = scaling == MOE_W4A16_ROTARY_GIVEN ? given[i] : std::pow(theta, -2.0 * i / dim);
+    if (scaling == MOE_W4A16_ROTARY_LINEAR) f /= factor;
+    if (bands) {
+      double keep = scaling == MOE_W4A16_ROTARY_TURNS
+                        ? (trained_length * f / two_pi - low) / (high - low)
+                        : 1 - (i - edge[0]) / (edge[1] - edge[0] > 0.001 ? edge[1] - edge[0] : 0.001);
+      keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+      f = keep * f + (1 - keep) * f / factor;
+    }
+    if (!std::isfinite(f)) return MOE_W4A16_ERR_INVALID_ARG;
+    const double t = f / two_pi;
+    const double part = t - std::floor(t);                    // turns, modulo one: exact
+    // (two steps, each exact: a double holds no more than 53 of the 64 bits)
+    const double top = std::floor(part * 4294967296.0);
+    const double rest = std::floor((part * 4294967296.0 - top) * 4294967296.0);
+    turns[i] = (static_cast<uint64_t>(top) << 32) + static_cast<uint64_t>(rest);
+  }
+  return MOE_W4A16_OK;
+}
+
+moe_w4a16_status moe_w4a16_rotary(const uint16_t* x, int64_t x_stride, int64_t x_head_stride, const int32_t* positions,
+                                  int num_tokens, int num_heads, int head_dim, const moe_w4a16_rotary_desc* rotary,
+                                  uint16_t* out, int64_t out_stride, int64_t out_head_stride,
+                                  moe_w4a16_stream_t stream) {
+  if (num_tokens < 0 || num_heads < 1 || num_heads > (1 << 16) || head_dim < 2 || head_dim > (1 << 16) ||
+      !rotary_ok(rotary, head_dim))
     return MOE_W4A16_ERR_INVALID_ARG;
   if (num_tokens == 0) return MOE_W4A16_OK;
-  if (k == nullptr || seq_ids == nullptr || positions == nullptr || !aligned16(k) || !aligned16(v))
+  const auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if (x == nullptr || out == nullptr || positions == nullptr || ((bits(x) | bits(out)) & 1u) != 0)
     return MOE_W4A16_ERR_INVALID_ARG;
-  AppendParams p{};
-  p.src[0] = k;
-  p.src[1] = v;
-  p.src_stride[0] = k_stride;
-  p.src_stride[1] = v_stride;
-  p.pages[0] = cache->k;
-  p.pages[1] = cache->v;
-  p.scale[0] = cache->k_scale;
-  p.scale[1] = cache->v_scale;
+  if (x_stride < 0 || x_head_stride < 0) return MOE_W4A16_ERR_INVALID_ARG;
+  // rows of out lie apart: heads within tokens, or tokens within heads
+  const int64_t heads_span = num_heads > 1 ? (num_heads - 1) * out_head_stride : 0;
+  const int64_t tokens_span = num_tokens > 1 ? (num_tokens - 1) * out_stride : 0;
+  const bool by_token = (num_heads == 1 || out_head_stride >= head_dim) &&
+                        (num_tokens == 1 || out_stride >= heads_span + head_dim);
+  const bool by_head = (num_tokens == 1 || out_stride >= head_dim) &&
+                       (num_heads == 1 || out_head_stride >= tokens_span + head_dim);
+  if (!by_token && !by_head) return MOE_W4A16_ERR_INVALID_ARG;
+  if (x == out && ((num_tokens > 1 && x_stride != out_stride) || (num_heads > 1 && x_head_stride != out_head_stride)))
+    return MOE_W4A16_ERR_INVALID_ARG;
+  int64_t units = head_dim | rotary->offset | (rotary->interleaved ? rotary->dim : rotary->dim / 2);
+  if (num_tokens > 1) units |= x_stride | out_stride;
+  if (num_heads > 1) units |= x_head_stride | out_head_stride;
+  int width = 8;
+  while (width > 1 && (units % width != 0 || ((bits(x) | bits(out)) & (2u * width - 1u)) != 0)) width /= 2;
+  RotaryParams p{};
+  p.x = x;
+  p.x_stride = x_stride;
+  p.x_head_stride = x_head_stride;
+  p.positions = positions;
   p.tokens = num_tokens;
   p.heads = num_heads;
   p.dim = head_dim;
+  p.r = rotary_view(rotary);
+  p.out = out;
+  p.out_stride = out_stride;
+  p.out_head_stride = out_head_stride;
+  int device = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&device));
+  MOE_CUDA_TRY(launch_rotary(p, width, device, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_W4A16_OK;
+}
+
+moe_w4a16_status moe_w4a16_paged_chunk_workspace_size(int num_heads, int num_kv_heads, int head_dim, size_t* bytes) {
+  if (bytes == nullptr || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0)
+    return MOE_W4A16_ERR_INVALID_ARG;
+  if (head_dim < 16 || head_dim % 16 != 0 || head_dim > MOE_W4A16_MAX_HEAD_DIM) return MOE_W4A16_ERR_UNSUPPORTED;
+  // header | the one-token calls' counters, left alone | scratch
+  *bytes = kBlockWsOffset + chunk_scratch_bytes(num_heads, num_kv_heads, head_dim);
+  return MOE_W4A16_OK;
+}
+
+moe_w4a16_status moe_w4a16_paged_chunk_attention(const uint16_t* q, int64_t q_stride, int num_tokens,
+                                                 const int32_t* starts, int batch, int num_heads, int num_kv_heads,
+                                                 int head_dim, const moe_w4a16_pages* cache, const int32_t* tables,
+                                                 int64_t table_stride, int max_pages, const int32_t* lens,
+                                                 const int32_t* seq_ids, int num_seqs, float scale, int window,
+                                                 uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                                 moe_w4a16_stream_t stream) {
+  if (num_tokens < 0 || batch < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || window < 0 ||
+      !std::isfinite(scale))
+    return MOE_W4A16_ERR_INVALID_ARG;
+  if (head_dim < 16 || head_dim % 16 != 0 || head_dim > MOE_W4A16_MAX_HEAD_DIM) return MOE_W4A16_ERR_UNSUPPORTED;
+  moe_w4a16_status st = check_pages(cache, num_kv_heads, head_dim, false);
+  if (st != MOE_W4A16_OK) return st;
+  if (static_cast<int64_t>(num_tokens) * num_heads >= (int64_t(1) << 31)) return MOE_W4A16_ERR_UNSUPPORTED;
+  size_t need = 0;
+  st = moe_w4a16_paged_chunk_workspace_size(num_heads, num_kv_heads, head_dim, &need);
+  if (st != MOE_W4A16_OK) return st;
+  if (!ws_fits(ws, ws_bytes, need)) return MOE_W4A16_ERR_WORKSPACE;
+  if (num_tokens == 0 || batch == 0) return MOE_W4A16_OK;
+  if (q == nullptr || out == nullptr || lens == nullptr || starts == nullptr || !aligned16(q) || !aligned16(out) ||
+      q_stride % 8 != 0 || q_stride < static_cast<int64_t>(num_heads) * head_dim)
+    return MOE_W4A16_ERR_INVALID_ARG;
+  if (seq_ids == nullptr && num_seqs < batch) return MOE_W4A16_ERR_INVALID_ARG;
+  if (!table_ok(tables, table_stride, max_pages, cache->page_size, num_seqs)) return MOE_W4A16_ERR_INVALID_ARG;
+  ChunkParams p{};
+  p.q = q;
+  p.q_stride = q_stride;
+  p.tokens = num_tokens;
+  p.starts = starts;
+  p.batch = batch;
+  p.heads = num_heads;
+  p.kv_heads = num_kv_heads;
+  p.group = num_heads / num_kv_heads;
+  p.dim = head_dim;
+  p.k = cache->k;
+  p.v = cache->v;
   p.page_stride = cache->page_stride;
   p.token_stride = cache->token_stride;
   p.head_stride = cache->head_stride;
   p.t = table_view(tables, table_stride, max_pages, cache->page_size, cache->num_pages, num_seqs);
+  p.lens = lens;
   p.seq_ids = seq_ids;
-  p.positions = positions;
+  p.score_scale = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
+  p.v_scale = cache->v_scale;
+  p.window = window;
+  p.out = out;
+  p.lse = lse;
   p.err = static_cast<int*>(ws);
-  MOE_CUDA_TRY(launch_cache_append(p, cache->dtype, reinterpret_cast<cudaStream_t>(stream)));
+  p.scratch = static_cast<uint8_t*>(ws) + kBlockWsOffset;
+  int device = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&device));
+  p.wait_ns = wait_limit_ns(device);
+  MOE_CUDA_TRY(launch_chunk_attention(p, cache->dtype, device, reinterpret_cast<cudaStream_t>(stream)));
   return MOE_W4A16_OK;
 }
 
