@@ -203,6 +203,22 @@ def test_long_rows_are_split_and_joined(batch, new, top, hkv, group, e4m3):
         assert torch.equal(a[:rows], b[:rows]) and torch.equal(la[:rows], lb[:rows])
 
 
+@pytest.mark.parametrize("dim,e4m3", [(128, False), (128, True), (64, False), (256, False), (256, True)])
+def test_many_chunks_of_odd_and_even_numbers_of_tiles(dim, e4m3):
+    """Batches whose rows' tiles are shared by both halves of a CTA, beside ones that are not, over pages that come from
+    HBM: no tile may be taken for another one's."""
+    rng = np.random.default_rng(dim + e4m3)
+    page, batch = 64, 40
+    for most in (4, 300):
+        chunks = [(int(rng.integers(1, most)) if rng.random() < 0.4 else 1, 0) for _ in range(batch)]
+        chunks = [(c, c + int(rng.integers(0, 3000))) for c, _ in chunks]
+        lens = [n for _, n in chunks]
+        tables, total = tables_for(rng, lens, page)
+        k, v = make_pages(rng, total, page, 4, dim, e4m3)
+        starts = starts_of([c for c, _ in chunks])
+        check(queries(rng, starts[-1], 16, dim, 1.5), starts, k, v, tables, lens)
+
+
 @pytest.mark.parametrize("dim,e4m3", [(128, False), (128, True), (256, False), (256, True), (96, False)])
 def test_wide_heads_split_and_joined(dim, e4m3):
     rng = np.random.default_rng(dim)

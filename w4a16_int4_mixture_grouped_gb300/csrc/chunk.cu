@@ -1,8 +1,27 @@
 // Attention of a chunk of new tokens per sequence over a paged cache, grouped heads.
 //
-// One warp a query row (token and head): lanes take 32 tokens' scores at a time, the softmax runs with a maximum and
-// a sum of its own, and lanes take channels for the value product.
-#include <cuda_fp8.h>
+// The query rows of a cache head -- its `group` heads times the chunk's tokens -- are the rows of one product with each
+// tile of 128 tokens:
+//
+//   S [rows x tokens] = Q [rows x D] . K^T          both operands in shared memory
+//   O [rows x D]     += P [rows x tokens] . V       P = exp2(S - base) in tensor memory, over its own S
+//
+// so keys and values are read once for up to 256 rows (two streams of 128; 129 to 256 channels: 128 rows), and a prompt is
+// bound by the tensor pipe, drafts by HBM. Both products run on tcgen05 with FP32 accumulators in TMEM.
+//
+//   * A CTA has two streams, each with its rows' queries, scores and accumulator, an issuing warp and four softmax
+//     warps, a thread a row. While one stream's softmax runs, the tensor pipe works for the other: O += P V of its last
+//     tile and S of its next. Rows of a chunk that fit one stream: both streams take the same rows and every other tile,
+//     and their accumulators are joined at the end.
+//   * 129 to 256 channels: one stream, as its accumulator takes half of TMEM; its scores have two buffers, and the next
+//     tile's are computed during a tile's softmax.
+//   * The base of a row's exponents moves when a score passes it by 2^8, not with every new maximum (BF16 probabilities keep
+//     their relative precision, FP32 sums their range), so the accumulator is seldom rescaled.
+//   * Four warps gather the tiles, token by token through the page table, with cp.async into a ring of 128-byte swizzled
+//     tiles (E4M3: into a buffer of their own, converted to FP16 on the way to the ring, exactly).
+//   * Every CTA takes an equal share of one line of tiles over all sequences, heads and row blocks, whatever the lengths;
+//     rows that cross CTAs are written as FP32 parts, which a second kernel joins in order.
+//   * Unseen slots (past the end, freed pages) are not read: their rows are zero-filled and their scores -infinity.
 #include <cuda_runtime.h>
 
 #include "block.h"
@@ -11,96 +30,1135 @@
 namespace moe {
 namespace chunk {
 
-constexpr int kWarps = 8;
-constexpr int kMaxDim = MOE_W4A16_MAX_HEAD_DIM;
+constexpr int kTile = 128;                    // tokens of a tile
+constexpr int kRows = 128;                    // query rows of a stream (MMA M)
+constexpr int kMaxCtas = 152;
+constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
+constexpr int kMaskBufs = 8;                  // tiles whose masks of seen tokens are kept
+constexpr int kChunkBytes = 128 * 128;        // 64 channels of 128 rows, 128-byte swizzled
 
-template <bool E4M3>
-__device__ __forceinline__ float element(const void* p, int64_t at) {
-  if (E4M3) {
-    __nv_fp8_e4m3 x;
-    x.__x = static_cast<const uint8_t*>(p)[at];
-    return static_cast<float>(x);
-  }
-  return bf16_to_f32(static_cast<const uint16_t*>(p)[at]);
+// warps: 0-3 and 4-7 the streams' softmax, 8-11 loaders, 12 and 13 issuers
+constexpr int kThreads = 512;
+// registers of a softmax thread and of the others: 256 x 184 + 256 x 72 = 512 x 128, what the launch has
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+
+template <int DP, bool E4M3>
+struct Cfg {
+  static constexpr bool kWide = DP == 256;
+  static constexpr int kStreams = kWide ? 1 : 2;
+  static constexpr int kUnitCh = DP < 128 ? DP : 128;              // channels of a ring slot
+  static constexpr int kHalves = DP / kUnitCh;                     // slots of a tile's keys, and of its values
+  static constexpr int kUnitBytes = kUnitCh / 64 * kChunkBytes;
+  static constexpr int kQBytes = DP / 64 * kChunkBytes;            // a stream's queries
+  static constexpr int kSlots = DP == 64 ? 8 : kWide && !E4M3 ? 5 : 4;
+  static constexpr int kLag = E4M3 ? 1 : 2;                        // units in flight behind the newest
+  static constexpr int kStages = kLag + 1;                         // raw 8-bit units of a loader warp
+  static constexpr int kStageBytes = 32 * kUnitCh;
+  static constexpr int kRingOff = kStreams * kQBytes;
+  static constexpr int kRawOff = kRingOff + kSlots * kUnitBytes;
+  static constexpr int kMiscOff = kRawOff + (E4M3 ? 4 * kStages * kStageBytes : 0);
+  static constexpr int kPartRows = kStreams * kRows;
+  static constexpr int kPartFloats = (2 + DP) * kPartRows;         // a part of a row block: bases, sums, O as [channel][row]
+};
+
+enum {
+  kBarFull = 0,                  // [8] ring slot loaded
+  kBarFree = 8,                  // [8] ring slot read by every product that takes it
+  kBarQ = 16,                    // [2] a stream's queries loaded
+  kBarScore = 18,                // [2] S of a tile computed (a stream's; wide: a buffer's)
+  kBarProb = 20,                 // [2] P of a tile written, O rescaled if need be
+  kBarOut = 22,                  // [2] O of a piece complete (wide: of a tile, even and odd ones)
+  kBarOutFree = 24,              // [2] O of a piece read
+  kBarPiece = 26,                // [4] piece listed
+  kBarPieceFree = 30,            // [4] piece done with by all warps
+  kBarBases = 34,                // bases and sums of a piece's two accumulators written, then read
+  kBarDrain = 35,                // [2]
+  kNumBars = 37
+};
+constexpr int kPieces = 4;       // pieces listed ahead
+constexpr int kUsers = 14;       // warps that read them
+
+// Where a CTA's share of the line of tiles begins.
+struct Share {
+  int64_t total, x, x_end, first, seq;       // seq: tiles of a work row of sequence b
+  int ctas, b, r, qt, tile;
+  int64_t sums[kThreads / 32];
+};
+// Some tiles of one block of rows: `n` tokens of a sequence's chunk, work row r. (tiles = 0: the share is done.)
+struct Piece {
+  int token, pos, n, r;          // the first token's row of q and position
+  int row, lo, hi;               // row of the tables, tokens [lo, hi) seen by the block
+  int j0, tiles;                 // token at which the first tile begins
+  int c0, c1;                    // CTAs that the block's tiles fall to
+};
+struct Misc {
+  unsigned long long bars[kNumBars];
+  uint32_t tmem;
+  int abort_flag;
+  uint32_t masks[kMaskBufs][4];              // seen tokens of a tile
+  Piece pieces[kPieces];
+  union {
+    float2 ml[2][kRows];                     // [stream] bases and sums of a piece's rows
+    Share share;                             // (before the roles part)
+  };
+};
+
+// How the rows of a chunk fall into blocks: `tokens` tokens of up to 128 heads of a cache head's group a stream.
+struct Blocks {
+  int heads;      // query heads of a block (of the last one of a cache head: fewer), rows of a token
+  int count;      // blocks of a cache head
+  int tokens;     // tokens of a stream
+};
+__host__ __device__ __forceinline__ Blocks blocks_of(int group) {
+  if (group <= kRows) return Blocks{group, 1, kRows / group};
+  return Blocks{kRows, (group + kRows - 1) / kRows, 1};
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) chunk_kernel(const ChunkParams p) {
-  __shared__ float q_s[kWarps][kMaxDim];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-  const ChunkRange c = chunk_range(p, b);
-  const int64_t rows = int64_t(c.n) * p.heads;
-  for (int64_t r = int64_t(blockIdx.x) * kWarps + warp; r < rows; r += int64_t(gridDim.x) * kWarps) {
-    const int i = static_cast<int>(r / p.heads), h = static_cast<int>(r % p.heads), tok = c.first + i;
-    const int pos = c.base + i, hi = c.row < 0 ? 0 : pos + 1, lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
-    const int64_t head = int64_t(h / p.group) * p.head_stride;
-    __syncwarp();
-    for (int d = lane; d < p.dim; d += 32) q_s[warp][d] = bf16_to_f32(p.q[tok * p.q_stride + int64_t(h) * p.dim + d]);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[kMaxDim / 32];
+__device__ __forceinline__ int tiles_of(int lo, int hi) { return hi > lo ? (hi - 1) / kTile + 1 - lo / kTile : 0; }
+// Seen tokens [lo, hi) of the n tokens from the i-th of a chunk on.
+__device__ __forceinline__ void seen_by(const ChunkParams& p, const ChunkRange& c, int i, int n, int& lo, int& hi) {
+  const int first = c.base + i;
+  hi = first + n;
+  lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
+  if (c.row < 0 || hi < 0) hi = 0;
+}
+__device__ __forceinline__ int64_t tiles_of_row(const ChunkParams& p, const ChunkRange& c, int step) {
+  int64_t sum = 0;
+  for (int64_t i = 0; i < c.n; i += step) {
+    int lo, hi;
+    seen_by(p, c, static_cast<int>(i), static_cast<int>(min(int64_t(step), c.n - i)), lo, hi);
+    sum += tiles_of(lo, hi);
+  }
+  return sum;
+}
+__device__ __forceinline__ int64_t cta_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
+  return static_cast<int>(((x + 1) * ctas - 1) / total);
+}
+
+// Fills *sh for CTA `cta` of `grid` (every thread calls it): sequence after sequence, their `rows` work rows (cache heads x
+// head blocks) one after the other, each the tiles of its blocks of `step` tokens. False: no work.
+__device__ __forceinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t line = 0;                                   // tiles of the sequences before these
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int64_t n = b < p.batch ? tiles_of_row(p, chunk_range(p, b), step) : 0;
+      int64_t pre = n;
 #pragma unroll
-    for (int k = 0; k < kMaxDim / 32; ++k) o[k] = 0.f;
-    const int32_t* table = p.t.tables + int64_t(c.row < 0 ? 0 : c.row) * p.t.table_stride;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-      const int j = j0 + lane;
-      int64_t at = -1;
-      if (j < hi) {
-        const int page = table[j / p.t.page_size];
-        if (page >= p.t.num_pages) set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
-        else if (page >= 0) at = int64_t(page) * p.page_stride + int64_t(j % p.t.page_size) * p.token_stride + head;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += y;
       }
-      float s = -INFINITY;
-      if (at >= 0) {
-        s = 0.f;
-        for (int d = 0; d < p.dim; ++d) s = fmaf(q_s[warp][d], element<E4M3>(p.k, at + d), s);
-        s *= p.score_scale;
+      __syncthreads();
+      if (lane == 31) sh->sums[warp] = pre;
+      __syncthreads();
+      int64_t before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sh->sums[w];
+        all += sh->sums[w];
       }
-      float top = s;
+      const int64_t at = line + (before + pre - n) * rows;
+      line += all * rows;
+      if (pass == 0 && b0 + kThreads >= p.batch) {
+        if (threadIdx.x == 0) {
+          int64_t ctas = line / kMinTiles;
+          ctas = ctas < 1 ? 1 : ctas > grid ? grid : ctas;
+          const bool work = line > 0 && cta < ctas;
+          sh->total = line;
+          sh->ctas = static_cast<int>(ctas);
+          sh->x = work ? cta_begin(line, static_cast<int>(ctas), cta) : 0;
+          sh->x_end = work ? cta_begin(line, static_cast<int>(ctas), cta + 1) : 0;
+        }
+        __syncthreads();
+        if (sh->x >= sh->x_end) return false;
+      }
+      // the sequence in which the share begins (one round of sequences: without a second pass)
+      if ((pass == 1 || p.batch <= kThreads) && n > 0 && sh->x >= at && sh->x < at + n * rows) {
+        sh->b = b;
+        sh->first = at;
+        sh->seq = n;
+      }
+      if (pass == 1 && sh->x < line) break;
+    }
+    if (p.batch <= kThreads) break;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // the work row, the block of tokens and the tile
+    const ChunkRange c = chunk_range(p, sh->b);
+    int64_t y = sh->x - sh->first;
+    const int r = static_cast<int>(y / sh->seq);
+    y -= r * sh->seq;
+    for (int q0 = 0; q0 * int64_t(step) < c.n; q0 += 32) {
+      const int64_t i = (q0 + lane) * int64_t(step);
+      int lo, hi, n = 0;
+      if (i < c.n) {
+        seen_by(p, c, static_cast<int>(i), min(step, c.n - static_cast<int>(i)), lo, hi);
+        n = tiles_of(lo, hi);
+      }
+      int64_t pre = n;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-      top = fmaxf(top, m);
-      const float base = top == -INFINITY ? 0.f : top, keep = exp2f(m - base);
-      const float e = at >= 0 ? exp2f(s - base) : 0.f;
-      float sum = e;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += v;
+      }
+      if (y < pre && y >= pre - n) {
+        sh->r = r;
+        sh->qt = q0 + lane;
+        sh->tile = static_cast<int>(y - (pre - n));
+      }
+      const int64_t sum = __shfl_sync(0xffffffffu, pre, 31);
+      if (y < sum) break;
+      y -= sum;
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// A walk through a CTA's share.
+struct Walk {
+  int64_t x, x_end, total;
+  ChunkRange c;
+  int b, r, qt, tile, ctas;
+  __device__ __forceinline__ void start(const ChunkParams& p, const Share& sh) {
+    x = sh.x;
+    x_end = sh.x_end;
+    total = sh.total;
+    ctas = sh.ctas;
+    b = sh.b;
+    r = sh.r;
+    qt = sh.qt;
+    tile = sh.tile;
+    c = chunk_range(p, b);
+  }
+  __device__ __forceinline__ bool next(const ChunkParams& p, int rows, int step, Piece& o) {
+    while (x < x_end) {
+      const int64_t i = qt * int64_t(step);
+      if (i >= c.n) {                              // the next work row, or sequence
+        qt = 0;
+        if (++r >= rows || c.n == 0) {
+          r = 0;
+          if (++b >= p.batch) return false;
+          c = chunk_range(p, b);
+        }
+        continue;
+      }
+      o.n = min(step, c.n - static_cast<int>(i));
+      seen_by(p, c, static_cast<int>(i), o.n, o.lo, o.hi);
+      const int ntiles = tiles_of(o.lo, o.hi);
+      ++qt;
+      if (ntiles == 0) continue;
+      const int64_t row0 = x - tile;               // line position of the block's first tile
+      o.token = c.first + static_cast<int>(i);
+      o.pos = c.base + static_cast<int>(i);
+      o.r = r;
+      o.row = c.row;
+      o.j0 = (o.lo / kTile + tile) * kTile;
+      o.tiles = static_cast<int>(min(int64_t(ntiles - tile), x_end - x));
+      o.c0 = cta_of(total, ctas, row0);
+      o.c1 = cta_of(total, ctas, row0 + ntiles - 1);
+      x += o.tiles;
+      tile = 0;
+      return true;
+    }
+    return false;
+  }
+};
+
+// What a CTA left for the join: a block of rows that starts in it and goes on in the next np - 1.
+struct Record {
+  int32_t np, token, n, r;                        // first token of q, tokens, work row
+};
+
+// ---------------------------------------------------------------------------
+// tensor memory and tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A in tensor memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A thread's lane and N columns from `addr` on.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+      "}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+      "%28,%29,%30,%31"
+      "}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// The 128 columns of a score tile; the loads are in flight together, and nothing reads r before the wait.
+__device__ __forceinline__ void tmem_ld_tile(uint32_t addr, uint32_t (&r)[128]) {
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
-      l = l * keep + sum;
-      m = top;
+  for (int k = 0; k < 4; ++k) tmem_ld32(addr + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * k));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-      for (int k = 0; k < kMaxDim / 32; ++k) o[k] *= keep;
-      for (int t = 0; t < 32; ++t) {
-        const int64_t v = __shfl_sync(~0u, at, t);
-        const float w = __shfl_sync(~0u, e, t);
-        if (v < 0) continue;
-#pragma unroll
-        for (int k = 0; k < kMaxDim / 32; ++k)
-          if (k * 32 + lane < p.dim) o[k] = fmaf(w, element<E4M3>(p.v, v + k * 32 + lane), o[k]);
+  for (int k = 0; k < 128; ++k) asm volatile("" : "+r"(r[k]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8"
+      "};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
+      "};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Operand tiles are rows of 128 bytes in 128-byte swizzle, 8-row groups of 1024 bytes. K-major (rows along M or N, 64
+// channels of the reduction a row): groups follow each other along the rows. N-major (rows along the reduction, 64 channels
+// of N a row): groups follow each other along the reduction, the next 64 channels are a chunk further.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return (static_cast<uint64_t>((addr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(kChunkBytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// kind::f16, FP32 accumulator, M = 128; bit 16: B N-major.
+__device__ __forceinline__ uint32_t instr_desc(bool f16, int n, bool n_major) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(kRows >> 4) << 24) | (n_major ? 1u << 16 : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// arithmetic
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
+  return r;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+// Bits below x of a word of 32.
+__device__ __forceinline__ uint32_t bits_below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
+
+// warp_wait without a call: one would keep the softmax warps from their registers.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, uint64_t limit) {
+  const bool suspend = limit >= kSuspendNs;
+  if (suspend && __all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_poll(bar, parity, suspend))) return true;
+    int stop = 0;
+    if ((threadIdx.x & 31) == 0) {
+      if (*abort_flag) {
+        stop = 1;
+      } else if (global_timer_ns() - t0 >= limit) {
+        set_error(err, MOE_W4A16_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+        stop = 1;
       }
     }
-    const float inv = l == 0.f ? 0.f : p.v_scale / l;
-    uint16_t* out = p.out + (int64_t(tok) * p.heads + h) * p.dim;
+    if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+  }
+}
+
+// Rows that stand before their sequence's first token, or have none: zeros and -infinity, spread over the CTAs.
+__device__ __forceinline__ void zero_unseeing(const ChunkParams& p) {
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    const ChunkRange c = chunk_range(p, b);
+    const int n = c.row < 0 ? c.n : c.base < 0 ? min(c.n, -c.base) : 0;
+    if (n == 0) continue;
+    uint4* out = reinterpret_cast<uint4*>(p.out + int64_t(c.first) * p.heads * p.dim);
+    for (int64_t e = threadIdx.x; e < int64_t(n) * p.heads * p.dim / 8; e += kThreads) out[e] = make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr)
+      for (int64_t h = threadIdx.x; h < int64_t(n) * p.heads; h += kThreads) p.lse[int64_t(c.first) * p.heads + h] = -INFINITY;
+  }
+}
+
+template <int DP, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p, Record* records, float* parts) {
+  using C = Cfg<DP, E4M3>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc& misc = *reinterpret_cast<Misc*>(smem + C::kMiscOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem), bars = smem_u32(misc.bars);
+  auto bar = [&](int i) { return bars + 8 * i; };
+  volatile int* abort_flag = &misc.abort_flag;
+  const Blocks blocks = blocks_of(p.group);
+  const int rows = p.kv_heads * blocks.count, step = C::kStreams * blocks.tokens;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  zero_unseeing(p);
+  if (threadIdx.x == 0) records[blockIdx.x].np = 0;
+  if (!find_share(p, blockIdx.x, gridDim.x, rows, step, &misc.share)) return;
+  if ((base & 1023u) != 0) {                 // the swizzle is a function of address bits
+    if (threadIdx.x == 0) set_error(p.err, MOE_W4A16_ERR_CUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(bar(kBarFull + i), 4);
+      mbar_init(bar(kBarFree + i), C::kStreams);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarQ + i), 4);
+      mbar_init(bar(kBarScore + i), 1);
+      mbar_init(bar(kBarProb + i), 4);
+      mbar_init(bar(kBarOut + i), 1);
+      mbar_init(bar(kBarOutFree + i), 4 * C::kStreams);
+      mbar_init(bar(kBarDrain + i), 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bar(kBarPiece + i), 1);
+      mbar_init(bar(kBarPieceFree + i), C::kWide ? kUsers - 5 : kUsers);
+    }
+    mbar_init(bar(kBarBases), 8);
+    misc.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&misc.tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&misc.tmem);
+  const uint32_t ring = base + C::kRingOff;
+  auto wait = [&](int i, uint32_t parity) { return wait_inline(bar(i), parity, abort_flag, p.err, p.wait_ns); };
+  // scores enter the exponentials as |scale| s, the queries negated where the scale is negative (zeroed where it is zero,
+  // so that the factor itself is never zero: an unseen token's -infinity stays one)
+  const bool flat = p.score_scale == 0.f, negate = p.score_scale < 0.f;
+  const float abs_scale = flat ? 1.f : fmaxf(fabsf(p.score_scale), 1.2e-38f);
+  constexpr int kAcc = 256;                              // columns: scores at 0 and 128, accumulators from 256 on
+
+  Walk walk;
+  if (warp == 14) walk.start(p, misc.share);
+  __syncthreads();                                       // (the share's memory is the bases' from here on)
+  // the k-th piece, listed by warp 14; freed once by each of the warps that read it
+  auto piece = [&](uint32_t k) -> const Piece& { return misc.pieces[k % kPieces]; };
+  auto piece_there = [&](uint32_t k) { return wait(kBarPiece + k % kPieces, (k / kPieces) & 1u); };
+  auto piece_done = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarPieceFree + k % kPieces));
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax, a thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int s = warp >> 2, rr = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    if (!C::kWide || s == 0) {
+      const int trow = rr / blocks.heads, hrow = rr - trow * blocks.heads;   // token and head of the row
+      const uint32_t qs = base + s * C::kQBytes + (warp & 3) * 32 * 128;     // this warp's 32 rows
+      uint32_t n_score = 0, n_out[2] = {0, 0}, n_tile = 0, n_bases = 0, k = 0;
+      auto split_of = [&](const Piece& x) { return C::kWide || x.n <= blocks.tokens; };
+      // This thread's row of a block: token relative to the block's first (-1: none), query head.
+      auto token_of = [&](const Piece& x) {
+        const int t = trow + (s == 1 && !split_of(x) ? blocks.tokens : 0);
+        return trow < blocks.tokens && t < x.n && x.r % blocks.count * blocks.heads + hrow < p.group ? t : -1;
+      };
+      auto head_of = [&](const Piece& x) { return x.r / blocks.count * p.group + x.r % blocks.count * blocks.heads + hrow; };
+      auto load_queries = [&](const Piece& x) {
+        const int t = token_of(x);
+        const int64_t off = t >= 0 && !flat ? int64_t(x.token + t) * p.q_stride + int64_t(head_of(x)) * p.dim : -1;
+        if (__any_sync(0xffffffffu, t >= 0)) {
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {
+            const int r = j * 4 + (lane >> 3);
+            const int64_t o = __shfl_sync(0xffffffffu, off, r);
+            const uint32_t to = qs + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
 #pragma unroll
-    for (int k = 0; k < kMaxDim / 32; ++k)
-      if (k * 32 + lane < p.dim) out[k * 32 + lane] = f32_to_bf16_rn(o[k] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[int64_t(tok) * p.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            for (int c = 0; c < DP / 64; ++c) {
+              const int ch = c * 64 + (lane & 7) * 8;
+              if (ch < p.dim) cp_async16(to + c * kChunkBytes, p.q + (o >= 0 ? o + ch : 0), o >= 0 ? 16 : 0);
+            }
+          }
+        }
+        cp_async_commit();
+      };
+      // Queries in place: E4M3: in FP16, scaled by a power of two. -> the row's factor of the scores.
+      auto finish_queries = [&]() {
+        cp_async_wait<0>();
+        __syncwarp();
+        float factor = abs_scale;
+        const uint32_t row = qs + lane * 128;
+        auto at = [&](int c16) { return row + (c16 >> 3) * kChunkBytes + (((c16 & 7) ^ (lane & 7)) << 4); };
+        const uint32_t flip = negate ? 0x80008000u : 0u;
+        if (E4M3) {
+          float top = 0.f;
+#pragma unroll 4
+          for (int c = 0; c < p.dim / 8; ++c) {
+            const uint4 v = lds128(at(c));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+          }
+          // top in [2^e, 2^(e+1)): scale by 2^(15-e) (two factors, each a normal number for any e), to below 2^16, where
+          // the FP16 range ends: channels keep their eight bits down to 2^-32 of the largest, and end at 2^-40 of it
+          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          if (top == 0.f || e > 127) e = 15;
+          e = max(e, -126) - 15;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
+          const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
+          factor = fmaxf(abs_scale * __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23) *
+                             __uint_as_float(static_cast<uint32_t>(127 + (e - e / 2)) << 23),
+                         1.2e-38f);
+#pragma unroll 2
+          for (int c = 0; c < p.dim / 8; ++c) {
+            const uint4 v = lds128(at(c));
+            uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack_f16x2_rn(__uint_as_float(w[j] << 16) * down * down2,
+                                   __uint_as_float(w[j] & 0xffff0000u) * down * down2);
+            sts128(at(c), w[0], w[1], w[2], w[3]);
+          }
+        } else if (negate) {
+          for (int c = 0; c < p.dim / 8; ++c) {
+            const uint4 v = lds128(at(c));
+            sts128(at(c), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQ + s));
+        return factor;
+      };
+
+      bool ok = piece_there(0);
+      float factor = 0.f;
+      if (ok && piece(0).tiles > 0) {
+        load_queries(piece(0));
+        factor = finish_queries();
+      }
+      while (ok) {
+        const int n = piece(k).tiles;
+        if (n == 0 || !(ok = piece_there(k + 1))) break;
+        const bool split = split_of(piece(k)), have_next = piece(k + 1).tiles > 0;
+        const int token = token_of(piece(k)), pos = piece(k).pos + token, j_first = piece(k).j0;
+        const bool active = __any_sync(0xffffffffu, token >= 0);
+        const int stride = !C::kWide && split ? 2 : 1, first = stride == 2 ? s : 0;
+        float m = -INFINITY, l = 0.f, next_factor = 0.f;
+        // what the exponents are taken against: a maximum that is taken when a score passes it by 2^kSlack. E4M3: FP16
+        // probabilities of 2^kLift to 2^15, which keep their bits down to 2^-22 of the largest, and end at 2^-32 of it
+        constexpr float kLift = E4M3 ? 8.f : 0.f, kSlack = E4M3 ? 7.f : 8.f;
+        for (int i = first; i < n; i += stride, ++n_score) {
+          const int buf = C::kWide ? n_score & 1 : s;
+          const uint32_t par = C::kWide ? (n_score >> 1) & 1u : n_score & 1u;
+          const uint32_t score = tmem + buf * 128 + lanes;
+          if (!(ok = wait(kBarScore + buf, par))) break;
+          tc_fence_after();
+          if (i + stride >= n && have_next) load_queries(piece(k + 1));      // the last product with these is done
+          if (active) {
+            uint32_t r[128];
+            tmem_ld_tile(score, r);
+            const int j0 = j_first + i * kTile;
+            const int above = pos - j0 + 1;                                  // tokens of the tile up to the row's own
+            const int below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
+            const volatile uint32_t* seen = misc.masks[(n_tile + i) % kMaskBufs];
+            const bool part = above < kTile || below > 0 || (seen[0] & seen[1] & seen[2] & seen[3]) != 0xffffffffu;
+            if (__any_sync(0xffffffffu, part)) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t w = seen[q] & bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!(w >> j & 1u)) r[32 * q + j] = 0xff800000u;
+              }
+            }
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 128; e += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                top4[j] = fmaxf(fmaxf(top4[j], __uint_as_float(r[e + 2 * j])), __uint_as_float(r[e + 2 * j + 1]));
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
+            const bool over = top > m + kSlack;                              // (m of -infinity: any seen score)
+            if (__any_sync(0xffffffffu, over)) {
+              float keep = 1.f;
+              if (over) {
+                keep = exp2_fast(m - top);
+                m = top;
+              }
+              l *= keep;
+              if (i != first) {
+                if (C::kWide) {                                              // the previous tile's product is done
+                  if (!(ok = wait(kBarOut + ((n_score - 1) & 1), ((n_score - 1) >> 1) & 1u))) break;
+                  tc_fence_after();
+                }
+                const uint32_t acc = tmem + kAcc + s * 128 + lanes;
+#pragma unroll 1
+                for (int c = 0; c < p.dim; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(acc + c, o);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                  tmem_st16(acc + c, o);
+                }
+              }
+            }
+            const float off = kLift - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint32_t packed[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int e = 16 * q + 2 * j;
+                const float x = exp2_fast(fmaf(__uint_as_float(r[e]), factor, off));
+                const float y = exp2_fast(fmaf(__uint_as_float(r[e + 1]), factor, off));
+                r[e] = __float_as_uint(x);
+                r[e + 1] = __float_as_uint(y);
+                packed[j] = E4M3 ? pack_f16x2_rn(x, y) : pack_bf16x2_rn(x, y);
+              }
+              tmem_st8(score + 8 * q, packed);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarProb + buf));
+            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 128; e += 4)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sum4[j] += __uint_as_float(r[e + j]);
+            l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarProb + buf));
+          }
+        }
+        if (!ok) break;
+        if (have_next && first < n) next_factor = finish_queries();
+
+        // ---- epilogue: O / l, or a part of it
+        const Piece& pc = piece(k);
+        const bool whole = pc.c0 == pc.c1;
+        const bool two = !C::kWide && split;             // both streams hold accumulators of the same rows
+        float f0 = 1.f, f1 = 0.f;
+        m -= kLift;
+        if (two) {
+          misc.ml[s][rr] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarBases));
+          if (!(ok = wait(kBarBases, n_bases++ & 1u))) break;
+          const float2 a = misc.ml[0][rr], b = misc.ml[1][rr];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarBases));
+          if (!(ok = wait(kBarBases, n_bases++ & 1u))) break;                // read before the next piece's are written
+          // (no tile for this stream: the next queries only now, when every warp has handed over this piece's)
+          if (first >= n && have_next) load_queries(piece(k + 1));
+          m = fmaxf(a.x, b.x);
+          const float at = m == -INFINITY ? 0.f : m;
+          f0 = exp2_fast(a.x - at);
+          f1 = exp2_fast(b.x - at);
+          l = a.y * f0 + b.y * f1;
+        }
+        if (C::kWide) {
+          ok = wait(kBarOut + ((n_score - 1) & 1), ((n_score - 1) >> 1) & 1u);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (!two || q < n) {
+              if (ok && (two || q == s)) ok = wait(kBarOut + q, n_out[q] & 1u);
+              ++n_out[q];
+            }
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          const bool valid = token >= 0;
+          const int64_t out_row = int64_t(pc.token + token) * p.heads + head_of(pc);
+          float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == pc.c0 ? 1 : 0)) * C::kPartFloats +
+                        (two || C::kWide ? rr : s * kRows + rr);
+          if (valid && (!two || s == 0)) {
+            if (!whole) {
+              __stcg(part, m);
+              __stcg(part + C::kPartRows, l);
+            } else if (p.lse != nullptr) {
+              p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+            }
+          }
+          const float inv = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
+          f0 *= inv;
+          f1 *= inv;
+          const int half = (p.dim / 16 + 1) / 2 * 16;    // two: a stream's warps take half of the channels each
+          const int from = two && s == 1 ? half : 0, to = two && s == 0 ? half : p.dim;
+          const bool second = two && n > 1;
+#pragma unroll 1
+          for (int c = from; c < to; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tmem + kAcc + (two ? 0 : s * 128) + c + lanes, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+            if (second) {
+              uint32_t o1[16];
+              tmem_ld16(tmem + kAcc + 128 + c + lanes, o1);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+            }
+            if (!valid) continue;
+            if (whole) {
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2_rn(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+              uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * p.dim + c);
+              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) __stcg(part + (2 + c + j) * C::kPartRows, __uint_as_float(o[j]));
+            }
+          }
+        }
+        if (!whole && static_cast<int>(blockIdx.x) == pc.c0 && threadIdx.x == 0)
+          records[blockIdx.x] = Record{pc.c1 - pc.c0 + 1, pc.token, pc.n, pc.r};
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (C::kWide) {
+            mbar_arrive(bar(kBarOutFree));
+          } else if (two) {
+            mbar_arrive(bar(kBarOutFree));
+            mbar_arrive(bar(kBarOutFree + 1));
+          } else {
+            mbar_arrive_n(bar(kBarOutFree + s), 2);
+          }
+        }
+        if (have_next && first >= n) next_factor = finish_queries();
+        n_tile += n;
+        piece_done(k);
+        ++k;
+        factor = next_factor;
+      }
+      cp_async_wait<0>();
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------- loaders: 32 tokens of every tile a warp, a lane a token
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    const int w = warp - 8;
+    bool ok = true;
+    uint32_t unit = 0, n_tile = 0;
+    const uint32_t to = ring + (w * 32 + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);   // BF16: rows 4 k + lane / 8
+    constexpr int kRawRows = 16 * 32 / C::kUnitCh;                           // E4M3: rows of an access, 16 bytes a lane
+    constexpr int kRawPer = C::kUnitCh / 16;
+    const uint32_t raw = base + C::kRawOff + w * C::kStages * C::kStageBytes + lane * 16;
+    // what is in flight is handed over kLag units later
+    auto hand_over = [&](uint32_t u) {
+      const uint32_t slot = u % C::kSlots;
+      if (E4M3) {
+        if (u >= C::kSlots && !(ok = wait(kBarFree + slot, (u / C::kSlots - 1) & 1u))) return;
+        const uint32_t from = raw + u % C::kStages * C::kStageBytes, dst = ring + slot * C::kUnitBytes + w * 32 * 128;
+        const int c = lane % kRawPer;                                        // 16 channels: half a 64-byte part of a chunk
+        const bool swap = c >> 2 & 1;                                        // (the two stores on different banks)
+#pragma unroll
+        for (int k = 0; k < 32 / kRawRows; ++k) {
+          const int r = k * kRawRows + lane / kRawPer;
+          const uint4 v = lds128(from + k * 512);
+          uint32_t h[8];
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[2 * j] = e4m3x2_to_f16x2(x[j] & 0xffffu);
+            h[2 * j + 1] = e4m3x2_to_f16x2(x[j] >> 16);
+          }
+          const uint32_t at = dst + (c >> 2) * kChunkBytes + r * 128;
+          const uint32_t a0 = at + (((2 * (c & 3)) ^ (r & 7)) << 4), a1 = at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4);
+          if (swap) {
+            sts128(a1, h[4], h[5], h[6], h[7]);
+            sts128(a0, h[0], h[1], h[2], h[3]);
+          } else {
+            sts128(a0, h[0], h[1], h[2], h[3]);
+            sts128(a1, h[4], h[5], h[6], h[7]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarFull + slot));
+    };
+    // one unit: channels ch0 .. of the 32 tokens at off (elements, -1: unseen)
+    auto load_unit = [&](const void* pages, int ch0, int64_t off) {
+      const uint8_t* src = static_cast<const uint8_t*>(pages);
+      const uint32_t slot = unit % C::kSlots;
+      if (!E4M3) {
+        if (unit >= C::kSlots && !(ok = wait(kBarFree + slot, (unit / C::kSlots - 1) & 1u))) return;
+        const uint32_t dst = to + slot * C::kUnitBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = k * 4 + (lane >> 3);
+          const int64_t o = __shfl_sync(0xffffffffu, off, r);
+          // (row 4 k + i: its swizzle is row i's with bit 2 flipped for odd k)
+          const uint32_t at = (dst + k * 512) ^ ((k & 1) << 6);
+#pragma unroll
+          for (int c = 0; c < C::kUnitCh / 64; ++c) {
+            const int ch = ch0 + c * 64 + (lane & 7) * 8;
+            if (ch < p.dim) cp_async16(at + c * kChunkBytes, src + (o >= 0 ? (o + ch) * 2 : 0), o >= 0 ? 16 : 0);
+          }
+        }
+      } else {
+        const uint32_t dst = raw + unit % C::kStages * C::kStageBytes;
+        const int ch = ch0 + lane % kRawPer * 16;
+#pragma unroll
+        for (int k = 0; k < 32 / kRawRows; ++k) {
+          const int64_t o = __shfl_sync(0xffffffffu, off, k * kRawRows + lane / kRawPer);
+          const bool have = o >= 0 && ch < p.dim;
+          cp_async16(dst + k * 512, src + (have ? o + ch : 0), have ? 16 : 0);
+        }
+      }
+      cp_async_commit();
+      if (unit >= C::kLag) {
+        cp_async_wait<C::kLag>();
+        hand_over(unit - C::kLag);
+      }
+      ++unit;
+    };
+    for (uint32_t piece_no = 0; ok; ++piece_no) {
+      if (!(ok = piece_there(piece_no))) break;
+      const Piece pc = piece(piece_no);
+      const int n = pc.tiles;
+      if (n == 0) break;
+      const int32_t* table = p.t.tables + int64_t(pc.row) * p.t.table_stride;
+      const int64_t head = int64_t(pc.r / blocks.count) * p.head_stride;
+      const int tok0 = pc.j0 + 32 * w + lane;
+      auto entry_of = [&](int i) -> int {
+        const int tok = tok0 + i * kTile;
+        return i < n && tok >= pc.lo && tok < pc.hi ? table[tok / p.t.page_size] : -1;
+      };
+      int entry = entry_of(0);
+      int64_t old_off = -1;                                                  // wide: of the tile before
+      for (int i = 0; ok && i < n; ++i) {
+        int64_t off = -1;
+        if (entry >= p.t.num_pages) set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
+        else if (entry >= 0)
+          off = int64_t(entry) * p.page_stride + int64_t((tok0 + i * kTile) % p.t.page_size) * p.token_stride + head;
+        entry = entry_of(i + 1);
+        const uint32_t seen = __ballot_sync(0xffffffffu, off >= 0);
+        if (lane == 0) misc.masks[(n_tile + i) % kMaskBufs][w] = seen;
+        // in the order in which the products take them (wide: the next tile's keys before this one's values)
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          if (ok) load_unit(p.k, h * 128, off);
+        if (!C::kWide) {
+          if (ok) load_unit(p.v, 0, off);
+        } else {
+          if (i > 0) {
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              if (ok) load_unit(p.v, h * 128, old_off);
+          }
+          if (i == n - 1) {
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              if (ok) load_unit(p.v, h * 128, off);
+          }
+          old_off = off;
+        }
+      }
+      n_tile += n;
+      piece_done(piece_no);
+    }
+    cp_async_wait<0>();
+    if (ok) {
+#pragma unroll
+      for (int k = C::kLag; k > 0; --k)
+        if (ok && unit >= static_cast<uint32_t>(k)) hand_over(unit - k);
+    }
+  } else {
+    // ------------------------------------------------------------- issuers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    const int s = warp - 12;
+    if (s < C::kStreams) {
+      bool ok = true;
+      const uint32_t score_desc = instr_desc(E4M3, kTile, false);
+      uint32_t n_prob = 0, n_piece = 0, n_tile = 0, unit = 0;
+      const int steps = p.dim / 16;
+      auto full = [&](uint32_t u) { return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1u); };
+      // S = Q K^T of the tile whose keys begin at unit u, into column d
+      auto issue_score = [&](uint32_t u, uint32_t d, int done_bar) {
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          if (!ok || !(ok = full(u + h))) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
+            const uint64_t b = smem_desc(ring + (u + h) % C::kSlots * C::kUnitBytes);
+#pragma unroll
+            for (int k = 0; k < C::kUnitCh / 16; ++k)                       // 16 channels = 32 bytes a step
+              if (h * 8 + k < steps)
+                tc_mma(d, a + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3), b + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
+                       score_desc, h + k == 0 ? 0u : 1u);
+            if (h == C::kHalves - 1) tc_commit(bar(done_bar));
+            tc_commit(bar(kBarFree + (u + h) % C::kSlots));
+          }
+          __syncwarp();
+        }
+      };
+      // O (+)= P V with the values from unit u on
+      auto issue_value = [&](uint32_t u, uint32_t prob, bool accumulate) {
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          if (!ok || !(ok = full(u + h))) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const int width = min(p.dim - 128 * h, 128);
+            if (width > 0) {
+              const uint32_t desc = instr_desc(E4M3, width, true);
+              const uint64_t b = smem_desc(ring + (u + h) % C::kSlots * C::kUnitBytes);
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)                           // 16 tokens = two 1024-byte groups a step
+                tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
+            }
+            tc_commit(bar(kBarFree + (u + h) % C::kSlots));
+          }
+          __syncwarp();
+        }
+      };
+      while (ok) {
+        if (!(ok = piece_there(n_piece))) break;
+        const int n = piece(n_piece).tiles;
+        const bool split = piece(n_piece).n <= blocks.tokens;
+        if (n == 0 || !(ok = wait(kBarQ + s, n_piece & 1u))) break;
+        if (!C::kWide) {
+          const int stride = split ? 2 : 1, first = split ? s : 0;
+          const uint32_t score = tmem + s * 128;
+          auto keys_of = [&](int i) { return 2 * (n_tile + i); };
+          // A tile of the other stream: its units are waited for and given back all the same, so that every phase of a slot is
+          // seen by both issuers (a parity tells two phases apart, not three).
+          auto pass = [&](int i) {
+            for (uint32_t u = keys_of(i); u < keys_of(i) + 2; ++u) {
+              if (!ok || !(ok = full(u))) return;
+              if (lane == 0) mbar_arrive(bar(kBarFree + u % C::kSlots));
+            }
+          };
+          if (split && s == 1) pass(0);
+          if (first < n) issue_score(keys_of(first), score, kBarScore + s);
+          if (n_piece > 0 && ok) ok = wait(kBarOutFree + s, (n_piece - 1) & 1u);
+          for (int i = first; ok && i < n; i += stride, ++n_prob) {
+            if (!(ok = wait(kBarProb + s, n_prob & 1u))) break;
+            tc_fence_after();
+            issue_value(keys_of(i) + 1, score, i != first);
+            if (ok && i + stride >= n) {
+              if (lane == 0) tc_commit(bar(kBarOut + s));
+              __syncwarp();
+            }
+            if (split && i + 1 < n) pass(i + 1);
+            if (ok && i + stride < n) issue_score(keys_of(i + stride), score, kBarScore + s);
+          }
+        } else {
+          // scores one tile ahead: the units come in this order
+          issue_score(unit, tmem + (n_prob & 1) * 128, kBarScore + (n_prob & 1));
+          unit += C::kHalves;
+          if (n_piece > 0 && ok) ok = wait(kBarOutFree, (n_piece - 1) & 1u);
+          for (int i = 0; ok && i < n; ++i, ++n_prob) {
+            if (i + 1 < n) {
+              issue_score(unit, tmem + ((n_prob + 1) & 1) * 128, kBarScore + ((n_prob + 1) & 1));
+              unit += C::kHalves;
+            }
+            if (!ok || !(ok = wait(kBarProb + (n_prob & 1), (n_prob >> 1) & 1u))) break;
+            tc_fence_after();
+            issue_value(unit, tmem + (n_prob & 1) * 128, i > 0);
+            unit += C::kHalves;
+            if (ok) {
+              if (lane == 0) tc_commit(bar(kBarOut + (n_prob & 1)));
+              __syncwarp();
+            }
+          }
+        }
+        n_tile += n;
+        piece_done(n_piece);
+        ++n_piece;
+      }
+      if (lane == 0) {
+        tc_commit(bar(kBarDrain + s));
+        mbar_drain(bar(kBarDrain + s), 0);
+      }
+    } else if (warp == 14) {
+      // ----------------------------------------------------------- the list of pieces
+      Piece pc;
+      for (uint32_t k = 0;; ++k) {
+        if (k >= kPieces && !wait(kBarPieceFree + k % kPieces, (k / kPieces - 1) & 1u)) break;
+        const bool more = walk.next(p, rows, step, pc);
+        if (!more) pc.tiles = 0;
+        if (lane == 0) {
+          misc.pieces[k % kPieces] = pc;
+          mbar_arrive(bar(kBarPiece + k % kPieces));
+        }
+        __syncwarp();
+        if (!more) break;
+      }
+    }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// Joins the blocks of rows that cross CTAs: a thread a row and 16 channels, the parts in the order of their CTAs.
+template <int DP, bool E4M3>
+__global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, const Record* records, const float* parts, int ctas) {
+  using C = Cfg<DP, E4M3>;
+  __shared__ int list[kMaxCtas], count_s;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x < 32) {
+    int count = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const int c = c0 + threadIdx.x;
+      const bool is = c < ctas && __ldcg(&records[c].np) > 1;
+      const uint32_t m = __ballot_sync(0xffffffffu, is);
+      if (is) list[count + __popc(m & ((1u << threadIdx.x) - 1u))] = c;
+      count += __popc(m);
+    }
+    if (threadIdx.x == 0) count_s = count;
+  }
+  __syncthreads();
+  const Blocks blocks = blocks_of(p.group);
+  const int cols = p.dim / 16;
+  for (int item = blockIdx.x; item < count_s * C::kStreams * cols; item += gridDim.x) {
+    const int c = list[item / (C::kStreams * cols)], rest = item % (C::kStreams * cols), s = rest / cols, ch = rest % cols * 16;
+    const Record rec = records[c];
+    if (s == 1 && rec.n <= blocks.tokens) continue;
+    const int trow = threadIdx.x / blocks.heads, hrow = threadIdx.x % blocks.heads, t = trow + s * blocks.tokens;
+    const int blk = rec.r % blocks.count, head = rec.r / blocks.count * p.group + blk * blocks.heads + hrow;
+    if (trow >= blocks.tokens || t >= rec.n || blk * blocks.heads + hrow >= p.group) continue;
+    const int prow = s * kRows + threadIdx.x;
+    auto part_at = [&](int i) { return parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * C::kPartFloats + prow; };
+    float m = -INFINITY;
+    for (int i = 0; i < rec.np; ++i) m = fmaxf(m, __ldcg(part_at(i)));
+    const float at = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < rec.np; ++i) {
+      const float* src = part_at(i);
+      const float f = exp2_fast(__ldcg(src) - at);
+      l = fmaf(f, __ldcg(src + C::kPartRows), l);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[k] = fmaf(f, __ldcg(src + (2 + ch + k) * C::kPartRows), o[k]);
+    }
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
+    const int64_t row = int64_t(rec.token + t) * p.heads + head;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+    uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.dim + ch);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (ch == 0 && p.lse != nullptr) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <int DP, bool E4M3>
+static cudaError_t launch(const ChunkParams& p, int device, cudaStream_t stream) {
+  using C = Cfg<DP, E4M3>;
+  constexpr int kSmem = C::kMiscOff + static_cast<int>(sizeof(Misc));
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+  static_assert(C::kMiscOff % 16 == 0 && C::kUnitBytes % 1024 == 0 && C::kQBytes % 1024 == 0, "swizzled tiles");
+  static bool attr_set[64] = {false};
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<DP, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[device] = true;
+  }
+  Record* records = static_cast<Record*>(p.scratch);
+  float* parts = reinterpret_cast<float*>(records + kMaxCtas);
+  int grid = device_info(device).sm_count;
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  chunk_kernel<DP, E4M3><<<grid, kThreads, kSmem, stream>>>(p, records, parts);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * 8));
+  cfg.blockDim = dim3(kRows);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, chunk_join_kernel<DP, E4M3>, p, static_cast<const Record*>(records),
+                         static_cast<const float*>(parts), grid);
+  note_launch(2);
+  return e;
 }
 
 }  // namespace chunk
 
-size_t chunk_scratch_bytes(int, int, int) { return 0; }
+size_t chunk_scratch_bytes(int, int, int dim) {
+  const size_t floats = dim <= 64 ? chunk::Cfg<64, false>::kPartFloats
+                        : dim <= 128 ? chunk::Cfg<128, false>::kPartFloats
+                                     : chunk::Cfg<256, false>::kPartFloats;
+  return chunk::kMaxCtas * (sizeof(chunk::Record) + 2 * floats * sizeof(float));
+}
 
-cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int, cudaStream_t stream) {
-  const int64_t rows = int64_t(p.tokens) * p.heads;
-  const int64_t want = (rows + chunk::kWarps - 1) / chunk::kWarps;
-  const dim3 grid(static_cast<unsigned>(want < 4096 ? want : 4096), p.batch < 65535 ? p.batch : 65535);
-  if (dtype == MOE_W4A16_CACHE_E4M3) chunk::chunk_kernel<true><<<grid, chunk::kWarps * 32, 0, stream>>>(p);
-  else chunk::chunk_kernel<false><<<grid, chunk::kWarps * 32, 0, stream>>>(p);
-  note_launch();
-  return cudaGetLastError();
+cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int device, cudaStream_t stream) {
+  const bool e4m3 = dtype == MOE_W4A16_CACHE_E4M3;
+  if (p.dim <= 64) return e4m3 ? chunk::launch<64, true>(p, device, stream) : chunk::launch<64, false>(p, device, stream);
+  if (p.dim <= 128) return e4m3 ? chunk::launch<128, true>(p, device, stream) : chunk::launch<128, false>(p, device, stream);
+  return e4m3 ? chunk::launch<256, true>(p, device, stream) : chunk::launch<256, false>(p, device, stream);
 }
 
 }  // namespace moe
