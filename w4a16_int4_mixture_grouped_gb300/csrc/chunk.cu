@@ -22,6 +22,7 @@
 //   * Every CTA takes an equal share of one line of tiles over all sequences, heads and row blocks, whatever the lengths;
 //     rows that cross CTAs are written as FP32 parts, which a second kernel joins in order.
 //   * Unseen slots (past the end, freed pages) are not read: their rows are zero-filled and their scores -infinity.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "block.h"
@@ -51,8 +52,8 @@ struct Cfg {
   static constexpr int kUnitBytes = kUnitCh / 64 * kChunkBytes;
   static constexpr int kQBytes = DP / 64 * kChunkBytes;            // a stream's queries
   static constexpr int kSlots = DP == 64 ? 8 : kWide && !E4M3 ? 5 : 4;
-  static constexpr int kLag = E4M3 ? 1 : 2;                        // units in flight behind the newest
-  static constexpr int kStages = kLag + 1;                         // raw 8-bit units of a loader warp
+  static constexpr int kLag = 1;                                   // E4M3: units in flight behind the newest
+  static constexpr int kStages = kLag + 1;                         // raw units of a loader warp
   static constexpr int kStageBytes = 32 * kUnitCh;
   static constexpr int kRingOff = kStreams * kQBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kUnitBytes;
@@ -87,7 +88,7 @@ struct Share {
 // Some tiles of one block of rows: `n` tokens of a sequence's chunk, work row r. (tiles = 0: the share is done.)
 struct Piece {
   int token, pos, n, r;          // the first token's row of q and position
-  int row, lo, hi;               // row of the tables, tokens [lo, hi) seen by the block
+  int row, len;                  // row of the tables, tokens that the sequence has
   int j0, tiles;                 // token at which the first tile begins
   int c0, c1;                    // CTAs that the block's tiles fall to
 };
@@ -95,7 +96,8 @@ struct Misc {
   unsigned long long bars[kNumBars];
   uint32_t tmem;
   int abort_flag;
-  uint32_t masks[kMaskBufs][4];              // seen tokens of a tile
+  uint32_t issued[4];                        // units that a loader warp has asked for
+  alignas(16) uint32_t masks[kMaskBufs][4];  // seen tokens of a tile
   Piece pieces[kPieces];
   union {
     float2 ml[2][kRows];                     // [stream] bases and sums of a piece's rows
@@ -248,8 +250,9 @@ struct Walk {
         continue;
       }
       o.n = min(step, c.n - static_cast<int>(i));
-      seen_by(p, c, static_cast<int>(i), o.n, o.lo, o.hi);
-      const int ntiles = tiles_of(o.lo, o.hi);
+      int lo, hi;
+      seen_by(p, c, static_cast<int>(i), o.n, lo, hi);
+      const int ntiles = tiles_of(lo, hi);
       ++qt;
       if (ntiles == 0) continue;
       const int64_t row0 = x - tile;               // line position of the block's first tile
@@ -257,7 +260,8 @@ struct Walk {
       o.pos = c.base + static_cast<int>(i);
       o.r = r;
       o.row = c.row;
-      o.j0 = (o.lo / kTile + tile) * kTile;
+      o.len = c.base + c.n;
+      o.j0 = (lo / kTile + tile) * kTile;
       o.tiles = static_cast<int>(min(int64_t(ntiles - tile), x_end - x));
       o.c0 = cta_of(total, ctas, row0);
       o.c1 = cta_of(total, ctas, row0 + ntiles - 1);
@@ -267,6 +271,13 @@ struct Walk {
     }
     return false;
   }
+};
+
+// Pages as a tensor of (channels, heads, tokens of a page, pages), in boxes of 64 channels of `rows` tokens (0: none, see
+// launch).
+struct PageMaps {
+  CUtensorMap k, v;
+  int rows;
 };
 
 // What a CTA left for the join: a block of rows that starts in it and goes on in the next np - 1.
@@ -365,12 +376,33 @@ __device__ __forceinline__ uint32_t instr_desc(bool f16, int n, bool n_major) {
          (static_cast<uint32_t>(kRows >> 4) << 24) | (n_major ? 1u << 16 : 0u);
 }
 
+// d (+)= A B^T over `steps` (1 .. MOST) times 16 channels, both K-major. A branch between two products costs more than a
+// product, so each number of steps has a sequence of its own (128 channels, a branch each: 1204 us where this takes @@).
+template <int STEPS>
+__device__ __forceinline__ void score_products(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const uint64_t off = (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3);       // 16 channels = 32 bytes a step
+    tc_mma(d, a + off, b + off, idesc, accumulate || k > 0 ? 1u : 0u);
+  }
+}
+template <int MOST>
+__device__ __forceinline__ void score_steps(int steps, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  if (steps == MOST) return score_products<MOST>(d, a, b, idesc, accumulate);
+  if constexpr (MOST > 1) score_steps<MOST - 1>(steps, d, a, b, idesc, accumulate);
+}
+
 // ---------------------------------------------------------------------------
 // arithmetic
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {           // (a NaN is passed over)
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi) {
@@ -415,6 +447,14 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volat
   }
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // Rows that stand before their sequence's first token, or have none: zeros and -infinity, spread over the CTAs.
 __device__ __forceinline__ void zero_unseeing(const ChunkParams& p) {
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -429,7 +469,8 @@ __device__ __forceinline__ void zero_unseeing(const ChunkParams& p) {
 }
 
 template <int DP, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p, Record* records, float* parts) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ PageMaps maps,
+                                                            Record* records, float* parts) {
   using C = Cfg<DP, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& misc = *reinterpret_cast<Misc*>(smem + C::kMiscOff);
@@ -607,16 +648,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
           if (i + stride >= n && have_next) load_queries(piece(k + 1));      // the last product with these is done
           if (active) {
             uint32_t r[128];
+            const uint4 seen4 = lds128(smem_u32(misc.masks[(n_tile + i) % kMaskBufs]));
             tmem_ld_tile(score, r);
             const int j0 = j_first + i * kTile;
             const int above = pos - j0 + 1;                                  // tokens of the tile up to the row's own
             const int below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
-            const volatile uint32_t* seen = misc.masks[(n_tile + i) % kMaskBufs];
-            const bool part = above < kTile || below > 0 || (seen[0] & seen[1] & seen[2] & seen[3]) != 0xffffffffu;
+            const bool part = above < kTile || below > 0 || (seen4.x & seen4.y & seen4.z & seen4.w) != 0xffffffffu;
             if (__any_sync(0xffffffffu, part)) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const uint32_t w = seen[q] & bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
+                const uint32_t w = (q == 0 ? seen4.x : q == 1 ? seen4.y : q == 2 ? seen4.z : seen4.w) & bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                   if (!(w >> j & 1u)) r[32 * q + j] = 0xff800000u;
@@ -627,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
             for (int e = 0; e < 128; e += 8)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                top4[j] = fmaxf(fmaxf(top4[j], __uint_as_float(r[e + 2 * j])), __uint_as_float(r[e + 2 * j + 1]));
+                top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
             const bool over = top > m + kSlack;                              // (m of -infinity: any seen score)
             if (__any_sync(0xffffffffu, over)) {
@@ -795,64 +836,49 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
     const int w = warp - 8;
     bool ok = true;
     uint32_t unit = 0, n_tile = 0;
-    const uint32_t to = ring + (w * 32 + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);   // BF16: rows 4 k + lane / 8
-    constexpr int kRawRows = 16 * 32 / C::kUnitCh;                           // E4M3: rows of an access, 16 bytes a lane
-    constexpr int kRawPer = C::kUnitCh / 16;
+    auto slot_free = [&](uint32_t u) { return u < C::kSlots || wait(kBarFree + u % C::kSlots, (u / C::kSlots - 1) & 1u); };
+    // ---- E4M3: a unit comes to a buffer of the warp's own, kLag units ahead, and is converted on its way to the ring
+    constexpr int kRawPer = C::kUnitCh / 16, kRawRows = 32 / kRawPer;        // lanes of a row, rows of an access
     const uint32_t raw = base + C::kRawOff + w * C::kStages * C::kStageBytes + lane * 16;
-    // what is in flight is handed over kLag units later
-    auto hand_over = [&](uint32_t u) {
-      const uint32_t slot = u % C::kSlots;
-      if (E4M3) {
-        if (u >= C::kSlots && !(ok = wait(kBarFree + slot, (u / C::kSlots - 1) & 1u))) return;
-        const uint32_t from = raw + u % C::kStages * C::kStageBytes, dst = ring + slot * C::kUnitBytes + w * 32 * 128;
-        const int c = lane % kRawPer;                                        // 16 channels: half a 64-byte part of a chunk
-        const bool swap = c >> 2 & 1;                                        // (the two stores on different banks)
+    auto convert = [&](uint32_t u) {
+      if (!(ok = slot_free(u))) return;
+      const uint32_t from = raw + u % C::kStages * C::kStageBytes, dst = ring + u % C::kSlots * C::kUnitBytes + w * 32 * 128;
+      const int c = lane % kRawPer;                                          // 16 channels: half a 64-byte part of a chunk
+      const bool swap = c >> 2 & 1;                                          // (the two stores on different banks)
 #pragma unroll
-        for (int k = 0; k < 32 / kRawRows; ++k) {
-          const int r = k * kRawRows + lane / kRawPer;
-          const uint4 v = lds128(from + k * 512);
-          uint32_t h[8];
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      for (int k = 0; k < 32 / kRawRows; ++k) {
+        const int r = k * kRawRows + lane / kRawPer;
+        const uint4 v = lds128(from + k * 512);
+        uint32_t h[8];
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[2 * j] = e4m3x2_to_f16x2(x[j] & 0xffffu);
-            h[2 * j + 1] = e4m3x2_to_f16x2(x[j] >> 16);
-          }
-          const uint32_t at = dst + (c >> 2) * kChunkBytes + r * 128;
-          const uint32_t a0 = at + (((2 * (c & 3)) ^ (r & 7)) << 4), a1 = at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4);
-          if (swap) {
-            sts128(a1, h[4], h[5], h[6], h[7]);
-            sts128(a0, h[0], h[1], h[2], h[3]);
-          } else {
-            sts128(a0, h[0], h[1], h[2], h[3]);
-            sts128(a1, h[4], h[5], h[6], h[7]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          h[2 * j] = e4m3x2_to_f16x2(x[j] & 0xffffu);
+          h[2 * j + 1] = e4m3x2_to_f16x2(x[j] >> 16);
+        }
+        const uint32_t at = dst + (c >> 2) * kChunkBytes + r * 128;
+        const uint32_t a0 = at + (((2 * (c & 3)) ^ (r & 7)) << 4), a1 = at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4);
+        if (swap) {
+          sts128(a1, h[4], h[5], h[6], h[7]);
+          sts128(a0, h[0], h[1], h[2], h[3]);
+        } else {
+          sts128(a0, h[0], h[1], h[2], h[3]);
+          sts128(a1, h[4], h[5], h[6], h[7]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarFull + slot));
+      if (lane == 0) mbar_arrive(bar(kBarFull + u % C::kSlots));
     };
-    // one unit: channels ch0 .. of the 32 tokens at off (elements, -1: unseen)
-    auto load_unit = [&](const void* pages, int ch0, int64_t off) {
+    // This lane's token of a tile: its page (-1: unseen) and place there.
+    struct Token {
+      int page, at;
+    };
+    // one unit: channels ch0 .. of the 32 tokens
+    auto load_unit = [&](const CUtensorMap* map, const void* pages, int head, int ch0, const Token& tok, bool all) {
       const uint8_t* src = static_cast<const uint8_t*>(pages);
-      const uint32_t slot = unit % C::kSlots;
-      if (!E4M3) {
-        if (unit >= C::kSlots && !(ok = wait(kBarFree + slot, (unit / C::kSlots - 1) & 1u))) return;
-        const uint32_t dst = to + slot * C::kUnitBytes;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = k * 4 + (lane >> 3);
-          const int64_t o = __shfl_sync(0xffffffffu, off, r);
-          // (row 4 k + i: its swizzle is row i's with bit 2 flipped for odd k)
-          const uint32_t at = (dst + k * 512) ^ ((k & 1) << 6);
-#pragma unroll
-          for (int c = 0; c < C::kUnitCh / 64; ++c) {
-            const int ch = ch0 + c * 64 + (lane & 7) * 8;
-            if (ch < p.dim) cp_async16(at + c * kChunkBytes, src + (o >= 0 ? (o + ch) * 2 : 0), o >= 0 ? 16 : 0);
-          }
-        }
-      } else {
+      const int64_t off = tok.page < 0 ? -1 : int64_t(tok.page) * p.page_stride + int64_t(tok.at) * p.token_stride + int64_t(head) * p.head_stride;
+      if (E4M3) {
         const uint32_t dst = raw + unit % C::kStages * C::kStageBytes;
         const int ch = ch0 + lane % kRawPer * 16;
 #pragma unroll
@@ -861,11 +887,41 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
           const bool have = o >= 0 && ch < p.dim;
           cp_async16(dst + k * 512, src + (have ? o + ch : 0), have ? 16 : 0);
         }
-      }
-      cp_async_commit();
-      if (unit >= C::kLag) {
-        cp_async_wait<C::kLag>();
-        hand_over(unit - C::kLag);
+        cp_async_commit();
+        if (unit >= C::kLag) {
+          cp_async_wait<C::kLag>();
+          convert(unit - C::kLag);
+        }
+      } else {
+        if (!(ok = slot_free(unit))) return;
+        const uint32_t full = bar(kBarFull + unit % C::kSlots), dst = ring + unit % C::kSlots * C::kUnitBytes + w * 32 * 128;
+        if (all && maps.rows > 0) {
+          // boxes of maps.rows tokens (8, 16 or 32) and 64 channels, a lane a box
+          const int chunks = min(C::kUnitCh / 64, (p.dim - ch0 + 63) / 64), boxes = 32 / maps.rows;
+          const int r = (lane & (boxes - 1)) * maps.rows, c = lane / boxes;
+          const int page = __shfl_sync(0xffffffffu, tok.page, r), at = __shfl_sync(0xffffffffu, tok.at, r);
+          if (lane == 0) mbar_arrive_expect_tx(full, chunks * 32 * 128);
+          __syncwarp();
+          if (c < chunks) tma_load_4d(dst + c * kChunkBytes + r * 128, map, ch0 + c * 64, head, at, page, full);
+        } else {
+          const uint32_t to = dst + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);          // rows 4 k + lane / 8
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int64_t o = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
+            // (row 4 k + i: its swizzle is row i's with bit 2 flipped for odd k)
+            const uint32_t at = (to + k * 512) ^ ((k & 1) << 6);
+#pragma unroll
+            for (int c = 0; c < C::kUnitCh / 64; ++c) {
+              const int ch = ch0 + c * 64 + (lane & 7) * 8;
+              if (ch < p.dim) cp_async16(at + c * kChunkBytes, src + (o >= 0 ? (o + ch) * 2 : 0), o >= 0 ? 16 : 0);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
       }
       ++unit;
     };
@@ -875,50 +931,56 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
       const int n = pc.tiles;
       if (n == 0) break;
       const int32_t* table = p.t.tables + int64_t(pc.row) * p.t.table_stride;
-      const int64_t head = int64_t(pc.r / blocks.count) * p.head_stride;
+      const int head = pc.r / blocks.count;
       const int tok0 = pc.j0 + 32 * w + lane;
+      // (tokens behind the block's last are read with the others, its rows' masks hide them)
       auto entry_of = [&](int i) -> int {
         const int tok = tok0 + i * kTile;
-        return i < n && tok >= pc.lo && tok < pc.hi ? table[tok / p.t.page_size] : -1;
+        return i < n && tok < pc.len ? table[tok / p.t.page_size] : -1;
       };
       int entry = entry_of(0);
-      int64_t old_off = -1;                                                  // wide: of the tile before
+      Token old{-1, 0};                                                      // wide: of the tile before
+      bool old_all = false;
       for (int i = 0; ok && i < n; ++i) {
-        int64_t off = -1;
-        if (entry >= p.t.num_pages) set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
-        else if (entry >= 0)
-          off = int64_t(entry) * p.page_stride + int64_t((tok0 + i * kTile) % p.t.page_size) * p.token_stride + head;
+        Token tok{entry, (tok0 + i * kTile) % p.t.page_size};
+        if (entry >= p.t.num_pages) {
+          set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
+          tok.page = -1;
+        }
         entry = entry_of(i + 1);
-        const uint32_t seen = __ballot_sync(0xffffffffu, off >= 0);
+        const uint32_t seen = __ballot_sync(0xffffffffu, tok.page >= 0);
+        const bool all = seen == 0xffffffffu;
         if (lane == 0) misc.masks[(n_tile + i) % kMaskBufs][w] = seen;
         // in the order in which the products take them (wide: the next tile's keys before this one's values)
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h)
-          if (ok) load_unit(p.k, h * 128, off);
+          if (ok) load_unit(&maps.k, p.k, head, h * 128, tok, all);
         if (!C::kWide) {
-          if (ok) load_unit(p.v, 0, off);
+          if (ok) load_unit(&maps.v, p.v, head, 0, tok, all);
         } else {
           if (i > 0) {
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-              if (ok) load_unit(p.v, h * 128, old_off);
+              if (ok) load_unit(&maps.v, p.v, head, h * 128, old, old_all);
           }
           if (i == n - 1) {
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-              if (ok) load_unit(p.v, h * 128, off);
+              if (ok) load_unit(&maps.v, p.v, head, h * 128, tok, all);
           }
-          old_off = off;
+          old = tok;
+          old_all = all;
         }
       }
       n_tile += n;
       piece_done(piece_no);
     }
     cp_async_wait<0>();
-    if (ok) {
+    if (lane == 0) misc.issued[w] = unit;
+    if (E4M3) {
 #pragma unroll
       for (int k = C::kLag; k > 0; --k)
-        if (ok && unit >= static_cast<uint32_t>(k)) hand_over(unit - k);
+        if (ok && unit >= static_cast<uint32_t>(k)) convert(unit - k);
     }
   } else {
     // ------------------------------------------------------------- issuers
@@ -930,42 +992,45 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
       uint32_t n_prob = 0, n_piece = 0, n_tile = 0, unit = 0;
       const int steps = p.dim / 16;
       auto full = [&](uint32_t u) { return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1u); };
-      // S = Q K^T of the tile whose keys begin at unit u, into column d
+      auto free_unit = [&](uint32_t u) { tc_commit(bar(kBarFree + u % C::kSlots)); };
+      // the products of S = Q K^T with the unit u (half h of a tile's keys), into column d
+      auto score = [&](uint32_t u, int h, uint32_t d) {
+        const uint64_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
+        const uint64_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
+        score_steps<C::kUnitCh / 16>(h < C::kHalves - 1 ? C::kUnitCh / 16 : steps - h * 8, d, a, b, score_desc, h > 0);
+      };
+      // S of the tile whose keys begin at unit u
       auto issue_score = [&](uint32_t u, uint32_t d, int done_bar) {
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
           if (!ok || !(ok = full(u + h))) return;
           tc_fence_after();
           if (lane == 0) {
-            const uint64_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
-            const uint64_t b = smem_desc(ring + (u + h) % C::kSlots * C::kUnitBytes);
-#pragma unroll
-            for (int k = 0; k < C::kUnitCh / 16; ++k)                       // 16 channels = 32 bytes a step
-              if (h * 8 + k < steps)
-                tc_mma(d, a + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3), b + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
-                       score_desc, h + k == 0 ? 0u : 1u);
+            score(u + h, h, d);
             if (h == C::kHalves - 1) tc_commit(bar(done_bar));
-            tc_commit(bar(kBarFree + (u + h) % C::kSlots));
+            free_unit(u + h);
           }
           __syncwarp();
         }
       };
-      // O (+)= P V with the values from unit u on
+      // the products of O (+)= P V with the unit u (half h of a tile's values): tokens 16 k0 .. 16 k1 - 1
+      auto value = [&](uint32_t u, int h, uint32_t prob, bool accumulate) {
+        const int width = min(p.dim - 128 * h, 128);
+        const uint32_t desc = instr_desc(E4M3, width, true);
+        const uint64_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)                                 // 16 tokens = two 1024-byte groups a step
+          tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
+      };
+      // O of the tile whose values begin at unit u
       auto issue_value = [&](uint32_t u, uint32_t prob, bool accumulate) {
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
           if (!ok || !(ok = full(u + h))) return;
           tc_fence_after();
           if (lane == 0) {
-            const int width = min(p.dim - 128 * h, 128);
-            if (width > 0) {
-              const uint32_t desc = instr_desc(E4M3, width, true);
-              const uint64_t b = smem_desc(ring + (u + h) % C::kSlots * C::kUnitBytes);
-#pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)                           // 16 tokens = two 1024-byte groups a step
-                tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
-            }
-            tc_commit(bar(kBarFree + (u + h) % C::kSlots));
+            value(u + h, h, prob, accumulate);
+            free_unit(u + h);
           }
           __syncwarp();
         }
@@ -977,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
         if (n == 0 || !(ok = wait(kBarQ + s, n_piece & 1u))) break;
         if (!C::kWide) {
           const int stride = split ? 2 : 1, first = split ? s : 0;
-          const uint32_t score = tmem + s * 128;
+          const uint32_t score_col = tmem + s * 128;
           auto keys_of = [&](int i) { return 2 * (n_tile + i); };
           // A tile of the other stream: its units are waited for and given back all the same, so that every phase of a slot is
           // seen by both issuers (a parity tells two phases apart, not three).
@@ -988,18 +1053,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
             }
           };
           if (split && s == 1) pass(0);
-          if (first < n) issue_score(keys_of(first), score, kBarScore + s);
+          if (first < n) issue_score(keys_of(first), score_col, kBarScore + s);
           if (n_piece > 0 && ok) ok = wait(kBarOutFree + s, (n_piece - 1) & 1u);
           for (int i = first; ok && i < n; i += stride, ++n_prob) {
+            const uint32_t v = keys_of(i) + 1, next = keys_of(i + stride);
+            const bool more = i + stride < n, near = more && stride == 1;
+            // everything that the products take is waited for before P, and nothing stands between O += P V and the next S:
+            // the softmax waits for that one
+            if (!(ok = full(v)) || (near && !(ok = full(next)))) break;
             if (!(ok = wait(kBarProb + s, n_prob & 1u))) break;
             tc_fence_after();
-            issue_value(keys_of(i) + 1, score, i != first);
-            if (ok && i + stride >= n) {
-              if (lane == 0) tc_commit(bar(kBarOut + s));
-              __syncwarp();
+            if (lane == 0) {
+              value(v, 0, score_col, i != first);
+              if (near) {
+                score(next, 0, score_col);
+                tc_commit(bar(kBarScore + s));
+                free_unit(next);
+              }
+              free_unit(v);
+              if (!more) tc_commit(bar(kBarOut + s));
             }
+            __syncwarp();
             if (split && i + 1 < n) pass(i + 1);
-            if (ok && i + stride < n) issue_score(keys_of(i + stride), score, kBarScore + s);
+            if (more && !near) issue_score(next, score_col, kBarScore + s);
           }
         } else {
           // scores one tile ahead: the units come in this order
@@ -1048,6 +1124,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p,
 
   tc_fence_before();
   __syncthreads();
+  if (!E4M3 && *abort_flag) {
+    // a wait gave up: the boxes in flight land before the CTA ends (the loaders' missing arrivals made up for)
+    if (warp >= 8 && warp < 12 && lane == 0) {
+      const uint32_t last = max(max(misc.issued[0], misc.issued[1]), max(misc.issued[2], misc.issued[3]));
+      for (uint32_t u = misc.issued[warp - 8]; u < last; ++u) mbar_arrive(bar(kBarFull + u % C::kSlots));
+      for (uint32_t u = last > C::kSlots ? last - C::kSlots : 0; u < last; ++u)
+        mbar_drain(bar(kBarFull + u % C::kSlots), (u / C::kSlots) & 1u);
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -1109,6 +1195,47 @@ __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, 
   }
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link needed).
+static EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiledFn>(nullptr);
+    return reinterpret_cast<EncodeTiledFn>(ptr);
+  }();
+  return fn;
+}
+// A tile's 32 tokens of a loader warp are boxes of tokens that lie behind each other in a page: as many as divide its size,
+// 8 at least (the swizzle's rows). Pages of other sizes, and of strides that a map cannot have, go token by token.
+static void page_maps(const ChunkParams& p, PageMaps* maps) {
+  maps->rows = 0;
+  int rows = 32;
+  while (rows >= 8 && p.t.page_size % rows != 0) rows /= 2;
+  EncodeTiledFn enc = encode_tiled();
+  if (rows < 8 || enc == nullptr) return;
+  const int64_t head_stride = p.kv_heads > 1 ? p.head_stride : p.dim;
+  const int64_t page_stride = p.t.num_pages > 1 ? p.page_stride : p.token_stride * p.t.page_size;
+  const int64_t most = int64_t(1) << 39;                 // elements: strides of a map end at 2^40 bytes
+  if (page_stride < 1 || page_stride >= most || p.token_stride >= most || head_stride >= most) return;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.kv_heads),
+                              static_cast<cuuint64_t>(p.t.page_size), static_cast<cuuint64_t>(p.t.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(p.token_stride) * 2,
+                                 static_cast<cuuint64_t>(page_stride) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
+  CUtensorMap* const map[2] = {&maps->k, &maps->v};
+  for (int i = 0; i < 2; ++i)
+    if (enc(map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i == 0 ? p.k : p.v), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  maps->rows = rows;
+}
+
 template <int DP, bool E4M3>
 static cudaError_t launch(const ChunkParams& p, int device, cudaStream_t stream) {
   using C = Cfg<DP, E4M3>;
@@ -1126,7 +1253,10 @@ static cudaError_t launch(const ChunkParams& p, int device, cudaStream_t stream)
   float* parts = reinterpret_cast<float*>(records + kMaxCtas);
   int grid = device_info(device).sm_count;
   if (grid > kMaxCtas) grid = kMaxCtas;
-  chunk_kernel<DP, E4M3><<<grid, kThreads, kSmem, stream>>>(p, records, parts);
+  PageMaps maps;
+  maps.rows = 0;
+  if (!E4M3) page_maps(p, &maps);
+  chunk_kernel<DP, E4M3><<<grid, kThreads, kSmem, stream>>>(p, maps, records, parts);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
