@@ -40,8 +40,6 @@ constexpr int kChunkBytes = 128 * 128;        // 64 channels of 128 rows, 128-by
 
 // warps: 0-3 and 4-7 the streams' softmax, 8-11 loaders, 12 and 13 issuers
 constexpr int kThreads = 512;
-// registers of a softmax thread and of the others: 256 x 184 + 256 x 72 = 512 x 128, what the launch has
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 
 template <int DP, bool E4M3>
 struct Cfg {
@@ -73,8 +71,9 @@ enum {
   kBarPiece = 26,                // [4] piece listed
   kBarPieceFree = 30,            // [4] piece done with by all warps
   kBarBases = 34,                // bases and sums of a piece's two accumulators written, then read
-  kBarDrain = 35,                // [2]
-  kNumBars = 37
+  kBarTurn = 35,                 // [2] a stream's products issued: the other's turn
+  kBarDrain = 37,                // [2]
+  kNumBars = 39
 };
 constexpr int kPieces = 4;       // pieces listed ahead
 constexpr int kUsers = 14;       // warps that read them
@@ -336,20 +335,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr)
       : "memory");
 }
-// The 128 columns of a score tile; the loads are in flight together, and nothing reads r before the wait.
-__device__ __forceinline__ void tmem_ld_tile(uint32_t addr, uint32_t (&r)[128]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) tmem_ld32(addr + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * k));
+// tmem_ld32's loads are there: nothing reads r before.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int k = 0; k < 128; ++k) asm volatile("" : "+r"(r[k]));
+  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8"
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31,%32"
       "};" ::"r"(addr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-        "r"(r[6]), "r"(r[7])
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
@@ -374,22 +376,6 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
 __device__ __forceinline__ uint32_t instr_desc(bool f16, int n, bool n_major) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24) | (n_major ? 1u << 16 : 0u);
-}
-
-// d (+)= A B^T over `steps` (1 .. MOST) times 16 channels, both K-major. A branch between two products costs more than a
-// product, so each number of steps has a sequence of its own (128 channels, a branch each: 1204 us where this takes @@).
-template <int STEPS>
-__device__ __forceinline__ void score_products(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-#pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    const uint64_t off = (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3);       // 16 channels = 32 bytes a step
-    tc_mma(d, a + off, b + off, idesc, accumulate || k > 0 ? 1u : 0u);
-  }
-}
-template <int MOST>
-__device__ __forceinline__ void score_steps(int steps, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  if (steps == MOST) return score_products<MOST>(d, a, b, idesc, accumulate);
-  if constexpr (MOST > 1) score_steps<MOST - 1>(steps, d, a, b, idesc, accumulate);
 }
 
 // ---------------------------------------------------------------------------
@@ -424,35 +410,82 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 // Bits below x of a word of 32.
 __device__ __forceinline__ uint32_t bits_below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
 
-// warp_wait without a call: one would keep the softmax warps from their registers.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, uint64_t limit) {
-  const bool suspend = limit >= kSuspendNs;
-  if (suspend && __all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (__all_sync(0xffffffffu, mbar_poll(bar, parity, suspend))) return true;
-    int stop = 0;
-    if ((threadIdx.x & 31) == 0) {
-      if (*abort_flag) {
-        stop = 1;
-      } else if (global_timer_ns() - t0 >= limit) {
-        set_error(err, MOE_W4A16_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
-        stop = 1;
-      }
-    }
-    if (__shfl_sync(0xffffffffu, stop, 0)) return false;
-  }
-}
-
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// A warp's 32 rows of queries on their way to shared memory (first row's chunk at qs); off: the lane's row in q, -1: zeros.
+template <int DP>
+static __device__ __noinline__ void load_queries(const uint16_t* q, int dim, uint32_t qs, int64_t off, bool any) {
+  const int lane = threadIdx.x & 31;
+  if (any) {
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+      const int r = j * 4 + (lane >> 3);
+      const int64_t o = __shfl_sync(0xffffffffu, off, r);
+      const uint32_t to = qs + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        const int ch = c * 64 + (lane & 7) * 8;
+        if (ch < dim) cp_async16(to + c * kChunkBytes, q + (o >= 0 ? o + ch : 0), o >= 0 ? 16 : 0);
+      }
+    }
+  }
+  cp_async_commit();
+}
+// They have come: negated where the scale is negative; E4M3: in FP16, a row scaled by a power of two. -> the row's factor of
+// the scores.
+template <bool E4M3>
+static __device__ __noinline__ float finish_queries(int dim, uint32_t qs, float abs_scale, bool negate) {
+  const int lane = threadIdx.x & 31;
+  cp_async_wait<0>();
+  __syncwarp();
+  float factor = abs_scale;
+  const uint32_t row = qs + lane * 128;
+  auto at = [&](int c16) { return row + (c16 >> 3) * kChunkBytes + (((c16 & 7) ^ (lane & 7)) << 4); };
+  const uint32_t flip = negate ? 0x80008000u : 0u;
+  if (E4M3) {
+    float top = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < dim / 8; ++c) {
+      const uint4 v = lds128(at(c));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+    }
+    // top in [2^e, 2^(e+1)): scale by 2^(15-e) (two factors, each a normal number for any e), to below 2^16, where the FP16
+    // range ends: channels keep their eight bits down to 2^-32 of the largest, and end at 2^-40 of it
+    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    if (top == 0.f || e > 127) e = 15;
+    e = max(e, -126) - 15;
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
+    const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
+    factor = fmaxf(abs_scale * __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23) *
+                       __uint_as_float(static_cast<uint32_t>(127 + (e - e / 2)) << 23),
+                   1.2e-38f);
+#pragma unroll 2
+    for (int c = 0; c < dim / 8; ++c) {
+      const uint4 v = lds128(at(c));
+      uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack_f16x2_rn(__uint_as_float(w[j] << 16) * down * down2, __uint_as_float(w[j] & 0xffff0000u) * down * down2);
+      sts128(at(c), w[0], w[1], w[2], w[3]);
+    }
+  } else if (negate) {
+    for (int c = 0; c < dim / 8; ++c) {
+      const uint4 v = lds128(at(c));
+      sts128(at(c), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return factor;
 }
 
 // Rows that stand before their sequence's first token, or have none: zeros and -infinity, spread over the CTAs.
@@ -501,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(bar(kBarOut + i), 1);
       mbar_init(bar(kBarOutFree + i), 4 * C::kStreams);
       mbar_init(bar(kBarDrain + i), 1);
+      mbar_init(bar(kBarTurn + i), 1);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(kBarPiece + i), 1);
@@ -520,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&misc.tmem);
   const uint32_t ring = base + C::kRingOff;
-  auto wait = [&](int i, uint32_t parity) { return wait_inline(bar(i), parity, abort_flag, p.err, p.wait_ns); };
+  auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.err, p.wait_ns); };
   // scores enter the exponentials as |scale| s, the queries negated where the scale is negative (zeroed where it is zero,
   // so that the factor itself is never zero: an unseen token's -infinity stays one)
   const bool flat = p.score_scale == 0.f, negate = p.score_scale < 0.f;
@@ -540,7 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax, a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2, rr = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     if (!C::kWide || s == 0) {
@@ -548,90 +581,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const uint32_t qs = base + s * C::kQBytes + (warp & 3) * 32 * 128;     // this warp's 32 rows
       uint32_t n_score = 0, n_out[2] = {0, 0}, n_tile = 0, n_bases = 0, k = 0;
       auto split_of = [&](const Piece& x) { return C::kWide || x.n <= blocks.tokens; };
+      // Whether this stream has tiles of a piece: queries and accumulators change hands for those alone (a phase that passes
+      // without its issuer would be taken for the one before).
+      auto has = [&](const Piece& x) { return x.tiles > (split_of(x) && !C::kWide ? s : 0); };
       // This thread's row of a block: token relative to the block's first (-1: none), query head.
       auto token_of = [&](const Piece& x) {
         const int t = trow + (s == 1 && !split_of(x) ? blocks.tokens : 0);
         return trow < blocks.tokens && t < x.n && x.r % blocks.count * blocks.heads + hrow < p.group ? t : -1;
       };
       auto head_of = [&](const Piece& x) { return x.r / blocks.count * p.group + x.r % blocks.count * blocks.heads + hrow; };
-      auto load_queries = [&](const Piece& x) {
+      // This thread's row as an offset in q (elements, -1: none), and its warp's rows on their way.
+      auto load = [&](const Piece& x) {
         const int t = token_of(x);
-        const int64_t off = t >= 0 && !flat ? int64_t(x.token + t) * p.q_stride + int64_t(head_of(x)) * p.dim : -1;
-        if (__any_sync(0xffffffffu, t >= 0)) {
-#pragma unroll 1
-          for (int j = 0; j < 8; ++j) {
-            const int r = j * 4 + (lane >> 3);
-            const int64_t o = __shfl_sync(0xffffffffu, off, r);
-            const uint32_t to = qs + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-#pragma unroll
-            for (int c = 0; c < DP / 64; ++c) {
-              const int ch = c * 64 + (lane & 7) * 8;
-              if (ch < p.dim) cp_async16(to + c * kChunkBytes, p.q + (o >= 0 ? o + ch : 0), o >= 0 ? 16 : 0);
-            }
-          }
-        }
-        cp_async_commit();
+        load_queries<DP>(p.q, p.dim, qs, t >= 0 && !flat ? int64_t(x.token + t) * p.q_stride + int64_t(head_of(x)) * p.dim : -1,
+                         __any_sync(0xffffffffu, t >= 0));
       };
-      // Queries in place: E4M3: in FP16, scaled by a power of two. -> the row's factor of the scores.
-      auto finish_queries = [&]() {
-        cp_async_wait<0>();
-        __syncwarp();
-        float factor = abs_scale;
-        const uint32_t row = qs + lane * 128;
-        auto at = [&](int c16) { return row + (c16 >> 3) * kChunkBytes + (((c16 & 7) ^ (lane & 7)) << 4); };
-        const uint32_t flip = negate ? 0x80008000u : 0u;
-        if (E4M3) {
-          float top = 0.f;
-#pragma unroll 4
-          for (int c = 0; c < p.dim / 8; ++c) {
-            const uint4 v = lds128(at(c));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-          }
-          // top in [2^e, 2^(e+1)): scale by 2^(15-e) (two factors, each a normal number for any e), to below 2^16, where
-          // the FP16 range ends: channels keep their eight bits down to 2^-32 of the largest, and end at 2^-40 of it
-          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-          if (top == 0.f || e > 127) e = 15;
-          e = max(e, -126) - 15;
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
-          const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
-          factor = fmaxf(abs_scale * __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23) *
-                             __uint_as_float(static_cast<uint32_t>(127 + (e - e / 2)) << 23),
-                         1.2e-38f);
-#pragma unroll 2
-          for (int c = 0; c < p.dim / 8; ++c) {
-            const uint4 v = lds128(at(c));
-            uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = pack_f16x2_rn(__uint_as_float(w[j] << 16) * down * down2,
-                                   __uint_as_float(w[j] & 0xffff0000u) * down * down2);
-            sts128(at(c), w[0], w[1], w[2], w[3]);
-          }
-        } else if (negate) {
-          for (int c = 0; c < p.dim / 8; ++c) {
-            const uint4 v = lds128(at(c));
-            sts128(at(c), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+      auto finish = [&]() {
+        const float factor = finish_queries<E4M3>(p.dim, qs, abs_scale, negate);
         if (lane == 0) mbar_arrive(bar(kBarQ + s));
         return factor;
       };
 
       bool ok = piece_there(0);
       float factor = 0.f;
-      if (ok && piece(0).tiles > 0) {
-        load_queries(piece(0));
-        factor = finish_queries();
+      if (ok && has(piece(0))) {
+        load(piece(0));
+        factor = finish();
       }
       while (ok) {
         const int n = piece(k).tiles;
         if (n == 0 || !(ok = piece_there(k + 1))) break;
-        const bool split = split_of(piece(k)), have_next = piece(k + 1).tiles > 0;
+        const bool split = split_of(piece(k)), have_next = has(piece(k + 1));
         const int token = token_of(piece(k)), pos = piece(k).pos + token, j_first = piece(k).j0;
         const bool active = __any_sync(0xffffffffu, token >= 0);
         const int stride = !C::kWide && split ? 2 : 1, first = stride == 2 ? s : 0;
@@ -645,30 +625,52 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const uint32_t score = tmem + buf * 128 + lanes;
           if (!(ok = wait(kBarScore + buf, par))) break;
           tc_fence_after();
-          if (i + stride >= n && have_next) load_queries(piece(k + 1));      // the last product with these is done
+          if (i + stride >= n && have_next) load(piece(k + 1));      // the last product with these is done
           if (active) {
-            uint32_t r[128];
             const uint4 seen4 = lds128(smem_u32(misc.masks[(n_tile + i) % kMaskBufs]));
-            tmem_ld_tile(score, r);
             const int j0 = j_first + i * kTile;
             const int above = pos - j0 + 1;                                  // tokens of the tile up to the row's own
             const int below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
-            const bool part = above < kTile || below > 0 || (seen4.x & seen4.y & seen4.z & seen4.w) != 0xffffffffu;
-            if (__any_sync(0xffffffffu, part)) {
+            const bool part = __any_sync(0xffffffffu, above < kTile || below > 0 ||
+                                                          (seen4.x & seen4.y & seen4.z & seen4.w) != 0xffffffffu);
+            uint32_t x[32], y[32];
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto maxima = [&](const uint32_t (&r)[32]) {
 #pragma unroll
+              for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
+            };
+            if (!part) {
+              tmem_ld32(score, x);
+              tmem_wait_ld(x);
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                tmem_ld32(score + 32 * (q + 1), y);
+                maxima(x);
+                tmem_wait_ld(y);
+                if (q < 2) tmem_ld32(score + 32 * (q + 2), x);
+                maxima(y);
+                if (q < 2) tmem_wait_ld(x);
+              }
+            } else {
+#pragma unroll 1
               for (int q = 0; q < 4; ++q) {
-                const uint32_t w = (q == 0 ? seen4.x : q == 1 ? seen4.y : q == 2 ? seen4.z : seen4.w) & bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
+                tmem_ld32(score + 32 * q, x);
+                tmem_wait_ld(x);
+                // tokens that the row does not see at -infinity, for the exponentials too
+                const uint32_t w = (q == 0 ? seen4.x : q == 1 ? seen4.y : q == 2 ? seen4.z : seen4.w) &
+                                   bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (!(w >> j & 1u)) r[32 * q + j] = 0xff800000u;
+                  if (!(w >> j & 1u)) x[j] = 0xff800000u;
+                tmem_st32(score + 32 * q, x);
+                maxima(x);
               }
+              tmem_wait_st();
             }
-            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 128; e += 8)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
+            tmem_ld32(score, x);                                             // for the exponentials
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
             const bool over = top > m + kSlack;                              // (m of -infinity: any seen score)
             if (__any_sync(0xffffffffu, over)) {
@@ -695,29 +697,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
             }
             const float off = kLift - (m == -INFINITY ? 0.f : m);
+            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+            auto exponentials = [&](const uint32_t (&r)[32], int q) {
+              uint32_t packed[16];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              uint32_t packed[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int e = 16 * q + 2 * j;
-                const float x = exp2_fast(fmaf(__uint_as_float(r[e]), factor, off));
-                const float y = exp2_fast(fmaf(__uint_as_float(r[e + 1]), factor, off));
-                r[e] = __float_as_uint(x);
-                r[e + 1] = __float_as_uint(y);
-                packed[j] = E4M3 ? pack_f16x2_rn(x, y) : pack_bf16x2_rn(x, y);
+              for (int j = 0; j < 16; ++j) {
+                const float e0 = exp2_fast(fmaf(__uint_as_float(r[2 * j]), factor, off));
+                const float e1 = exp2_fast(fmaf(__uint_as_float(r[2 * j + 1]), factor, off));
+                sum4[j & 1] += e0;
+                sum4[2 + (j & 1)] += e1;
+                packed[j] = E4M3 ? pack_f16x2_rn(e0, e1) : pack_bf16x2_rn(e0, e1);
               }
-              tmem_st8(score + 8 * q, packed);
+              tmem_st16(score + 16 * q, packed);                             // (over scores that have been read)
+            };
+            tmem_wait_ld(x);
+#pragma unroll 1
+            for (int q = 0; q < 4; q += 2) {
+              tmem_ld32(score + 32 * (q + 1), y);
+              exponentials(x, q);
+              tmem_wait_ld(y);
+              if (q == 0) tmem_ld32(score + 64, x);
+              exponentials(y, q + 1);
+              if (q == 0) tmem_wait_ld(x);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarProb + buf));
-            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 128; e += 4)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) sum4[j] += __uint_as_float(r[e + j]);
             l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
           } else {
             tc_fence_before();
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
         }
         if (!ok) break;
-        if (have_next && first < n) next_factor = finish_queries();
+        if (have_next && first < n) next_factor = finish();
 
         // ---- epilogue: O / l, or a part of it
         const Piece& pc = piece(k);
@@ -743,8 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarBases));
           if (!(ok = wait(kBarBases, n_bases++ & 1u))) break;                // read before the next piece's are written
-          // (no tile for this stream: the next queries only now, when every warp has handed over this piece's)
-          if (first >= n && have_next) load_queries(piece(k + 1));
+          if (first >= n && have_next) load(piece(k + 1));
           m = fmaxf(a.x, b.x);
           const float at = m == -INFINITY ? 0.f : m;
           f0 = exp2_fast(a.x - at);
@@ -817,12 +822,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_arrive(bar(kBarOutFree));
           } else if (two) {
             mbar_arrive(bar(kBarOutFree));
-            mbar_arrive(bar(kBarOutFree + 1));
+            if (n > 1) mbar_arrive(bar(kBarOutFree + 1));
           } else {
             mbar_arrive_n(bar(kBarOutFree + s), 2);
           }
         }
-        if (have_next && first >= n) next_factor = finish_queries();
+        if (have_next && first >= n) next_factor = finish();
         n_tile += n;
         piece_done(k);
         ++k;
@@ -832,7 +837,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------- loaders: 32 tokens of every tile a warp, a lane a token
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const int w = warp - 8;
     bool ok = true;
     uint32_t unit = 0, n_tile = 0;
@@ -952,25 +956,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const bool all = seen == 0xffffffffu;
         if (lane == 0) misc.masks[(n_tile + i) % kMaskBufs][w] = seen;
         // in the order in which the products take them (wide: the next tile's keys before this one's values)
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          if (ok) load_unit(&maps.k, p.k, head, h * 128, tok, all);
-        if (!C::kWide) {
-          if (ok) load_unit(&maps.v, p.v, head, 0, tok, all);
-        } else {
-          if (i > 0) {
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-              if (ok) load_unit(&maps.v, p.v, head, h * 128, old, old_all);
-          }
-          if (i == n - 1) {
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-              if (ok) load_unit(&maps.v, p.v, head, h * 128, tok, all);
-          }
-          old = tok;
-          old_all = all;
+        const int values = C::kWide ? (i > 0) + (i == n - 1) : 1, units = C::kHalves * (1 + values);
+#pragma unroll 1
+        for (int k = 0; ok && k < units; ++k) {
+          const bool is_key = k < C::kHalves, before = C::kWide && !is_key && i > 0 && k < 2 * C::kHalves;
+          load_unit(is_key ? &maps.k : &maps.v, is_key ? p.k : p.v, head, k % C::kHalves * 128, before ? old : tok, before ? old_all : all);
         }
+        old = tok;
+        old_all = all;
       }
       n_tile += n;
       piece_done(piece_no);
@@ -984,12 +977,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------- issuers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const int s = warp - 12;
     if (s < C::kStreams) {
       bool ok = true;
       const uint32_t score_desc = instr_desc(E4M3, kTile, false);
-      uint32_t n_prob = 0, n_piece = 0, n_tile = 0, unit = 0;
+      uint32_t n_prob = 0, n_piece = 0, n_own = 0, n_tile = 0, unit = 0, n_turn = 0;
       const int steps = p.dim / 16;
       auto full = [&](uint32_t u) { return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1u); };
       auto free_unit = [&](uint32_t u) { tc_commit(bar(kBarFree + u % C::kSlots)); };
@@ -997,49 +989,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       auto score = [&](uint32_t u, int h, uint32_t d) {
         const uint64_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
         const uint64_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
-        score_steps<C::kUnitCh / 16>(h < C::kHalves - 1 ? C::kUnitCh / 16 : steps - h * 8, d, a, b, score_desc, h > 0);
-      };
-      // S of the tile whose keys begin at unit u
-      auto issue_score = [&](uint32_t u, uint32_t d, int done_bar) {
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-          if (!ok || !(ok = full(u + h))) return;
-          tc_fence_after();
-          if (lane == 0) {
-            score(u + h, h, d);
-            if (h == C::kHalves - 1) tc_commit(bar(done_bar));
-            free_unit(u + h);
-          }
-          __syncwarp();
-        }
+        for (int k = 0; k < C::kUnitCh / 16; ++k)                           // 16 channels = 32 bytes a step
+          if (h * 8 + k < steps)
+            tc_mma(d, a + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3), b + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
+                   score_desc, h > 0 || k > 0 ? 1u : 0u);
       };
-      // the products of O (+)= P V with the unit u (half h of a tile's values): tokens 16 k0 .. 16 k1 - 1
+      // the products of O (+)= P V with the unit u (half h of a tile's values)
       auto value = [&](uint32_t u, int h, uint32_t prob, bool accumulate) {
-        const int width = min(p.dim - 128 * h, 128);
-        const uint32_t desc = instr_desc(E4M3, width, true);
+        const uint32_t desc = instr_desc(E4M3, min(p.dim - 128 * h, 128), true);
         const uint64_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)                                 // 16 tokens = two 1024-byte groups a step
           tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
       };
-      // O of the tile whose values begin at unit u
-      auto issue_value = [&](uint32_t u, uint32_t prob, bool accumulate) {
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-          if (!ok || !(ok = full(u + h))) return;
-          tc_fence_after();
-          if (lane == 0) {
-            value(u + h, h, prob, accumulate);
-            free_unit(u + h);
-          }
-          __syncwarp();
-        }
-      };
       while (ok) {
         if (!(ok = piece_there(n_piece))) break;
         const int n = piece(n_piece).tiles;
         const bool split = piece(n_piece).n <= blocks.tokens;
-        if (n == 0 || !(ok = wait(kBarQ + s, n_piece & 1u))) break;
+        if (n == 0) break;
+        const bool own = n > (split && !C::kWide ? s : 0);   // tiles of this stream
+        if (own && !(ok = wait(kBarQ + s, n_own & 1u))) break;
+        bool freed = n_own == 0;                             // the accumulator, read by the piece before
+        auto acc_free = [&]() {
+          if (!freed) ok = wait(kBarOutFree + s, (n_own - 1) & 1u);
+          freed = true;
+          return ok;
+        };
         if (!C::kWide) {
           const int stride = split ? 2 : 1, first = split ? s : 0;
           const uint32_t score_col = tmem + s * 128;
@@ -1047,57 +1023,87 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           // A tile of the other stream: its units are waited for and given back all the same, so that every phase of a slot is
           // seen by both issuers (a parity tells two phases apart, not three).
           auto pass = [&](int i) {
-            for (uint32_t u = keys_of(i); u < keys_of(i) + 2; ++u) {
-              if (!ok || !(ok = full(u))) return;
-              if (lane == 0) mbar_arrive(bar(kBarFree + u % C::kSlots));
+            for (uint32_t u = keys_of(i); ok && u < keys_of(i) + 2; ++u) {
+              ok = full(u);
+              if (ok && lane == 0) mbar_arrive(bar(kBarFree + u % C::kSlots));
             }
+            return ok;
           };
+          // Both streams with the same tiles: their products are issued in turns, a tile's O += P V and next S of one, then of
+          // the other. In no order, the tensor pipe takes them by turns one at a time, both streams get their scores
+          // together and run their softmax against each other.
+          auto my_turn = [&]() { return s == 0 ? n_turn == 0 || wait(kBarTurn + 1, (n_turn - 1) & 1u) : wait(kBarTurn, n_turn & 1u); };
           if (split && s == 1) pass(0);
-          if (first < n) issue_score(keys_of(first), score_col, kBarScore + s);
-          if (n_piece > 0 && ok) ok = wait(kBarOutFree + s, (n_piece - 1) & 1u);
-          for (int i = first; ok && i < n; i += stride, ++n_prob) {
-            const uint32_t v = keys_of(i) + 1, next = keys_of(i + stride);
-            const bool more = i + stride < n, near = more && stride == 1;
-            // everything that the products take is waited for before P, and nothing stands between O += P V and the next S:
-            // the softmax waits for that one
-            if (!(ok = full(v)) || (near && !(ok = full(next)))) break;
-            if (!(ok = wait(kBarProb + s, n_prob & 1u))) break;
+          // Step i: O += P V of tile i (none in the first step), S of the next. A stream of its own tiles waits for all that
+          // both take before P, and issues them together: the softmax waits for the second. With every other tile, what
+          // a product does not take is not waited for: the slots are given back early.
+          for (int i = first - stride; ok && i < n; i += stride) {
+            const bool values = i >= first, scores = i + stride < n;
+            const uint32_t v = keys_of(i) + 1, q = keys_of(i + stride);
+            if (values && !(acc_free() && (ok = full(v)))) break;
+            if (!split && scores && !(ok = full(q))) break;
+            if (values && !(ok = wait(kBarProb + s, n_prob++ & 1u))) break;
+            if (!split && !(ok = my_turn())) break;
             tc_fence_after();
+            if (values && lane == 0) value(v, 0, score_col, i != first);
+            if (split) {
+              if (values && lane == 0) free_unit(v);
+              if (values && !scores && lane == 0) tc_commit(bar(kBarOut + s));
+              if (values && i + 1 < n && !pass(i + 1)) break;
+              if (scores && !(ok = full(q))) break;
+              tc_fence_after();
+            }
             if (lane == 0) {
-              value(v, 0, score_col, i != first);
-              if (near) {
-                score(next, 0, score_col);
+              if (scores) score(q, 0, score_col);
+              if (!split) mbar_arrive(bar(kBarTurn + s));
+              if (scores) {
                 tc_commit(bar(kBarScore + s));
-                free_unit(next);
+                free_unit(q);
               }
-              free_unit(v);
-              if (!more) tc_commit(bar(kBarOut + s));
+              if (values && !split) {
+                free_unit(v);
+                if (!scores) tc_commit(bar(kBarOut + s));
+              }
             }
             __syncwarp();
-            if (split && i + 1 < n) pass(i + 1);
-            if (more && !near) issue_score(next, score_col, kBarScore + s);
+            if (!split) ++n_turn;
           }
         } else {
-          // scores one tile ahead: the units come in this order
-          issue_score(unit, tmem + (n_prob & 1) * 128, kBarScore + (n_prob & 1));
-          unit += C::kHalves;
-          if (n_piece > 0 && ok) ok = wait(kBarOutFree, (n_piece - 1) & 1u);
-          for (int i = 0; ok && i < n; ++i, ++n_prob) {
-            if (i + 1 < n) {
-              issue_score(unit, tmem + ((n_prob + 1) & 1) * 128, kBarScore + ((n_prob + 1) & 1));
-              unit += C::kHalves;
+          // scores one tile ahead; the units come in this order
+          for (int i = 0; ok && i <= n; ++i) {
+            if (i < n) {
+              const uint32_t buf = (n_prob + (i > 0)) & 1;
+#pragma unroll 1
+              for (int h = 0; ok && h < C::kHalves; ++h, ++unit) {
+                if (!(ok = full(unit))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                  score(unit, h, tmem + buf * 128);
+                  if (h == C::kHalves - 1) tc_commit(bar(kBarScore + buf));
+                  free_unit(unit);
+                }
+                __syncwarp();
+              }
             }
-            if (!ok || !(ok = wait(kBarProb + (n_prob & 1), (n_prob >> 1) & 1u))) break;
-            tc_fence_after();
-            issue_value(unit, tmem + (n_prob & 1) * 128, i > 0);
-            unit += C::kHalves;
-            if (ok) {
-              if (lane == 0) tc_commit(bar(kBarOut + (n_prob & 1)));
+            if (!ok || i == 0) continue;
+            if (!acc_free() || !(ok = wait(kBarProb + (n_prob & 1), (n_prob >> 1) & 1u))) break;
+#pragma unroll 1
+            for (int h = 0; ok && h < C::kHalves; ++h, ++unit) {
+              if (!(ok = full(unit))) break;
+              tc_fence_after();
+              if (lane == 0) {
+                value(unit, h, tmem + (n_prob & 1) * 128, i > 1);
+                if (h == C::kHalves - 1) tc_commit(bar(kBarOut + (n_prob & 1)));
+                free_unit(unit);
+              }
               __syncwarp();
             }
+            ++n_prob;
           }
         }
+        if (!ok) break;
         n_tile += n;
+        n_own += own;
         piece_done(n_piece);
         ++n_piece;
       }
