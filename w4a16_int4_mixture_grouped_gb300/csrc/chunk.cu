@@ -139,7 +139,7 @@ __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
 
 // Fills *sh for CTA `cta` of `grid` (every thread calls it): sequence after sequence, their `rows` work rows (cache heads x
 // head blocks) one after the other, each the tiles of its blocks of `step` tokens. False: no work.
-__device__ __forceinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
+static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int pass = 0; pass < 2; ++pass) {
     int64_t line = 0;                                   // tiles of the sequences before these
@@ -292,21 +292,29 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Operand tiles are rows of 128 bytes in 128-byte swizzle, 8-row groups of 1024 bytes. K-major (rows along M or N, 64
+// channels of the reduction a row): groups follow each other along the rows. N-major (rows along the reduction, 64 channels
+// of N a row): groups follow each other along the reduction, the next 64 channels are a chunk further.
+// (A descriptor's upper word is the same for all; the lower one's address advances in 16 bytes.)
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr) { return (addr & 0x3FFFFu) >> 4 | static_cast<uint32_t>(kChunkBytes >> 4) << 16; }
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
 // A in tensor memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
 // A thread's lane and N columns from `addr` on.
@@ -365,13 +373,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Operand tiles are rows of 128 bytes in 128-byte swizzle, 8-row groups of 1024 bytes. K-major (rows along M or N, 64
-// channels of the reduction a row): groups follow each other along the rows. N-major (rows along the reduction, 64 channels
-// of N a row): groups follow each other along the reduction, the next 64 channels are a chunk further.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  return (static_cast<uint64_t>((addr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(kChunkBytes >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
 // kind::f16, FP32 accumulator, M = 128; bit 16: B N-major.
 __device__ __forceinline__ uint32_t instr_desc(bool f16, int n, bool n_major) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(n >> 3) << 17) |
@@ -488,8 +489,30 @@ static __device__ __noinline__ float finish_queries(int dim, uint32_t qs, float 
   return factor;
 }
 
+// 32 tokens of a unit one by one: the lane's at off in the pages (elements, -1: zeros), to the rows from dst on.
+template <int CHANNELS>
+static __device__ __noinline__ void load_tokens(const uint8_t* src, int dim, int ch0, int64_t off, uint32_t dst) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t to = dst + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);                  // rows 4 k + lane / 8
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t o = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
+    // (row 4 k + i: its swizzle is row i's with bit 2 flipped for odd k)
+    const uint32_t at = (to + k * 512) ^ ((k & 1) << 6);
+#pragma unroll
+    for (int c = 0; c < CHANNELS / 64; ++c) {
+      const int ch = ch0 + c * 64 + (lane & 7) * 8;
+      if (ch < dim) cp_async16(at + c * kChunkBytes, src + (o >= 0 ? (o + ch) * 2 : 0), o >= 0 ? 16 : 0);
+    }
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Rows that stand before their sequence's first token, or have none: zeros and -infinity, spread over the CTAs.
-__device__ __forceinline__ void zero_unseeing(const ChunkParams& p) {
+static __device__ __noinline__ void zero_unseeing(const ChunkParams& p) {
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
     const ChunkRange c = chunk_range(p, b);
     const int n = c.row < 0 ? c.n : c.base < 0 ? min(c.n, -c.base) : 0;
@@ -908,22 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           __syncwarp();
           if (c < chunks) tma_load_4d(dst + c * kChunkBytes + r * 128, map, ch0 + c * 64, head, at, page, full);
         } else {
-          const uint32_t to = dst + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);          // rows 4 k + lane / 8
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int64_t o = __shfl_sync(0xffffffffu, off, k * 4 + (lane >> 3));
-            // (row 4 k + i: its swizzle is row i's with bit 2 flipped for odd k)
-            const uint32_t at = (to + k * 512) ^ ((k & 1) << 6);
-#pragma unroll
-            for (int c = 0; c < C::kUnitCh / 64; ++c) {
-              const int ch = ch0 + c * 64 + (lane & 7) * 8;
-              if (ch < p.dim) cp_async16(at + c * kChunkBytes, src + (o >= 0 ? (o + ch) * 2 : 0), o >= 0 ? 16 : 0);
-            }
-          }
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
+          load_tokens<C::kUnitCh>(src, p.dim, ch0, off, dst);
           if (lane == 0) mbar_arrive(full);
         }
       }
@@ -987,8 +995,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       auto free_unit = [&](uint32_t u) { tc_commit(bar(kBarFree + u % C::kSlots)); };
       // the products of S = Q K^T with the unit u (half h of a tile's keys), into column d
       auto score = [&](uint32_t u, int h, uint32_t d) {
-        const uint64_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
-        const uint64_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
+        const uint32_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
+        const uint32_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
 #pragma unroll
         for (int k = 0; k < C::kUnitCh / 16; ++k)                           // 16 channels = 32 bytes a step
           if (h * 8 + k < steps)
@@ -998,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // the products of O (+)= P V with the unit u (half h of a tile's values)
       auto value = [&](uint32_t u, int h, uint32_t prob, bool accumulate) {
         const uint32_t desc = instr_desc(E4M3, min(p.dim - 128 * h, 128), true);
-        const uint64_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
+        const uint32_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)                                 // 16 tokens = two 1024-byte groups a step
           tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
