@@ -287,6 +287,13 @@ struct Record {
 // ---------------------------------------------------------------------------
 // tensor memory and tcgen05
 // ---------------------------------------------------------------------------
+// One lane of the warp. (Behind this instruction, unlike a comparison of the lane's number, the compiler keeps addresses and
+// descriptors in uniform registers: eight products issued beside two softmax warps take 413 cycles, else 699.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -377,6 +384,22 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ uint32_t instr_desc(bool f16, int n, bool n_major) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24) | (n_major ? 1u << 16 : 0u);
+}
+
+// d (+)= A B^T over `steps` (1 .. MOST) times 16 channels, both K-major. A thread issues a product every 67 cycles, with a
+// branch before each every 147 (a product takes 64): each number of steps has a sequence of its own.
+template <int STEPS>
+__device__ __forceinline__ void score_products(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const uint32_t off = (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3);       // 16 channels = 32 bytes a step
+    tc_mma(d, a + off, b + off, idesc, accumulate || k > 0 ? 1u : 0u);
+  }
+}
+template <int MOST>
+__device__ __forceinline__ void score_steps(int steps, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+  if (steps == MOST) return score_products<MOST>(d, a, b, idesc, accumulate);
+  if constexpr (MOST > 1) score_steps<MOST - 1>(steps, d, a, b, idesc, accumulate);
 }
 
 // ---------------------------------------------------------------------------
@@ -656,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const int below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
             const bool part = __any_sync(0xffffffffu, above < kTile || below > 0 ||
                                                           (seen4.x & seen4.y & seen4.z & seen4.w) != 0xffffffffu);
-            uint32_t x[32], y[32];
+            uint32_t x[32];
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             auto maxima = [&](const uint32_t (&r)[32]) {
 #pragma unroll
@@ -665,23 +688,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int j = 0; j < 4; ++j)
                   top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
             };
-            if (!part) {
-              tmem_ld32(score, x);
-              tmem_wait_ld(x);
-#pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                tmem_ld32(score + 32 * (q + 1), y);
-                maxima(x);
-                tmem_wait_ld(y);
-                if (q < 2) tmem_ld32(score + 32 * (q + 2), x);
-                maxima(y);
-                if (q < 2) tmem_wait_ld(x);
-              }
-            } else {
 #pragma unroll 1
-              for (int q = 0; q < 4; ++q) {
-                tmem_ld32(score + 32 * q, x);
-                tmem_wait_ld(x);
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld32(score + 32 * q, x);
+              tmem_wait_ld(x);
+              if (part) {
                 // tokens that the row does not see at -infinity, for the exponentials too
                 const uint32_t w = (q == 0 ? seen4.x : q == 1 ? seen4.y : q == 2 ? seen4.z : seen4.w) &
                                    bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
@@ -689,10 +700,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int j = 0; j < 32; ++j)
                   if (!(w >> j & 1u)) x[j] = 0xff800000u;
                 tmem_st32(score + 32 * q, x);
-                maxima(x);
               }
-              tmem_wait_st();
+              maxima(x);
             }
+            if (part) tmem_wait_st();
             tmem_ld32(score, x);                                             // for the exponentials
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
             const bool over = top > m + kSlack;                              // (m of -infinity: any seen score)
@@ -733,15 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               tmem_st16(score + 16 * q, packed);                             // (over scores that have been read)
             };
-            tmem_wait_ld(x);
 #pragma unroll 1
-            for (int q = 0; q < 4; q += 2) {
-              tmem_ld32(score + 32 * (q + 1), y);
+            for (int q = 0; q < 4; ++q) {
+              tmem_wait_ld(x);
               exponentials(x, q);
-              tmem_wait_ld(y);
-              if (q == 0) tmem_ld32(score + 64, x);
-              exponentials(y, q + 1);
-              if (q == 0) tmem_wait_ld(x);
+              if (q < 3) tmem_ld32(score + 32 * (q + 1), x);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -997,11 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       auto score = [&](uint32_t u, int h, uint32_t d) {
         const uint32_t a = smem_desc(base + s * C::kQBytes + h * 2 * kChunkBytes);
         const uint32_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
-#pragma unroll
-        for (int k = 0; k < C::kUnitCh / 16; ++k)                           // 16 channels = 32 bytes a step
-          if (h * 8 + k < steps)
-            tc_mma(d, a + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3), b + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
-                   score_desc, h > 0 || k > 0 ? 1u : 0u);
+        score_steps<C::kUnitCh / 16>(min(C::kUnitCh / 16, steps - h * 8), d, a, b, score_desc, h > 0);
       };
       // the products of O (+)= P V with the unit u (half h of a tile's values)
       auto value = [&](uint32_t u, int h, uint32_t prob, bool accumulate) {
@@ -1053,15 +1056,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (values && !(ok = wait(kBarProb + s, n_prob++ & 1u))) break;
             if (!split && !(ok = my_turn())) break;
             tc_fence_after();
-            if (values && lane == 0) value(v, 0, score_col, i != first);
+            if (values && elect_one()) value(v, 0, score_col, i != first);
             if (split) {
-              if (values && lane == 0) free_unit(v);
-              if (values && !scores && lane == 0) tc_commit(bar(kBarOut + s));
+              if (values && elect_one()) free_unit(v);
+              if (values && !scores && elect_one()) tc_commit(bar(kBarOut + s));
               if (values && i + 1 < n && !pass(i + 1)) break;
               if (scores && !(ok = full(q))) break;
               tc_fence_after();
             }
-            if (lane == 0) {
+            if (elect_one()) {
               if (scores) score(q, 0, score_col);
               if (!split) mbar_arrive(bar(kBarTurn + s));
               if (scores) {
@@ -1085,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               for (int h = 0; ok && h < C::kHalves; ++h, ++unit) {
                 if (!(ok = full(unit))) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                   score(unit, h, tmem + buf * 128);
                   if (h == C::kHalves - 1) tc_commit(bar(kBarScore + buf));
                   free_unit(unit);
@@ -1099,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             for (int h = 0; ok && h < C::kHalves; ++h, ++unit) {
               if (!(ok = full(unit))) break;
               tc_fence_after();
-              if (lane == 0) {
+              if (elect_one()) {
                 value(unit, h, tmem + (n_prob & 1) * 128, i > 1);
                 if (h == C::kHalves - 1) tc_commit(bar(kBarOut + (n_prob & 1)));
                 free_unit(unit);
@@ -1115,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         piece_done(n_piece);
         ++n_piece;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         tc_commit(bar(kBarDrain + s));
         mbar_drain(bar(kBarDrain + s), 0);
       }
