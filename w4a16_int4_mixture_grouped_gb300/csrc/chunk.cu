@@ -34,7 +34,10 @@ namespace chunk {
 constexpr int kTile = 128;                    // tokens of a tile
 constexpr int kRows = 128;                    // query rows of a stream (MMA M)
 constexpr int kMaxCtas = 152;
-constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
+// A block of rows costs about as much as kBlockTiles tiles on top of its own (queries, first scores, epilogue): the line that
+// the CTAs share has as many places before its tiles.
+constexpr int kBlockTiles = 2;
+constexpr int kMinPlaces = 4;                 // places of the line that a CTA takes at least
 constexpr int kMaskBufs = 8;                  // tiles whose masks of seen tokens are kept
 constexpr int kChunkBytes = 128 * 128;        // 64 channels of 128 rows, 128-byte swizzled
 
@@ -78,10 +81,10 @@ enum {
 constexpr int kPieces = 4;       // pieces listed ahead
 constexpr int kUsers = 14;       // warps that read them
 
-// Where a CTA's share of the line of tiles begins.
+// Where a CTA's share of the line begins.
 struct Share {
-  int64_t total, x, x_end, first, seq;       // seq: tiles of a work row of sequence b
-  int ctas, b, r, qt, tile;
+  int64_t total, x, x_end, first, seq;       // seq: places of a work row of sequence b
+  int ctas, b, r, qt, place;
   int64_t sums[kThreads / 32];
 };
 // Some tiles of one block of rows: `n` tokens of a sequence's chunk, work row r. (tiles = 0: the share is done.)
@@ -123,12 +126,14 @@ __device__ __forceinline__ void seen_by(const ChunkParams& p, const ChunkRange& 
   lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
   if (c.row < 0 || hi < 0) hi = 0;
 }
-__device__ __forceinline__ int64_t tiles_of_row(const ChunkParams& p, const ChunkRange& c, int step) {
+// Places on the line.
+__device__ __forceinline__ int places_of(int tiles) { return tiles > 0 ? tiles + kBlockTiles : 0; }
+__device__ __forceinline__ int64_t places_of_row(const ChunkParams& p, const ChunkRange& c, int step) {
   int64_t sum = 0;
   for (int64_t i = 0; i < c.n; i += step) {
     int lo, hi;
     seen_by(p, c, static_cast<int>(i), static_cast<int>(min(int64_t(step), c.n - i)), lo, hi);
-    sum += tiles_of(lo, hi);
+    sum += places_of(tiles_of(lo, hi));
   }
   return sum;
 }
@@ -138,14 +143,14 @@ __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
 }
 
 // Fills *sh for CTA `cta` of `grid` (every thread calls it): sequence after sequence, their `rows` work rows (cache heads x
-// head blocks) one after the other, each the tiles of its blocks of `step` tokens. False: no work.
+// head blocks) one after the other, each the places of its blocks of `step` tokens. False: no work.
 static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int pass = 0; pass < 2; ++pass) {
-    int64_t line = 0;                                   // tiles of the sequences before these
+    int64_t line = 0;                                   // places of the sequences before these
     for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      const int64_t n = b < p.batch ? tiles_of_row(p, chunk_range(p, b), step) : 0;
+      const int64_t n = b < p.batch ? places_of_row(p, chunk_range(p, b), step) : 0;
       int64_t pre = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -165,7 +170,7 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
       line += all * rows;
       if (pass == 0 && b0 + kThreads >= p.batch) {
         if (threadIdx.x == 0) {
-          int64_t ctas = line / kMinTiles;
+          int64_t ctas = line / kMinPlaces;
           ctas = ctas < 1 ? 1 : ctas > grid ? grid : ctas;
           const bool work = line > 0 && cta < ctas;
           sh->total = line;
@@ -188,7 +193,7 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
   }
   __syncthreads();
   if (warp == 0) {
-    // the work row, the block of tokens and the tile
+    // the work row, the block of tokens and the place in it
     const ChunkRange c = chunk_range(p, sh->b);
     int64_t y = sh->x - sh->first;
     const int r = static_cast<int>(y / sh->seq);
@@ -198,7 +203,7 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
       int lo, hi, n = 0;
       if (i < c.n) {
         seen_by(p, c, static_cast<int>(i), min(step, c.n - static_cast<int>(i)), lo, hi);
-        n = tiles_of(lo, hi);
+        n = places_of(tiles_of(lo, hi));
       }
       int64_t pre = n;
 #pragma unroll
@@ -209,7 +214,7 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
       if (y < pre && y >= pre - n) {
         sh->r = r;
         sh->qt = q0 + lane;
-        sh->tile = static_cast<int>(y - (pre - n));
+        sh->place = static_cast<int>(y - (pre - n));
       }
       const int64_t sum = __shfl_sync(0xffffffffu, pre, 31);
       if (y < sum) break;
@@ -224,7 +229,7 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
 struct Walk {
   int64_t x, x_end, total;
   ChunkRange c;
-  int b, r, qt, tile, ctas;
+  int b, r, qt, place, ctas;
   __device__ __forceinline__ void start(const ChunkParams& p, const Share& sh) {
     x = sh.x;
     x_end = sh.x_end;
@@ -233,7 +238,7 @@ struct Walk {
     b = sh.b;
     r = sh.r;
     qt = sh.qt;
-    tile = sh.tile;
+    place = sh.place;
     c = chunk_range(p, b);
   }
   __device__ __forceinline__ bool next(const ChunkParams& p, int rows, int step, Piece& o) {
@@ -254,18 +259,21 @@ struct Walk {
       const int ntiles = tiles_of(lo, hi);
       ++qt;
       if (ntiles == 0) continue;
-      const int64_t row0 = x - tile;               // line position of the block's first tile
+      const int64_t tile0 = x - place + kBlockTiles;   // line position of the block's first tile
+      const int from = max(0, place - kBlockTiles);
+      const int to = static_cast<int>(max(int64_t(0), min(int64_t(ntiles), x_end - tile0)));
+      x = min(x_end, tile0 + ntiles);
+      place = 0;
+      if (to <= from) continue;                        // the share ends before its tiles
       o.token = c.first + static_cast<int>(i);
       o.pos = c.base + static_cast<int>(i);
       o.r = r;
       o.row = c.row;
       o.len = c.base + c.n;
-      o.j0 = (lo / kTile + tile) * kTile;
-      o.tiles = static_cast<int>(min(int64_t(ntiles - tile), x_end - x));
-      o.c0 = cta_of(total, ctas, row0);
-      o.c1 = cta_of(total, ctas, row0 + ntiles - 1);
-      x += o.tiles;
-      tile = 0;
+      o.j0 = (lo / kTile + from) * kTile;
+      o.tiles = to - from;
+      o.c0 = cta_of(total, ctas, tile0);
+      o.c1 = cta_of(total, ctas, tile0 + ntiles - 1);
       return true;
     }
     return false;
@@ -350,11 +358,32 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr)
       : "memory");
 }
-// tmem_ld32's loads are there: nothing reads r before.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+// 16 lanes x 32 columns as fragments: registers 4j, 4j + 1 hold lane t / 4, columns 8j + 2 (t % 4), + 1 (thread t),
+// registers 4j + 2, 4j + 3 the same of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+// Word w[k] of lane i of four goes to word w[i] of lane k.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int i) {
+  const bool odd = i & 1, high = i & 2;
+  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), b = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+  if (odd) w[0] = a, w[2] = b;
+  else w[1] = a, w[3] = b;
+  a = __shfl_xor_sync(0xffffffffu, high ? w[0] : w[2], 2), b = __shfl_xor_sync(0xffffffffu, high ? w[1] : w[3], 2);
+  if (high) w[0] = a, w[1] = b;
+  else w[2] = a, w[3] = b;
+}
+// tmem_ld32's loads are there: nothing reads them before.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32], uint32_t (&r2)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
+  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]), "+r"(r2[k]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -679,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const int below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
             const bool part = __any_sync(0xffffffffu, above < kTile || below > 0 ||
                                                           (seen4.x & seen4.y & seen4.z & seen4.w) != 0xffffffffu);
-            uint32_t x[32];
+            uint32_t x[32], y[32];
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             auto maxima = [&](const uint32_t (&r)[32]) {
 #pragma unroll
@@ -688,23 +717,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int j = 0; j < 4; ++j)
                   top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
             };
+            // the second half for its maximum, then the first, which stays in registers for the exponentials
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              tmem_ld32(score + 32 * q, x);
-              tmem_wait_ld(x);
-              if (part) {
-                // tokens that the row does not see at -infinity, for the exponentials too
-                const uint32_t w = (q == 0 ? seen4.x : q == 1 ? seen4.y : q == 2 ? seen4.z : seen4.w) &
-                                   bits_below(above - 32 * q) & ~bits_below(below - 32 * q);
+            for (int half = 1; half >= 0; --half) {
+              tmem_ld32(score + 64 * half, x);
+              tmem_ld32(score + 64 * half + 32, y);
+              tmem_wait_ld(x, y);
+              if (part) {                                                    // tokens that the row does not see at -infinity
+                const uint32_t w0 = (half ? seen4.z : seen4.x) & bits_below(above - 64 * half) & ~bits_below(below - 64 * half);
+                const uint32_t w1 = (half ? seen4.w : seen4.y) & bits_below(above - 64 * half - 32) & ~bits_below(below - 64 * half - 32);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(w >> j & 1u)) x[j] = 0xff800000u;
-                tmem_st32(score + 32 * q, x);
+                for (int j = 0; j < 32; ++j) {
+                  if (!(w0 >> j & 1u)) x[j] = 0xff800000u;
+                  if (!(w1 >> j & 1u)) y[j] = 0xff800000u;
+                }
+                if (half) {
+                  tmem_st32(score + 64, x);
+                  tmem_st32(score + 96, y);
+                  tmem_wait_st();
+                }
               }
               maxima(x);
+              maxima(y);
             }
-            if (part) tmem_wait_st();
-            tmem_ld32(score, x);                                             // for the exponentials
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
             const bool over = top > m + kSlack;                              // (m of -infinity: any seen score)
             if (__any_sync(0xffffffffu, over)) {
@@ -744,12 +779,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               tmem_st16(score + 16 * q, packed);                             // (over scores that have been read)
             };
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              tmem_wait_ld(x);
-              exponentials(x, q);
-              if (q < 3) tmem_ld32(score + 32 * (q + 1), x);
-            }
+            exponentials(x, 0);
+            tmem_ld32(score + 64, x);
+            exponentials(y, 1);
+            tmem_ld32(score + 96, y);
+            tmem_wait_ld(x, y);
+            exponentials(x, 2);
+            exponentials(y, 3);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -814,32 +850,59 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const float inv = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
           f0 *= inv;
           f1 *= inv;
-          const int half = (p.dim / 16 + 1) / 2 * 16;    // two: a stream's warps take half of the channels each
+          const int half = (p.dim + 63) / 64 * 32;       // two: a stream's warps take half of the channels each
           const int from = two && s == 1 ? half : 0, to = two && s == 0 ? half : p.dim;
           const bool second = two && n > 1;
+          if (whole) {
+            // Fragments of 16 rows x 32 columns; the four lanes of a row trade words, so that each stores 16 bytes of the
+            // 64 that are theirs (a thread a row stores to 32 lines at once, four times as long).
+            const int64_t off = valid ? out_row * p.dim : -1;
 #pragma unroll 1
-          for (int c = from; c < to; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tmem + kAcc + (two ? 0 : s * 128) + c + lanes, o);
+            for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll 1
+              for (int c = from; c < to; c += 32) {
+                uint32_t o[16];
+                tmem_ld_frag(tmem + kAcc + (two ? 0 : s * 128) + c + lanes + (hh << 20), o);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
-            if (second) {
-              uint32_t o1[16];
-              tmem_ld16(tmem + kAcc + 128 + c + lanes, o1);
+                for (int j = 0; j < 16; ++j)
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(0xffffffffu, f0, 16 * hh + 8 * (j >> 1 & 1) + (lane >> 2)));
+                if (second) {
+                  uint32_t o1[16];
+                  tmem_ld_frag(tmem + kAcc + 128 + c + lanes + (hh << 20), o1);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+                  for (int j = 0; j < 16; ++j)
+                    o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), __shfl_sync(0xffffffffu, f1, 16 * hh + 8 * (j >> 1 & 1) + (lane >> 2)),
+                                                __uint_as_float(o[j])));
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2_rn(__uint_as_float(o[4 * j + 2 * k]), __uint_as_float(o[4 * j + 2 * k + 1]));
+                  transpose4(w, lane & 3);
+                  const int64_t at = __shfl_sync(0xffffffffu, off, 16 * hh + 8 * k + (lane >> 2));
+                  const int ch = c + 8 * (lane & 3);
+                  if (at >= 0 && ch < p.dim) *reinterpret_cast<uint4*>(p.out + at + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
             }
-            if (!valid) continue;
-            if (whole) {
-              uint32_t w[8];
+          } else {
+#pragma unroll 1
+            for (int c = from; c < min(to, p.dim); c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem + kAcc + (two ? 0 : s * 128) + c + lanes, o);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2_rn(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
-              uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * p.dim + c);
-              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+              if (second) {
+                uint32_t o1[16];
+                tmem_ld16(tmem + kAcc + 128 + c + lanes, o1);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) __stcg(part + (2 + c + j) * C::kPartRows, __uint_as_float(o[j]));
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+              }
+              if (valid) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) __stcg(part + (2 + c + j) * C::kPartRows, __uint_as_float(o[j]));
+              }
             }
           }
         }
