@@ -55,6 +55,7 @@ struct Cfg {
   static constexpr int kSlots = DP == 64 ? 8 : kWide && !E4M3 ? 5 : 4;
   static constexpr int kLag = 1;                                   // E4M3: units in flight behind the newest
   static constexpr int kStages = kLag + 1;                         // raw units of a loader warp
+  static_assert(kStages == 2, "barriers");
   static constexpr int kStageBytes = 32 * kUnitCh;
   static constexpr int kRingOff = kStreams * kQBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kUnitBytes;
@@ -76,7 +77,8 @@ enum {
   kBarBases = 34,                // bases and sums of a piece's two accumulators written, then read
   kBarTurn = 35,                 // [2] a stream's products issued: the other's turn
   kBarDrain = 37,                // [2]
-  kNumBars = 39
+  kBarRaw = 39,                  // [4][2] E4M3: a loader warp's raw unit has come
+  kNumBars = 47
 };
 constexpr int kPieces = 4;       // pieces listed ahead
 constexpr int kUsers = 14;       // warps that read them
@@ -280,8 +282,8 @@ struct Walk {
   }
 };
 
-// Pages as a tensor of (channels, heads, tokens of a page, pages), in boxes of 64 channels of `rows` tokens (0: none, see
-// launch).
+// Pages as a tensor of (channels, heads, tokens of a page, pages), in boxes of 64 channels (E4M3: a unit's) of `rows` tokens
+// (0: none, see page_maps).
 struct PageMaps {
   CUtensorMap k, v;
   int rows;
@@ -541,7 +543,22 @@ static __device__ __noinline__ float finish_queries(int dim, uint32_t qs, float 
   return factor;
 }
 
-// 32 tokens of a unit one by one: the lane's at off in the pages (elements, -1: zeros), to the rows from dst on.
+// 32 tokens of a unit one by one: the lane's at off in the pages (elements, -1: zeros), to the rows from dst on. E4M3: as they
+// are, row behind row.
+template <int CHANNELS>
+static __device__ __noinline__ void load_raw_tokens(const uint8_t* src, int dim, int ch0, int64_t off, uint32_t dst) {
+  constexpr int kPer = CHANNELS / 16;
+  const int lane = threadIdx.x & 31, ch = ch0 + lane % kPer * 16;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t o = __shfl_sync(0xffffffffu, off, k * (32 / kPer) + lane / kPer);
+    const bool have = o >= 0 && ch < dim;
+    cp_async16(dst + k * 512 + lane * 16, src + (have ? o + ch : 0), have ? 16 : 0);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
+}
 template <int CHANNELS>
 static __device__ __noinline__ void load_tokens(const uint8_t* src, int dim, int ch0, int64_t off, uint32_t dst) {
   const int lane = threadIdx.x & 31;
@@ -616,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(bar(kBarPieceFree + i), C::kWide ? kUsers - 5 : kUsers);
     }
     mbar_init(bar(kBarBases), 8);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(kBarRaw + i), 1);
     misc.abort_flag = 0;
     fence_mbar_init();
   }
@@ -937,30 +955,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // ---- E4M3: a unit comes to a buffer of the warp's own, kLag units ahead, and is converted on its way to the ring
     constexpr int kRawPer = C::kUnitCh / 16, kRawRows = 32 / kRawPer;        // lanes of a row, rows of an access
     const uint32_t raw = base + C::kRawOff + w * C::kStages * C::kStageBytes + lane * 16;
+    auto raw_bar = [&](uint32_t u) { return kBarRaw + 2 * w + static_cast<int>(u % C::kStages); };
     auto convert = [&](uint32_t u) {
-      if (!(ok = slot_free(u))) return;
+      if (!(ok = wait(raw_bar(u), (u / C::kStages) & 1u)) || !(ok = slot_free(u))) return;
       const uint32_t from = raw + u % C::kStages * C::kStageBytes, dst = ring + u % C::kSlots * C::kUnitBytes + w * 32 * 128;
       const int c = lane % kRawPer;                                          // 16 channels: half a 64-byte part of a chunk
       const bool swap = c >> 2 & 1;                                          // (the two stores on different banks)
+      constexpr int kBatch = 4;                                              // reads in flight together
+#pragma unroll 1
+      for (int k0 = 0; k0 < 32 / kRawRows; k0 += kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-      for (int k = 0; k < 32 / kRawRows; ++k) {
-        const int r = k * kRawRows + lane / kRawPer;
-        const uint4 v = lds128(from + k * 512);
-        uint32_t h[8];
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        for (int k = 0; k < kBatch; ++k) v[k] = lds128(from + (k0 + k) * 512);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[2 * j] = e4m3x2_to_f16x2(x[j] & 0xffffu);
-          h[2 * j + 1] = e4m3x2_to_f16x2(x[j] >> 16);
-        }
-        const uint32_t at = dst + (c >> 2) * kChunkBytes + r * 128;
-        const uint32_t a0 = at + (((2 * (c & 3)) ^ (r & 7)) << 4), a1 = at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4);
-        if (swap) {
-          sts128(a1, h[4], h[5], h[6], h[7]);
-          sts128(a0, h[0], h[1], h[2], h[3]);
-        } else {
-          sts128(a0, h[0], h[1], h[2], h[3]);
-          sts128(a1, h[4], h[5], h[6], h[7]);
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = (k0 + k) * kRawRows + lane / kRawPer;
+          uint32_t h[8];
+          const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[2 * j] = e4m3x2_to_f16x2(x[j] & 0xffffu);
+            h[2 * j + 1] = e4m3x2_to_f16x2(x[j] >> 16);
+          }
+          const uint32_t at = dst + (c >> 2) * kChunkBytes + r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
+          if (swap) {                                                        // (the pair of a chunk of 16 bytes: bit 4)
+            sts128(at ^ 16, h[4], h[5], h[6], h[7]);
+            sts128(at, h[0], h[1], h[2], h[3]);
+          } else {
+            sts128(at, h[0], h[1], h[2], h[3]);
+            sts128(at ^ 16, h[4], h[5], h[6], h[7]);
+          }
         }
       }
       fence_proxy_async_smem();
@@ -975,28 +999,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     auto load_unit = [&](const CUtensorMap* map, const void* pages, int head, int ch0, const Token& tok, bool all) {
       const uint8_t* src = static_cast<const uint8_t*>(pages);
       const int64_t off = tok.page < 0 ? -1 : int64_t(tok.page) * p.page_stride + int64_t(tok.at) * p.token_stride + int64_t(head) * p.head_stride;
+      const int boxes = maps.rows > 0 ? 32 / maps.rows : 1;                  // of maps.rows tokens (8, 16 or 32)
+      const int r = (lane & (boxes - 1)) * maps.rows;
+      const int page = __shfl_sync(0xffffffffu, tok.page, r), at = __shfl_sync(0xffffffffu, tok.at, r);
       if (E4M3) {
-        const uint32_t dst = raw + unit % C::kStages * C::kStageBytes;
-        const int ch = ch0 + lane % kRawPer * 16;
-#pragma unroll
-        for (int k = 0; k < 32 / kRawRows; ++k) {
-          const int64_t o = __shfl_sync(0xffffffffu, off, k * kRawRows + lane / kRawPer);
-          const bool have = o >= 0 && ch < p.dim;
-          cp_async16(dst + k * 512, src + (have ? o + ch : 0), have ? 16 : 0);
+        const uint32_t dst = raw - lane * 16 + unit % C::kStages * C::kStageBytes, there = bar(raw_bar(unit));
+        if (all && maps.rows > 0) {
+          if (lane == 0) mbar_arrive_expect_tx(there, C::kStageBytes);
+          __syncwarp();
+          if (lane < boxes) tma_load_4d(dst + r * C::kUnitCh, map, ch0, head, at, page, there);
+        } else {
+          load_raw_tokens<C::kUnitCh>(src, p.dim, ch0, off, dst);
+          if (lane == 0) mbar_arrive(there);
         }
-        cp_async_commit();
-        if (unit >= C::kLag) {
-          cp_async_wait<C::kLag>();
-          convert(unit - C::kLag);
-        }
+        if (unit >= C::kLag) convert(unit - C::kLag);
       } else {
         if (!(ok = slot_free(unit))) return;
         const uint32_t full = bar(kBarFull + unit % C::kSlots), dst = ring + unit % C::kSlots * C::kUnitBytes + w * 32 * 128;
         if (all && maps.rows > 0) {
-          // boxes of maps.rows tokens (8, 16 or 32) and 64 channels, a lane a box
-          const int chunks = min(C::kUnitCh / 64, (p.dim - ch0 + 63) / 64), boxes = 32 / maps.rows;
-          const int r = (lane & (boxes - 1)) * maps.rows, c = lane / boxes;
-          const int page = __shfl_sync(0xffffffffu, tok.page, r), at = __shfl_sync(0xffffffffu, tok.at, r);
+          const int chunks = min(C::kUnitCh / 64, (p.dim - ch0 + 63) / 64), c = lane / boxes;      // a lane a box
           if (lane == 0) mbar_arrive_expect_tx(full, chunks * 32 * 128);
           __syncwarp();
           if (c < chunks) tma_load_4d(dst + c * kChunkBytes + r * 128, map, ch0 + c * 64, head, at, page, full);
@@ -1048,10 +1069,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     cp_async_wait<0>();
     if (lane == 0) misc.issued[w] = unit;
-    if (E4M3) {
-#pragma unroll
-      for (int k = C::kLag; k > 0; --k)
-        if (ok && unit >= static_cast<uint32_t>(k)) convert(unit - k);
+    if (E4M3 && unit > 0) {
+      if (ok) convert(unit - 1);
+      if (!ok)                                               // a wait gave up: what is in flight lands before the CTA ends
+        for (uint32_t u = unit > 1 ? unit - 2 : 0; u < unit; ++u) mbar_drain(bar(raw_bar(u)), (u / C::kStages) & 1u);
     }
   } else {
     // ------------------------------------------------------------- issuers
@@ -1292,7 +1313,7 @@ static EncodeTiledFn encode_tiled() {
 }
 // A tile's 32 tokens of a loader warp are boxes of tokens that lie behind each other in a page: as many as divide its size,
 // 8 at least (the swizzle's rows). Pages of other sizes, and of strides that a map cannot have, go token by token.
-static void page_maps(const ChunkParams& p, PageMaps* maps) {
+static void page_maps(const ChunkParams& p, bool e4m3, int unit_channels, PageMaps* maps) {
   maps->rows = 0;
   int rows = 32;
   while (rows >= 8 && p.t.page_size % rows != 0) rows /= 2;
@@ -1300,17 +1321,20 @@ static void page_maps(const ChunkParams& p, PageMaps* maps) {
   if (rows < 8 || enc == nullptr) return;
   const int64_t head_stride = p.kv_heads > 1 ? p.head_stride : p.dim;
   const int64_t page_stride = p.t.num_pages > 1 ? p.page_stride : p.token_stride * p.t.page_size;
-  const int64_t most = int64_t(1) << 39;                 // elements: strides of a map end at 2^40 bytes
+  const int64_t most = int64_t(1) << 39;                 // strides of a map end at 2^40 bytes
   if (page_stride < 1 || page_stride >= most || p.token_stride >= most || head_stride >= most) return;
+  const cuuint64_t size = e4m3 ? 1 : 2;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.kv_heads),
                               static_cast<cuuint64_t>(p.t.page_size), static_cast<cuuint64_t>(p.t.num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(p.token_stride) * 2,
-                                 static_cast<cuuint64_t>(page_stride) * 2};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_stride) * size, static_cast<cuuint64_t>(p.token_stride) * size,
+                                 static_cast<cuuint64_t>(page_stride) * size};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(e4m3 ? unit_channels : 64), 1, static_cast<cuuint32_t>(rows), 1},
+                   ones[4] = {1, 1, 1, 1};
   CUtensorMap* const map[2] = {&maps->k, &maps->v};
   for (int i = 0; i < 2; ++i)
-    if (enc(map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i == 0 ? p.k : p.v), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    if (enc(map[i], e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(i == 0 ? p.k : p.v), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return;
   maps->rows = rows;
@@ -1334,8 +1358,7 @@ static cudaError_t launch(const ChunkParams& p, int device, cudaStream_t stream)
   int grid = device_info(device).sm_count;
   if (grid > kMaxCtas) grid = kMaxCtas;
   PageMaps maps;
-  maps.rows = 0;
-  if (!E4M3) page_maps(p, &maps);
+  page_maps(p, E4M3, C::kUnitCh, &maps);
   chunk_kernel<DP, E4M3><<<grid, kThreads, kSmem, stream>>>(p, maps, records, parts);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
