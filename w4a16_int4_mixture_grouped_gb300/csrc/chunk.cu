@@ -451,10 +451,10 @@ __device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
-  return r;
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t word, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(word));
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -973,10 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           uint32_t h[8];
           const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[2 * j] = e4m3x2_to_f16x2(x[j] & 0xffffu);
-            h[2 * j + 1] = e4m3x2_to_f16x2(x[j] >> 16);
-          }
+          for (int j = 0; j < 4; ++j) e4m3x4_to_f16x4(x[j], h[2 * j], h[2 * j + 1]);
           const uint32_t at = dst + (c >> 2) * kChunkBytes + r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
           if (swap) {                                                        // (the pair of a chunk of 16 bytes: bit 4)
             sts128(at ^ 16, h[4], h[5], h[6], h[7]);
@@ -991,43 +988,47 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarFull + u % C::kSlots));
     };
-    // This lane's token of a tile: its page (-1: unseen) and place there.
+    // This lane's token of a tile: its page (-1: unseen) and place there; of the lane's box its first token's.
     struct Token {
-      int page, at;
+      int page, at, box_page, box_at;
+      bool all;                                                              // every lane's is seen
     };
+    // Boxes of maps.rows tokens (8, 16 or 32), a lane a box (BF16: of 64 channels).
+    const int boxes = maps.rows > 0 ? 32 / maps.rows : 1, box_row = (lane & (boxes - 1)) * maps.rows;
     // one unit: channels ch0 .. of the 32 tokens
-    auto load_unit = [&](const CUtensorMap* map, const void* pages, int head, int ch0, const Token& tok, bool all) {
-      const uint8_t* src = static_cast<const uint8_t*>(pages);
-      const int64_t off = tok.page < 0 ? -1 : int64_t(tok.page) * p.page_stride + int64_t(tok.at) * p.token_stride + int64_t(head) * p.head_stride;
-      const int boxes = maps.rows > 0 ? 32 / maps.rows : 1;                  // of maps.rows tokens (8, 16 or 32)
-      const int r = (lane & (boxes - 1)) * maps.rows;
-      const int page = __shfl_sync(0xffffffffu, tok.page, r), at = __shfl_sync(0xffffffffu, tok.at, r);
+    auto load_unit = [&](bool is_key, int head, int ch0, const Token& tok) {
+      const bool by_box = tok.all && maps.rows > 0;
+      const CUtensorMap* map = is_key ? &maps.k : &maps.v;
+      auto offset = [&]() {
+        return tok.page < 0 ? -1 : int64_t(tok.page) * p.page_stride + int64_t(tok.at) * p.token_stride + int64_t(head) * p.head_stride;
+      };
       if (E4M3) {
         const uint32_t dst = raw - lane * 16 + unit % C::kStages * C::kStageBytes, there = bar(raw_bar(unit));
-        if (all && maps.rows > 0) {
+        if (by_box) {
           if (lane == 0) mbar_arrive_expect_tx(there, C::kStageBytes);
           __syncwarp();
-          if (lane < boxes) tma_load_4d(dst + r * C::kUnitCh, map, ch0, head, at, page, there);
+          if (lane < boxes) tma_load_4d(dst + box_row * C::kUnitCh, map, ch0, head, tok.box_at, tok.box_page, there);
         } else {
-          load_raw_tokens<C::kUnitCh>(src, p.dim, ch0, off, dst);
+          load_raw_tokens<C::kUnitCh>(static_cast<const uint8_t*>(is_key ? p.k : p.v), p.dim, ch0, offset(), dst);
           if (lane == 0) mbar_arrive(there);
         }
         if (unit >= C::kLag) convert(unit - C::kLag);
       } else {
         if (!(ok = slot_free(unit))) return;
         const uint32_t full = bar(kBarFull + unit % C::kSlots), dst = ring + unit % C::kSlots * C::kUnitBytes + w * 32 * 128;
-        if (all && maps.rows > 0) {
-          const int chunks = min(C::kUnitCh / 64, (p.dim - ch0 + 63) / 64), c = lane / boxes;      // a lane a box
+        if (by_box) {
+          const int chunks = min(C::kUnitCh / 64, (p.dim - ch0 + 63) / 64), c = lane / boxes;
           if (lane == 0) mbar_arrive_expect_tx(full, chunks * 32 * 128);
           __syncwarp();
-          if (c < chunks) tma_load_4d(dst + c * kChunkBytes + r * 128, map, ch0 + c * 64, head, at, page, full);
+          if (c < chunks) tma_load_4d(dst + c * kChunkBytes + box_row * 128, map, ch0 + c * 64, head, tok.box_at, tok.box_page, full);
         } else {
-          load_tokens<C::kUnitCh>(src, p.dim, ch0, off, dst);
+          load_tokens<C::kUnitCh>(static_cast<const uint8_t*>(is_key ? p.k : p.v), p.dim, ch0, offset(), dst);
           if (lane == 0) mbar_arrive(full);
         }
       }
       ++unit;
     };
+    const int step_col = kTile / p.t.page_size, step_at = kTile % p.t.page_size;
     for (uint32_t piece_no = 0; ok; ++piece_no) {
       if (!(ok = piece_there(piece_no))) break;
       const Piece pc = piece(piece_no);
@@ -1035,34 +1036,39 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       if (n == 0) break;
       const int32_t* table = p.t.tables + int64_t(pc.row) * p.t.table_stride;
       const int head = pc.r / blocks.count;
-      const int tok0 = pc.j0 + 32 * w + lane;
+      // the lane's token, its column of the table and place in the page, a tile further with every step
       // (tokens behind the block's last are read with the others, its rows' masks hide them)
-      auto entry_of = [&](int i) -> int {
-        const int tok = tok0 + i * kTile;
-        return i < n && tok < pc.len ? table[tok / p.t.page_size] : -1;
-      };
-      int entry = entry_of(0);
-      Token old{-1, 0};                                                      // wide: of the tile before
-      bool old_all = false;
+      int left = pc.len - (pc.j0 + 32 * w + lane);                           // tokens of the sequence from it on
+      int col = (pc.j0 + 32 * w + lane) / p.t.page_size, at = (pc.j0 + 32 * w + lane) % p.t.page_size;
+      int entry = left > 0 ? table[col] : -1;
+      Token old{-1, 0, 0, 0, false};                                         // wide: of the tile before
       for (int i = 0; ok && i < n; ++i) {
-        Token tok{entry, (tok0 + i * kTile) % p.t.page_size};
+        Token tok;
+        tok.page = entry;
+        tok.at = at;
         if (entry >= p.t.num_pages) {
           set_error(p.err, MOE_W4A16_ERR_BAD_INDEX);
           tok.page = -1;
         }
-        entry = entry_of(i + 1);
+        left -= kTile;
+        col += step_col;
+        at += step_at;
+        if (at >= p.t.page_size) {
+          at -= p.t.page_size;
+          ++col;
+        }
+        entry = i + 1 < n && left > 0 ? table[col] : -1;
         const uint32_t seen = __ballot_sync(0xffffffffu, tok.page >= 0);
-        const bool all = seen == 0xffffffffu;
+        tok.all = seen == 0xffffffffu;
+        tok.box_page = __shfl_sync(0xffffffffu, tok.page, box_row);
+        tok.box_at = __shfl_sync(0xffffffffu, tok.at, box_row);
         if (lane == 0) misc.masks[(n_tile + i) % kMaskBufs][w] = seen;
         // in the order in which the products take them (wide: the next tile's keys before this one's values)
         const int values = C::kWide ? (i > 0) + (i == n - 1) : 1, units = C::kHalves * (1 + values);
 #pragma unroll 1
-        for (int k = 0; ok && k < units; ++k) {
-          const bool is_key = k < C::kHalves, before = C::kWide && !is_key && i > 0 && k < 2 * C::kHalves;
-          load_unit(is_key ? &maps.k : &maps.v, is_key ? p.k : p.v, head, k % C::kHalves * 128, before ? old : tok, before ? old_all : all);
-        }
-        old = tok;
-        old_all = all;
+        for (int k = 0; ok && k < units; ++k)
+          load_unit(k < C::kHalves, head, k % C::kHalves * 128, C::kWide && i > 0 && k >= C::kHalves && k < 2 * C::kHalves ? old : tok);
+        if (C::kWide) old = tok;
       }
       n_tile += n;
       piece_done(piece_no);
