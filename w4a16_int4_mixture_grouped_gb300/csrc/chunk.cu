@@ -441,6 +441,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two FP32 numbers an instruction: the same pipe time, half the issue slots, for which the CTA's warps compete.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {           // (a NaN is passed over)
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -784,15 +806,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
             }
             const float off = kLift - (m == -INFINITY ? 0.f : m);
-            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t sums[2] = {0, 0};
+            const uint64_t factor2 = pack2(__float_as_uint(factor), __float_as_uint(factor)),
+                           off2 = pack2(__float_as_uint(off), __float_as_uint(off));
             auto exponentials = [&](const uint32_t (&r)[32], int q) {
               uint32_t packed[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float e0 = exp2_fast(fmaf(__uint_as_float(r[2 * j]), factor, off));
-                const float e1 = exp2_fast(fmaf(__uint_as_float(r[2 * j + 1]), factor, off));
-                sum4[j & 1] += e0;
-                sum4[2 + (j & 1)] += e1;
+                float e0, e1;
+                unpack2(fma2(pack2(r[2 * j], r[2 * j + 1]), factor2, off2), e0, e1);
+                e0 = exp2_fast(e0);
+                e1 = exp2_fast(e1);
+                sums[j & 1] = add2(sums[j & 1], pack2(__float_as_uint(e0), __float_as_uint(e1)));
                 packed[j] = E4M3 ? pack_f16x2_rn(e0, e1) : pack_bf16x2_rn(e0, e1);
               }
               tmem_st16(score + 16 * q, packed);                             // (over scores that have been read)
@@ -808,7 +833,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarProb + buf));
-            l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+            float sum_lo, sum_hi;
+            unpack2(add2(sums[0], sums[1]), sum_lo, sum_hi);
+            l += sum_lo + sum_hi;
           } else {
             tc_fence_before();
             __syncwarp();
