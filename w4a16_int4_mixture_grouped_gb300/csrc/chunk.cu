@@ -742,13 +742,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           tc_fence_after();
           if (i + stride >= n && have_next) load(piece(k + 1));      // the last product with these is done
           if (active) {
+            uint32_t x[32], y[32];
+            // the second half for its maximum, then the first, which stays in registers for the exponentials
+            tmem_ld32(score + 64, x);
+            tmem_ld32(score + 96, y);
             const uint4 seen4 = lds128(smem_u32(misc.masks[(n_tile + i) % kMaskBufs]));
             const int j0 = j_first + i * kTile;
             const int above = pos - j0 + 1;                                  // tokens of the tile up to the row's own
             const int below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
             const bool part = __any_sync(0xffffffffu, above < kTile || below > 0 ||
                                                           (seen4.x & seen4.y & seen4.z & seen4.w) != 0xffffffffu);
-            uint32_t x[32], y[32];
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             auto maxima = [&](const uint32_t (&r)[32]) {
 #pragma unroll
@@ -757,11 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int j = 0; j < 4; ++j)
                   top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
             };
-            // the second half for its maximum, then the first, which stays in registers for the exponentials
 #pragma unroll 1
             for (int half = 1; half >= 0; --half) {
-              tmem_ld32(score + 64 * half, x);
-              tmem_ld32(score + 64 * half + 32, y);
               tmem_wait_ld(x, y);
               if (part) {                                                    // tokens that the row does not see at -infinity
                 const uint32_t w0 = (half ? seen4.z : seen4.x) & bits_below(above - 64 * half) & ~bits_below(below - 64 * half);
@@ -779,6 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               maxima(x);
               maxima(y);
+              if (half) {
+                tmem_ld32(score, x);
+                tmem_ld32(score + 32, y);
+              }
             }
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
             const bool over = top > m + kSlack;                              // (m of -infinity: any seen score)
@@ -1170,8 +1174,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const uint32_t v = keys_of(i) + 1, q = keys_of(i + stride);
             if (values && !(acc_free() && (ok = full(v)))) break;
             if (!split && scores && !(ok = full(q))) break;
-            if (values && !(ok = wait(kBarProb + s, n_prob++ & 1u))) break;
             if (!split && !(ok = my_turn())) break;
+            if (values && !(ok = wait(kBarProb + s, n_prob++ & 1u))) break;
             tc_fence_after();
             if (values && elect_one()) value(v, 0, score_col, i != first);
             if (split) {
