@@ -77,8 +77,9 @@ enum {
   kBarBases = 34,                // bases and sums of a piece's two accumulators written, then read
   kBarTurn = 35,                 // [2] a stream's products issued: the other's turn
   kBarDrain = 37,                // [2]
+  kBarHalf = 47,                 // [2] P of a tile's first 64 tokens
   kBarRaw = 39,                  // [4][2] E4M3: a loader warp's raw unit has come
-  kNumBars = 47
+  kNumBars = 49
 };
 constexpr int kPieces = 4;       // pieces listed ahead
 constexpr int kUsers = 14;       // warps that read them
@@ -645,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(bar(kBarQ + i), 4);
       mbar_init(bar(kBarScore + i), 1);
       mbar_init(bar(kBarProb + i), 4);
+      mbar_init(bar(kBarHalf + i), 4);
       mbar_init(bar(kBarOut + i), 1);
       mbar_init(bar(kBarOutFree + i), 4 * C::kStreams);
       mbar_init(bar(kBarDrain + i), 1);
@@ -830,6 +832,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             tmem_ld32(score + 64, x);
             exponentials(y, 1);
             tmem_ld32(score + 96, y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarHalf + buf));
             tmem_wait_ld(x, y);
             exponentials(x, 2);
             exponentials(y, 3);
@@ -843,7 +849,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarProb + buf));
+            if (lane == 0) {
+              mbar_arrive(bar(kBarHalf + buf));
+              mbar_arrive(bar(kBarProb + buf));
+            }
           }
         }
         if (!ok) break;
@@ -1128,12 +1137,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         score_steps<C::kUnitCh / 16>(min(C::kUnitCh / 16, steps - h * 8), d, a, b, score_desc, h > 0);
       };
       // the products of O (+)= P V with the unit u (half h of a tile's values)
-      auto value = [&](uint32_t u, int h, uint32_t prob, bool accumulate) {
+      auto value = [&](uint32_t u, int h, uint32_t prob, bool accumulate, int half) {
         const uint32_t desc = instr_desc(E4M3, min(p.dim - 128 * h, 128), true);
-        const uint32_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes);
+        const uint32_t b = smem_desc(ring + u % C::kSlots * C::kUnitBytes) + half * 512;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)                                 // 16 tokens = two 1024-byte groups a step
-          tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
+        for (int k = 0; k < kTile / 32; ++k)                                 // 16 tokens = two 1024-byte groups a step
+          tc_mma_ts(tmem + kAcc + s * 128 + h * 128, prob + 32 * half + 8 * k, b + k * 128, desc, accumulate || k > 0 ? 1u : 0u);
       };
       while (ok) {
         if (!(ok = piece_there(n_piece))) break;
@@ -1175,9 +1184,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (values && !(acc_free() && (ok = full(v)))) break;
             if (!split && scores && !(ok = full(q))) break;
             if (!split && !(ok = my_turn())) break;
-            if (values && !(ok = wait(kBarProb + s, n_prob++ & 1u))) break;
+            if (values) {
+              if (!(ok = wait(kBarHalf + s, n_prob & 1u))) break;
+              tc_fence_after();
+              if (elect_one()) value(v, 0, score_col, i != first, 0);
+              if (!(ok = wait(kBarProb + s, n_prob++ & 1u))) break;
+              tc_fence_after();
+              if (elect_one()) value(v, 0, score_col, true, 1);
+            }
             tc_fence_after();
-            if (values && elect_one()) value(v, 0, score_col, i != first);
             if (split) {
               if (values && elect_one()) free_unit(v);
               if (values && !scores && elect_one()) tc_commit(bar(kBarOut + s));
@@ -1218,13 +1233,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
             }
             if (!ok || i == 0) continue;
-            if (!acc_free() || !(ok = wait(kBarProb + (n_prob & 1), (n_prob >> 1) & 1u))) break;
+            if (!acc_free() || !(ok = wait(kBarHalf + (n_prob & 1), (n_prob >> 1) & 1u)) || !(ok = wait(kBarProb + (n_prob & 1), (n_prob >> 1) & 1u))) break;
 #pragma unroll 1
             for (int h = 0; ok && h < C::kHalves; ++h, ++unit) {
               if (!(ok = full(unit))) break;
               tc_fence_after();
               if (elect_one()) {
-                value(unit, h, tmem + (n_prob & 1) * 128, i > 1);
+                value(unit, h, tmem + (n_prob & 1) * 128, i > 1, 0);
+                value(unit, h, tmem + (n_prob & 1) * 128, true, 1);
                 if (h == C::kHalves - 1) tc_commit(bar(kBarOut + (n_prob & 1)));
                 free_unit(unit);
               }
