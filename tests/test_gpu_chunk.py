@@ -333,7 +333,7 @@ def test_a_length_at_the_end_of_32_bits(dim, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("what", ["query", "key", "value", "later key"])
+@pytest.mark.parametrize("what", ["query", "key", "value", "later key", "later value"])
 def test_a_number_that_is_none_stays_where_it_is_seen(what, e4m3):
     """A NaN query channel reaches its own row, a NaN key the rows of its cache head and sequence that see it, a NaN value
     their channel; what comes after a row's own token reaches it in no case."""
@@ -346,7 +346,7 @@ def test_a_number_that_is_none_stays_where_it_is_seen(what, e4m3):
     starts = starts_of([c for c, _ in chunks])
     q = queries(rng, starts[-1], hkv * group, dim)
     nan = torch.zeros(q.shape, dtype=torch.bool, device=DEV)
-    tok = 70 if what != "later key" else 165                 # of sequence 1, whose chunk stands at 140 .. 199
+    tok = 165 if what.startswith("later") else 70            # of sequence 1, whose chunk stands at 140 .. 199
     first = 20 + max(0, tok - 140)
     at = (int(tables[1, tok // page]), tok % page, 1)
     if what == "query":
@@ -354,16 +354,48 @@ def test_a_number_that_is_none_stays_where_it_is_seen(what, e4m3):
         ref = C.attention(q, starts, k, v, tables, lens, dim ** -0.5)
         q[25, 3, 20] = math.nan
     else:
-        pages = v if what == "value" else k
-        nan[first:80, group:2 * group, 33 if what == "value" else slice(None)] = True
+        pages = v if what.endswith("value") else k
+        nan[first:80, group:2 * group, 33 if what.endswith("value") else slice(None)] = True
         ref = C.attention(q, starts, k, v, tables, lens, dim ** -0.5)
-        (pages.view(torch.uint8) if e4m3 else pages)[at + (33 if what == "value" else 9,)] = 0x7F if e4m3 else math.nan
+        (pages.view(torch.uint8) if e4m3 else pages)[at + (33 if what.endswith("value") else 9,)] = 0x7F if e4m3 else math.nan
     ws = M.paged_chunk_workspace(hkv * group, hkv, dim)
     out, lse = M.paged_chunk_attention(q, i32(starts), k, v, i32(tables), i32(lens), ws)
     assert M.get_device_error(ws) == 0
     assert torch.isnan(out[nan]).all() and ((out.double() - ref[0]).abs() <= ref[1])[~nan].all()
     rows = nan.all(2)
     assert torch.isnan(lse[rows]).all() and ((lse.double() - ref[2]).abs() <= ref[3])[~rows].all()
+
+
+@pytest.mark.parametrize("dim,e4m3", [(64, False), (128, True), (128, False), (256, False), (256, True), (96, False)])
+@pytest.mark.parametrize("length,new,group", [(200, 60, 4), (200, 200, 1), (6000, 90, 2)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_values_that_are_none_reach_the_rows_that_see_them_alone(bad, length, new, group, dim, e4m3):
+    """Values of a token within the chunk, and of one that the window has passed for some rows: in the same tiles as the
+    tokens that the other rows see, in blocks of one CTA and in blocks of several."""
+    if e4m3 and not math.isnan(bad):
+        pytest.skip("no infinities in the type")
+    rng = np.random.default_rng(dim + length)
+    page, window = 16, new // 2
+    tables, total = tables_for(rng, [length], page)
+    k, v = make_pages(rng, total, page, 1, dim, e4m3)
+    q = queries(rng, new, group, dim)
+    ws = M.paged_chunk_workspace(group, 1, dim)
+    first = length - new
+    for tok, w in ((length - 1, 0), (length - new // 3, 0), (first + new // 4, window), (max(0, first - window + 3), window)):
+        ref = C.attention(q, [0, new], k, v, tables, [length], dim ** -0.5, w)
+        keep = v.clone()
+        at = (int(tables[0, tok // page]), tok % page, 0, 3)
+        (v.view(torch.uint8) if e4m3 else v)[at] = 0x7F if e4m3 else bad
+        out, lse = M.paged_chunk_attention(q, i32([0, new]), k, v, i32(tables), i32([length]), ws, window=w)
+        assert M.get_device_error(ws) == 0
+        pos = torch.arange(first, length, device=DEV)
+        sees = (pos >= tok) & ((pos < tok + w) if w else True)
+        hit = torch.zeros(q.shape, dtype=torch.bool, device=DEV)
+        hit[sees, :, 3] = True
+        got = out.double()
+        assert (torch.isnan(got[hit]) if math.isnan(bad) else got[hit] == bad).all()
+        assert ((got - ref[0]).abs() <= ref[1])[~hit].all() and ((lse.double() - ref[2]).abs() <= ref[3]).all()
+        v = keep
 
 
 @pytest.mark.parametrize("sign", [1.0, -1.0])

@@ -293,6 +293,7 @@ struct PageMaps {
 // What a CTA left for the join: a block of rows that starts in it and goes on in the next np - 1.
 struct Record {
   int32_t np, token, n, r;                        // first token of q, tokens, work row
+  int32_t pos, row, len, reserved;                // as in Piece
 };
 
 // ---------------------------------------------------------------------------
@@ -365,12 +366,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
 // registers 4j + 2, 4j + 3 the same of lane t / 4 + 8.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_wait_frags(uint32_t (&r)[2][16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k >> 4][k & 15]));
 }
 // Word w[k] of lane i of four goes to word w[i] of lane k.
 __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int i) {
@@ -478,6 +483,11 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t word, uint32_t& lo, uin
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(word));
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -613,6 +623,118 @@ static __device__ __noinline__ void zero_unseeing(const ChunkParams& p) {
     for (int64_t e = threadIdx.x; e < int64_t(n) * p.heads * p.dim / 8; e += kThreads) out[e] = make_uint4(0, 0, 0, 0);
     if (p.lse != nullptr)
       for (int64_t h = threadIdx.x; h < int64_t(n) * p.heads; h += kThreads) p.lse[int64_t(c.first) * p.heads + h] = -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// values that are no numbers
+// ---------------------------------------------------------------------------
+// A product takes every token of a tile for every row, those that a row does not see with a probability of zero; a value there
+// that is infinite or no number makes the row's sum one too. Rows that come out so are looked at once more: if a token
+// that some row of the block does not see has such a value, they are computed again, token by token.
+
+__device__ __forceinline__ float bf16_or_e4m3(const void* pages, bool e4m3, int64_t at) {
+  if (!e4m3) return bf16_to_f32(static_cast<const uint16_t*>(pages)[at]);
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(static_cast<const uint8_t*>(pages)[at], lo, hi);
+  float r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(r) : "r"(lo));
+  return r;
+}
+// Place of token j of a sequence in the pages (elements, its head's first channel), -1: not there.
+__device__ __forceinline__ int64_t token_at(const ChunkParams& p, int row, int kvh, int j) {
+  const int page = p.t.tables[row * p.t.table_stride + j / p.t.page_size];
+  if (page < 0 || page >= p.t.num_pages) return -1;
+  return int64_t(page) * p.page_stride + int64_t(j % p.t.page_size) * p.token_stride + int64_t(kvh) * p.head_stride;
+}
+// The tokens that the tiles of a block hold and not all its rows see: behind its first row's, and before its last row's window.
+struct Hidden {
+  int low, low_end, high, high_end;
+};
+__device__ __forceinline__ Hidden hidden_of(const ChunkParams& p, int pos, int n, int len) {
+  Hidden h{0, 0, max(pos + 1, 0), 0};
+  const int hi = pos + n;                                // the block's tokens
+  h.high_end = static_cast<int>(min(int64_t(len), (int64_t(hi - 1) / kTile + 1) * kTile));
+  if (p.window > 0 && hi - 1 >= p.window) {
+    h.low_end = hi - p.window;
+    h.low = (pos >= p.window ? pos - p.window + 1 : 0) / kTile * kTile;
+  }
+  return h;
+}
+// Whether one of them has such a value among the channels [c0, c1) (a warp).
+static __device__ __noinline__ bool hidden_values(const ChunkParams& p, bool e4m3, int row, int kvh, int pos, int n, int len, int c0,
+                                                  int c1) {
+  const int lane = threadIdx.x & 31;
+  const Hidden h = hidden_of(p, pos, n, len);
+  bool found = false;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int from = part == 0 ? h.low : h.high, to = part == 0 ? h.low_end : h.high_end;
+#pragma unroll 1
+    for (int j = from + lane; j < to; j += 32) {
+      const int64_t at = token_at(p, row, kvh, j);
+#pragma unroll 1
+      for (int c = c0; at >= 0 && c < c1; ++c) found |= !isfinite(bf16_or_e4m3(p.v, e4m3, at + c));
+    }
+  }
+  return __any_sync(0xffffffffu, found);
+}
+// One row's channels [c0, c1) again (a warp): the query at q, position pos, to out.
+static __device__ __noinline__ void repair_row(const ChunkParams& p, bool e4m3, const uint16_t* q, int row, int kvh, int pos, int c0,
+                                               int c1, uint16_t* out) {
+  constexpr int kEach = MOE_W4A16_MAX_HEAD_DIM / 32;     // channels of a lane
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, o[kEach];
+#pragma unroll 1
+  for (int k = 0; k < kEach; ++k) o[k] = 0.f;
+#pragma unroll 1
+  for (int j0 = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0; j0 <= pos; j0 += 32) {
+    const int64_t at = j0 + lane <= pos ? token_at(p, row, kvh, j0 + lane) : -1;
+    float s = -INFINITY;
+    if (at >= 0) {
+      s = 0.f;
+#pragma unroll 1
+      for (int d = 0; d < p.dim; ++d) s = fmaf(bf16_to_f32(q[d]), bf16_or_e4m3(p.k, e4m3, at + d), s);
+      s *= p.score_scale;
+    }
+    float top = s;
+#pragma unroll 1
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    top = fmaxf(top, m);
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2_fast(m - base), e = at >= 0 ? exp2_fast(s - base) : 0.f;
+    float sum = e;
+#pragma unroll 1
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = l * keep + sum;
+    m = top;
+#pragma unroll 1
+    for (int k = 0; k < kEach; ++k) o[k] *= keep;
+#pragma unroll 1
+    for (int t = 0; t < 32; ++t) {
+      const int64_t v = __shfl_sync(0xffffffffu, at, t);
+      const float w = __shfl_sync(0xffffffffu, e, t);
+#pragma unroll 1
+      for (int k = 0; v >= 0 && k < kEach; ++k)
+        if (c0 + 32 * k + lane < c1) o[k] = fmaf(w, bf16_or_e4m3(p.v, e4m3, v + c0 + 32 * k + lane), o[k]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : p.v_scale / l;
+#pragma unroll 1
+  for (int k = 0; k < kEach; ++k)
+    if (c0 + 32 * k + lane < c1) out[c0 + 32 * k + lane] = f32_to_bf16_rn(o[k] * inv);
+}
+
+// Rows `none` of a warp's, if need be: each lane's token of q, position and head; table row, first position, tokens of the block
+// and of its sequence.
+static __device__ __noinline__ void repair_rows(const ChunkParams& p, bool e4m3, uint32_t none, int token, int pos, int head, int row,
+                                                int pos0, int n, int len, int c0, int c1) {
+  __syncwarp();
+  const int kvh = __shfl_sync(0xffffffffu, head, __ffs(none) - 1) / p.group;
+  if (!hidden_values(p, e4m3, row, kvh, pos0, n, len, c0, c1)) return;
+  for (; none != 0; none &= none - 1) {
+    const int r = __ffs(none) - 1, t = __shfl_sync(0xffffffffu, token, r), h = __shfl_sync(0xffffffffu, head, r);
+    repair_row(p, e4m3, p.q + t * p.q_stride + int64_t(h) * p.dim, row, kvh, __shfl_sync(0xffffffffu, pos, r), c0, c1,
+               p.out + (int64_t(t) * p.heads + h) * p.dim);
   }
 }
 
@@ -913,36 +1035,64 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const bool second = two && n > 1;
           if (whole) {
             // Fragments of 16 rows x 32 columns; the four lanes of a row trade words, so that each stores 16 bytes of the
-            // 64 that are theirs (a thread a row stores to 32 lines at once, four times as long).
+            // 64 that are theirs (a thread a row stores to 32 lines at once, four times as long). A lane has rows lane / 4 + 8 q.
+            float g0[4], g1[4];
+            int64_t at[4];
+            uint32_t zero[4] = {0u, 0u, 0u, 0u};             // of its channels: zeros, or no numbers
             const int64_t off = valid ? out_row * p.dim : -1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int r = 8 * q + (lane >> 2);
+              g0[q] = __shfl_sync(0xffffffffu, f0, r);
+              g1[q] = __shfl_sync(0xffffffffu, f1, r);
+              at[q] = __shfl_sync(0xffffffffu, off, r);
+            }
 #pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll 1
-              for (int c = from; c < to; c += 32) {
-                uint32_t o[16];
-                tmem_ld_frag(tmem + kAcc + (two ? 0 : s * 128) + c + lanes + (hh << 20), o);
+            for (int c = from; c < to; c += 32) {
+              uint32_t o[2][16];
+              const uint32_t acc = tmem + kAcc + (two ? 0 : s * 128) + c + lanes;
+              tmem_ld_frag(acc, o[0]);
+              tmem_ld_frag(acc + (16u << 16), o[1]);
+              tmem_wait_frags(o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * __shfl_sync(0xffffffffu, f0, 16 * hh + 8 * (j >> 1 & 1) + (lane >> 2)));
-                if (second) {
-                  uint32_t o1[16];
-                  tmem_ld_frag(tmem + kAcc + 128 + c + lanes + (hh << 20), o1);
+              for (int j = 0; j < 32; ++j)
+                o[j >> 4][j & 15] = __float_as_uint(__uint_as_float(o[j >> 4][j & 15]) * g0[2 * (j >> 4) + (j >> 1 & 1)]);
+              if (second) {
+                uint32_t o1[2][16];
+                tmem_ld_frag(acc + 128, o1[0]);
+                tmem_ld_frag(acc + 128 + (16u << 16), o1[1]);
+                tmem_wait_frags(o1);
 #pragma unroll
-                  for (int j = 0; j < 16; ++j)
-                    o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), __shfl_sync(0xffffffffu, f1, 16 * hh + 8 * (j >> 1 & 1) + (lane >> 2)),
-                                                __uint_as_float(o[j])));
-                }
+                for (int j = 0; j < 32; ++j)
+                  o[j >> 4][j & 15] = __float_as_uint(fmaf(__uint_as_float(o1[j >> 4][j & 15]), g1[2 * (j >> 4) + (j >> 1 & 1)],
+                                                           __uint_as_float(o[j >> 4][j & 15])));
+              }
+              const int ch = c + 8 * (lane & 3);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  uint32_t w[4];
+              for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2_rn(__uint_as_float(o[4 * j + 2 * k]), __uint_as_float(o[4 * j + 2 * k + 1]));
-                  transpose4(w, lane & 3);
-                  const int64_t at = __shfl_sync(0xffffffffu, off, 16 * hh + 8 * k + (lane >> 2));
-                  const int ch = c + 8 * (lane & 3);
-                  if (at >= 0 && ch < p.dim) *reinterpret_cast<uint4*>(p.out + at + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int j = 0; j < 4; ++j)
+                  w[j] = pack_bf16x2_rn(__uint_as_float(o[q >> 1][4 * j + 2 * (q & 1)]), __uint_as_float(o[q >> 1][4 * j + 2 * (q & 1) + 1]));
+                transpose4(w, lane & 3);
+                if (at[q] >= 0 && ch < p.dim) {
+                  *reinterpret_cast<uint4*>(p.out + at[q] + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) zero[q] = fma_bf16x2(w[j], 0u, zero[q]);
                 }
               }
+            }
+            // a channel that is infinite or no number, in a row whose sum is one (no number: its scores')
+            if (__any_sync(0xffffffffu, ((zero[0] | zero[1] | zero[2] | zero[3]) & 0x7fff7fffu) != 0u)) {
+              uint32_t none = 0;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q)
+                for (uint32_t b = __ballot_sync(0xffffffffu, ((q == 0 ? zero[0] : q == 1 ? zero[1] : q == 2 ? zero[2] : zero[3]) & 0x7fff7fffu) != 0u);
+                     b != 0; b &= b - 1)
+                  none |= 1u << (8 * q + (__ffs(b) - 1) / 4);
+              none &= __ballot_sync(0xffffffffu, valid && l == l);
+              if (none != 0)
+                repair_rows(p, E4M3, none, pc.token + token, pc.pos + token, head_of(pc), pc.row, pc.pos, pc.n, pc.len, from, min(to, p.dim));
             }
           } else {
 #pragma unroll 1
@@ -965,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
         }
         if (!whole && static_cast<int>(blockIdx.x) == pc.c0 && threadIdx.x == 0)
-          records[blockIdx.x] = Record{pc.c1 - pc.c0 + 1, pc.token, pc.n, pc.r};
+          records[blockIdx.x] = Record{pc.c1 - pc.c0 + 1, pc.token, pc.n, pc.r, pc.pos, pc.row, pc.len, 0};
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -1320,32 +1470,42 @@ __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, 
     if (s == 1 && rec.n <= blocks.tokens) continue;
     const int trow = threadIdx.x / blocks.heads, hrow = threadIdx.x % blocks.heads, t = trow + s * blocks.tokens;
     const int blk = rec.r % blocks.count, head = rec.r / blocks.count * p.group + blk * blocks.heads + hrow;
-    if (trow >= blocks.tokens || t >= rec.n || blk * blocks.heads + hrow >= p.group) continue;
-    const int prow = s * kRows + threadIdx.x;
-    auto part_at = [&](int i) { return parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * C::kPartFloats + prow; };
-    float m = -INFINITY;
-    for (int i = 0; i < rec.np; ++i) m = fmaxf(m, __ldcg(part_at(i)));
-    const float at = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < rec.np; ++i) {
-      const float* src = part_at(i);
-      const float f = exp2_fast(__ldcg(src) - at);
-      l = fmaf(f, __ldcg(src + C::kPartRows), l);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = fmaf(f, __ldcg(src + (2 + ch + k) * C::kPartRows), o[k]);
-    }
-    const float inv = l == 0.f ? 0.f : p.v_scale / l;
+    const bool valid = trow < blocks.tokens && t < rec.n && blk * blocks.heads + hrow < p.group;
     const int64_t row = int64_t(rec.token + t) * p.heads + head;
-    uint32_t w[8];
+    bool none = false;                                     // a channel that is infinite or no number, of a sum that is one
+    if (valid) {
+      const int prow = s * kRows + threadIdx.x;
+      auto part_at = [&](int i) { return parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * C::kPartFloats + prow; };
+      float m = -INFINITY;
+      for (int i = 0; i < rec.np; ++i) m = fmaxf(m, __ldcg(part_at(i)));
+      const float at = m == -INFINITY ? 0.f : m;
+      float l = 0.f, o[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-    uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.dim + ch);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (ch == 0 && p.lse != nullptr) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+      for (int k = 0; k < 16; ++k) o[k] = 0.f;
+#pragma unroll 2
+      for (int i = 0; i < rec.np; ++i) {
+        const float* src = part_at(i);
+        const float f = exp2_fast(__ldcg(src) - at);
+        l = fmaf(f, __ldcg(src + C::kPartRows), l);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = fmaf(f, __ldcg(src + (2 + ch + k) * C::kPartRows), o[k]);
+      }
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
+      float zero = 0.f;
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        zero = fmaf(o[2 * k] * inv, 0.f, fmaf(o[2 * k + 1] * inv, 0.f, zero));
+        w[k] = pack_bf16x2_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+      }
+      none = zero != 0.f && l == l;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.dim + ch);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      if (ch == 0 && p.lse != nullptr) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+    }
+    const uint32_t rows = __ballot_sync(0xffffffffu, none);
+    if (rows != 0) repair_rows(p, E4M3, rows, rec.token + t, rec.pos + t, head, rec.row, rec.pos, rec.n, rec.len, ch, ch + 16);
   }
 }
 
