@@ -7,9 +7,10 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import (LATENT_DIM, MoeW4A16Error, attention_workspace, cache_append, cache_compact, cache_copy, cache_extend,
-               cache_fork, cache_free, cache_workspace, clear_device_error, get_device_error, latent_attention,
-               paged_attention)
+from . import (LATENT_DIM, MoeW4A16Error, Rotary, attention_workspace, attention_workspace_size, cache_append,
+               cache_append_rotary, cache_compact, cache_copy, cache_extend, cache_fork, cache_free, cache_workspace,
+               clear_device_error, get_device_error, latent_attention, paged_attention, paged_chunk_attention,
+               paged_chunk_workspace, paged_chunk_workspace_size)
 
 
 class PagedCache:
@@ -33,7 +34,11 @@ class PagedCache:
         self.tables = torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=dev)
         self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
         self.ws = cache_workspace(num_pages, max_seqs, dev)
-        self.attn_ws = attention_workspace(max_seqs, num_q_heads, *((1, LATENT_DIM) if self.latent else row), device=dev)
+        # one for the calls on single tokens and on chunks (ordered on one stream), of the larger's size
+        if row[-1] == LATENT_DIM or attention_workspace_size(num_q_heads, *row) >= paged_chunk_workspace_size(num_q_heads, *row):
+            self.attn_ws = attention_workspace(max_seqs, num_q_heads, *((1, LATENT_DIM) if self.latent else row), device=dev)
+        else:
+            self.attn_ws = paged_chunk_workspace(num_q_heads, *row, device=dev)
 
     def pages(self, layer: int) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """(keys, values) of a layer; a latent cache's rows are both: (rows, None)."""
@@ -43,11 +48,31 @@ class PagedCache:
         """Room for counts (default one) new tokens a sequence -> their first positions, -1 where there is none."""
         return cache_extend(self.refs, self.tables, self.lens, seq_ids, self.page_size, self.ws, counts=counts)
 
+    def extend_chunk(self, seq_ids: torch.Tensor, starts: torch.Tensor,
+                     num_tokens: int) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Room for a chunk of starts[b + 1] - starts[b] new tokens of each of the sequences -> (sequence, position) of the
+        num_tokens rows: what append and DecoderLayer.forward take. Rows of no chunk, and of one that did not fit, stand at -1."""
+        if seq_ids.numel() == 0:
+            return tuple(torch.full((num_tokens,), -1, dtype=torch.int32, device=starts.device) for _ in range(2))
+        first = self.extend(seq_ids, counts=starts[1:] - starts[:-1])
+        t = torch.arange(num_tokens, dtype=torch.int32, device=starts.device)
+        b = torch.searchsorted(starts[1:], t, right=True).clamp_(max=seq_ids.numel() - 1)
+        at = t - starts[b]
+        there = (at >= 0) & (t < starts[-1]) & (first[b] >= 0)
+        return seq_ids[b], torch.where(there, first[b] + at, torch.full_like(at, -1))
+
     def append(self, layer: int, k: torch.Tensor, v: Optional[torch.Tensor], seq_ids: torch.Tensor,
                positions: torch.Tensor) -> None:
         kp, vp = self.pages(layer)
         cache_append(k, kp, self.tables, seq_ids, positions, self.ws, v=v, v_pages=vp, k_scale=self.k_scale,
                      v_scale=self.v_scale)
+
+    def append_rotary(self, layer: int, q: Optional[torch.Tensor], k: torch.Tensor, v: Optional[torch.Tensor],
+                      seq_ids: torch.Tensor, positions: torch.Tensor, rotary: Rotary) -> Optional[torch.Tensor]:
+        """append with the keys turned by their positions -> the queries turned by them."""
+        kp, vp = self.pages(layer)
+        return cache_append_rotary(q, k, kp, self.tables, seq_ids, positions, rotary, self.ws, v=v, v_pages=vp,
+                                   k_scale=self.k_scale, v_scale=self.v_scale)
 
     def attend(self, layer: int, q: torch.Tensor, seq_ids: torch.Tensor, scale: float, window: int = 0) -> torch.Tensor:
         """Attention of one new token (already appended) of each of the sequences."""
@@ -56,6 +81,17 @@ class PagedCache:
             return latent_attention(q, kp, self.tables, self.lens, self.attn_ws, scale, window=window, seq_ids=seq_ids)[0]
         return paged_attention(q, kp, vp, self.tables, self.lens, self.attn_ws, scale=scale, window=window,
                                k_scale=self.k_scale, v_scale=self.v_scale, seq_ids=seq_ids)[0]
+
+    def attend_chunk(self, layer: int, q: torch.Tensor, starts: torch.Tensor, seq_ids: torch.Tensor, scale: float,
+                     window: int = 0) -> torch.Tensor:
+        """Causal attention of a chunk of new tokens (already appended) of each of the sequences, grouped heads: rows
+        starts[b] .. starts[b + 1] - 1 are sequence seq_ids[b]'s last tokens. Rows of no chunk give zeros."""
+        if self.latent:
+            raise ValueError("a latent cache is attended one token at a time")
+        kp, vp = self.pages(layer)
+        return paged_chunk_attention(q, starts, kp, vp, self.tables, self.lens, self.attn_ws, scale=scale, window=window,
+                                     k_scale=self.k_scale, v_scale=self.v_scale, seq_ids=seq_ids,
+                                     out=torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device))[0]
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor) -> None:
         cache_fork(self.pool, self.refs, self.tables, self.lens, parents, children, self.page_size, self.ws)

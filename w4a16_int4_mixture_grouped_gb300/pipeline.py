@@ -10,20 +10,21 @@ Indexed layout: the gate_up GEMM writes SwiGLU(h) in sorted_ids slot order
 (FLAG_OUT_SORTED), so the down GEMM reads its rows consecutively
 (FLAG_A_SORTED) and combines them back per token.
 
-DecoderLayer is the decode step of one layer: attention over a PagedCache, the
-MoE FFN, and the norms between them and the residual stream. Its dense
+DecoderLayer is the step of one layer, for single new tokens (decode) or chunks
+of them (prompts, drafts to verify): attention over a PagedCache, the MoE FFN,
+and the norms between them and the residual stream. Its dense
 projections (queries, keys and values, output, router) are plain library
 products, the router's softmax and top-k torch operators.
 """
 
 from __future__ import annotations
 
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
 from . import (FLAG_A_SORTED, FLAG_COMBINE, FLAG_OUT_SORTED, FLAG_SPLIT, FLAG_SWIGLU, KERNEL_SPLIT, LAYOUT_CONTIGUOUS,
-               LAYOUT_INDEXED, LATENT_DIM, MODE_GATE_UP, MODE_PLAIN, PreparedWeight, align, align_size,
+               LAYOUT_INDEXED, LATENT_DIM, MODE_GATE_UP, MODE_PLAIN, PreparedWeight, Rotary, align, align_size,
                block_norm, contiguous, contiguous_layout, gather_rows, gather_sorted, indexed, plan, workspace)
 from .cache import PagedCache
 
@@ -123,19 +124,21 @@ class MoEFFN:
 
 
 class DecoderLayer:
-    """One layer's decode step over a PagedCache: attention, MoE FFN, and the norms before and after both.
+    """One layer's step over a PagedCache: attention, MoE FFN, and the norms before and after both.
 
     w_qkv bf16 [hidden, (Hq + 2 Hkv) * D] (latent: [hidden, Hq * 576 + 576], queries in the latent space, then the
     row to cache), w_o bf16 [Hq * D, hidden] (latent: [Hq * 512, hidden]), w_router bf16 [hidden, E]; norms bf16
     [hidden]: after attention, before the FFN, after the FFN (each None: that norm is left out; the one before the FFN is
     needed). scale multiplies the scores: default D ** -0.5; a latent cache's rows do not say how wide the heads were
-    before they were taken into the latent space, so give that width ** -0.5 unless it is LATENT_HEAD_DIM. A position
-    encoding is the caller's: rotate inside `project`."""
+    before they were taken into the latent space, so give that width ** -0.5 unless it is LATENT_HEAD_DIM. rotary turns
+    queries and keys by their positions on the way into the cache (a latent row and its queries: the channels that the
+    Rotary's offset names); without it a position encoding is the caller's, inside `project`."""
 
     def __init__(self, cache: PagedCache, layer: int, ffn: MoEFFN, num_heads: int, w_qkv: torch.Tensor, w_o: torch.Tensor,
                  w_router: torch.Tensor, norm_ffn: torch.Tensor, norm_post_attn: Optional[torch.Tensor] = None,
                  norm_post_ffn: Optional[torch.Tensor] = None, eps: float = 1e-6, window: int = 0,
-                 scale: Optional[float] = None):
+                 scale: Optional[float] = None, rotary: Optional[Rotary] = None):
+        self.rotary = rotary
         self.cache, self.layer, self.ffn, self.heads = cache, layer, ffn, num_heads
         self.w_qkv, self.w_o, self.w_router = w_qkv, w_o, w_router
         self.norm_ffn, self.norm_post_attn, self.norm_post_ffn = norm_ffn, norm_post_attn, norm_post_ffn
@@ -157,11 +160,20 @@ class DecoderLayer:
         return q, x[:, self.heads:self.heads + self.kv_heads], x[:, self.heads + self.kv_heads:]
 
     def forward(self, residual: torch.Tensor, y: torch.Tensor, seq_ids: torch.Tensor, positions: torch.Tensor,
-                next_norm: Optional[torch.Tensor] = None):
-        """residual [B, hidden] and its norm y for this layer -> (residual, y normed by next_norm, or None)."""
+                next_norm: Optional[torch.Tensor] = None, chunk: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+        """residual [B, hidden] and its norm y for this layer -> (residual, y normed by next_norm, or None).
+
+        Rows are new tokens, seq_ids and positions [B] theirs: one a sequence, or with chunk = (starts, sequences) rows
+        starts[i] .. starts[i + 1] - 1 of sequence sequences[i] (see PagedCache.extend_chunk). The FFN is for B tokens."""
         q, k, v = self.project(y, positions)
-        self.cache.append(self.layer, k, v, seq_ids, positions)
-        o = self.cache.attend(self.layer, q, seq_ids, self.scale, self.window)
+        if self.rotary is not None:
+            q = self.cache.append_rotary(self.layer, q, k, v, seq_ids, positions, self.rotary)
+        else:
+            self.cache.append(self.layer, k, v, seq_ids, positions)
+        if chunk is not None:
+            o = self.cache.attend_chunk(self.layer, q, *chunk, self.scale, self.window)
+        else:
+            o = self.cache.attend(self.layer, q, seq_ids, self.scale, self.window)
         residual, y = block_norm(o.view(y.shape[0], -1) @ self.w_o, residual, w_post=self.norm_post_attn,
                                  w_pre=self.norm_ffn, eps=self.eps)
         top = torch.topk(torch.softmax((y @ self.w_router).float(), -1), self.ffn.top_k)
