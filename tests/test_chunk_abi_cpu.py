@@ -87,7 +87,7 @@ def append(c=None, q=FAKE, qs=8 * 64, qh=8, qo=FAKE, qos=8 * 64, k=FAKE, ks=128,
     (dict(n=-1), ARG), (dict(heads=0), ARG), (dict(dim=60), UNSUPPORTED), (dict(ks=64), ARG), (dict(vs=132), ARG),
     (dict(k=None), ARG), (dict(k=FAKE + 8), ARG), (dict(v=None), ARG), (dict(seq=None), ARG), (dict(pos=None), ARG),
     (dict(ws=None), WORKSPACE), (dict(c=pages(v=None)), ARG), (dict(q=None), ARG), (dict(qo=None), ARG), (dict(qh=0), ARG),
-    (dict(qs=64), ARG), (dict(qos=8 * 64 + 2), ARG), (dict(q=FAKE + 2), ARG), (dict(qo=FAKE + 8), ARG),
+    (dict(qs=64), ARG), (dict(qos=8 * 64 + 2), ARG), (dict(qos=9 * 64), ARG), (dict(qs=9 * 64), ARG), (dict(q=FAKE + 2), ARG), (dict(qo=FAKE + 8), ARG),
     (dict(r=desc(dim=8)), UNSUPPORTED), (dict(r=desc(dim=32, offset=4)), UNSUPPORTED), (dict(r=desc(dim=128)), ARG),
     (dict(r=desc(dim=4, interleaved=1)), UNSUPPORTED), (dict(n=0), OK), (dict(n=0, q=None, qo=None, k=None, v=None), OK),
 ])

@@ -343,8 +343,8 @@ def cache_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, k_pages: tor
                         v: Optional[torch.Tensor] = None, v_pages: Optional[torch.Tensor] = None, k_scale: float = 1.0,
                         v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """cache_append of keys turned by their positions (a Rotary's) on the way, and the same rotation of the queries
-    q [T, Hq, dim] (or None) -> q_out, a new dense tensor unless given (it may be q). Every query row is turned, whatever
-    becomes of its key."""
+    q [T, Hq, dim] (or None) -> q_out, a new dense tensor unless given (q itself: in place; else it overlaps neither q nor k
+    and v). Every query row is turned, whatever becomes of its key."""
     latent = v_pages is None
     if (v is None) != latent:
         raise ValueError("v and v_pages go together")

@@ -269,6 +269,7 @@ moe_w4a16_status moe_w4a16_cache_append_rotary(
     if (num_q_heads < 1 || num_q_heads > (1 << 16) || q_stride < width || q_out_stride < width || q_stride % 8 != 0 ||
         q_out_stride % 8 != 0 || (num_tokens > 0 && (q == nullptr || q_out == nullptr)) || !aligned16(q) || !aligned16(q_out))
       return MOE_W4A16_ERR_INVALID_ARG;
+    if (q == q_out && num_tokens > 1 && q_stride != q_out_stride) return MOE_W4A16_ERR_INVALID_ARG;   // rows over other rows
     p.q = q;
     p.q_stride = q_stride;
     p.q_out = q_out;
