@@ -483,6 +483,30 @@ def test_another_stream_and_a_graph(dim, e4m3):
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("dim,e4m3", [(128, False), (64, True), (128, True), (256, False), (256, True)])
+def test_a_wait_that_runs_out_is_recorded_and_the_next_call_is_right(dim, e4m3):
+    """The limit lowered to zero: the first wait for a tile that is still on its way gives up (every copy and product does
+    arrive, and is waited for before the kernel ends). Restored, the same workspace serves the next calls."""
+    rng = np.random.default_rng(15)
+    page, lens, starts = 32, [9000, 700], [0, 200, 700]
+    tables, total = tables_for(rng, lens, page)
+    k, v = make_pages(rng, total, page, 2, dim, e4m3)
+    q = queries(rng, 700, 8, dim)
+    ws = M.paged_chunk_workspace(8, 2, dim)
+    td, ld, sd = i32(tables), i32(lens), i32(starts)
+    torch.cuda.synchronize()
+    try:
+        M.set_wait_limit_ns(0)
+        M.paged_chunk_attention(q, sd, k, v, td, ld, ws)
+        code = M.get_device_error(ws)
+    finally:
+        M.set_wait_limit_ns(M.WAIT_LIMIT_NS)
+    assert code == 6, f"expected the timed-out wait to be recorded, got error word {code}"
+    M.workspace_init(ws)
+    for _ in range(2):
+        check(q, starts, k, v, tables, lens, ws=ws)
+
+
 def test_one_workspace_for_the_calls_on_cache_and_attention():
     """Calls of different shapes, and the decode and append calls, on the largest of their workspaces in turn."""
     rng = np.random.default_rng(13)

@@ -231,6 +231,24 @@ def test_append_latent(interleaved):
     check_append(rng, 700, 2, 1, 576, 64, 512, interleaved, 16, latent=True)
 
 
+@pytest.mark.parametrize("t", [2431, 2437, 4864, 5003])
+@pytest.mark.parametrize("e4m3,interleaved,in_place", [(False, False, False), (True, True, True), (True, False, False)])
+def test_append_of_many_tokens(t, e4m3, interleaved, in_place):
+    """Groups of tokens, the last one not full, rows without a place between them."""
+    rng = np.random.default_rng(t)
+    check_append(rng, t, 2, 1, 64, 32, 16, interleaved, 16, e4m3, in_place=in_place, skip=(0, 1, 2, 3, 6, 2000, t - 1))
+
+
+@pytest.mark.parametrize("t", [2437, 4865])
+def test_many_tokens(t):
+    rng = np.random.default_rng(t)
+    x, pos = rows(rng, t, 3, 96), i32(rng.integers(-5, 10 ** 6, t))
+    rotation = M.Rotary(64, offset=16)
+    want = M.rotary(x, pos, rotation)
+    inside(want, *C.rotate(f64(x), pos.tolist(), plain(64), 16, False, 1.0))
+    assert torch.equal(M.rotary(x, pos, rotation, out=x), want)
+
+
 def test_append_is_rotary_then_append():
     """Bit for bit over BF16 pages, and the plain append's elements for the values."""
     rng = np.random.default_rng(9)
