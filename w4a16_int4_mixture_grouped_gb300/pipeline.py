@@ -165,6 +165,8 @@ class DecoderLayer:
 
         Rows are new tokens, seq_ids and positions [B] theirs: one a sequence, or with chunk = (starts, sequences) rows
         starts[i] .. starts[i + 1] - 1 of sequence sequences[i] (see PagedCache.extend_chunk). The FFN is for B tokens."""
+        if chunk is not None and self.cache.latent:
+            raise ValueError("a latent cache is attended one token at a time")
         q, k, v = self.project(y, positions)
         if self.rotary is not None:
             q = self.cache.append_rotary(self.layer, q, k, v, seq_ids, positions, self.rotary)
