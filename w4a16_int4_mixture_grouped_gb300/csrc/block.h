@@ -124,20 +124,21 @@ __device__ __forceinline__ ChunkRange chunk_range(const ChunkParams& p, int b) {
   ChunkRange c{-1, 0, 0, 0};
   const int from = p.starts[b], to = p.starts[b + 1];
   const int row = p.seq_ids != nullptr ? p.seq_ids[b] : b;
+  const bool there = row >= 0 && row < p.t.num_seqs;
+  int len = there ? p.lens[row] : 0;     // (asked for before the first answers are looked at)
   if (from < 0 || to > p.tokens || from > to) {
     atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
     return c;
   }
   c.first = from;
   c.n = to - from;
-  if (row < 0 || row >= p.t.num_seqs) {
+  if (!there) {
     if (c.n > 0) atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
     c.base = -c.n;                     // its rows see nothing
     return c;
   }
   c.row = row;
   const int cap = p.t.max_pages * p.t.page_size;
-  int len = p.lens[row];
   if (len < 0 || len > cap) {
     atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
     len = len < 0 ? 0 : cap;

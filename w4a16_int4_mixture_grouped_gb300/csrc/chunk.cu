@@ -41,7 +41,7 @@ constexpr int kMinPlaces = 4;                 // places of the line that a CTA t
 constexpr int kMaskBufs = 8;                  // tiles whose masks of seen tokens are kept
 constexpr int kChunkBytes = 128 * 128;        // 64 channels of 128 rows, 128-byte swizzled
 
-// warps: 0-3 and 4-7 the streams' softmax, 8-11 loaders, 12 and 13 issuers
+// warps: 0-3 and 4-7 the streams' softmax, 8-11 loaders, 12 and 13 issuers, 14 the list of pieces, 15 rows that see nothing
 constexpr int kThreads = 512;
 
 template <int DP, bool E4M3>
@@ -95,7 +95,7 @@ struct Piece {
   int token, pos, n, r;          // the first token's row of q and position
   int row, len;                  // row of the tables, tokens that the sequence has
   int j0, tiles;                 // token at which the first tile begins
-  int c0, c1;                    // CTAs that the block's tiles fall to
+  int np;                        // CTAs that the block's tiles fall to, if its first one is here; else 0
 };
 struct Misc {
   unsigned long long bars[kNumBars];
@@ -140,14 +140,19 @@ __device__ __forceinline__ int64_t places_of_row(const ChunkParams& p, const Chu
   }
   return sum;
 }
-__device__ __forceinline__ int64_t cta_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+// (A division of 64 bits takes some hundred cycles, and a CTA does nothing else meanwhile: 32 bits where they do.)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (a >> 32 == 0 && b >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+__device__ __forceinline__ int64_t cta_begin(int64_t total, int ctas, int c) { return divide(total * c, ctas); }
 __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
-  return static_cast<int>(((x + 1) * ctas - 1) / total);
+  return static_cast<int>(divide((x + 1) * ctas - 1, total));
 }
 
 // Fills *sh for CTA `cta` of `grid` (every thread calls it): sequence after sequence, their `rows` work rows (cache heads x
 // head blocks) one after the other, each the places of its blocks of `step` tokens. False: no work.
-static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
+static __device__ __forceinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int pass = 0; pass < 2; ++pass) {
     int64_t line = 0;                                   // places of the sequences before these
@@ -172,14 +177,18 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
       const int64_t at = line + (before + pre - n) * rows;
       line += all * rows;
       if (pass == 0 && b0 + kThreads >= p.batch) {
-        if (threadIdx.x == 0) {
+        if (threadIdx.x < 2) {                          // begin and end
           int64_t ctas = line / kMinPlaces;
           ctas = ctas < 1 ? 1 : ctas > grid ? grid : ctas;
           const bool work = line > 0 && cta < ctas;
-          sh->total = line;
-          sh->ctas = static_cast<int>(ctas);
-          sh->x = work ? cta_begin(line, static_cast<int>(ctas), cta) : 0;
-          sh->x_end = work ? cta_begin(line, static_cast<int>(ctas), cta + 1) : 0;
+          const int64_t x = work ? cta_begin(line, static_cast<int>(ctas), cta + threadIdx.x) : 0;
+          if (threadIdx.x == 0) {
+            sh->total = line;
+            sh->ctas = static_cast<int>(ctas);
+            sh->x = x;
+          } else {
+            sh->x_end = x;
+          }
         }
         __syncthreads();
         if (sh->x >= sh->x_end) return false;
@@ -199,8 +208,11 @@ static __device__ __noinline__ bool find_share(const ChunkParams& p, int cta, in
     // the work row, the block of tokens and the place in it
     const ChunkRange c = chunk_range(p, sh->b);
     int64_t y = sh->x - sh->first;
-    const int r = static_cast<int>(y / sh->seq);
-    y -= r * sh->seq;
+    const int64_t seq = sh->seq;
+    int r = 0;                                          // work rows before it
+    for (int more = 32; more == 32; r += more)
+      more = __popc(__ballot_sync(0xffffffffu, r + lane + 1 < rows && (r + lane + 1) * seq <= y));
+    y -= r * seq;
     for (int q0 = 0; q0 * int64_t(step) < c.n; q0 += 32) {
       const int64_t i = (q0 + lane) * int64_t(step);
       int lo, hi, n = 0;
@@ -275,8 +287,7 @@ struct Walk {
       o.len = c.base + c.n;
       o.j0 = (lo / kTile + from) * kTile;
       o.tiles = to - from;
-      o.c0 = cta_of(total, ctas, tile0);
-      o.c1 = cta_of(total, ctas, tile0 + ntiles - 1);
+      o.np = from > 0 ? 0 : tile0 + ntiles <= x_end ? 1 : cta_of(total, ctas, tile0 + ntiles - 1) - static_cast<int>(blockIdx.x) + 1;
       return true;
     }
     return false;
@@ -613,16 +624,26 @@ static __device__ __noinline__ void load_tokens(const uint8_t* src, int dim, int
   __syncwarp();
 }
 
-// Rows that stand before their sequence's first token, or have none: zeros and -infinity, spread over the CTAs.
+// Rows that stand before their sequence's first token, or have none: zeros and -infinity, spread over the CTAs (a warp of each).
 static __device__ __noinline__ void zero_unseeing(const ChunkParams& p) {
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    const ChunkRange c = chunk_range(p, b);
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const ChunkRange c = b0 + lane < p.batch ? chunk_range(p, b0 + lane) : ChunkRange{-1, 0, 0, 0};
     const int n = c.row < 0 ? c.n : c.base < 0 ? min(c.n, -c.base) : 0;
-    if (n == 0) continue;
-    uint4* out = reinterpret_cast<uint4*>(p.out + int64_t(c.first) * p.heads * p.dim);
-    for (int64_t e = threadIdx.x; e < int64_t(n) * p.heads * p.dim / 8; e += kThreads) out[e] = make_uint4(0, 0, 0, 0);
-    if (p.lse != nullptr)
-      for (int64_t h = threadIdx.x; h < int64_t(n) * p.heads; h += kThreads) p.lse[int64_t(c.first) * p.heads + h] = -INFINITY;
+#pragma unroll 1
+    for (uint32_t m = __ballot_sync(0xffffffffu, n > 0); m != 0; m &= m - 1) {
+      const int first = __shfl_sync(0xffffffffu, c.first, __ffs(m) - 1), count = __shfl_sync(0xffffffffu, n, __ffs(m) - 1);
+#pragma unroll 1
+      for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        const int64_t row = int64_t(first + i) * p.heads;
+        uint4* out = reinterpret_cast<uint4*>(p.out + row * p.dim);
+#pragma unroll 1
+        for (int e = lane; e < p.heads * (p.dim / 8); e += 32) out[e] = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr)
+          for (int h = lane; h < p.heads; h += 32) p.lse[row + h] = -INFINITY;
+      }
+    }
   }
 }
 
@@ -752,14 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const int rows = p.kv_heads * blocks.count, step = C::kStreams * blocks.tokens;
 
   asm volatile("griddepcontrol.launch_dependents;");
-  zero_unseeing(p);
   if (threadIdx.x == 0) records[blockIdx.x].np = 0;
-  if (!find_share(p, blockIdx.x, gridDim.x, rows, step, &misc.share)) return;
-  if ((base & 1023u) != 0) {                 // the swizzle is a function of address bits
-    if (threadIdx.x == 0) set_error(p.err, MOE_W4A16_ERR_CUDA);
-    return;
-  }
-  if (threadIdx.x == 0) {
+  // (set up while the others look for the share)
+  if (warp == 12 && lane == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(bar(kBarFull + i), 4);
       mbar_init(bar(kBarFree + i), C::kStreams);
@@ -783,15 +799,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     misc.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&misc.tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  __syncwarp();
+  const bool aligned = (base & 1023u) == 0;  // the swizzle is a function of address bits
+  if (!aligned && threadIdx.x == 0) set_error(p.err, MOE_W4A16_ERR_CUDA);
+  const bool work = find_share(p, blockIdx.x, gridDim.x, rows, step, &misc.share) && aligned;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&misc.tmem);
+  if (!work) {
+    if (warp == 15) zero_unseeing(p);
+    if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    return;
+  }
   const uint32_t ring = base + C::kRingOff;
   auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.err, p.wait_ns); };
   // scores enter the exponentials as |scale| s, the queries negated where the scale is negative (zeroed where it is zero,
@@ -982,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
         // ---- epilogue: O / l, or a part of it
         const Piece& pc = piece(k);
-        const bool whole = pc.c0 == pc.c1;
+        const bool whole = pc.np == 1;
         const bool two = !C::kWide && split;             // both streams hold accumulators of the same rows
         float f0 = 1.f, f1 = 0.f;
         m -= kLift;
@@ -1017,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (active) {
           const bool valid = token >= 0;
           const int64_t out_row = int64_t(pc.token + token) * p.heads + head_of(pc);
-          float* part = parts + (int64_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == pc.c0 ? 1 : 0)) * C::kPartFloats +
+          float* part = parts + (int64_t(blockIdx.x) * 2 + (pc.np > 0 ? 1 : 0)) * C::kPartFloats +
                         (two || C::kWide ? rr : s * kRows + rr);
           if (valid && (!two || s == 0)) {
             if (!whole) {
@@ -1114,8 +1139,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
           }
         }
-        if (!whole && static_cast<int>(blockIdx.x) == pc.c0 && threadIdx.x == 0)
-          records[blockIdx.x] = Record{pc.c1 - pc.c0 + 1, pc.token, pc.n, pc.r, pc.pos, pc.row, pc.len, 0};
+        if (pc.np > 1 && threadIdx.x == 0)
+          records[blockIdx.x] = Record{pc.np, pc.token, pc.n, pc.r, pc.pos, pc.row, pc.len, 0};
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -1423,6 +1448,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         __syncwarp();
         if (!more) break;
       }
+    } else if (warp == 15) {
+      zero_unseeing(p);
     }
   }
 
@@ -1448,23 +1475,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 template <int DP, bool E4M3>
 __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, const Record* records, const float* parts, int ctas) {
   using C = Cfg<DP, E4M3>;
-  __shared__ int list[kMaxCtas], count_s;
+  static_assert(kMaxCtas <= 2 * kRows, "a thread looks at two records");
+  __shared__ int list[kMaxCtas], counts[2 * kRows / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x < 32) {
-    int count = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const int c = c0 + threadIdx.x;
-      const bool is = c < ctas && __ldcg(&records[c].np) > 1;
-      const uint32_t m = __ballot_sync(0xffffffffu, is);
-      if (is) list[count + __popc(m & ((1u << threadIdx.x) - 1u))] = c;
-      count += __popc(m);
-    }
-    if (threadIdx.x == 0) count_s = count;
+  bool is[2];
+  uint32_t found[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = i * kRows + threadIdx.x;
+    is[i] = c < ctas && __ldcg(&records[c].np) > 1;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    found[i] = __ballot_sync(0xffffffffu, is[i]);
+    if ((threadIdx.x & 31) == 0) counts[i * (kRows / 32) + threadIdx.x / 32] = __popc(found[i]);
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int g = 0; g < 2 * kRows / 32; ++g) {
+    const int i = g / (kRows / 32);
+    if (g % (kRows / 32) == threadIdx.x / 32 && is[i])
+      list[count + __popc(found[i] & ((1u << (threadIdx.x & 31)) - 1u))] = i * kRows + threadIdx.x;
+    count += counts[g];
   }
   __syncthreads();
   const Blocks blocks = blocks_of(p.group);
   const int cols = p.dim / 16;
-  for (int item = blockIdx.x; item < count_s * C::kStreams * cols; item += gridDim.x) {
+  for (int item = blockIdx.x; item < count * C::kStreams * cols; item += gridDim.x) {
     const int c = list[item / (C::kStreams * cols)], rest = item % (C::kStreams * cols), s = rest / cols, ch = rest % cols * 16;
     const Record rec = records[c];
     if (s == 1 && rec.n <= blocks.tokens) continue;
@@ -1477,6 +1515,7 @@ __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, 
       const int prow = s * kRows + threadIdx.x;
       auto part_at = [&](int i) { return parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * C::kPartFloats + prow; };
       float m = -INFINITY;
+#pragma unroll 4
       for (int i = 0; i < rec.np; ++i) m = fmaxf(m, __ldcg(part_at(i)));
       const float at = m == -INFINITY ? 0.f : m;
       float l = 0.f, o[16];
