@@ -79,7 +79,8 @@ enum {
   kBarDrain = 37,                // [2]
   kBarHalf = 47,                 // [2] P of a tile's first 64 tokens
   kBarRaw = 39,                  // [4][2] E4M3: a loader warp's raw unit has come
-  kNumBars = 49
+  kBarPair = 49,                 // [4] wide: two softmax warps of the same rows have exchanged numbers
+  kNumBars = 53
 };
 constexpr int kPieces = 4;       // pieces listed ahead
 constexpr int kUsers = 14;       // warps that read them
@@ -106,6 +107,7 @@ struct Misc {
   Piece pieces[kPieces];
   union {
     float2 ml[2][kRows];                     // [stream] bases and sums of a piece's rows
+    float pair[2][2][kRows];                 // wide: what the two threads of a row exchange
     Share share;                             // (before the roles part)
   };
 };
@@ -786,15 +788,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(bar(kBarProb + i), 4);
       mbar_init(bar(kBarHalf + i), 4);
       mbar_init(bar(kBarOut + i), 1);
-      mbar_init(bar(kBarOutFree + i), 4 * C::kStreams);
+      mbar_init(bar(kBarOutFree + i), 8);
       mbar_init(bar(kBarDrain + i), 1);
       mbar_init(bar(kBarTurn + i), 1);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(kBarPiece + i), 1);
-      mbar_init(bar(kBarPieceFree + i), C::kWide ? kUsers - 5 : kUsers);
+      mbar_init(bar(kBarPieceFree + i), C::kWide ? kUsers - 1 : kUsers);
     }
     mbar_init(bar(kBarBases), 8);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(kBarPair + i), 2);
     for (int i = 0; i < 8; ++i) mbar_init(bar(kBarRaw + i), 1);
     misc.abort_flag = 0;
     fence_mbar_init();
@@ -840,17 +843,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // ------------------------------------------------------------- softmax, a thread a row
     const int s = warp >> 2, rr = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    if (!C::kWide || s == 0) {
+    {
       const int trow = rr / blocks.heads, hrow = rr - trow * blocks.heads;   // token and head of the row
       const uint32_t qs = base + s * C::kQBytes + (warp & 3) * 32 * 128;     // this warp's 32 rows
-      uint32_t n_score = 0, n_out[2] = {0, 0}, n_tile = 0, n_bases = 0, k = 0;
+      uint32_t n_score = 0, n_out[2] = {0, 0}, n_tile = 0, n_bases = 0, n_pair = 0, k = 0;
       auto split_of = [&](const Piece& x) { return C::kWide || x.n <= blocks.tokens; };
       // Whether this stream has tiles of a piece: queries and accumulators change hands for those alone (a phase that passes
       // without its issuer would be taken for the one before).
       auto has = [&](const Piece& x) { return x.tiles > (split_of(x) && !C::kWide ? s : 0); };
+      // Wide: the two threads of a row trade x; false: a wait gave up.
+      auto trade = [&](float& x) {
+        misc.pair[n_pair & 1][s][rr] = x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPair + (warp & 3)));
+        if (!wait(kBarPair + (warp & 3), n_pair & 1u)) return false;
+        x = misc.pair[n_pair++ & 1][s ^ 1][rr];
+        return true;
+      };
       // This thread's row of a block: token relative to the block's first (-1: none), query head.
       auto token_of = [&](const Piece& x) {
-        const int t = trow + (s == 1 && !split_of(x) ? blocks.tokens : 0);
+        const int t = trow + (s == 1 && !split_of(x) ? blocks.tokens : 0);   // (wide: both groups of warps have the same rows)
         return trow < blocks.tokens && t < x.n && x.r % blocks.count * blocks.heads + hrow < p.group ? t : -1;
       };
       auto head_of = [&](const Piece& x) { return x.r / blocks.count * p.group + x.r % blocks.count * blocks.heads + hrow; };
@@ -868,18 +880,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
       bool ok = piece_there(0);
       float factor = 0.f;
-      if (ok && has(piece(0))) {
+      const bool loads = !C::kWide || s == 0;            // wide: the first group's warps bring the queries
+      if (ok && has(piece(0)) && loads) {
         load(piece(0));
         factor = finish();
       }
       while (ok) {
         const int n = piece(k).tiles;
         if (n == 0 || !(ok = piece_there(k + 1))) break;
-        const bool split = split_of(piece(k)), have_next = has(piece(k + 1));
+        const bool split = split_of(piece(k)), have_next = has(piece(k + 1)) && loads;
         const int token = token_of(piece(k)), pos = piece(k).pos + token, j_first = piece(k).j0;
         const bool active = __any_sync(0xffffffffu, token >= 0);
         const int stride = !C::kWide && split ? 2 : 1, first = stride == 2 ? s : 0;
         float m = -INFINITY, l = 0.f, next_factor = 0.f;
+        if (C::kWide) {
+          float x = factor;
+          if (!(ok = trade(x))) break;
+          if (s == 1) factor = x;
+        }
         // what the exponents are taken against: a maximum that is taken when a score passes it by 2^kSlack. E4M3: FP16
         // probabilities of 2^kLift to 2^15, which keep their bits down to 2^-22 of the largest, and end at 2^-32 of it
         constexpr float kLift = E4M3 ? 8.f : 0.f, kSlack = E4M3 ? 7.f : 8.f;
@@ -890,7 +908,86 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (!(ok = wait(kBarScore + buf, par))) break;
           tc_fence_after();
           if (i + stride >= n && have_next) load(piece(k + 1));      // the last product with these is done
-          if (active) {
+          if (C::kWide) {
+            // a thread has half of a row's tokens, in registers from the scores to the probabilities
+            if (active) {
+              uint32_t x[32], y[32];
+              tmem_ld32(score + 64 * s, x);
+              tmem_ld32(score + 64 * s + 32, y);
+              const uint32_t* seen = misc.masks[(n_tile + i) % kMaskBufs] + 2 * s;
+              const uint32_t seen0 = seen[0], seen1 = seen[1];
+              const int j0 = j_first + i * kTile + 64 * s;
+              const int above = pos - j0 + 1, below = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;
+              const bool part = __any_sync(0xffffffffu, above < 64 || below > 0 || (seen0 & seen1) != 0xffffffffu);
+              tmem_wait_ld(x, y);
+              if (part) {
+                const uint32_t w0 = seen0 & bits_below(above) & ~bits_below(below);
+                const uint32_t w1 = seen1 & bits_below(above - 32) & ~bits_below(below - 32);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  if (!(w0 >> j & 1u)) x[j] = 0xff800000u;
+                  if (!(w1 >> j & 1u)) y[j] = 0xff800000u;
+                }
+              }
+              float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  top4[j] = max3(top4[j], __uint_as_float(x[e + 2 * j]), __uint_as_float(x[e + 2 * j + 1]));
+                  top4[2 + j] = max3(top4[2 + j], __uint_as_float(y[e + 2 * j]), __uint_as_float(y[e + 2 * j + 1]));
+                }
+              const float mine = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+              float top = mine;
+              // (from here on the other's scores have been read too: its probabilities may lie over them)
+              if (!(ok = trade(top))) break;
+              top = fmaxf(top, mine) * factor;
+              const bool over = top > m + kSlack;
+              if (__any_sync(0xffffffffu, over)) {
+                float keep = 1.f;
+                if (over) {
+                  keep = exp2_fast(m - top);
+                  m = top;
+                }
+                l *= keep;
+                if (i != first) {
+                  if (!(ok = wait(kBarOut + ((n_score - 1) & 1), ((n_score - 1) >> 1) & 1u))) break;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int c = 16 * s; c < p.dim; c += 32) {                 // each thread half of the channels
+                    uint32_t o[16];
+                    tmem_ld16(tmem + kAcc + lanes + c, o);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                    tmem_st16(tmem + kAcc + lanes + c, o);
+                  }
+                }
+              }
+              const float off = kLift - (m == -INFINITY ? 0.f : m);
+              uint64_t sums[2] = {0, 0};
+              const uint64_t factor2 = pack2(__float_as_uint(factor), __float_as_uint(factor)),
+                             off2 = pack2(__float_as_uint(off), __float_as_uint(off));
+              uint32_t packed[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const uint32_t a = j < 16 ? x[2 * j & 31] : y[2 * j & 31], b = j < 16 ? x[(2 * j + 1) & 31] : y[(2 * j + 1) & 31];
+                float e0, e1;
+                unpack2(fma2(pack2(a, b), factor2, off2), e0, e1);
+                e0 = exp2_fast(e0);
+                e1 = exp2_fast(e1);
+                sums[j & 1] = add2(sums[j & 1], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+                packed[j] = E4M3 ? pack_f16x2_rn(e0, e1) : pack_bf16x2_rn(e0, e1);
+              }
+              tmem_st32(score + 32 * s, packed);
+              tmem_wait_st();
+              float sum_lo, sum_hi;
+              unpack2(add2(sums[0], sums[1]), sum_lo, sum_hi);
+              l += sum_lo + sum_hi;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar((s == 0 ? kBarHalf : kBarProb) + buf));
+          } else if (active) {
             uint32_t x[32], y[32];
             // the second half for its maximum, then the first, which stays in registers for the exponentials
             tmem_ld32(score + 64, x);
@@ -943,10 +1040,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               l *= keep;
               if (i != first) {
-                if (C::kWide) {                                              // the previous tile's product is done
-                  if (!(ok = wait(kBarOut + ((n_score - 1) & 1), ((n_score - 1) >> 1) & 1u))) break;
-                  tc_fence_after();
-                }
                 const uint32_t acc = tmem + kAcc + s * 128 + lanes;
 #pragma unroll 1
                 for (int c = 0; c < p.dim; c += 16) {
@@ -1011,6 +1104,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const bool two = !C::kWide && split;             // both streams hold accumulators of the same rows
         float f0 = 1.f, f1 = 0.f;
         m -= kLift;
+        if (C::kWide) {
+          float other = l;
+          if (!(ok = trade(other))) break;
+          l += other;
+        }
         if (two) {
           misc.ml[s][rr] = make_float2(m, l);
           __syncwarp();
@@ -1027,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           f1 = exp2_fast(b.x - at);
           l = a.y * f0 + b.y * f1;
         }
-        if (C::kWide) {
+        if (C::kWide) {                                  // (the last tile's product)
           ok = wait(kBarOut + ((n_score - 1) & 1), ((n_score - 1) >> 1) & 1u);
         } else {
 #pragma unroll
@@ -1044,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const int64_t out_row = int64_t(pc.token + token) * p.heads + head_of(pc);
           float* part = parts + (int64_t(blockIdx.x) * 2 + (pc.np > 0 ? 1 : 0)) * C::kPartFloats +
                         (two || C::kWide ? rr : s * kRows + rr);
-          if (valid && (!two || s == 0)) {
+          if (valid && ((!two && !C::kWide) || s == 0)) {
             if (!whole) {
               __stcg(part, m);
               __stcg(part + C::kPartRows, l);
@@ -1055,8 +1153,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const float inv = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
           f0 *= inv;
           f1 *= inv;
-          const int half = (p.dim + 63) / 64 * 32;       // two: a stream's warps take half of the channels each
-          const int from = two && s == 1 ? half : 0, to = two && s == 0 ? half : p.dim;
+          const int half = (p.dim + 63) / 64 * 32;       // shared rows: half of the channels each
+          const bool shared = two || C::kWide;
+          const int from = shared && s == 1 ? half : 0, to = shared && s == 0 ? half : p.dim;
           const bool second = two && n > 1;
           if (whole) {
             // Fragments of 16 rows x 32 columns; the four lanes of a row trade words, so that each stores 16 bytes of the
@@ -1075,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll 1
             for (int c = from; c < to; c += 32) {
               uint32_t o[2][16];
-              const uint32_t acc = tmem + kAcc + (two ? 0 : s * 128) + c + lanes;
+              const uint32_t acc = tmem + kAcc + (shared ? 0 : s * 128) + c + lanes;
               tmem_ld_frag(acc, o[0]);
               tmem_ld_frag(acc + (16u << 16), o[1]);
               tmem_wait_frags(o);
@@ -1123,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll 1
             for (int c = from; c < min(to, p.dim); c += 16) {
               uint32_t o[16];
-              tmem_ld16(tmem + kAcc + (two ? 0 : s * 128) + c + lanes, o);
+              tmem_ld16(tmem + kAcc + (shared ? 0 : s * 128) + c + lanes, o);
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
               if (second) {
