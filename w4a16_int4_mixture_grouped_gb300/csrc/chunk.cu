@@ -37,7 +37,7 @@ constexpr int kMaxCtas = 152;
 // A block of rows costs about as much as kBlockTiles tiles on top of its own (queries, first scores, epilogue): the line that
 // the CTAs share has as many places before its tiles.
 constexpr int kBlockTiles = 2;
-constexpr int kMinPlaces = 4;                 // places of the line that a CTA takes at least
+constexpr int kMinPlaces = 2;                 // places of the line that a CTA takes at least
 constexpr int kMaskBufs = 8;                  // tiles whose masks of seen tokens are kept
 constexpr int kChunkBytes = 128 * 128;        // 64 channels of 128 rows, 128-byte swizzled
 
@@ -1715,7 +1715,10 @@ static cudaError_t launch(const ChunkParams& p, int device, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   // the join may be set up while the first kernel runs; it waits for that kernel's end before it reads
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid * 8));
+  // at most one block of rows of each CTA to join, and no more than there are
+  const Blocks blocks = blocks_of(p.group);
+  const int64_t most = (p.tokens / (C::kStreams * blocks.tokens) + int64_t(p.batch)) * p.kv_heads * blocks.count;
+  cfg.gridDim = dim3(static_cast<unsigned>((most < grid ? most : grid) * (C::kStreams * (p.dim / 16))));
   cfg.blockDim = dim3(kRows);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
