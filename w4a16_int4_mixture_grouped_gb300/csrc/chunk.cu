@@ -7,21 +7,32 @@
 //   O [rows x D]     += P [rows x tokens] . V       P = exp2(S - base) in tensor memory, over its own S
 //
 // so keys and values are read once for up to 256 rows (two streams of 128; 129 to 256 channels: 128 rows), and a prompt is
-// bound by the tensor pipe, drafts by HBM. Both products run on tcgen05 with FP32 accumulators in TMEM.
+// bound by its products, drafts by HBM. Both products run on tcgen05 with FP32 accumulators in TMEM.
 //
 //   * A CTA has two streams, each with its rows' queries, scores and accumulator, an issuing warp and four softmax
 //     warps, a thread a row. While one stream's softmax runs, the tensor pipe works for the other: O += P V of its last
-//     tile and S of its next. Rows of a chunk that fit one stream: both streams take the same rows and every other tile,
-//     and their accumulators are joined at the end.
+//     tile and S of its next, the two streams in turns (in no order prompts take 1.12 times as long). Rows of a chunk that
+//     fit one stream: both streams take the same rows and every other tile, and their accumulators are joined at the end.
+//   * P is handed over in halves, so that the first half's products run while the second's exponentials are taken.
 //   * 129 to 256 channels: one stream, as its accumulator takes half of TMEM; its scores have two buffers, and the next
-//     tile's are computed during a tile's softmax.
+//     tile's are computed during a tile's softmax, which has two threads a row.
 //   * The base of a row's exponents moves when a score passes it by 2^8, not with every new maximum (BF16 probabilities keep
 //     their relative precision, FP32 sums their range), so the accumulator is seldom rescaled.
-//   * Four warps gather the tiles, token by token through the page table, with cp.async into a ring of 128-byte swizzled
-//     tiles (E4M3: into a buffer of their own, converted to FP16 on the way to the ring, exactly).
+//   * Four warps bring the tiles into a ring of 128-byte swizzled ones, each 32 tokens: boxes of 8 to 32 tokens by TMA where
+//     they lie behind each other in a page and all are seen, else token by token with cp.async. E4M3 comes to a buffer of
+//     its own and is converted to FP16 on the way to the ring, exactly.
 //   * Every CTA takes an equal share of one line of tiles over all sequences, heads and row blocks, whatever the lengths;
 //     rows that cross CTAs are written as FP32 parts, which a second kernel joins in order.
 //   * Unseen slots (past the end, freed pages) are not read: their rows are zero-filled and their scores -infinity.
+//
+// Measured (GB300; 64 query and 8 cache heads of 128 channels where not said otherwise; floors: HBM at 6.78 TB/s, products at
+// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 566 us (338), a chunk of 1024 tokens over 32768 in E4M3 776 us (563), four
+// drafts of each of 64 sequences of up to 8191 tokens 223 us (196), a window of 1024 over 256 channels 62 us (16).
+// What bounds a prompt is the way of one stream's tile, about 3300 cycles for both streams' 2048 of products: scores,
+// their maximum, the exponentials (512 of a softmax's 1900 cycles on the special-function pipe), the products' second half.
+// Of registers there are 128 a thread, as 512 threads take all; a split by roles would free some, but functions that stay
+// out of line cannot be called in a kernel that changes its registers, and inlined they are more code than the instruction
+// cache keeps up with (163 KB took 1.14 to 1.17 times as long as 96).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -35,9 +46,12 @@ constexpr int kTile = 128;                    // tokens of a tile
 constexpr int kRows = 128;                    // query rows of a stream (MMA M)
 constexpr int kMaxCtas = 152;
 // A block of rows costs about as much as kBlockTiles tiles on top of its own (queries, first scores, epilogue): the line that
-// the CTAs share has as many places before its tiles.
+// the CTAs share has as many places before its tiles. (A prompt's chunk among single tokens: 1 70.5 us, 2 63.7; prompts: 1 626,
+// 2 590, 3 591 then.)
 constexpr int kBlockTiles = 2;
-constexpr int kMinPlaces = 2;                 // places of the line that a CTA takes at least
+// Places of the line that a CTA takes at least: a block of one tile has three, and is not cut. (20 tokens of 2 cache heads: 4
+// 14.4 us, both blocks on one CTA, 2 10.4; 512 of 8: 24.4 and 21.6; 1512 of 8: 19.4 and 20.2, for more parts to join.)
+constexpr int kMinPlaces = 2;
 constexpr int kMaskBufs = 8;                  // tiles whose masks of seen tokens are kept
 constexpr int kChunkBytes = 128 * 128;        // 64 channels of 128 rows, 128-byte swizzled
 
@@ -153,7 +167,8 @@ __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t x) {
 }
 
 // Fills *sh for CTA `cta` of `grid` (every thread calls it): sequence after sequence, their `rows` work rows (cache heads x
-// head blocks) one after the other, each the places of its blocks of `step` tokens. False: no work.
+// head blocks) one after the other, each the places of its blocks of `step` tokens. False: no work. (In line: arguments by
+// reference out of line are read through memory, and the first tile of a cold call comes 5000 cycles later.)
 static __device__ __forceinline__ bool find_share(const ChunkParams& p, int cta, int grid, int rows, int step, Share* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int pass = 0; pass < 2; ++pass) {
