@@ -483,6 +483,74 @@ def test_another_stream_and_a_graph(dim, e4m3):
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_more_sequences_than_a_cta_has_threads(e4m3):
+    rng = np.random.default_rng(17)
+    page, batch = 16, 1100
+    counts = [int(x) for x in rng.integers(0, 12, batch)]
+    lens = [c + int(x) for c, x in zip(counts, rng.integers(0, 700, batch))]
+    ids = [int(x) for x in rng.permutation(batch)]
+    tables, total = tables_for(rng, [lens[ids.index(i)] for i in range(batch)], page)
+    k, v = make_pages(rng, total, page, 2, 64, e4m3)
+    starts = starts_of(counts)
+    rows = [0] * batch
+    for b, i in enumerate(ids):
+        rows[i] = lens[b]
+    check(queries(rng, starts[-1] + 3, 6, 64), starts, k, v, tables, rows, seq_ids=ids)
+
+
+@pytest.mark.parametrize("dims", [(128, 256), (64, 64), (128, 128)])
+def test_two_calls_at_once(dims):
+    """On two streams with a workspace each, over and over: the bits of each by itself."""
+    calls, want = [], []
+    for i, dim in enumerate(dims):
+        rng = np.random.default_rng(18 + i)
+        page, lens = 32, [5000, 333, 80]
+        tables, total = tables_for(rng, lens, page)
+        k, v = make_pages(rng, total, page, 4, dim, i == 1)
+        q = queries(rng, 400, 16, dim)
+        args = (q, i32([0, 5, 320, 400]), k, v, i32(tables), i32(lens), M.paged_chunk_workspace(16, 4, dim))
+        calls.append(args)
+        want.append(M.paged_chunk_attention(*args))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(10):
+        for i, (stream, args) in enumerate(zip(streams, calls)):
+            with torch.cuda.stream(stream):
+                got[i].append(M.paged_chunk_attention(*args))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert M.get_device_error(calls[i][-1]) == 0
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_two_graphs_on_one_workspace():
+    rng = np.random.default_rng(19)
+    page, shapes = 16, [(8, 2, 64), (4, 1, 256)]
+    ws = M.paged_chunk_workspace(4, 1, 256)
+    graphs = []
+    for h, hkv, dim in shapes:
+        lens = [4000, 100]
+        tables, total = tables_for(rng, lens, page)
+        k, v = make_pages(rng, total, page, hkv, dim, False)
+        args = queries(rng, 70, h, dim), i32([0, 60, 70]), k, v, i32(tables), i32(lens)
+        want = M.paged_chunk_attention(*args, M.paged_chunk_workspace(h, hkv, dim))
+        out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            M.paged_chunk_attention(*args, ws, out=out, lse=lse)
+        graphs.append((graph, out, lse, want, args))
+    for _ in range(4):
+        for graph, *_ in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, lse, want, _ in graphs:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert M.get_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("dim,e4m3", [(128, False), (64, True), (128, True), (256, False), (256, True)])
 def test_a_wait_that_runs_out_is_recorded_and_the_next_call_is_right(dim, e4m3):
     """The limit lowered to zero: the first wait for a tile that is still on its way gives up (every copy and product does
