@@ -24,7 +24,7 @@ HEADER = open(os.path.join(ROOT, "include", "moe_w4a16.h")).read()
 
 
 def chunk(c=None, q=FAKE, stride=8 * 64, tokens=6, starts=FAKE, batch=2, heads=8, kv=2, dim=64, table=FAKE, tstride=4,
-          width=4, lens=FAKE, seqs=2, scale=0.125, window=0, out=FAKE, ws=FAKE, bytes_=BIG):
+          width=4, lens=FAKE, seqs=2, scale=0.125, window=0, out=FAKE + (1 << 20), ws=FAKE, bytes_=BIG):
     return B._FN["paged_chunk_attention"](q, stride, tokens, starts, batch, heads, kv, dim, ctypes.byref(c or pages()), table,
                                           tstride, width, lens, None, seqs, scale, window, out, None, ws, bytes_, None)
 
@@ -33,7 +33,7 @@ def chunk(c=None, q=FAKE, stride=8 * 64, tokens=6, starts=FAKE, batch=2, heads=8
     (dict(tokens=-1), ARG), (dict(batch=-1), ARG), (dict(heads=7), ARG), (dict(heads=0), ARG), (dict(kv=0), ARG),
     (dict(dim=72), UNSUPPORTED), (dict(dim=272), UNSUPPORTED), (dict(dim=0), UNSUPPORTED), (dict(window=-1), ARG),
     (dict(scale=float("nan")), ARG), (dict(q=None), ARG), (dict(q=FAKE + 2), ARG), (dict(stride=8 * 64 - 8), ARG),
-    (dict(stride=8 * 64 + 4), ARG), (dict(out=None), ARG), (dict(out=FAKE + 4), ARG), (dict(lens=None), ARG),
+    (dict(stride=8 * 64 + 4), ARG), (dict(out=None), ARG), (dict(out=FAKE + 4), ARG), (dict(out=FAKE), ARG), (dict(lens=None), ARG),
     (dict(starts=None), ARG), (dict(table=None), ARG), (dict(width=0), ARG), (dict(tstride=3), ARG), (dict(seqs=1), ARG),
     (dict(ws=None), WORKSPACE), (dict(bytes_=100), WORKSPACE), (dict(width=1 << 28, tstride=1 << 28), ARG),
     (dict(tokens=1 << 29), UNSUPPORTED), (dict(tokens=0), OK), (dict(batch=0), OK),

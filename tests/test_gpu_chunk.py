@@ -619,6 +619,9 @@ def test_refusals():
         with pytest.raises(error):
             M.paged_chunk_attention(*args, **kw)
     with pytest.raises(M.MoeW4A16Error) as e:
+        M.paged_chunk_attention(q, s, k, v, t, n, ws, out=q)
+    assert e.value.name == "ERR_INVALID_ARG"
+    with pytest.raises(M.MoeW4A16Error) as e:
         M.paged_chunk_attention(q, s, k, v, t, n, ws, window=-1)
     assert e.value.name == "ERR_INVALID_ARG"
     with pytest.raises(M.MoeW4A16Error) as e:

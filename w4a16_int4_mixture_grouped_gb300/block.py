@@ -285,7 +285,7 @@ def paged_chunk_attention(q: torch.Tensor, starts: torch.Tensor, k_pages: torch.
     Rows starts[b] .. starts[b + 1] - 1 of q (starts int32 [B + 1]) are the last tokens of the sequence that row
     seq_ids[b] (default: b) of tables and lens describes, their keys and values appended already. A row sees the tokens
     up to its own, with a window the newest `window` of them. Rows of no chunk are left as they were (as they come from
-    the allocator, where out and lse are not given)."""
+    the allocator, where out and lse are not given); out does not overlap q."""
     _rows_dense(_need(q, "q", _BF16, 3), "q")
     index = q.get_device()
     t, h, d = q.shape

@@ -399,7 +399,7 @@ moe_w4a16_status moe_w4a16_paged_chunk_attention(const uint16_t* q, int64_t q_st
   if (st != MOE_W4A16_OK) return st;
   if (!ws_fits(ws, ws_bytes, need)) return MOE_W4A16_ERR_WORKSPACE;
   if (num_tokens == 0 || batch == 0) return MOE_W4A16_OK;
-  if (q == nullptr || out == nullptr || lens == nullptr || starts == nullptr || !aligned16(q) || !aligned16(out) ||
+  if (q == nullptr || out == nullptr || out == q || lens == nullptr || starts == nullptr || !aligned16(q) || !aligned16(out) ||
       q_stride % 8 != 0 || q_stride < static_cast<int64_t>(num_heads) * head_dim)
     return MOE_W4A16_ERR_INVALID_ARG;
   if (seq_ids == nullptr && num_seqs < batch) return MOE_W4A16_ERR_INVALID_ARG;
