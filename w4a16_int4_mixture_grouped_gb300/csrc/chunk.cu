@@ -26,8 +26,8 @@
 //   * Unseen slots (past the end, freed pages) are not read: their rows are zero-filled and their scores -infinity.
 //
 // Measured (GB300; 64 query and 8 cache heads of 128 channels where not said otherwise; floors: HBM at 6.78 TB/s, products at
-// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 566 us (338), a chunk of 1024 tokens over 32768 in E4M3 776 us (563), four
-// drafts of each of 64 sequences of up to 8191 tokens 223 us (196), a window of 1024 over 256 channels 62 us (16).
+// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 553 us (338), a chunk of 1024 tokens over 32768 in E4M3 773 us (563), four
+// drafts of each of 64 sequences of up to 8191 tokens 221 us (196), a window of 1024 over 256 channels 62 us (16).
 // What bounds a prompt is the way of one stream's tile, about 3300 cycles for both streams' 2048 of products: scores,
 // their maximum, the exponentials (512 of a softmax's 1900 cycles on the special-function pipe), the products' second half.
 // Of registers there are 128 a thread, as 512 threads take all; a split by roles would free some, but functions that stay
@@ -108,6 +108,7 @@ struct Share {
 // Some tiles of one block of rows: `n` tokens of a sequence's chunk, work row r. (tiles = 0: the share is done.)
 struct Piece {
   int token, pos, n, r;          // the first token's row of q and position
+  int head, blk;                 // of the work row: cache head, block of its query heads
   int row, len;                  // row of the tables, tokens that the sequence has
   int j0, tiles;                 // token at which the first tile begins
   int np;                        // CTAs that the block's tiles fall to, if its first one is here; else 0
@@ -273,7 +274,7 @@ struct Walk {
     place = sh.place;
     c = chunk_range(p, b);
   }
-  __device__ __forceinline__ bool next(const ChunkParams& p, int rows, int step, Piece& o) {
+  __device__ __forceinline__ bool next(const ChunkParams& p, int rows, int step, int count, Piece& o) {
     while (x < x_end) {
       const int64_t i = qt * int64_t(step);
       if (i >= c.n) {                              // the next work row, or sequence
@@ -300,6 +301,8 @@ struct Walk {
       o.token = c.first + static_cast<int>(i);
       o.pos = c.base + static_cast<int>(i);
       o.r = r;
+      o.head = r / count;
+      o.blk = r - o.head * count;
       o.row = c.row;
       o.len = c.base + c.n;
       o.j0 = (lo / kTile + from) * kTile;
@@ -878,9 +881,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // This thread's row of a block: token relative to the block's first (-1: none), query head.
       auto token_of = [&](const Piece& x) {
         const int t = trow + (s == 1 && !split_of(x) ? blocks.tokens : 0);   // (wide: both groups of warps have the same rows)
-        return trow < blocks.tokens && t < x.n && x.r % blocks.count * blocks.heads + hrow < p.group ? t : -1;
+        return trow < blocks.tokens && t < x.n && x.blk * blocks.heads + hrow < p.group ? t : -1;
       };
-      auto head_of = [&](const Piece& x) { return x.r / blocks.count * p.group + x.r % blocks.count * blocks.heads + hrow; };
+      auto head_of = [&](const Piece& x) { return x.head * p.group + x.blk * blocks.heads + hrow; };
       // This thread's row as an offset in q (elements, -1: none), and its warp's rows on their way.
       auto load = [&](const Piece& x) {
         const int t = token_of(x);
@@ -1364,7 +1367,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int n = pc.tiles;
       if (n == 0) break;
       const int32_t* table = p.t.tables + int64_t(pc.row) * p.t.table_stride;
-      const int head = pc.r / blocks.count;
+      const int head = pc.head;
       // the lane's token, its column of the table and place in the page, a tile further with every step
       // (tokens behind the block's last are read with the others, its rows' masks hide them)
       int left = pc.len - (pc.j0 + 32 * w + lane);                           // tokens of the sequence from it on
@@ -1553,7 +1556,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       Piece pc;
       for (uint32_t k = 0;; ++k) {
         if (k >= kPieces && !wait(kBarPieceFree + k % kPieces, (k / kPieces - 1) & 1u)) break;
-        const bool more = walk.next(p, rows, step, pc);
+        const bool more = walk.next(p, rows, step, blocks.count, pc);
         if (!more) pc.tiles = 0;
         if (lane == 0) {
           misc.pieces[k % kPieces] = pc;
