@@ -26,8 +26,8 @@
 //   * Unseen slots (past the end, freed pages) are not read: their rows are zero-filled and their scores -infinity.
 //
 // Measured (GB300; 64 query and 8 cache heads of 128 channels where not said otherwise; floors: HBM at 6.78 TB/s, products at
-// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 553 us (338), a chunk of 1024 tokens over 32768 in E4M3 773 us (563), four
-// drafts of each of 64 sequences of up to 8191 tokens 221 us (196), a window of 1024 over 256 channels 62 us (16).
+// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 543 us (338), a chunk of 1024 tokens over 32768 in E4M3 772 us (563), four
+// drafts of each of 64 sequences of up to 8191 tokens 220 us (196), a window of 1024 over 256 channels 62 us (16).
 // What bounds a prompt is the way of one stream's tile, about 3300 cycles for both streams' 2048 of products: scores,
 // their maximum, the exponentials (512 of a softmax's 1900 cycles on the special-function pipe), the products' second half.
 // Of registers there are 128 a thread, as 512 threads take all; a split by roles would free some, but functions that stay
@@ -1024,10 +1024,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int j = 0; j < 4; ++j)
                   top4[j] = max3(top4[j], __uint_as_float(r[e + 2 * j]), __uint_as_float(r[e + 2 * j + 1]));
             };
-#pragma unroll 1
-            for (int half = 1; half >= 0; --half) {
+            if (!part) {                                                     // (a straight line: 539 us for the prompts, else 549)
               tmem_wait_ld(x, y);
-              if (part) {                                                    // tokens that the row does not see at -infinity
+              maxima(x);
+              tmem_ld32(score, x);
+              maxima(y);
+              tmem_ld32(score + 32, y);
+              tmem_wait_ld(x, y);
+              maxima(x);
+              maxima(y);
+            } else {                                                         // tokens that the row does not see at -infinity
+#pragma unroll 1
+              for (int half = 1; half >= 0; --half) {
+                tmem_wait_ld(x, y);
                 const uint32_t w0 = (half ? seen4.z : seen4.x) & bits_below(above - 64 * half) & ~bits_below(below - 64 * half);
                 const uint32_t w1 = (half ? seen4.w : seen4.y) & bits_below(above - 64 * half - 32) & ~bits_below(below - 64 * half - 32);
 #pragma unroll
@@ -1040,12 +1049,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                   tmem_st32(score + 96, y);
                   tmem_wait_st();
                 }
-              }
-              maxima(x);
-              maxima(y);
-              if (half) {
-                tmem_ld32(score, x);
-                tmem_ld32(score + 32, y);
+                maxima(x);
+                maxima(y);
+                if (half) {
+                  tmem_ld32(score, x);
+                  tmem_ld32(score + 32, y);
+                }
               }
             }
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * factor;
