@@ -627,3 +627,85 @@ def test_refusals():
     with pytest.raises(M.MoeW4A16Error) as e:
         M.paged_chunk_attention(q, s, k, v, t, n, ws[:64])
     assert e.value.name == "ERR_WORKSPACE"
+
+
+@pytest.mark.parametrize("dim,e4m3", [(64, False), (128, False), (128, True), (256, False), (256, True)])
+def test_a_value_that_is_none_at_the_end_of_a_long_row(dim, e4m3):
+    """The last of 70001 tokens has a value that is none: over a hundred tokens share its tiles and do not see it, each with
+    all those before it to go through again. That is over far below the limit of the kernels' waits, no wait runs out, and
+    the sequence beside it keeps its bits."""
+    rng = np.random.default_rng(71)
+    page, lens, starts, group = 64, [70001, 900], [0, 300, 360], 8
+    tables, total = tables_for(rng, lens, page)
+    k, v = make_pages(rng, total, page, 1, dim, e4m3)
+    q = queries(rng, 360, group, dim)
+    ws = M.paged_chunk_workspace(group, 1, dim)
+    args = (q, i32(starts), k, v, i32(tables), i32(lens), ws)
+    clean = M.paged_chunk_attention(*args)
+    ref = C.attention(q[:300], [0, 300], k, v, tables[:1], lens[:1], dim ** -0.5)
+    (v.view(torch.uint8) if e4m3 else v)[int(tables[0, 70000 // page]), 70000 % page, 0, 3] = 0x7F if e4m3 else math.inf
+    times = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    times[0].record()
+    out, lse = M.paged_chunk_attention(*args)
+    times[1].record()
+    assert M.get_device_error(ws) == 0
+    assert times[0].elapsed_time(times[1]) < 0.25e-6 * M.WAIT_LIMIT_NS           # (ms: a quarter of the limit)
+    assert torch.equal(out[300:], clean[0][300:]) and torch.equal(lse, clean[1])
+    compare(out[:299], lse[:299], *(x[:299] for x in ref))
+    last = out[299].double()
+    assert not torch.isfinite(last[:, 3]).any()
+    last[:, 3] = ref[0][299, :, 3]
+    assert ((last - ref[0][299]).abs() <= ref[1][299]).all()
+
+
+@pytest.mark.parametrize("dim,e4m3", [(64, False), (128, True), (256, False)])
+@pytest.mark.parametrize("lens", [[300, 7], [9001, 4000]])
+def test_a_value_that_is_none_and_seen_by_all(lens, dim, e4m3):
+    """No row has to be computed again: the channel is none in every row of the head, of one CTA and of several, and all else
+    keeps its bits."""
+    rng = np.random.default_rng(72)
+    page, group, hkv = 32, 3, 2
+    starts = [0, 150, 157]
+    tables, total = tables_for(rng, lens, page)
+    k, v = make_pages(rng, total, page, hkv, dim, e4m3)
+    q = queries(rng, 157, group * hkv, dim)
+    ws = M.paged_chunk_workspace(group * hkv, hkv, dim)
+    args = (q, i32(starts), k, v, i32(tables), i32(lens), ws)
+    clean = M.paged_chunk_attention(*args)
+    (v.view(torch.uint8) if e4m3 else v)[int(tables[0, 0]), 5, 1, 20] = 0x7F if e4m3 else -math.inf
+    out, lse = M.paged_chunk_attention(*args)
+    assert M.get_device_error(ws) == 0 and torch.equal(lse, clean[1])
+    hit = torch.zeros(q.shape, dtype=torch.bool, device=DEV)
+    hit[:150, group:, 20] = True
+    assert (torch.isnan(out[hit]) if e4m3 else out[hit] == -math.inf).all() and torch.equal(out[~hit], clean[0][~hit])
+
+
+def test_values_that_are_none_in_a_graph_and_the_calls_after_it():
+    """Flagged rows of one replay, none of the next: nothing is kept from call to call."""
+    rng = np.random.default_rng(73)
+    page, lens, starts, dim = 16, [5000, 400], [0, 60, 130], 128
+    tables, total = tables_for(rng, lens, page)
+    k, v = make_pages(rng, total, page, 2, dim, False)
+    q = queries(rng, 130, 8, dim)
+    ws = M.paged_chunk_workspace(8, 2, dim)
+    args = (q, i32(starts), k, v, i32(tables), i32(lens), ws)
+    clean = M.paged_chunk_attention(*args)
+    places = [(int(tables[b, (n - 1) // page]), (n - 1) % page, 1, 7) for b, n in enumerate(lens)]
+    kept = [v[at].clone() for at in places]
+    for at in places:
+        v[at] = math.nan
+    want = M.paged_chunk_attention(*args)
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.paged_chunk_attention(*args, out=out, lse=lse)
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+        for at, x in zip(places, kept):
+            v[at] = x
+        graph.replay()
+        assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+        for at in places:
+            v[at] = math.nan
+    assert M.get_device_error(ws) == 0

@@ -24,15 +24,17 @@
 //   * Every CTA takes an equal share of one line of tiles over all sequences, heads and row blocks, whatever the lengths;
 //     rows that cross CTAs are written as FP32 parts, which a second kernel joins in order.
 //   * Unseen slots (past the end, freed pages) are not read: their rows are zero-filled and their scores -infinity.
+//   * Nothing in this kernel takes longer than the tiles before it, as its waits are bounded: rows that a hidden value which is no
+//     number reaches are flagged here and computed again by the third kernel.
 //
 // Measured (GB300; 64 query and 8 cache heads of 128 channels where not said otherwise; floors: HBM at 6.78 TB/s, products at
 // 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 543 us (338), a chunk of 1024 tokens over 32768 in E4M3 772 us (563), four
 // drafts of each of 64 sequences of up to 8191 tokens 220 us (196), a window of 1024 over 256 channels 62 us (16).
 // What bounds a prompt is the way of one stream's tile, about 3300 cycles for both streams' 2048 of products: scores,
 // their maximum, the exponentials (512 of a softmax's 1900 cycles on the special-function pipe), the products' second half.
-// Of registers there are 128 a thread, as 512 threads take all; a split by roles would free some, but functions that stay
-// out of line cannot be called in a kernel that changes its registers, and inlined they are more code than the instruction
-// cache keeps up with (163 KB took 1.14 to 1.17 times as long as 96).
+// Of registers there are 128 a thread, as 512 threads take all; a split by roles would free some, but the functions that stay
+// out of line (copies of queries and of single tokens, rows that see nothing) cannot be called in a kernel that changes its
+// registers, and code in line that the instruction cache does not hold is slow (163 KB took 1.14 to 1.17 times as long as 96).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -324,7 +326,7 @@ struct PageMaps {
 // What a CTA left for the join: a block of rows that starts in it and goes on in the next np - 1.
 struct Record {
   int32_t np, token, n, r;                        // first token of q, tokens, work row
-  int32_t pos, row, len, reserved;                // as in Piece
+  int32_t none;                                   // not 0: an output of this CTA is infinite or no number
 };
 
 // ---------------------------------------------------------------------------
@@ -667,117 +669,8 @@ static __device__ __noinline__ void zero_unseeing(const ChunkParams& p) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// values that are no numbers
-// ---------------------------------------------------------------------------
-// A product takes every token of a tile for every row, those that a row does not see with a probability of zero; a value there
-// that is infinite or no number makes the row's sum one too. Rows that come out so are looked at once more: if a token
-// that some row of the block does not see has such a value, they are computed again, token by token.
-
-__device__ __forceinline__ float bf16_or_e4m3(const void* pages, bool e4m3, int64_t at) {
-  if (!e4m3) return bf16_to_f32(static_cast<const uint16_t*>(pages)[at]);
-  uint32_t lo, hi;
-  e4m3x4_to_f16x4(static_cast<const uint8_t*>(pages)[at], lo, hi);
-  float r;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(r) : "r"(lo));
-  return r;
-}
-// Place of token j of a sequence in the pages (elements, its head's first channel), -1: not there.
-__device__ __forceinline__ int64_t token_at(const ChunkParams& p, int row, int kvh, int j) {
-  const int page = p.t.tables[row * p.t.table_stride + j / p.t.page_size];
-  if (page < 0 || page >= p.t.num_pages) return -1;
-  return int64_t(page) * p.page_stride + int64_t(j % p.t.page_size) * p.token_stride + int64_t(kvh) * p.head_stride;
-}
-// The tokens that the tiles of a block hold and not all its rows see: behind its first row's, and before its last row's window.
-struct Hidden {
-  int low, low_end, high, high_end;
-};
-__device__ __forceinline__ Hidden hidden_of(const ChunkParams& p, int pos, int n, int len) {
-  Hidden h{0, 0, max(pos + 1, 0), 0};
-  const int hi = pos + n;                                // the block's tokens
-  h.high_end = static_cast<int>(min(int64_t(len), (int64_t(hi - 1) / kTile + 1) * kTile));
-  if (p.window > 0 && hi - 1 >= p.window) {
-    h.low_end = hi - p.window;
-    h.low = (pos >= p.window ? pos - p.window + 1 : 0) / kTile * kTile;
-  }
-  return h;
-}
-// Whether one of them has such a value among the channels [c0, c1) (a warp).
-static __device__ __noinline__ bool hidden_values(const ChunkParams& p, bool e4m3, int row, int kvh, int pos, int n, int len, int c0,
-                                                  int c1) {
-  const int lane = threadIdx.x & 31;
-  const Hidden h = hidden_of(p, pos, n, len);
-  bool found = false;
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const int from = part == 0 ? h.low : h.high, to = part == 0 ? h.low_end : h.high_end;
-#pragma unroll 1
-    for (int j = from + lane; j < to; j += 32) {
-      const int64_t at = token_at(p, row, kvh, j);
-#pragma unroll 1
-      for (int c = c0; at >= 0 && c < c1; ++c) found |= !isfinite(bf16_or_e4m3(p.v, e4m3, at + c));
-    }
-  }
-  return __any_sync(0xffffffffu, found);
-}
-// One row's channels [c0, c1) again (a warp): the query at q, position pos, to out.
-static __device__ __noinline__ void repair_row(const ChunkParams& p, bool e4m3, const uint16_t* q, int row, int kvh, int pos, int c0,
-                                               int c1, uint16_t* out) {
-  constexpr int kEach = MOE_W4A16_MAX_HEAD_DIM / 32;     // channels of a lane
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f, o[kEach];
-#pragma unroll 1
-  for (int k = 0; k < kEach; ++k) o[k] = 0.f;
-#pragma unroll 1
-  for (int j0 = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0; j0 <= pos; j0 += 32) {
-    const int64_t at = j0 + lane <= pos ? token_at(p, row, kvh, j0 + lane) : -1;
-    float s = -INFINITY;
-    if (at >= 0) {
-      s = 0.f;
-#pragma unroll 1
-      for (int d = 0; d < p.dim; ++d) s = fmaf(bf16_to_f32(q[d]), bf16_or_e4m3(p.k, e4m3, at + d), s);
-      s *= p.score_scale;
-    }
-    float top = s;
-#pragma unroll 1
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    top = fmaxf(top, m);
-    const float base = top == -INFINITY ? 0.f : top, keep = exp2_fast(m - base), e = at >= 0 ? exp2_fast(s - base) : 0.f;
-    float sum = e;
-#pragma unroll 1
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * keep + sum;
-    m = top;
-#pragma unroll 1
-    for (int k = 0; k < kEach; ++k) o[k] *= keep;
-#pragma unroll 1
-    for (int t = 0; t < 32; ++t) {
-      const int64_t v = __shfl_sync(0xffffffffu, at, t);
-      const float w = __shfl_sync(0xffffffffu, e, t);
-#pragma unroll 1
-      for (int k = 0; v >= 0 && k < kEach; ++k)
-        if (c0 + 32 * k + lane < c1) o[k] = fmaf(w, bf16_or_e4m3(p.v, e4m3, v + c0 + 32 * k + lane), o[k]);
-    }
-  }
-  const float inv = l == 0.f ? 0.f : p.v_scale / l;
-#pragma unroll 1
-  for (int k = 0; k < kEach; ++k)
-    if (c0 + 32 * k + lane < c1) out[c0 + 32 * k + lane] = f32_to_bf16_rn(o[k] * inv);
-}
-
-// Rows `none` of a warp's, if need be: each lane's token of q, position and head; table row, first position, tokens of the block
-// and of its sequence.
-static __device__ __noinline__ void repair_rows(const ChunkParams& p, bool e4m3, uint32_t none, int token, int pos, int head, int row,
-                                                int pos0, int n, int len, int c0, int c1) {
-  __syncwarp();
-  const int kvh = __shfl_sync(0xffffffffu, head, __ffs(none) - 1) / p.group;
-  if (!hidden_values(p, e4m3, row, kvh, pos0, n, len, c0, c1)) return;
-  for (; none != 0; none &= none - 1) {
-    const int r = __ffs(none) - 1, t = __shfl_sync(0xffffffffu, token, r), h = __shfl_sync(0xffffffffu, head, r);
-    repair_row(p, e4m3, p.q + t * p.q_stride + int64_t(h) * p.dim, row, kvh, __shfl_sync(0xffffffffu, pos, r), c0, c1,
-               p.out + (int64_t(t) * p.heads + h) * p.dim);
-  }
-}
+// A row of this CTA's outputs has a channel that is infinite or no number (a call: rare, and out of the way of the code around it).
+static __device__ __noinline__ void flag_none(Record* records) { atomicExch(&records[blockIdx.x].none, 1); }
 
 template <int DP, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ PageMaps maps,
@@ -793,7 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const int rows = p.kv_heads * blocks.count, step = C::kStreams * blocks.tokens;
 
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) records[blockIdx.x].np = 0;
+  if (threadIdx.x == 0) {
+    records[blockIdx.x].np = 0;
+    records[blockIdx.x].none = 0;
+  }
   // (set up while the others look for the share)
   if (warp == 12 && lane == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -1189,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // 64 that are theirs (a thread a row stores to 32 lines at once, four times as long). A lane has rows lane / 4 + 8 q.
             float g0[4], g1[4];
             int64_t at[4];
-            uint32_t zero[4] = {0u, 0u, 0u, 0u};             // of its channels: zeros, or no numbers
+            uint32_t none = 0u;             // of its channels: zeros, or no numbers (repair_kernel's)
             const int64_t off = valid ? out_row * p.dim : -1;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1229,23 +1125,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 if (at[q] >= 0 && ch < p.dim) {
                   *reinterpret_cast<uint4*>(p.out + at[q] + ch) = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) zero[q] = fma_bf16x2(w[j], 0u, zero[q]);
+                  for (int j = 0; j < 4; ++j) none = fma_bf16x2(w[j], 0u, none);
                 }
               }
             }
-            // a channel that is infinite or no number, in a row whose sum is one (no number: its scores')
-            if (__any_sync(0xffffffffu, ((zero[0] | zero[1] | zero[2] | zero[3]) & 0x7fff7fffu) != 0u)) {
-              uint32_t none = 0;
-#pragma unroll 1
-              for (int q = 0; q < 4; ++q)
-                for (uint32_t b = __ballot_sync(0xffffffffu, ((q == 0 ? zero[0] : q == 1 ? zero[1] : q == 2 ? zero[2] : zero[3]) & 0x7fff7fffu) != 0u);
-                     b != 0; b &= b - 1)
-                  none |= 1u << (8 * q + (__ffs(b) - 1) / 4);
-              none &= __ballot_sync(0xffffffffu, valid && l == l);
-              if (none != 0)
-                repair_rows(p, E4M3, none, pc.token + token, pc.pos + token, head_of(pc), pc.row, pc.pos, pc.n, pc.len, from, min(to, p.dim));
-            }
+            if ((none & 0x7fff7fffu) != 0u) flag_none(records);
           } else {
+            float zero = 0.f;
 #pragma unroll 1
             for (int c = from; c < min(to, p.dim); c += 16) {
               uint32_t o[16];
@@ -1260,13 +1146,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               if (valid) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) __stcg(part + (2 + c + j) * C::kPartRows, __uint_as_float(o[j]));
+                for (int j = 0; j < 16; ++j) {
+                  __stcg(part + (2 + c + j) * C::kPartRows, __uint_as_float(o[j]));
+                  zero = fmaf(__uint_as_float(o[j]), 0.f, zero);
+                }
               }
             }
+            if (zero != 0.f) flag_none(records);
           }
         }
-        if (pc.np > 1 && threadIdx.x == 0)
-          records[blockIdx.x] = Record{pc.np, pc.token, pc.n, pc.r, pc.pos, pc.row, pc.len, 0};
+        if (pc.np > 1 && threadIdx.x == 0) {
+          Record& rec = records[blockIdx.x];               // (but for the flag)
+          rec.np = pc.np;
+          rec.token = pc.token;
+          rec.n = pc.n;
+          rec.r = pc.r;
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -1603,6 +1498,7 @@ __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, 
   using C = Cfg<DP, E4M3>;
   static_assert(kMaxCtas <= 2 * kRows, "a thread looks at two records");
   __shared__ int list[kMaxCtas], counts[2 * kRows / 32];
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool is[2];
   uint32_t found[2];
@@ -1636,7 +1532,6 @@ __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, 
     const int blk = rec.r % blocks.count, head = rec.r / blocks.count * p.group + blk * blocks.heads + hrow;
     const bool valid = trow < blocks.tokens && t < rec.n && blk * blocks.heads + hrow < p.group;
     const int64_t row = int64_t(rec.token + t) * p.heads + head;
-    bool none = false;                                     // a channel that is infinite or no number, of a sum that is one
     if (valid) {
       const int prow = s * kRows + threadIdx.x;
       auto part_at = [&](int i) { return parts + (int64_t(c + i) * 2 + (i == 0 ? 1 : 0)) * C::kPartFloats + prow; };
@@ -1656,21 +1551,214 @@ __global__ void __launch_bounds__(kRows) chunk_join_kernel(const ChunkParams p, 
         for (int k = 0; k < 16; ++k) o[k] = fmaf(f, __ldcg(src + (2 + ch + k) * C::kPartRows), o[k]);
       }
       const float inv = l == 0.f ? 0.f : p.v_scale / l;
-      float zero = 0.f;
       uint32_t w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        zero = fmaf(o[2 * k] * inv, 0.f, fmaf(o[2 * k + 1] * inv, 0.f, zero));
-        w[k] = pack_bf16x2_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-      }
-      none = zero != 0.f && l == l;
+      for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
       uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.dim + ch);
       dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
       dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       if (ch == 0 && p.lse != nullptr) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
     }
-    const uint32_t rows = __ballot_sync(0xffffffffu, none);
-    if (rows != 0) repair_rows(p, E4M3, rows, rec.token + t, rec.pos + t, head, rec.row, rec.pos, rec.n, rec.len, ch, ch + 16);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// values that are no numbers
+// ---------------------------------------------------------------------------
+// A product takes every token of a tile for every row, those that a row does not see with a probability of zero; a value there
+// that is infinite or no number makes the row's sum one too. The first kernel flags such sums, and then the third looks
+// through the outputs: if a token that some row of a block does not see has such a value, the rows that are none are computed
+// again, token by token, 16 channels where one is, a CTA a row. That takes milliseconds for a long row, so it stands where nothing
+// waits for it (GB300, one infinite value in the last token: 7.7 ms for 300 new of 65536 tokens, 8 heads of 128 channels, 0.12
+// without it; 146 ms for 1024 new of 131072 in E4M3, 64 heads, 3.1 without; bound by the latency of the scores' reads).
+// Where nothing is flagged its start and end are 0.8 us of the shortest call, 3 of drafts of 64 sequences, none of prompts (in
+// the join, on a path that is not taken, the same code made calls 2 to 4 us longer), whatever its grid: one CTA an SM.
+constexpr int kRepairThreads = 512, kRepairWarps = kRepairThreads / 32;
+struct RepairShared {
+  uint32_t channels[kRepairWarps];                       // of a row each: those to compute again, 16 a bit
+  float q[MOE_W4A16_MAX_HEAD_DIM], prob[kRepairThreads], most[kRepairWarps], sum[kRepairWarps];
+  int64_t at[kRepairThreads];
+  float out[kRepairThreads * 8];
+};
+
+// Eight channels of a token, from element `at` of the pages on.
+template <bool E4M3>
+__device__ __forceinline__ void load8(const void* pages, int64_t at, float (&x)[8]) {
+  if constexpr (E4M3) {
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + at);
+    uint32_t h[4];
+    e4m3x4_to_f16x4(v.x, h[0], h[1]);
+    e4m3x4_to_f16x4(v.y, h[2], h[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+          : "=f"(x[2 * j]), "=f"(x[2 * j + 1])
+          : "r"(h[j]));
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pages) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+// Place of token j of a sequence in the pages (elements, its head's first channel), -1: not there.
+__device__ __forceinline__ int64_t token_at(const ChunkParams& p, int row, int kvh, int j) {
+  const int page = p.t.tables[row * p.t.table_stride + j / p.t.page_size];
+  if (page < 0 || page >= p.t.num_pages) return -1;
+  return int64_t(page) * p.page_stride + int64_t(j % p.t.page_size) * p.token_stride + int64_t(kvh) * p.head_stride;
+}
+// The tokens that the tiles of a block hold and not all its rows see: behind its first row's, and before its last row's window.
+struct Hidden {
+  int low, low_end, high, high_end;
+};
+__device__ __forceinline__ Hidden hidden_of(const ChunkParams& p, int pos, int n, int len) {
+  Hidden h{0, 0, max(pos + 1, 0), 0};
+  const int hi = pos + n;                                // the block's tokens
+  h.high_end = static_cast<int>(min(int64_t(len), (int64_t(hi - 1) / kTile + 1) * kTile));
+  if (p.window > 0 && hi - 1 >= p.window) {
+    h.low_end = hi - p.window;
+    h.low = (pos >= p.window ? pos - p.window + 1 : 0) / kTile * kTile;
+  }
+  return h;
+}
+// Whether one of them has such a value (every thread of the CTA calls it).
+template <bool E4M3>
+static __device__ bool hidden_values(const ChunkParams& p, int row, int kvh, int pos, int n, int len) {
+  const Hidden h = hidden_of(p, pos, n, len);
+  float zero = 0.f;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int from = part == 0 ? h.low : h.high, to = part == 0 ? h.low_end : h.high_end;
+#pragma unroll 1
+    for (int j = from + static_cast<int>(threadIdx.x); j < to; j += kRepairThreads) {
+      const int64_t at = token_at(p, row, kvh, j);
+      if (at < 0) continue;
+#pragma unroll 1
+      for (int c = 0; c < p.dim; c += 8) {
+        float x[8];
+        load8<E4M3>(p.v, at + c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) zero = fmaf(x[k], 0.f, zero);
+      }
+    }
+  }
+  return __syncthreads_or(zero != 0.f);
+}
+// One row's channels again, 16 for every bit of `channels` (every thread calls it, a token each at a time).
+template <bool E4M3>
+static __device__ void repair_row(const ChunkParams& p, int token, int head, int row, int pos, uint32_t channels, RepairShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, kvh = head / p.group;
+  const uint16_t* q = p.q + token * p.q_stride + int64_t(head) * p.dim;
+  for (int d = tid; d < p.dim; d += kRepairThreads) sh.q[d] = bf16_to_f32(q[d]);
+  const int lanes = p.dim / 8, groups = kRepairThreads / lanes, g = tid / lanes, ch = (tid - g * lanes) * 8;   // of the values
+  float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+#pragma unroll 1
+  for (int64_t j0 = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0; j0 <= pos; j0 += kRepairThreads) {
+    const int64_t at = j0 + tid <= pos ? token_at(p, row, kvh, static_cast<int>(j0) + tid) : -1;
+    float s = -INFINITY;
+    if (at >= 0) {
+      s = 0.f;
+#pragma unroll 2
+      for (int d = 0; d < p.dim; d += 8) {
+        float x[8];
+        load8<E4M3>(p.k, at + d, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(sh.q[d + k], x[k], s);
+      }
+      s *= p.score_scale;
+    }
+    float top = s;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (lane == 0) sh.most[warp] = top;
+    __syncthreads();
+    top = m;
+#pragma unroll
+    for (int w = 0; w < kRepairWarps; ++w) top = fmaxf(top, sh.most[w]);
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2_fast(m - base), e = at >= 0 ? exp2_fast(s - base) : 0.f;
+    m = top;
+    l = fmaf(l, keep, e);
+    sh.prob[tid] = e;
+    sh.at[tid] = at;
+    __syncthreads();                                     // (the next tile's are written behind its first barrier)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] *= keep;
+    if (g < groups) {
+#pragma unroll 2
+      for (int t = g; t < kRepairThreads; t += groups) {
+        const int64_t v = sh.at[t];
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (v >= 0) load8<E4M3>(p.v, v + ch, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = fmaf(sh.prob[t], x[k], o[k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  if (lane == 0) sh.sum[warp] = l;
+  if (g < groups)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sh.out[g * p.dim + ch + k] = o[k];
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kRepairWarps; ++w) l += sh.sum[w];
+  const float inv = l == 0.f ? 0.f : p.v_scale / l;
+  uint16_t* out = p.out + (int64_t(token) * p.heads + head) * p.dim;
+  for (int d = tid; d < p.dim; d += kRepairThreads) {
+    if (!(channels >> (d / 16) & 1u)) continue;
+    float x = 0.f;
+    for (int k = 0; k < groups; ++k) x += sh.out[k * p.dim + d];
+    out[d] = f32_to_bf16_rn(x * inv);
+  }
+  __syncthreads();                                       // (read before the next row's)
+}
+
+// Behind the join: nothing, if no CTA has flagged an output; else all rows of the call, a warp a row until one is none.
+template <int DP, bool E4M3>
+__global__ void __launch_bounds__(kRepairThreads, 1) chunk_repair_kernel(const __grid_constant__ ChunkParams p, const Record* records,
+                                                                         int ctas) {
+  __shared__ RepairShared sh;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int flags = 0;
+  for (int c = threadIdx.x; c < ctas; c += kRepairThreads) flags |= __ldcg(&records[c].none);
+  if (!__syncthreads_or(flags)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int step = Cfg<DP, E4M3>::kStreams * blocks_of(p.group).tokens;
+#pragma unroll 1
+  for (int b = 0; b < p.batch; ++b) {
+    const ChunkRange c = chunk_range(p, b);
+    if (c.row < 0) continue;                             // (all zeros)
+    const int64_t rows = int64_t(c.n) * p.heads;
+#pragma unroll 1
+    for (int64_t r0 = blockIdx.x; r0 < rows; r0 += int64_t(gridDim.x) * kRepairWarps) {
+      const int64_t mine = r0 + int64_t(warp) * gridDim.x;
+      bool none = false;                                 // 16 channels a lane
+      if (mine < rows && lane < p.dim / 16) {
+        const uint32_t* out = reinterpret_cast<const uint32_t*>(p.out + (int64_t(c.first) * p.heads + mine) * p.dim) + lane * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) none |= (out[k] & 0x7f80u) == 0x7f80u || (out[k] & 0x7f800000u) == 0x7f800000u;
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, none);
+      if (lane == 0) sh.channels[warp] = found;
+      if (!__syncthreads_or(found != 0)) continue;
+#pragma unroll 1
+      for (int w = 0; w < kRepairWarps; ++w) {
+        const uint32_t channels = sh.channels[w];
+        if (channels == 0) continue;
+        const int64_t row = r0 + int64_t(w) * gridDim.x;
+        const int i = static_cast<int>(row / p.heads), head = static_cast<int>(row - int64_t(i) * p.heads);
+        const int i0 = i / step * step;                  // its block
+        if (hidden_values<E4M3>(p, c.row, head / p.group, c.base + i0, min(step, c.n - i0), c.base + c.n))
+          repair_row<E4M3>(p, c.first + i, head, c.row, c.base + i, channels, sh);
+      }
+      __syncthreads();                                   // (sh.channels has been read)
+    }
   }
 }
 
@@ -1755,7 +1843,12 @@ static cudaError_t launch(const ChunkParams& p, int device, cudaStream_t stream)
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, chunk_join_kernel<DP, E4M3>, p, static_cast<const Record*>(records),
                          static_cast<const float*>(parts), grid);
-  note_launch(2);
+  if (e != cudaSuccess) return e;
+  // the third waits for both
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kRepairThreads);
+  e = cudaLaunchKernelEx(&cfg, chunk_repair_kernel<DP, E4M3>, p, static_cast<const Record*>(records), grid);
+  note_launch(3);
   return e;
 }
 
