@@ -620,6 +620,16 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_attention(
     int max_pages, const int32_t* lens, const int32_t* seq_ids, int num_seqs, float scale, int window, uint16_t* out,
     float* lse, void* ws, size_t ws_bytes, moe_w4a16_stream_t stream);
 
+/* The same for chunks that may not have fitted into the cache (moe_w4a16_cache_extend):
+ *   positions int32 [num_tokens], as moe_w4a16_cache_append takes them, or NULL: a chunk whose first token's is negative was not
+ *            appended, so that the sequence's last tokens are others; its rows give zeros and -infinity, and nothing is
+ *            recorded here */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_attention_at(
+    const uint16_t* q, int64_t q_stride, int num_tokens, const int32_t* starts, const int32_t* positions, int batch,
+    int num_heads, int num_kv_heads, int head_dim, const moe_w4a16_pages* cache, const int32_t* tables,
+    int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* seq_ids, int num_seqs, float scale,
+    int window, uint16_t* out, float* lse, void* ws, size_t ws_bytes, moe_w4a16_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Rotation of positions. Of a head's channels, `dim` from `offset` on turn in pairs: at position p pair i becomes
  *   a' = magnitude * (a cos w - b sin w),  b' = magnitude * (a sin w + b cos w),  w = p * f_i,

@@ -246,3 +246,78 @@ def test_the_example_with_a_prompt(latent, e4m3, prompt):
     finally:
         sys.path.pop(0)
     decode.main(latent, e4m3, steps=20, prompt=prompt)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_chunk_that_does_not_fit_attends_to_nothing(e4m3):
+    """Two sequences with tokens, one with a chunk that the pool has no room for: its rows are not the tokens that the
+    sequence ends with, so they see none of them; the other sequence's are what they are without it. Then the chunk goes in,
+    a page having been given back."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    cache = PagedCache(1, 8, PAGE, 3, 8, HEADS, KV_HEADS, DIM, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16)
+    rotary = M.Rotary(DIM)
+
+    def step(counts, seqs):
+        starts = i32([0] + [int(x) for x in np.cumsum(counts)])
+        t = sum(counts) + 3
+        q, k, v = rows(g, t, HEADS, DIM), rows(g, t, KV_HEADS, DIM), rows(g, t, KV_HEADS, DIM)
+        seq_rows, pos = cache.extend_chunk(i32(seqs), starts, t)
+        q = cache.append_rotary(0, q, k, v, seq_rows, pos, rotary)
+        return q, starts, pos, cache.attend_chunk(0, q, starts, i32(seqs), 0.125, 0, pos)
+
+    def right(q, starts, out, seqs, at):
+        kp, vp = cache.pages(0)
+        ref = C.attention(q, starts.tolist(), kp, vp, cache.tables.tolist(), cache.lens.tolist(), 0.125, seq_ids=seqs)
+        compare(out[at], ref[0][at], ref[1][at])
+
+    q, starts, pos, out = step([40, 20, 30], [0, 1, 2])                # 3 + 2 + 2 pages of 8
+    right(q, starts, out, [0, 1, 2], slice(0, 90))
+    cache.check()
+    q, starts, pos, out = step([12, 30], [0, 1])                       # the last page, then two of none
+    assert pos.tolist() == list(range(40, 52)) + [-1] * 33 and cache.lens.tolist() == [52, 20, 30]
+    assert (out[12:] == 0).all()
+    right(q, starts, out, [0, 1], slice(0, 12))
+    kp, vp = cache.pages(0)
+    for positions, lse_there in ((pos, False), (None, True)):
+        lse = M.paged_chunk_attention(q, starts, kp, vp, cache.tables, cache.lens, cache.attn_ws, scale=0.125, seq_ids=i32([0, 1]),
+                                      positions=positions)[1]
+        assert torch.isfinite(lse[:12]).all()
+        assert torch.isfinite(lse[32:42]).any() if lse_there else (lse[12:42] == -math.inf).all()
+    assert M.get_device_error(cache.attn_ws) == 0                      # the append's error is the cache's
+    with pytest.raises(M.MoeW4A16Error) as e:
+        cache.check()
+    assert e.value.name == "ERR_CAPACITY"
+    cache.check()
+    cache.free(i32([2]))
+    q, starts, pos, out = step([30, 12], [1, 0])
+    assert cache.lens.tolist() == [64, 50, 0]
+    right(q, starts, out, [1, 0], slice(0, 42))
+    cache.check()
+
+
+def test_the_layer_leaves_a_chunk_out_that_does_not_fit():
+    """DecoderLayer.forward: attention of zeros for it, so that its residual stream differs from its input by the FFN of its
+    own norm alone; the same for a chunk of a sequence without tokens."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    cache = PagedCache(1, 6, PAGE, 2, 8, HEADS, KV_HEADS, DIM)
+    layer, = layer_for(cache, [48], rotary=M.Rotary(DIM))
+    seen = []
+    real = cache.attend_chunk
+    cache.attend_chunk = lambda *a: seen.append(real(*a)) or seen[-1]
+    x, y = rows(g, 48, 512), rows(g, 48, 512)
+    for counts, want in (([30, 18], [30, 18]), ([8, 40], [38, 18])):
+        starts = i32([0, counts[0], sum(counts)])
+        seq_rows, pos = cache.extend_chunk(i32([0, 1]), starts, 48)
+        layer.forward(x, y, seq_rows, pos, chunk=(starts, i32([0, 1])))
+        assert cache.lens.tolist() == want
+    assert (seen[0] != 0).any(2).any(1).all() and (seen[1][:8] != 0).any(2).any(1).all() and (seen[1][8:] == 0).all()
+
+
+def test_positions_of_another_kind_are_refused():
+    q = torch.zeros((5, 8, 64), dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros((3, 16, 2, 64), dtype=torch.bfloat16, device=DEV)
+    ws = M.paged_chunk_workspace(8, 2, 64)
+    for error, positions in ((TypeError, torch.zeros(5, dtype=torch.int64, device=DEV)), (ValueError, i32([0] * 4)),
+                             (ValueError, torch.zeros(5, dtype=torch.int32))):
+        with pytest.raises(error):
+            M.paged_chunk_attention(q, i32([0, 2, 5]), k, k.clone(), i32([[0], [1]]), i32([2, 3]), ws, positions=positions)

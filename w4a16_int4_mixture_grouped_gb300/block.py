@@ -66,6 +66,7 @@ _SIGNATURES = {
     "cache_compact": [_POOL, _P, _P, _L, _I, _I, _P, _P, _P, _P, _P, _SZ, _P],
     "paged_chunk_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
     "paged_chunk_attention": [_P, _L, _I, _P, _I, _I, _I, _I, _PAGES, _P, _L, _I, _P, _P, _I, _F, _I, _P, _P, _P, _SZ, _P],
+    "paged_chunk_attention_at": [_P, _L, _I, _P, _P, _I, _I, _I, _I, _PAGES, _P, _L, _I, _P, _P, _I, _F, _I, _P, _P, _P, _SZ, _P],
     "cache_append_rotary": [_P, _L, _I, _P, _L, _P, _L, _P, _L, _I, _I, _I, _P, _PAGES, _P, _L, _I, _I, _P, _P, _P, _SZ, _P],
     "block_norm": [_P, _L, _P, _L, _I, _P, _I, _P, _P, _I, _I, _F, _F, _F, _P, _L, _P, _L, _P],
 }
@@ -279,13 +280,16 @@ def paged_chunk_attention(q: torch.Tensor, starts: torch.Tensor, k_pages: torch.
                           tables: torch.Tensor, lens: torch.Tensor, ws: torch.Tensor, scale: Optional[float] = None,
                           window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
                           seq_ids: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                          lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                          lse: Optional[torch.Tensor] = None,
+                          positions: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """A chunk of new tokens per sequence over its pages, causal: q [T, H, D] -> (out bf16 [T, H, D], lse float [T, H]).
 
     Rows starts[b] .. starts[b + 1] - 1 of q (starts int32 [B + 1]) are the last tokens of the sequence that row
     seq_ids[b] (default: b) of tables and lens describes, their keys and values appended already. A row sees the tokens
     up to its own, with a window the newest `window` of them. Rows of no chunk are left as they were (as they come from
-    the allocator, where out and lse are not given); out does not overlap q."""
+    the allocator, where out and lse are not given); out does not overlap q. positions int32 [T], as cache_append takes
+    them: a chunk whose first row stands at a negative one did not fit into the cache, and gives zeros and -infinity
+    (without them its rows would be taken for the sequence's last tokens)."""
     _rows_dense(_need(q, "q", _BF16, 3), "q")
     index = q.get_device()
     t, h, d = q.shape
@@ -301,8 +305,9 @@ def paged_chunk_attention(q: torch.Tensor, starts: torch.Tensor, k_pages: torch.
     ta, ts, mp, ns = _table(tables, index)
     out, lse = _attention_out(q, t, h, d, index, out, lse)
     wa, wn = _ws(ws, index)
-    _run("paged_chunk_attention", index, _FN["paged_chunk_attention"], q.data_ptr(), q.stride(0) if t > 1 else h * d, t,
-         starts.data_ptr(), b, h, heads, d, c, ta, ts, mp, _vector(lens, "lens", ns, index),
+    _run("paged_chunk_attention", index, _FN["paged_chunk_attention_at"], q.data_ptr(), q.stride(0) if t > 1 else h * d, t,
+         starts.data_ptr(), None if positions is None else _vector(positions, "positions", t, index), b, h, heads, d, c, ta, ts,
+         mp, _vector(lens, "lens", ns, index),
          None if seq_ids is None else _vector(seq_ids, "seq_ids", b, index), ns, d ** -0.5 if scale is None else scale, window,
          out.data_ptr(), lse.data_ptr(), wa, wn)
     return out, lse

@@ -83,15 +83,17 @@ class PagedCache:
                                k_scale=self.k_scale, v_scale=self.v_scale, seq_ids=seq_ids)[0]
 
     def attend_chunk(self, layer: int, q: torch.Tensor, starts: torch.Tensor, seq_ids: torch.Tensor, scale: float,
-                     window: int = 0) -> torch.Tensor:
+                     window: int = 0, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Causal attention of a chunk of new tokens (already appended) of each of the sequences, grouped heads: rows
-        starts[b] .. starts[b + 1] - 1 are sequence seq_ids[b]'s last tokens. Rows of no chunk give zeros."""
+        starts[b] .. starts[b + 1] - 1 are sequence seq_ids[b]'s last tokens. Rows of no chunk give zeros, and so do, given
+        extend_chunk's positions, the rows of a chunk that did not fit: without them those would be taken for the last tokens
+        that the sequence has."""
         if self.latent:
             raise ValueError("a latent cache is attended one token at a time")
         kp, vp = self.pages(layer)
         return paged_chunk_attention(q, starts, kp, vp, self.tables, self.lens, self.attn_ws, scale=scale, window=window,
                                      k_scale=self.k_scale, v_scale=self.v_scale, seq_ids=seq_ids,
-                                     out=torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device))[0]
+                                     out=torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device), positions=positions)[0]
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor) -> None:
         cache_fork(self.pool, self.refs, self.tables, self.lens, parents, children, self.page_size, self.ws)

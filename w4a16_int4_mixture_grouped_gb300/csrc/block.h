@@ -97,6 +97,7 @@ struct ChunkParams {
   int64_t q_stride;
   int tokens;
   const int32_t* starts;               // [batch + 1]
+  const int32_t* positions;            // [tokens] or null
   int batch, heads, kv_heads, group;
   int dim;
   const void* k;
@@ -132,8 +133,10 @@ __device__ __forceinline__ ChunkRange chunk_range(const ChunkParams& p, int b) {
   }
   c.first = from;
   c.n = to - from;
-  if (!there) {
-    if (c.n > 0) atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
+  // a chunk that did not fit: the sequence's last tokens are not its
+  const bool absent = p.positions != nullptr && c.n > 0 && p.positions[from] < 0;
+  if (!there || absent) {
+    if (!there && c.n > 0) atomicCAS(p.err, 0, MOE_W4A16_ERR_BAD_INDEX);
     c.base = -c.n;                     // its rows see nothing
     return c;
   }

@@ -387,6 +387,19 @@ moe_w4a16_status moe_w4a16_paged_chunk_attention(const uint16_t* q, int64_t q_st
                                                  const int32_t* seq_ids, int num_seqs, float scale, int window,
                                                  uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                                                  moe_w4a16_stream_t stream) {
+  return moe_w4a16_paged_chunk_attention_at(q, q_stride, num_tokens, starts, nullptr, batch, num_heads, num_kv_heads,
+                                            head_dim, cache, tables, table_stride, max_pages, lens, seq_ids, num_seqs,
+                                            scale, window, out, lse, ws, ws_bytes, stream);
+}
+
+moe_w4a16_status moe_w4a16_paged_chunk_attention_at(const uint16_t* q, int64_t q_stride, int num_tokens,
+                                                    const int32_t* starts, const int32_t* positions, int batch,
+                                                    int num_heads, int num_kv_heads, int head_dim,
+                                                    const moe_w4a16_pages* cache, const int32_t* tables,
+                                                    int64_t table_stride, int max_pages, const int32_t* lens,
+                                                    const int32_t* seq_ids, int num_seqs, float scale, int window,
+                                                    uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                                    moe_w4a16_stream_t stream) {
   if (num_tokens < 0 || batch < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || window < 0 ||
       !std::isfinite(scale))
     return MOE_W4A16_ERR_INVALID_ARG;
@@ -409,6 +422,7 @@ moe_w4a16_status moe_w4a16_paged_chunk_attention(const uint16_t* q, int64_t q_st
   p.q_stride = q_stride;
   p.tokens = num_tokens;
   p.starts = starts;
+  p.positions = positions;
   p.batch = batch;
   p.heads = num_heads;
   p.kv_heads = num_kv_heads;

@@ -164,7 +164,8 @@ class DecoderLayer:
         """residual [B, hidden] and its norm y for this layer -> (residual, y normed by next_norm, or None).
 
         Rows are new tokens, seq_ids and positions [B] theirs: one a sequence, or with chunk = (starts, sequences) rows
-        starts[i] .. starts[i + 1] - 1 of sequence sequences[i] (see PagedCache.extend_chunk). The FFN is for B tokens."""
+        starts[i] .. starts[i + 1] - 1 of sequence sequences[i] (see PagedCache.extend_chunk; a chunk that did not fit has
+        an attention of zeros). The FFN is for B tokens."""
         if chunk is not None and self.cache.latent:
             raise ValueError("a latent cache is attended one token at a time")
         q, k, v = self.project(y, positions)
@@ -173,7 +174,7 @@ class DecoderLayer:
         else:
             self.cache.append(self.layer, k, v, seq_ids, positions)
         if chunk is not None:
-            o = self.cache.attend_chunk(self.layer, q, *chunk, self.scale, self.window)
+            o = self.cache.attend_chunk(self.layer, q, *chunk, self.scale, self.window, positions)
         else:
             o = self.cache.attend(self.layer, q, seq_ids, self.scale, self.window)
         residual, y = block_norm(o.view(y.shape[0], -1) @ self.w_o, residual, w_post=self.norm_post_attn,
