@@ -613,7 +613,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_workspace_size(int num_head
  *   starts   int32 [batch + 1], ascending, 0 .. num_tokens; a chunk that does not lie within them is skipped and recorded as
  *            MOE_W4A16_ERR_BAD_INDEX
  *   seq_ids  int32 [batch]: the row of tables and lens of each chunk (NULL: chunk b reads row b)
- *   out      bf16 [num_tokens, num_heads, head_dim] dense, not over q; lse float [num_tokens, num_heads] or NULL */
+ *   out      bf16 [num_tokens, num_heads, head_dim] dense; lse float [num_tokens, num_heads] or NULL; q, out and lse do not
+ *            overlap (INVALID_ARG; out may lie between q's rows) */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_attention(
     const uint16_t* q, int64_t q_stride, int num_tokens, const int32_t* starts, int batch, int num_heads,
     int num_kv_heads, int head_dim, const moe_w4a16_pages* cache, const int32_t* tables, int64_t table_stride,

@@ -152,3 +152,21 @@ def test_constants_and_struct_match_the_header():
     names = [x.strip().split()[-1].lstrip("*") for x in re.sub(r"/\*.*?\*/", "", body, flags=re.S).split(";") if x.strip()]
     assert names == [f[0] for f in P.RotaryDesc._fields_]
     assert set(re.findall(r"\bmoe_w4a16_(rotary\w*)\s*\(", HEADER)) == set(P._SIGNATURES)
+
+
+@pytest.mark.parametrize("out", [16, 8 * 64 * 2, 5 * 8 * 64 * 2 + 1008, -6 * 8 * 64 * 2 + 16, -16])
+def test_chunk_attention_refuses_an_output_that_begins_within_its_queries(out):
+    assert chunk(q=FAKE + (1 << 16), out=FAKE + (1 << 16) + out) == ARG
+
+
+def test_chunk_attention_refuses_an_output_between_rows_that_it_does_not_fit():
+    # rows of 1024 bytes, 3072 apart; outputs of 1024 behind each other run into the next query
+    assert chunk(stride=3 * 8 * 64, out=FAKE + 1024) == ARG and chunk(stride=3 * 8 * 64, out=FAKE + 5 * 3072 - 16) == ARG
+
+
+def test_chunk_attention_refuses_sums_over_its_queries_or_outputs():
+    def call(lse):
+        return B._FN["paged_chunk_attention"](FAKE, 512, 6, FAKE, 2, 8, 2, 64, ctypes.byref(pages()), FAKE, 4, 4, FAKE, None, 2, 0.125, 0,
+                                              FAKE + (1 << 20), lse, FAKE, BIG, None)
+    for lse in (FAKE, FAKE + 6 * 1024 - 4, FAKE + (1 << 20), FAKE + (1 << 20) + 6 * 1024 - 4, FAKE + (1 << 20) - 6 * 8 * 4 + 4):
+        assert call(lse) == ARG

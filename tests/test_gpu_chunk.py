@@ -709,3 +709,35 @@ def test_values_that_are_none_in_a_graph_and_the_calls_after_it():
         for at in places:
             v[at] = math.nan
     assert M.get_device_error(ws) == 0
+
+
+def test_outputs_between_the_queries_rows_and_over_them():
+    """Outputs in a gap of the queries' buffer are theirs alone; any that share a byte with a query are refused."""
+    rng = np.random.default_rng(74)
+    page, n, heads, dim = 16, 9, 4, 64
+    tables, total = tables_for(rng, [200], page)
+    k, v = make_pages(rng, total, page, 2, dim, False)
+    wide = torch.zeros((n, (n + 2) * heads * dim), dtype=torch.bfloat16, device=DEV)
+    q = wide[:, :heads * dim].view(n, heads, dim)
+    q.copy_(queries(rng, n, heads, dim))
+    ws = M.paged_chunk_workspace(heads, 2, dim)
+    args = (i32([0, n]), k, v, i32(tables), i32([200]), ws)
+    want = M.paged_chunk_attention(q.contiguous(), *args)
+    flat, size = wide.view(-1), n * heads * dim
+    for at, fits in ((heads * dim, True), (2 * heads * dim, True), (2 * heads * dim + 8, False), (heads * dim - 8, False),
+                     (wide.stride(0) * 8 + heads * dim, True), (wide.stride(0) * 8 - size + 8, False)):
+        out = flat[at:at + size].view(n, heads, dim)
+        if fits:
+            M.paged_chunk_attention(q, *args, out=out)
+            assert torch.equal(out, want[0])
+        else:
+            with pytest.raises(M.MoeW4A16Error) as e:
+                M.paged_chunk_attention(q, *args, out=out)
+            assert e.value.name == "ERR_INVALID_ARG"
+    sums = flat[heads * dim:heads * dim + 2 * n * heads].view(torch.float32).view(n, heads)
+    M.paged_chunk_attention(q, *args, lse=sums)
+    assert torch.equal(sums, want[1])
+    for lse in (flat[:2 * n * heads], flat[heads * dim - 2:heads * dim - 2 + 2 * n * heads]):
+        with pytest.raises(M.MoeW4A16Error) as e:
+            M.paged_chunk_attention(q, *args, lse=lse.view(torch.float32).view(n, heads))
+        assert e.value.name == "ERR_INVALID_ARG"

@@ -287,7 +287,7 @@ def paged_chunk_attention(q: torch.Tensor, starts: torch.Tensor, k_pages: torch.
     Rows starts[b] .. starts[b + 1] - 1 of q (starts int32 [B + 1]) are the last tokens of the sequence that row
     seq_ids[b] (default: b) of tables and lens describes, their keys and values appended already. A row sees the tokens
     up to its own, with a window the newest `window` of them. Rows of no chunk are left as they were (as they come from
-    the allocator, where out and lse are not given); out does not overlap q. positions int32 [T], as cache_append takes
+    the allocator, where out and lse are not given); q, out and lse do not overlap. positions int32 [T], as cache_append takes
     them: a chunk whose first row stands at a negative one did not fit into the cache, and gives zeros and -infinity
     (without them its rows would be taken for the sequence's last tokens)."""
     _rows_dense(_need(q, "q", _BF16, 3), "q")

@@ -23,6 +23,53 @@ bool ws_fits(const void* ws, size_t bytes, size_t need) {
   return ws != nullptr && aligned16(ws) && bytes >= need && bytes >= MOE_W4A16_WS_HEADER_BYTES;
 }
 
+// Places in memory: `tokens` x `heads` rows of `width` bytes.
+struct Rows {
+  int64_t at, tokens, token_stride, heads, head_stride, width;
+  Rows(const void* p, int64_t t, int64_t ts, int64_t h, int64_t hs, int64_t w)
+      : at(static_cast<int64_t>(reinterpret_cast<uintptr_t>(p))), tokens(t), token_stride(ts), heads(h), head_stride(hs), width(w) {
+    if (token_stride == 0) tokens = 1;                     // (a broadcast row is one)
+    if (head_stride == 0) heads = 1;
+    if (heads > 1 && head_stride == width) width *= heads, heads = 1;
+    if (tokens > 1 && token_stride == width) width *= tokens, tokens = 1;
+  }
+  int64_t end() const { return at + (tokens - 1) * token_stride + (heads - 1) * head_stride + width; }
+};
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0) ? 1 : 0); }
+// Whether x + k * stride lies between low and high (neither included) for a k of from .. to.
+bool between(int64_t x, int64_t stride, int64_t from, int64_t to, int64_t low, int64_t high) {
+  if (from > to) return false;
+  if (stride <= 0) return low < x && x < high;
+  const int64_t first = floor_div(low - x, stride) + 1, k = first > from ? first : from;
+  return k <= to && x + k * stride < high;
+}
+// Whether a byte is in both, exactly; the rows of b lie apart from each other. Rows that lie between each other's (queries and keys
+// of one buffer) are no overlap.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.end() <= b.at || b.end() <= a.at) return false;
+  if ((a.tokens == 1 || b.tokens == 1 || a.token_stride == b.token_stride) &&
+      (a.heads == 1 || b.heads == 1 || a.head_stride == b.head_stride)) {
+    // all distances between rows are x + token steps + head steps
+    const int64_t ts = a.tokens > 1 ? a.token_stride : b.token_stride, hs = a.heads > 1 ? a.head_stride : b.head_stride;
+    for (int64_t h = 1 - a.heads; h < b.heads; ++h)
+      if (between(b.at - a.at + h * hs, b.tokens > 1 || a.tokens > 1 ? ts : 0, 1 - a.tokens, b.tokens - 1, -b.width, a.width)) return true;
+    return false;
+  }
+  // row by row of a (rare): b's outer steps near it, then the inner ones
+  const bool by_token = b.heads == 1 || (b.tokens > 1 && b.token_stride >= b.head_stride);
+  const int64_t outer = by_token ? b.tokens : b.heads, outer_step = by_token ? b.token_stride : b.head_stride;
+  const int64_t inner = by_token ? b.heads : b.tokens, inner_step = by_token ? b.head_stride : b.token_stride;
+  const int64_t span = (inner - 1) * inner_step + b.width;
+  for (int64_t t = 0; t < a.tokens; ++t)
+    for (int64_t h = 0; h < a.heads; ++h) {
+      const int64_t x = a.at + t * a.token_stride + h * a.head_stride - b.at;
+      int64_t o = outer > 1 ? floor_div(x - span, outer_step) + 1 : 0;
+      for (o = o < 0 ? 0 : o; o < outer && o * outer_step < x + a.width; ++o)
+        if (between(o * outer_step - x, inner > 1 ? inner_step : 0, 0, inner - 1, -b.width, a.width)) return true;
+    }
+  return false;
+}
+
 // A layer's pages for rows of `heads` heads of `dim` channels.
 moe_w4a16_status check_pages(const moe_w4a16_pages* c, int heads, int dim, bool latent) {
   if (c == nullptr || c->k == nullptr || (c->v == nullptr) != latent) return MOE_W4A16_ERR_INVALID_ARG;
@@ -412,9 +459,17 @@ moe_w4a16_status moe_w4a16_paged_chunk_attention_at(const uint16_t* q, int64_t q
   if (st != MOE_W4A16_OK) return st;
   if (!ws_fits(ws, ws_bytes, need)) return MOE_W4A16_ERR_WORKSPACE;
   if (num_tokens == 0 || batch == 0) return MOE_W4A16_OK;
-  if (q == nullptr || out == nullptr || out == q || lens == nullptr || starts == nullptr || !aligned16(q) || !aligned16(out) ||
-      q_stride % 8 != 0 || q_stride < static_cast<int64_t>(num_heads) * head_dim)
+  const int64_t width = static_cast<int64_t>(num_heads) * head_dim;
+  if (q == nullptr || out == nullptr || lens == nullptr || starts == nullptr || !aligned16(q) || !aligned16(out) ||
+      q_stride % 8 != 0 || q_stride < width)
     return MOE_W4A16_ERR_INVALID_ARG;
+  // outputs are stored while other rows' queries are still to be read
+  const Rows queries(q, num_tokens, 2 * q_stride, 1, 0, 2 * width), outs(out, num_tokens, 2 * width, 1, 0, 2 * width);
+  if (overlap(queries, outs)) return MOE_W4A16_ERR_INVALID_ARG;
+  if (lse != nullptr) {
+    const Rows sums(lse, num_tokens, int64_t(4) * num_heads, 1, 0, int64_t(4) * num_heads);
+    if (overlap(queries, sums) || overlap(outs, sums)) return MOE_W4A16_ERR_INVALID_ARG;
+  }
   if (seq_ids == nullptr && num_seqs < batch) return MOE_W4A16_ERR_INVALID_ARG;
   if (!table_ok(tables, table_stride, max_pages, cache->page_size, num_seqs)) return MOE_W4A16_ERR_INVALID_ARG;
   ChunkParams p{};
