@@ -680,7 +680,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_rotary(const uint16_t* x, int64_t x_str
  * element nearest to the turned key / k_scale, without a rounding to BF16 between); v is written as it is; q, turned by the
  * same positions, goes to q_out. Query rows are turned whatever becomes of their key: a negative position turns back.
  *   q, q_out bf16 [num_tokens, num_q_heads, head_dim], strides between tokens, 16-byte aligned; both NULL: keys and values
- *            alone. q_out may be q (the same address and stride), else the two do not overlap; it does not overlap k or v.
+ *            alone. q_out may be q (the same address and stride), else the two do not overlap; it does not overlap k or v
+ *            (INVALID_ARG; rows may lie between each other's, as queries and keys of one buffer do).
  *   rotary   offset and dim multiples of 8, dim of 16 unless interleaved (else UNSUPPORTED); offset + dim <= head_dim
  * Other arguments as for moe_w4a16_cache_append. */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_cache_append_rotary(

@@ -170,3 +170,21 @@ def test_chunk_attention_refuses_sums_over_its_queries_or_outputs():
                                               FAKE + (1 << 20), lse, FAKE, BIG, None)
     for lse in (FAKE, FAKE + 6 * 1024 - 4, FAKE + (1 << 20), FAKE + (1 << 20) + 6 * 1024 - 4, FAKE + (1 << 20) - 6 * 8 * 4 + 4):
         assert call(lse) == ARG
+
+
+KEYS, VALUES = FAKE + (1 << 20), FAKE + (2 << 20)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=FAKE + 16), dict(qo=FAKE + 1024), dict(qo=FAKE - 1024), dict(q=FAKE + 2 * 1024, qo=FAKE), dict(qo=FAKE + 8192 - 2048, qs=4096),
+    dict(qo=KEYS), dict(qo=KEYS + 2 * 256 + 240), dict(qo=KEYS - 2 * 1024 - 16), dict(qo=VALUES), dict(qo=VALUES + 16),
+    dict(q=KEYS - 1024 + 16, qo=KEYS - 1024 + 16, qs=1024, qos=1024, ks=1024, k=KEYS)])
+def test_append_rotary_refuses_turned_queries_over_its_other_rows(kw):
+    args = dict(q=FAKE, qo=FAKE + (3 << 20), k=KEYS, v=VALUES)
+    args.update(kw)
+    assert append(**args) == ARG
+
+
+def test_append_rotary_refuses_turned_queries_over_a_latent_row():
+    args = dict(c=pages(v=None), v=None, vs=0, heads=1, dim=64, ks=64, qh=8, r=desc(dim=64), q=FAKE, k=KEYS)
+    assert append(qo=KEYS + 64, **args) == ARG

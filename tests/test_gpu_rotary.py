@@ -337,3 +337,24 @@ def test_refusals():
         with pytest.raises(M.MoeW4A16Error) as e:
             M.cache_append_rotary(**{**good, **kw})
         assert e.value.name == name
+
+
+def test_append_turns_queries_beside_keys_and_values_of_one_buffer():
+    """Queries in place, or to a free part of each row, beside the keys and values: refused only where they meet."""
+    rng = np.random.default_rng(75)
+    t, h, kv, d, page = 40, 4, 2, 64, 16
+    pos = np.arange(t)
+    tables, (ka, va) = cache_for(rng, pos, [0], page, (kv, d), False, False)
+    kb, vb = ka.clone(), va.clone()
+    buffer = rows(rng, t, 2 * h + 2 * kv, d)
+    q, k, v, spare = buffer[:, :h], buffer[:, h:h + kv], buffer[:, h + kv:h + 2 * kv], buffer[:, h + 2 * kv:]
+    rotation, ws = M.Rotary(d), M.cache_workspace(0, 1)
+    args = i32(tables), i32([0] * t), i32(pos), rotation, ws
+    want = M.cache_append_rotary(q.contiguous(), k.contiguous(), ka, *args, v=v.contiguous(), v_pages=va)
+    for bad in (buffer[:, 1:1 + h], buffer[:, h + kv + 1:2 * h + kv + 1], buffer[:, h:2 * h], buffer.view(-1)[8:8 + t * h * d].view(t, h, d)):
+        with pytest.raises(M.MoeW4A16Error) as e:
+            M.cache_append_rotary(q, k, kb, *args, v=v, v_pages=vb, q_out=bad)
+        assert e.value.name == "ERR_INVALID_ARG"
+    for out in (spare, q):
+        got = M.cache_append_rotary(q, k, kb, *args, v=v, v_pages=vb, q_out=out)
+        assert got is out and torch.equal(got, want) and torch.equal(ka, kb) and torch.equal(va, vb)

@@ -316,7 +316,17 @@ moe_w4a16_status moe_w4a16_cache_append_rotary(
     if (num_q_heads < 1 || num_q_heads > (1 << 16) || q_stride < width || q_out_stride < width || q_stride % 8 != 0 ||
         q_out_stride % 8 != 0 || (num_tokens > 0 && (q == nullptr || q_out == nullptr)) || !aligned16(q) || !aligned16(q_out))
       return MOE_W4A16_ERR_INVALID_ARG;
-    if (q == q_out && num_tokens > 1 && q_stride != q_out_stride) return MOE_W4A16_ERR_INVALID_ARG;   // rows over other rows
+    if (num_tokens > 0) {
+      // in place, row by row, or apart; and apart from the keys and values, which other threads read meanwhile
+      const Rows turned(q_out, num_tokens, 2 * q_out_stride, 1, 0, 2 * width);
+      const int64_t key_width = int64_t(2) * num_heads * head_dim;
+      if (!(q == q_out && (num_tokens == 1 || q_stride == q_out_stride)) &&
+          overlap(Rows(q, num_tokens, 2 * q_stride, 1, 0, 2 * width), turned))
+        return MOE_W4A16_ERR_INVALID_ARG;
+      if (overlap(Rows(k, num_tokens, 2 * k_stride, 1, 0, key_width), turned) ||
+          (v != nullptr && overlap(Rows(v, num_tokens, 2 * v_stride, 1, 0, key_width), turned)))
+        return MOE_W4A16_ERR_INVALID_ARG;
+    }
     p.q = q;
     p.q_stride = q_stride;
     p.q_out = q_out;
