@@ -667,7 +667,8 @@ typedef struct moe_w4a16_rotary_desc {
 
 /* out = x turned by its positions.
  *   x, out   bf16 [num_tokens, num_heads, head_dim] with any strides (elements) between tokens and between heads; out may be
- *            x (the same address and strides: turned in place), else the two do not overlap. Rows of out do not overlap.
+ *            x (the same address and strides: turned in place), else the two do not overlap (INVALID_ARG; their rows may lie
+ *            between each other's). Rows of out do not overlap.
  *            The wider the power of two, up to 8, that divides head_dim, offset, dim / 2 (interleaved: dim) and the strides, with
  *            pointers aligned alike, the wider the accesses.
  *   positions int32 [num_tokens] */

@@ -188,3 +188,11 @@ def test_append_rotary_refuses_turned_queries_over_its_other_rows(kw):
 def test_append_rotary_refuses_turned_queries_over_a_latent_row():
     args = dict(c=pages(v=None), v=None, vs=0, heads=1, dim=64, ks=64, qh=8, r=desc(dim=64), q=FAKE, k=KEYS)
     assert append(qo=KEYS + 64, **args) == ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=FAKE + 2), dict(out=FAKE + 128), dict(out=FAKE + 256), dict(out=FAKE + 2 * 256 + 126), dict(out=FAKE - 2 * 256 - 126),
+    dict(out=FAKE + 128, xs=128, xh=256), dict(xs=512, xh=64, out=FAKE + 256, os_=512, oh=64, heads=3),
+    dict(xs=64, xh=3 * 64, out=FAKE + 6 * 128 - 2), dict(xs=0, xh=0, out=FAKE + 126, os_=128), dict(xs=1024, xh=0, out=FAKE + 2048 + 126)])
+def test_rotary_refuses_outputs_over_other_rows(kw):
+    assert turn(**kw) == ARG

@@ -358,3 +358,42 @@ def test_append_turns_queries_beside_keys_and_values_of_one_buffer():
     for out in (spare, q):
         got = M.cache_append_rotary(q, k, kb, *args, v=v, v_pages=vb, q_out=out)
         assert got is out and torch.equal(got, want) and torch.equal(ka, kb) and torch.equal(va, vb)
+
+
+def test_outputs_in_the_buffer_of_the_rows():
+    """Both anywhere in one buffer, with strides of all kinds: refused where a byte is in both, else turned as from apart."""
+    rng = np.random.default_rng(76)
+    flat = rows(rng, 6000)
+    kept, met, apart = flat.clone(), 0, 0
+    for trial in range(600):
+        t, h, d = (int(rng.integers(1, n)) for n in (7, 6, 5))
+        d *= 2
+
+        def strides():
+            gaps = [int(x) * int(rng.integers(0, 2)) for x in rng.integers(0, 90, 2)]
+            if rng.integers(0, 2):
+                hs = d + gaps[0]
+                return (h - 1) * hs + d + gaps[1], hs
+            ts = d + gaps[0]
+            return ts, (t - 1) * ts + d + gaps[1]
+
+        so = strides()
+        sx = [so, strides(), tuple(int(x) for x in rng.integers(0, 60, 2))][int(rng.integers(0, 3))]
+        ax, ao = (int(x) for x in rng.integers(0, 400, 2))
+        places = [{a + i * s[0] + j * s[1] + c for i in range(t) for j in range(h) for c in range(d)} for a, s in ((ax, sx), (ao, so))]
+        x, out = (flat.as_strided((t, h, d), s + (1,), a) for a, s in ((ax, sx), (ao, so)))
+        # in place: the same address, and the same strides where there is more than one
+        same = ax == ao and (t == 1 or sx[0] == so[0]) and (h == 1 or sx[1] == so[1])
+        rotation, pos = M.Rotary(2, offset=d - 2), i32(rng.integers(0, 99, t))
+        if places[0] & places[1] and not same:
+            met += 1
+            with pytest.raises(M.MoeW4A16Error) as e:
+                M.rotary(x, pos, rotation, out=out)
+            assert e.value.name == "ERR_INVALID_ARG" and torch.equal(flat, kept)
+        else:
+            apart += 1
+            want = M.rotary(x.contiguous(), pos, rotation)
+            M.rotary(x, pos, rotation, out=out)
+            assert torch.equal(out, want)
+            kept.copy_(flat)
+    assert met > 50 and apart > 50

@@ -405,6 +405,9 @@ moe_w4a16_status moe_w4a16_rotary(const uint16_t* x, int64_t x_stride, int64_t x
   if (!by_token && !by_head) return MOE_W4A16_ERR_INVALID_ARG;
   if (x == out && ((num_tokens > 1 && x_stride != out_stride) || (num_heads > 1 && x_head_stride != out_head_stride)))
     return MOE_W4A16_ERR_INVALID_ARG;
+  if (x != out && overlap(Rows(x, num_tokens, 2 * x_stride, num_heads, 2 * x_head_stride, int64_t(2) * head_dim),
+                          Rows(out, num_tokens, 2 * out_stride, num_heads, 2 * out_head_stride, int64_t(2) * head_dim)))
+    return MOE_W4A16_ERR_INVALID_ARG;
   int64_t units = head_dim | rotary->offset | (rotary->interleaved ? rotary->dim : rotary->dim / 2);
   if (num_tokens > 1) units |= x_stride | out_stride;
   if (num_heads > 1) units |= x_head_stride | out_head_stride;
