@@ -635,9 +635,10 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_paged_chunk_attention_at(
  * Rotation of positions. Of a head's channels, `dim` from `offset` on turn in pairs: at position p pair i becomes
  *   a' = magnitude * (a cos w - b sin w),  b' = magnitude * (a sin w + b cos w),  w = p * f_i,
  * with (a, b) the channels offset + i and offset + i + dim / 2, or, interleaved, offset + 2i and offset + 2i + 1. The
- * other channels are copied. A frequency f_i (radians a token, in double precision) is kept in 1/2^64 of a turn, and
- * p * f_i modulo a turn is taken in whole numbers, so that far positions (negative ones turn back) lose nothing beyond the
- * frequency's own 2^-53; sines, cosines and products are FP32, the result is rounded once.
+ * other channels are copied. A frequency f_i (radians a token, in double precision) is kept in whole 2^-64 turns, off by
+ * one of them and 2^-52 of itself at most, and p * f_i modulo a turn is taken in whole numbers: at position p (a negative
+ * one turns back) the angle is off by |p| (2^-64 + 2^-52 f_i / 2 pi) turns at most (one radian a token at p = 2^27:
+ * less than 2^-27 of a turn), before it is rounded to FP32; sines, cosines and products are FP32, the result is rounded once.
  * ------------------------------------------------------------------------- */
 
 /* Frequencies for contexts longer than the trained one (`trained_length` tokens), by a factor >= 1, in double

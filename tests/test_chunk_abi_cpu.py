@@ -4,6 +4,7 @@ needed."""
 import ctypes
 import os
 import re
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -196,3 +197,32 @@ def test_append_rotary_refuses_turned_queries_over_a_latent_row():
     dict(xs=64, xh=3 * 64, out=FAKE + 6 * 128 - 2), dict(xs=0, xh=0, out=FAKE + 126, os_=128), dict(xs=1024, xh=0, out=FAKE + 2048 + 126)])
 def test_rotary_refuses_outputs_over_other_rows(kw):
     assert turn(**kw) == ARG
+
+
+PI = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)          # to 2^-160
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_frequencies_against_exact_turns(sign):
+    """Each is off by a cut to 2^-64 turns and, for the division and two pi in double precision, 2^-52 of itself: small ones
+    of either sign keep their own bits."""
+    rng = np.random.default_rng(3)
+    given = [1.0, 0.5, 1e-3, 1e-6, 1e-9, 1e-12, 1e-15, 1e-18, 3e-20, 1e-25, 0.0, 6.0, 7.0, 100.0, 12345.678, 2.0 ** -11]
+    given += [float(x) for x in np.exp(rng.uniform(-50, 3, 200))]
+    got = M.rotary_frequencies(2 * len(given), scaling="given", given=[sign * f for f in given]).numpy().view(np.uint64)
+    for f, bits in zip(given, got):
+        want = Fraction(f) / (2 * PI) * 2 ** 64
+        off = (sign * int(bits) - want) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= 1 + want / 2 ** 52, (sign * f, int(bits))
+
+
+def test_scaled_frequencies_turn_as_far_as_exact_ones():
+    """p f_i at far positions, from the frequency in double precision and exact numbers on: |p| (2^-64 + 2^-52 f / 2 pi)
+    turns, and what two ways of computing a power differ by."""
+    for dim, theta in ((128, 1e6), (64, 10000.0)):
+        bits = M.rotary_frequencies(dim, theta).numpy().view(np.uint64)
+        for w, f in zip(bits, C.frequencies(dim, theta)):
+            t = Fraction(f) / (2 * PI)
+            for p in (1, -1, 131071, 1 << 24, (1 << 31) - 1, -(1 << 31)):
+                off = (Fraction(p * int(w), 2 ** 64) - p * t) % 1
+                assert min(off, 1 - off) <= abs(p) * (Fraction(1, 2 ** 64) + t / 2 ** 50)

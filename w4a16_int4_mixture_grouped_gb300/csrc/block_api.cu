@@ -373,12 +373,13 @@ moe_w4a16_status moe_w4a16_rotary_frequencies(int dim, double theta, int scaling
       f = keep * f + (1 - keep) * f / factor;
     }
     if (!std::isfinite(f)) return MOE_W4A16_ERR_INVALID_ARG;
-    const double t = f / two_pi;
-    const double part = t - std::floor(t);                    // turns, modulo one: exact
-    // (two steps, each exact: a double holds no more than 53 of the 64 bits)
+    const double t = std::fabs(f) / two_pi;                   // within 2^-52 of itself, as 2 pi is rounded too
+    const double part = t - std::floor(t);                    // modulo one turn: exact, as t is not negative
+    // 32 bits at a time; what lies below 2^-64 is cut off
     const double top = std::floor(part * 4294967296.0);
     const double rest = std::floor((part * 4294967296.0 - top) * 4294967296.0);
-    turns[i] = (static_cast<uint64_t>(top) << 32) + static_cast<uint64_t>(rest);
+    const uint64_t bits = (static_cast<uint64_t>(top) << 32) + static_cast<uint64_t>(rest);
+    turns[i] = f < 0 ? 0 - bits : bits;
   }
   return MOE_W4A16_OK;
 }

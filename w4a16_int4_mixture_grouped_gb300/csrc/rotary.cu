@@ -1,7 +1,7 @@
 // Rotation of positions: of queries or keys by themselves, and of a step's queries and keys on the way into the cache.
 //
 // A pair (a, b) at position p turns by the angle p f_i. The frequency is kept as f_i / 2 pi modulo one, in units of
-// 2^-64 turns: p times that, modulo 2^64, is the angle modulo a turn with no rounding however far p is (an FP32 product
+// 2^-64 turns: p times that, modulo 2^64, is its angle modulo a turn with no further rounding however far p is (an FP32 product
 // is off by 0.008 radians at position 131072). Its upper half, as a signed number of turns in [-0.5, 0.5), goes to the
 // sine and cosine.
 //
