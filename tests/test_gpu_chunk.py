@@ -741,3 +741,40 @@ def test_outputs_between_the_queries_rows_and_over_them():
         with pytest.raises(M.MoeW4A16Error) as e:
             M.paged_chunk_attention(q, *args, lse=lse.view(torch.float32).view(n, heads))
         assert e.value.name == "ERR_INVALID_ARG"
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n", [2000, 9000])
+@pytest.mark.parametrize("gap", [8.0, 17.0, 20.0])
+@pytest.mark.parametrize("sink", [0, 700])
+def test_many_small_probabilities_behind_a_large_one_over_an_8_bit_cache(sink, gap, n, dim):
+    """One token with a value of zero takes nearly all of the probability, thousands of equal ones `gap` nats below it make
+    the output. Probabilities enter the product as FP16 numbers of 2^8 and more for the largest: off by 2^-11 of themselves, or
+    half of the subnormals' spacing of 2^-24, which is 2^-33 of the largest."""
+    rng = np.random.default_rng(n + dim)
+    page, new, group = 32, 40, 2
+    tables, total = tables_for(rng, [n], page)
+    k = torch.zeros((total, page, 1, dim), dtype=torch.bfloat16, device=DEV)
+    v = (torch.rand((total, page, 1, dim), generator=torch.Generator(device="cuda").manual_seed(n), device="cuda") * 1.5 + 0.5)
+    at = int(tables[0, sink // page]), sink % page, 0
+    k[at + (3,)] = 1.0
+    v[at] = 0.0
+    k, v = k.to(torch.float8_e4m3fn), v.to(torch.bfloat16).to(torch.float8_e4m3fn)
+    q = torch.zeros((new, group, dim), dtype=torch.bfloat16, device=DEV)
+    q[..., 3] = gap
+    ws = M.paged_chunk_workspace(group, 1, dim)
+    out, _ = M.paged_chunk_attention(q, i32([0, new]), k, v, i32(tables), i32([n]), ws, scale=1.0)
+    assert M.get_device_error(ws) == 0
+    values = v.float()[i32(tables)[0, :n // page + 1].long().clamp(min=0)].view(-1, dim)[:n].double()
+    seen = torch.arange(n - new, n, device=DEV) + 1
+    small = math.exp(-gap)
+    sums = torch.cumsum(values, 0)[seen - 1] * small
+    total_p = (1 + (seen - 1) * small)[:, None]
+    want = sums / total_p
+    # the scores' and the exponentials' errors as in chunk_ref: 2 e + 2^-16, and the sums'
+    rel = 2.0 ** -11 + 2 * (dim + 8) * 2.0 ** -23 * gap + 2.0 ** -16 + (n / 16 + 64) * 2.0 ** -23
+    bound = 2.0 ** -8 * 1.01 * want + rel * want + n * 2.0 ** -33 * 2.0 / total_p
+    assert (bound <= 0.1 * want).all()
+    for head in range(group):
+        err = (out[:, head].double() - want).abs()
+        assert (err <= bound).all(), (err / bound).max().item()
