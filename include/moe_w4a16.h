@@ -317,7 +317,7 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_workspace_init(void* ws, size_t ws_byte
 MOE_W4A16_API moe_w4a16_status moe_w4a16_get_device_error(const void* ws, moe_w4a16_stream_t stream, int32_t* code);
 
 /* Diagnostics and tests: sets, for the current device, the limit after which a
- * pipeline wait of a GEMM or the latent attention kernel gives up (default MOE_W4A16_WAIT_LIMIT_NS, about
+ * pipeline wait of a GEMM, the latent or the chunk attention kernel gives up (default MOE_W4A16_WAIT_LIMIT_NS, about
  * two seconds; larger values are INVALID_ARG). A wait that runs out records
  * MOE_W4A16_ERR_DEVICE_TIMEOUT in the workspace error word; the kernel then
  * stops its CTA's pipeline, lets copies already in flight land (those drains

@@ -321,3 +321,47 @@ def test_positions_of_another_kind_are_refused():
                              (ValueError, torch.zeros(5, dtype=torch.int32))):
         with pytest.raises(error):
             M.paged_chunk_attention(q, i32([0, 2, 5]), k, k.clone(), i32([[0], [1]]), i32([2, 3]), ws, positions=positions)
+
+
+@pytest.mark.parametrize("accepted", [0, 2, 4])
+def test_drafts_of_which_some_are_rejected(accepted):
+    """Drafts go into a fork: if all are accepted it takes the sequence's place, else it is freed and the accepted ones' rows
+    go into the sequence. No page is lost, and the attention of the next token is that of the accepted tokens alone."""
+    g = torch.Generator(device="cuda").manual_seed(14)
+    cache = PagedCache(1, 12, PAGE, 2, 8, HEADS, KV_HEADS, DIM)
+    rotary = M.Rotary(DIM)
+
+    def put(seq, q, k, v):
+        starts = i32([0, q.shape[0]])
+        seq_rows, pos = cache.extend_chunk(i32([seq]), starts, q.shape[0])
+        return starts, cache.append_rotary(0, q, k, v, seq_rows, pos, rotary), pos
+
+    def tokens(n):
+        return rows(g, n, HEADS, DIM), rows(g, n, KV_HEADS, DIM), rows(g, n, KV_HEADS, DIM)
+
+    prompt, drafts, last = tokens(46), tokens(4), tokens(1)           # the drafts end in a page of their own
+    put(0, *prompt)
+    cache.fork(i32([0]), i32([1]))
+    starts, q, pos = put(1, *drafts)
+    out = cache.attend_chunk(0, q, starts, i32([1]), 0.125, 0, pos)
+    kp, vp = cache.pages(0)
+    ref = C.attention(q, [0, 4], kp, vp, cache.tables.tolist(), cache.lens.tolist(), 0.125, seq_ids=[1])
+    compare(out, ref[0], ref[1])
+    seq = 1 if accepted == 4 else 0
+    cache.free(i32([1 - seq]))
+    if seq == 0 and accepted:
+        put(0, *(x[:accepted] for x in drafts))
+    starts, q, pos = put(seq, *last)
+    assert cache.lens[seq] == 47 + accepted and int((cache.refs > 0).sum()) == -(-(47 + accepted) // PAGE)
+    got = cache.attend_chunk(0, q, starts, i32([seq]), 0.125, 0, pos)
+    # the same tokens in a cache that never held the rejected ones
+    plain = PagedCache(1, 12, PAGE, 2, 8, HEADS, KV_HEADS, DIM)
+    cache, kept = plain, cache
+    for x in (prompt, [d[:accepted] for d in drafts], last):
+        if x[0].shape[0]:
+            starts, q, pos = put(0, *x)
+    assert torch.equal(got, plain.attend_chunk(0, q, starts, i32([0]), 0.125, 0, pos))
+    kept.free(i32([seq]))
+    assert int((kept.refs != 0).sum()) == 0
+    kept.check()
+    plain.check()

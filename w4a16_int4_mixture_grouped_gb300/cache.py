@@ -51,7 +51,9 @@ class PagedCache:
     def extend_chunk(self, seq_ids: torch.Tensor, starts: torch.Tensor,
                      num_tokens: int) -> Tuple[torch.Tensor, torch.Tensor]:
         """Room for a chunk of starts[b + 1] - starts[b] new tokens of each of the sequences -> (sequence, position) of the
-        num_tokens rows: what append and DecoderLayer.forward take. Rows of no chunk, and of one that did not fit, stand at -1."""
+        num_tokens rows: what append and DecoderLayer.forward take. Rows of no chunk, and of one that did not fit, stand at -1.
+        No call takes tokens back (a length that is lowered by hand leaves pages in use): drafts that may be rejected go into a
+        fork, which takes the sequence's place or is freed."""
         if seq_ids.numel() == 0:
             return tuple(torch.full((num_tokens,), -1, dtype=torch.int32, device=starts.device) for _ in range(2))
         first = self.extend(seq_ids, counts=starts[1:] - starts[:-1])
