@@ -16,8 +16,10 @@
 //   * P is handed over in halves, so that the first half's products run while the second's exponentials are taken.
 //   * 129 to 256 channels: one stream, as its accumulator takes half of TMEM; its scores have two buffers, and the next
 //     tile's are computed during a tile's softmax, which has two threads a row.
-//   * The base of a row's exponents moves when a score passes it by 2^8, not with every new maximum (BF16 probabilities keep
-//     their relative precision, FP32 sums their range), so the accumulator is seldom rescaled.
+//   * The base of a row's exponents moves when a score passes it by 2^8, not with every new maximum, so the accumulator is
+//     seldom rescaled. BF16 probabilities keep their relative precision (2^-8) above the base, FP32 sums their range; what is lost
+//     is a largest probability of one, which is not rounded (as in the attention of single tokens, which has the time for it).
+//     Prompts' errors against 64 bits: 0.0021; against the exact maximum 0.0019, in 607 us for 550; the outputs' own 0.0016.
 //   * Four warps bring the tiles into a ring of 128-byte swizzled ones, each 32 tokens: boxes of 8 to 32 tokens by TMA where
 //     they lie behind each other in a page and all are seen, else token by token with cp.async. E4M3 comes to a buffer of
 //     its own and is converted to FP16 on the way to the ring, exactly.
@@ -28,8 +30,8 @@
 //     number reaches are flagged here and computed again by the third kernel.
 //
 // Measured (GB300; 64 query and 8 cache heads of 128 channels where not said otherwise; floors: HBM at 6.78 TB/s, products at
-// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 543 us (338), a chunk of 1024 tokens over 32768 in E4M3 772 us (563), four
-// drafts of each of 64 sequences of up to 8191 tokens 220 us (196), a window of 1024 over 256 channels 62 us (16).
+// 1919 TFLOP/s): prompts of 3 x up to 4096 tokens 546 us (338), a chunk of 1024 tokens over 32768 in E4M3 781 us (563), four
+// drafts of each of 64 sequences of up to 8191 tokens 221 us (196), a window of 1024 over 256 channels 65 us (16).
 // What bounds a prompt is the way of one stream's tile, about 3300 cycles for both streams' 2048 of products: scores,
 // their maximum, the exponentials (512 of a softmax's 1900 cycles on the special-function pipe), the products' second half.
 // Of registers there are 128 a thread, as 512 threads take all; a split by roles would free some, but the functions that stay
