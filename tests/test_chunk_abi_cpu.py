@@ -161,8 +161,8 @@ def test_chunk_attention_refuses_an_output_that_begins_within_its_queries(out):
 
 
 def test_chunk_attention_refuses_an_output_between_rows_that_it_does_not_fit():
-    # rows of 1024 bytes, 3072 apart; outputs of 1024 behind each other run into the next query
-    assert chunk(stride=3 * 8 * 64, out=FAKE + 1024) == ARG and chunk(stride=3 * 8 * 64, out=FAKE + 5 * 3072 - 16) == ARG
+    # rows of 1024 bytes, 4096 apart; outputs of 1024 behind each other run into the next query
+    assert chunk(stride=4 * 8 * 64, out=FAKE + 1024) == ARG and chunk(stride=4 * 8 * 64, out=FAKE + 5 * 4096 - 16) == ARG
 
 
 def test_chunk_attention_refuses_sums_over_its_queries_or_outputs():
