@@ -778,3 +778,24 @@ def test_many_small_probabilities_behind_a_large_one_over_an_8_bit_cache(sink, g
     for head in range(group):
         err = (out[:, head].double() - want).abs()
         assert (err <= bound).all(), (err / bound).max().item()
+
+
+@pytest.mark.parametrize("dim,e4m3", [(64, False), (128, True), (256, False)])
+def test_a_value_that_is_none_at_the_end_of_32_bits(dim, e4m3):
+    """The last of 2^31 - 64 tokens, most of them without a page: the rows before it see what they do without it."""
+    page, window, heads, n = 64, 100, 4, 30
+    rng = np.random.default_rng(77)
+    k, v = make_pages(rng, 4, page, 1, dim, e4m3)
+    q = queries(rng, n, heads, dim)
+    width = (1 << 25) - 1
+    tables = torch.full((1, width), -1, dtype=torch.int32, device=DEV)
+    tables[0, -3:] = i32([2, 0, 3])
+    ws = M.paged_chunk_workspace(heads, 1, dim)
+    args = (q, i32([0, n]), k, v, tables, i32([width * page]), ws)
+    clean = M.paged_chunk_attention(*args, window=window)
+    ref = C.attention(q, [0, n], k, v, [[2, 0, 3]], [192], dim ** -0.5, window)
+    (v.view(torch.uint8) if e4m3 else v)[3, page - 1, 0, 3] = 0x7F if e4m3 else math.nan
+    out, lse = M.paged_chunk_attention(*args, window=window)
+    assert M.get_device_error(ws) == 0 and torch.equal(lse, clean[1])
+    compare(out[:-1], lse[:-1], *(x[:-1] for x in ref))
+    assert torch.isnan(out[-1, :, 3]).all() and torch.isfinite(out[-1, :, 4:]).all()

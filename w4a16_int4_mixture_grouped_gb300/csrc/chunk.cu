@@ -1635,8 +1635,8 @@ static __device__ bool hidden_values(const ChunkParams& p, int row, int kvh, int
   for (int part = 0; part < 2; ++part) {
     const int from = part == 0 ? h.low : h.high, to = part == 0 ? h.low_end : h.high_end;
 #pragma unroll 1
-    for (int j = from + static_cast<int>(threadIdx.x); j < to; j += kRepairThreads) {
-      const int64_t at = token_at(p, row, kvh, j);
+    for (int64_t j = int64_t(from) + threadIdx.x; j < to; j += kRepairThreads) {      // (lengths end less than a step below 2^31)
+      const int64_t at = token_at(p, row, kvh, static_cast<int>(j));
       if (at < 0) continue;
 #pragma unroll 1
       for (int c = 0; c < p.dim; c += 8) {
